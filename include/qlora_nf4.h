@@ -251,6 +251,111 @@ qlora_status qlora_merge_lora(const qlora_nf4_t* W, const void* A,
                               const void* B, int32_t r, float alpha,
                               void* out, qlora_dtype out_dtype, void* stream);
 
+/* Low-rank adapters of many requests beside one quantized weight (P1 §七:
+ * the frozen base is shared, an adapter is what differs between tasks).  A
+ * pool holds `count` adapters of one width r, all device memory:
+ *   A      bf16 [count, r, K];  B  bf16 [count, N, r];
+ *   scale  fp32 [count], s_a = alpha_a / r_a of each adapter.
+ * r is a multiple of 8, 8 <= r <= 256, and 1 <= count <= 1024; an adapter of
+ * a smaller rank r_a takes the first r_a rows of its A and columns of its B
+ * and zeros behind them (their gradients are then zero as well). */
+typedef struct {
+  const void* A;
+  const void* B;
+  const float* scale;
+  int32_t count;
+  int32_t r;
+} qlora_adapters_t;
+#define QLORA_ADAPTERS_MAX 1024
+
+/* Byte counts for a batch of up to M_max tokens.  Workspace sizes cover every
+ * M in [0, M_max]; a plan has exactly the size of its own M. */
+typedef struct {
+  size_t plan_bytes;    /* plan of M_max tokens */
+  size_t fwd_ws_bytes;  /* workspace of qlora_adapters_fwd for M <= M_max */
+  size_t bwd_ws_bytes;  /* workspace of qlora_adapters_bwd for M <= M_max */
+} qlora_adapters_sizes_t;
+qlora_status qlora_adapters_sizes(int64_t N, int64_t K, int64_t M_max, int32_t r,
+                                  int32_t count, qlora_adapters_sizes_t* out);
+
+/* The plan of one batch: its tokens sorted by adapter.  It depends on the
+ * tokens' adapters alone, so one plan serves the forward and the backward
+ * pass of every linear layer of a step.
+ *   index  device int32 [M], the adapter of every token, in any order; a
+ *          value outside [0, count) means no adapter;
+ *   plan   device, at least plan_bytes of (M, count), written by the call.
+ * 0 <= M < 2^24. */
+qlora_status qlora_adapters_plan(const int32_t* index, int64_t M, int32_t count,
+                                 void* plan, size_t plan_bytes, void* stream);
+
+/* The linear layer of a batch whose tokens carry different adapters, bf16
+ * compute: with a the adapter of token m,
+ *   Y[m] = X[m]·Ŵᵀ + s_a·(X[m]·A_aᵀ)·B_aᵀ   (no second term without one),
+ * accumulated in fp32 and rounded once.
+ *   X, Y, y_dtype as in qlora_linear_fwd;
+ *   plan    of this M and of the pool's count (qlora_adapters_plan);
+ *   T_save  device fp32 [M, r] receiving T[m] = X[m]·A_aᵀ (zeros for a token
+ *           without an adapter), or NULL.
+ * Limits as for qlora_linear_fwd, r·max(N, K) < 2^30 and 6·M·round_up(r, 32) < 2^31.
+ * An adapter that no token carries is not read.  A NaN or infinity in a
+ * token's X reaches no other token's outputs. */
+qlora_status qlora_adapters_fwd(const qlora_nf4_t* W, const void* X, int64_t M,
+                                const qlora_adapters_t* adapters, const void* plan,
+                                size_t plan_bytes, void* Y, qlora_dtype y_dtype,
+                                float* T_save, void* ws, size_t ws_bytes, void* stream);
+
+/* Its gradients, the frozen weight excepted: with U[m] = dY[m]·B_a,
+ *   dX[m] = dY[m]·Ŵ + s_a·U[m]·A_a,
+ *   dA_a = s_a·Σ U[m]ᵀ·X[m],  dB_a = s_a·Σ dY[m]ᵀ·T[m]  over the tokens of a.
+ *   T_saved  device fp32 [M, r] from qlora_adapters_fwd, or NULL to recompute;
+ *   dX       device [M, K], bf16 or fp32 (dx_dtype);
+ *   dA, dB   device fp32 [count, r, K] and [count, N, r], overwritten: zeros
+ *            for an adapter without tokens.
+ * Sums over tokens run in a fixed order: equal calls give equal bits. */
+qlora_status qlora_adapters_bwd(const qlora_nf4_t* W, const void* X, const void* dY,
+                                int64_t M, const qlora_adapters_t* adapters,
+                                const void* plan, size_t plan_bytes,
+                                const float* T_saved, void* dX, qlora_dtype dx_dtype,
+                                float* dA, float* dB, void* ws, size_t ws_bytes,
+                                void* stream);
+
+/* Distillation from a teacher's top logits: the loss that trains the adapters
+ * of a quantized model on what the 16-bit model answers, and its gradient.
+ * Per token m, with z the student's logits over V columns and t_i the
+ * teacher's k largest logits, at columns c_i:
+ *   p = softmax(t / tau) over the k entries, q = softmax(z / tau) over V,
+ *   loss = w·tau²·Σ_i p_i·(log p_i − log q_{c_i}),
+ *   dZ[v] = w·tau·(q_v − Σ_{i: c_i = v} p_i).
+ *   Z          device [M, ldz], z_dtype QLORA_F32, QLORA_BF16 or QLORA_F16;
+ *              columns [V, ldz) are padding and not read;
+ *   top        device [M, k], top_dtype as z_dtype's choices;
+ *   top_index  device int32 [M, k]; a value outside [0, V) is no entry (a
+ *              row with fewer than k); a column may come twice;
+ *   weight     device fp32 [M], the w of every token, or NULL for 1;
+ *   loss, lse  device fp32 [M]: the loss and log Σ_v exp(z_v / tau); lse may
+ *              be NULL;
+ *   dZ         device [M, ldz] in z_dtype, the gradient of Σ_m loss[m], with
+ *              zeros in the padding columns; it may be Z itself; NULL: the
+ *              loss alone.
+ * 1 <= k <= 512, V <= ldz, 1e-6 <= tau <= 1e6, M·ldz < 2^40, M < 2^31.
+ * A token of weight 0 or without entries has loss 0 and a zero gradient
+ * whatever its logits are.  A logit of −infinity is a masked column (q = 0);
+ * a row whose largest logit is below -1e30 has no columns: loss 0, zero
+ * gradient, lse −infinity.  An entry of logit −infinity has p = 0. */
+qlora_status qlora_distill_fwd(const void* Z, qlora_dtype z_dtype, int64_t M, int64_t V,
+                               int64_t ldz, const void* top, qlora_dtype top_dtype,
+                               const int32_t* top_index, int32_t k, float tau,
+                               const float* weight, float* loss, float* lse, void* dZ,
+                               void* stream);
+
+/* The gradient alone, from the lse that qlora_distill_fwd saved; weight is
+ * then w times the gradient that reaches loss[m].  dZ may be Z itself. */
+qlora_status qlora_distill_bwd(const void* Z, qlora_dtype z_dtype, int64_t M, int64_t V,
+                               int64_t ldz, const void* top, qlora_dtype top_dtype,
+                               const int32_t* top_index, int32_t k, float tau,
+                               const float* lse, const float* weight, void* dZ,
+                               void* stream);
+
 /* Comparison formats of the frozen weight (a second workload: P4 §三, NF4's
  * fp32 block constants before double quantization; P2 §4.1 and P4 trade-off
  * ②, uniform 4-bit integers against NF4; P3 公式导读 2, absmax INT8).  Each

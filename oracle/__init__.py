@@ -33,10 +33,13 @@ Modules:
              output) and its re-quantization
   variants   comparison formats: NF4 without double quantization, absmax
              INT4 and INT8 (fp32 constant per 64-block)
+  adapters   the linear layer of a batch whose tokens carry different
+             adapters, and its gradients
+  distill    the loss against a teacher's top logits, and its gradient
 
 Parity status: every function here is pinned by a ``-m "not gpu"`` test
 against something other than itself (page values, closed forms, brute force,
 finite differences); none is "parity unpinned".
 """
 
-from . import nf4, linalg, int8, footprint, adamw, merge, variants  # noqa: F401
+from . import nf4, linalg, int8, footprint, adamw, merge, variants, adapters, distill  # noqa: F401

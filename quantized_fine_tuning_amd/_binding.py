@@ -30,7 +30,9 @@ EXPORTS = ("qlora_nf4_sizes", "qlora_nf4_quantize", "qlora_dequantize", "qlora_l
            "qlora_time_next_launch", "qlora_adamw_step", "qlora_merge_lora",
            "qlora_quantize_format", "qlora_dequantize_format", "qlora_gemv_format",
            "qlora_linear_fwd_ex", "qlora_linear_bwd_ex", "qlora_linear_fwd_noalloc",
-           "qlora_bench_mfma_peak", "qlora_bench_copy", "qlora_bench_wall_clock_khz")
+           "qlora_bench_mfma_peak", "qlora_bench_copy", "qlora_bench_wall_clock_khz",
+           "qlora_adapters_sizes", "qlora_adapters_plan", "qlora_adapters_fwd", "qlora_adapters_bwd",
+           "qlora_distill_fwd", "qlora_distill_bwd")
 
 QLORA_KERNEL_NONE = 0
 QLORA_KERNEL_FWD_GEMM = 1
@@ -45,6 +47,7 @@ QLORA_FMT_INT4 = 2
 QLORA_FMT_INT8 = 3
 FORMATS = {"nf4": QLORA_FMT_NF4, "int4": QLORA_FMT_INT4, "int8": QLORA_FMT_INT8}
 QLORA_ADAMW_MAX_TENSORS = 8
+QLORA_ADAPTERS_MAX = 1024
 
 
 class QloraError(RuntimeError):
@@ -74,6 +77,16 @@ class qlora_adamw_tensor_t(ctypes.Structure):
 class qlora_qtensor_t(ctypes.Structure):
     _fields_ = [("n_rows", ctypes.c_int64), ("n_cols", ctypes.c_int64), ("format", ctypes.c_int32),
                 ("codes", ctypes.c_void_p), ("absmax", ctypes.c_void_p)]
+
+
+class qlora_adapters_t(ctypes.Structure):
+    _fields_ = [("A", ctypes.c_void_p), ("B", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+                ("count", ctypes.c_int32), ("r", ctypes.c_int32)]
+
+
+class qlora_adapters_sizes_t(ctypes.Structure):
+    _fields_ = [("plan_bytes", ctypes.c_size_t), ("fwd_ws_bytes", ctypes.c_size_t),
+                ("bwd_ws_bytes", ctypes.c_size_t)]
 
 
 def _load():
@@ -130,6 +143,16 @@ def _load():
     lib.qlora_dequantize_format.argtypes = [P(qlora_qtensor_t), vp, i32, vp]
     lib.qlora_gemv_format.argtypes = [P(qlora_qtensor_t), vp, i64, vp, i32, vp]
     for name in ("qlora_quantize_format", "qlora_dequantize_format", "qlora_gemv_format"):
+        getattr(lib, name).restype = i32
+    lib.qlora_adapters_sizes.argtypes = [i64, i64, i64, i32, i32, P(qlora_adapters_sizes_t)]
+    lib.qlora_adapters_plan.argtypes = [vp, i64, i32, vp, sz, vp]
+    lib.qlora_adapters_fwd.argtypes = [P(qlora_nf4_t), vp, i64, P(qlora_adapters_t), vp, sz, vp, i32, vp, vp, sz, vp]
+    lib.qlora_adapters_bwd.argtypes = [P(qlora_nf4_t), vp, vp, i64, P(qlora_adapters_t), vp, sz, vp, vp, i32, vp, vp,
+                                       vp, sz, vp]
+    lib.qlora_distill_fwd.argtypes = [vp, i32, i64, i64, i64, vp, i32, vp, i32, f32, vp, vp, vp, vp, vp]
+    lib.qlora_distill_bwd.argtypes = [vp, i32, i64, i64, i64, vp, i32, vp, i32, f32, vp, vp, vp, vp]
+    for name in ("qlora_adapters_sizes", "qlora_adapters_plan", "qlora_adapters_fwd", "qlora_adapters_bwd",
+                 "qlora_distill_fwd", "qlora_distill_bwd"):
         getattr(lib, name).restype = i32
     return lib
 
@@ -432,6 +455,164 @@ def qlora_merge_lora(W: Nf4Tensor, A, B, r: int, alpha: float, out, stream=None)
     st = W.c_struct()
     _check(lib.qlora_merge_lora(ctypes.byref(st), _ptr(A, "A"), _ptr(B, "B"), r, float(alpha),
                                 _ptr(out, "out"), _dtype(out, "out"), _stream(stream)))
+
+
+def _one_device(stream, **tensors):
+    """Every tensor, and the stream, on the current device: the library
+    launches there."""
+    torch = _torch()
+    for name, t in tensors.items():
+        if t is not None and not t.is_cuda:
+            raise ValueError(f"{name} must be a GPU tensor")
+    want = torch.device("cuda", torch.cuda.current_device())
+    if getattr(stream, "device", want) != want:
+        raise ValueError(f"stream is on {stream.device}, the current device is {want}")
+    for name, t in tensors.items():
+        if t is not None and t.device != want:
+            raise ValueError(f"{name} is on {t.device}, the current device is {want}")
+
+
+class AdapterPool:
+    """`count` low-rank adapters of one width r: A bf16 [count, r, K], B bf16
+    [count, N, r], scale fp32 [count] (alpha / rank of each).  r is a multiple
+    of 8; an adapter of a smaller rank is padded with zero rows of A and zero
+    columns of B."""
+
+    def __init__(self, A, B, scale):
+        torch = _torch()
+        if A is None or A.dim() != 3 or B is None or B.dim() != 3:
+            raise ValueError("A must be [count, r, K] and B [count, N, r]")
+        self.count, self.r, self.n_cols = (int(x) for x in A.shape)
+        self.n_rows = int(B.shape[1])
+        _expect(A, "A", (self.count, self.r, self.n_cols), (torch.bfloat16,))
+        _expect(B, "B", (self.count, self.n_rows, self.r), (torch.bfloat16,))
+        _expect(scale, "scale", (self.count,), (torch.float32,))
+        self.A, self.B, self.scale = A, B, scale
+
+    def c_struct(self) -> qlora_adapters_t:
+        return qlora_adapters_t(_ptr(self.A, "A"), _ptr(self.B, "B"), _ptr(self.scale, "scale"), self.count, self.r)
+
+
+class AdapterPlan:
+    """The tokens of one batch sorted by adapter (qlora_adapters_plan): a
+    device buffer for M tokens and a pool of `count` adapters.  One plan serves
+    both passes of every linear layer of a step."""
+
+    def __init__(self, M: int, count: int, buffer):
+        self.M, self.count, self.buffer = int(M), int(count), buffer
+
+    @classmethod
+    def empty(cls, M: int, count: int, device="cuda"):
+        torch = _torch()
+        n = qlora_adapters_sizes(8, 64, M, 8, count)["plan_bytes"]
+        return cls(M, count, torch.empty(n, dtype=torch.uint8, device=device))
+
+
+def qlora_adapters_sizes(N: int, K: int, M_max: int, r: int, count: int) -> dict:
+    out = qlora_adapters_sizes_t()
+    _check(lib.qlora_adapters_sizes(N, K, M_max, r, count, ctypes.byref(out)))
+    return {name: int(getattr(out, name)) for name, _ in qlora_adapters_sizes_t._fields_}
+
+
+def qlora_adapters_plan(index, plan: AdapterPlan, stream=None) -> None:
+    """index int32 [M]: the adapter of every token; outside [0, count): none."""
+    torch = _torch()
+    _expect(index, "index", (plan.M,), (torch.int32,))
+    _one_device(stream, index=index, plan=plan.buffer)
+    _check(lib.qlora_adapters_plan(_ptr(index, "index"), plan.M, plan.count, _ptr(plan.buffer, "plan"),
+                                   _bytes(plan.buffer, "plan"), _stream(stream)))
+
+
+def _check_adapters(W: Nf4Tensor, X, pool: AdapterPool, plan: AdapterPlan):
+    torch = _torch()
+    if X is None or X.dim() != 2:
+        raise ValueError("X must be [M, K]")
+    _expect(X, "X", (X.shape[0], W.n_cols), (torch.bfloat16,))
+    if (pool.n_rows, pool.n_cols) != (W.n_rows, W.n_cols):
+        raise ValueError(f"the adapters are for a [{pool.n_rows}, {pool.n_cols}] weight, W is "
+                         f"[{W.n_rows}, {W.n_cols}]")
+    if plan.M != X.shape[0] or plan.count != pool.count:
+        raise ValueError(f"the plan is for {plan.M} tokens and {plan.count} adapters, the call has {X.shape[0]} and "
+                         f"{pool.count}")
+    return X.shape[0]
+
+
+def qlora_adapters_fwd(W: Nf4Tensor, X, pool: AdapterPool, plan: AdapterPlan, Y, T_save, ws, stream=None) -> None:
+    """Y[m] = X[m]·Ŵᵀ + s_a·(X[m]·A_aᵀ)·B_aᵀ, a the adapter of token m in the plan."""
+    torch = _torch()
+    M = _check_adapters(W, X, pool, plan)
+    _expect(Y, "Y", (M, W.n_rows), (torch.float32, torch.bfloat16))
+    if T_save is not None:
+        _expect(T_save, "T_save", (M, pool.r), (torch.float32,))
+    _one_device(stream, W=W.codes, X=X, A=pool.A, B=pool.B, scale=pool.scale, plan=plan.buffer, Y=Y, T_save=T_save,
+                ws=ws)
+    st, ad = W.c_struct(), pool.c_struct()
+    _check(lib.qlora_adapters_fwd(ctypes.byref(st), _ptr(X, "X"), M, ctypes.byref(ad), _ptr(plan.buffer, "plan"),
+                                  _bytes(plan.buffer, "plan"), _ptr(Y, "Y"), _dtype(Y, "Y"), _ptr(T_save, "T_save"),
+                                  _ptr(ws, "ws"), _bytes(ws, "ws"), _stream(stream)))
+
+
+def qlora_adapters_bwd(W: Nf4Tensor, X, dY, pool: AdapterPool, plan: AdapterPlan, T_saved, dX, dA, dB, ws,
+                       stream=None) -> None:
+    """dX, and dA, dB of every adapter of the pool (zeros without tokens)."""
+    torch = _torch()
+    M = _check_adapters(W, X, pool, plan)
+    _expect(dY, "dY", (M, W.n_rows), (torch.bfloat16,))
+    if T_saved is not None:
+        _expect(T_saved, "T_saved", (M, pool.r), (torch.float32,))
+    _expect(dX, "dX", (M, W.n_cols), (torch.float32, torch.bfloat16))
+    _expect(dA, "dA", (pool.count, pool.r, W.n_cols), (torch.float32,))
+    _expect(dB, "dB", (pool.count, W.n_rows, pool.r), (torch.float32,))
+    _one_device(stream, W=W.codes, X=X, dY=dY, A=pool.A, B=pool.B, scale=pool.scale, plan=plan.buffer,
+                T_saved=T_saved, dX=dX, dA=dA, dB=dB, ws=ws)
+    st, ad = W.c_struct(), pool.c_struct()
+    _check(lib.qlora_adapters_bwd(ctypes.byref(st), _ptr(X, "X"), _ptr(dY, "dY"), M, ctypes.byref(ad),
+                                  _ptr(plan.buffer, "plan"), _bytes(plan.buffer, "plan"), _ptr(T_saved, "T_saved"),
+                                  _ptr(dX, "dX"), _dtype(dX, "dX"), _ptr(dA, "dA"), _ptr(dB, "dB"), _ptr(ws, "ws"),
+                                  _bytes(ws, "ws"), _stream(stream)))
+
+
+def _check_distill(Z, top, top_index, weight, vocab):
+    torch = _torch()
+    floats = (torch.float32, torch.bfloat16, torch.float16)
+    if Z is None or Z.dim() != 2 or top is None or top.dim() != 2:
+        raise ValueError("Z must be [M, ldz] and top [M, k]")
+    M, ldz = Z.shape
+    _expect(Z, "Z", (M, ldz), floats)
+    _expect(top, "top", (M, top.shape[1]), floats)
+    _expect(top_index, "top_index", (M, top.shape[1]), (torch.int32,))
+    if weight is not None:
+        _expect(weight, "weight", (M,), (torch.float32,))
+    return M, ldz, ldz if vocab is None else int(vocab), top.shape[1]
+
+
+def qlora_distill_fwd(Z, top, top_index, tau: float, weight, loss, lse=None, dZ=None, vocab=None, stream=None) -> None:
+    """loss[m] = w·tau²·KL(softmax(top / tau) || softmax(Z / tau)) per token,
+    its log-sum-exp and, if dZ is given (it may be Z), the gradient of their
+    sum.  vocab: the columns of Z that count (all of them by default)."""
+    torch = _torch()
+    M, ldz, V, k = _check_distill(Z, top, top_index, weight, vocab)
+    _expect(loss, "loss", (M,), (torch.float32,))
+    if lse is not None:
+        _expect(lse, "lse", (M,), (torch.float32,))
+    if dZ is not None:
+        _expect(dZ, "dZ", (M, ldz), (Z.dtype,))
+    _one_device(stream, Z=Z, top=top, top_index=top_index, weight=weight, loss=loss, lse=lse, dZ=dZ)
+    _check(lib.qlora_distill_fwd(_ptr(Z, "Z"), _dtype(Z, "Z"), M, V, ldz, _ptr(top, "top"), _dtype(top, "top"),
+                                 _ptr(top_index, "top_index"), k, float(tau), _ptr(weight, "weight"),
+                                 _ptr(loss, "loss"), _ptr(lse, "lse"), _ptr(dZ, "dZ"), _stream(stream)))
+
+
+def qlora_distill_bwd(Z, top, top_index, tau: float, lse, weight, dZ, vocab=None, stream=None) -> None:
+    """The gradient alone, from the lse of qlora_distill_fwd; dZ may be Z."""
+    torch = _torch()
+    M, ldz, V, k = _check_distill(Z, top, top_index, weight, vocab)
+    _expect(lse, "lse", (M,), (torch.float32,))
+    _expect(dZ, "dZ", (M, ldz), (Z.dtype,))
+    _one_device(stream, Z=Z, top=top, top_index=top_index, weight=weight, lse=lse, dZ=dZ)
+    _check(lib.qlora_distill_bwd(_ptr(Z, "Z"), _dtype(Z, "Z"), M, V, ldz, _ptr(top, "top"), _dtype(top, "top"),
+                                 _ptr(top_index, "top_index"), k, float(tau), _ptr(lse, "lse"),
+                                 _ptr(weight, "weight"), _ptr(dZ, "dZ"), _stream(stream)))
 
 
 class QTensor:

@@ -390,6 +390,200 @@ qlora_status qlora_merge_lora(const qlora_nf4_t* W, const void* A, const void* B
 
 namespace {
 
+qlora_status check_adapter_shape(const char* fn, int32_t r, int32_t count) {
+  if (r < 8 || r > 256 || r % 8 != 0)
+    return fail(QLORA_ERR_INVALID_ARG, "%s: r=%d is not a multiple of 8 in [8, 256]", fn, r);
+  if (count < 1 || count > QLORA_ADAPTERS_MAX)
+    return fail(QLORA_ERR_INVALID_ARG, "%s: count=%d outside [1, %d]", fn, count, QLORA_ADAPTERS_MAX);
+  return QLORA_OK;
+}
+
+// Limits of one pass with adapters: those of a linear pass (qlora_linear_fwd)
+// and the 32-bit byte offsets into one adapter's matrices and into the
+// three-part splits of the low-rank factors.
+qlora_status check_adapter_limits(const char* fn, int64_t M, int64_t N, int64_t K, int32_t r) {
+  const qlora_status st = check_linear_limits(fn, M, N, K, r);
+  if (st != QLORA_OK) return st;
+  const int64_t wide = N > K ? N : K;
+  if (r * wide >= (int64_t(1) << 30))
+    return fail(QLORA_ERR_INVALID_ARG, "%s: r*max(N, K) = %lld elements (limit 2^30)", fn, (long long)(r * wide));
+  if (6 * M * ((r + 31) / 32 * 32) >= (int64_t(1) << 31))
+    return fail(QLORA_ERR_INVALID_ARG, "%s: M=%lld too large for rank %d", fn, (long long)M, r);
+  return QLORA_OK;
+}
+
+qlora_status check_plan(const char* fn, const void* plan, int64_t M, int32_t count, size_t plan_bytes) {
+  CHECK_PTR(plan);
+  if (plan_bytes < qnf4::plan_bytes(M, count))
+    return fail(QLORA_ERR_WORKSPACE_TOO_SMALL, "%s: plan %zu < %zu bytes", fn, plan_bytes, qnf4::plan_bytes(M, count));
+  return QLORA_OK;
+}
+
+// Arguments that both passes with adapters share, the workspace excepted.
+qlora_status check_adapter_args(const char* fn, const qlora_nf4_t* W, const void* X, int64_t M,
+                                const qlora_adapters_t* ad, const void* plan, size_t plan_bytes) {
+  qlora_status st = check_tensor(fn, W);
+  if (st != QLORA_OK) return st;
+  if (ad == nullptr) return fail(QLORA_ERR_INVALID_ARG, "%s: adapters is NULL", fn);
+  if ((st = check_adapter_shape(fn, ad->r, ad->count)) != QLORA_OK) return st;
+  if (M < 0) return fail(QLORA_ERR_INVALID_ARG, "%s: M=%lld < 0", fn, (long long)M);
+  if ((st = check_adapter_limits(fn, M, W->n_rows, W->n_cols, ad->r)) != QLORA_OK) return st;
+  const void* A = ad->A;
+  const void* B = ad->B;
+  const float* scale = ad->scale;
+  CHECK_PTR(A);
+  CHECK_PTR(B);
+  CHECK_PTR(scale);
+  if ((st = check_plan(fn, plan, M, ad->count, plan_bytes)) != QLORA_OK) return st;
+  if (M > 0) CHECK_PTR(X);
+  return QLORA_OK;
+}
+
+qnf4::AdapterView view(const qlora_adapters_t* ad) {
+  return qnf4::AdapterView{static_cast<const uint16_t*>(ad->A), static_cast<const uint16_t*>(ad->B), ad->scale,
+                           ad->count, ad->r};
+}
+qnf4::PlanView plan_of(const void* plan, int64_t M, int32_t count) {
+  return qnf4::plan_view(const_cast<void*>(plan), M, count);
+}
+
+}  // namespace
+
+qlora_status qlora_adapters_sizes(int64_t N, int64_t K, int64_t M_max, int32_t r, int32_t count,
+                                  qlora_adapters_sizes_t* out) {
+  const char* fn = "qlora_adapters_sizes";
+  if (out == nullptr) return fail(QLORA_ERR_INVALID_ARG, "%s: out is NULL", fn);
+  qlora_status st = check_shape(fn, N, K);
+  if (st != QLORA_OK) return st;
+  if ((st = check_adapter_shape(fn, r, count)) != QLORA_OK) return st;
+  if (M_max < 0) return fail(QLORA_ERR_INVALID_ARG, "%s: M_max=%lld < 0", fn, (long long)M_max);
+  if ((st = check_adapter_limits(fn, M_max, N, K, r)) != QLORA_OK) return st;
+  out->plan_bytes = qnf4::plan_bytes(M_max, count);
+  out->fwd_ws_bytes = qnf4::adapters_fwd_ws_max(M_max, N, K, r, count);
+  out->bwd_ws_bytes = qnf4::adapters_bwd_ws_max(M_max, N, K, r, count);
+  return ok();
+}
+
+qlora_status qlora_adapters_plan(const int32_t* index, int64_t M, int32_t count, void* plan, size_t plan_bytes,
+                                 void* stream) {
+  const char* fn = "qlora_adapters_plan";
+  qlora_status st = check_adapter_shape(fn, 8, count);
+  if (st != QLORA_OK) return st;
+  if (M < 0 || M >= (int64_t(1) << 24))
+    return fail(QLORA_ERR_INVALID_ARG, "%s: M=%lld outside [0, 2^24)", fn, (long long)M);
+  if (M > 0) CHECK_PTR(index);
+  if ((st = check_plan(fn, plan, M, count, plan_bytes)) != QLORA_OK) return st;
+  return hip_status(fn, qnf4::launch_adapters_plan(index, M, count, plan_of(plan, M, count),
+                                                   static_cast<hipStream_t>(stream)));
+}
+
+qlora_status qlora_adapters_fwd(const qlora_nf4_t* W, const void* X, int64_t M, const qlora_adapters_t* adapters,
+                                const void* plan, size_t plan_bytes, void* Y, qlora_dtype y_dtype, float* T_save,
+                                void* ws, size_t ws_bytes, void* stream) {
+  const char* fn = "qlora_adapters_fwd";
+  qlora_status st = check_adapter_args(fn, W, X, M, adapters, plan, plan_bytes);
+  if (st != QLORA_OK) return st;
+  if (y_dtype != QLORA_F32 && y_dtype != QLORA_BF16)
+    return fail(QLORA_ERR_UNSUPPORTED_DTYPE, "%s: y_dtype=%d (F32 or BF16)", fn, y_dtype);
+  if (M > 0) CHECK_PTR(Y);
+  CHECK_OPT_PTR(T_save);
+  const qnf4::AdaptersFwdLayout L =
+      qnf4::adapters_fwd_layout(M, W->n_rows, W->n_cols, adapters->r, adapters->count);
+  if (ws_bytes < L.total)
+    return fail(QLORA_ERR_WORKSPACE_TOO_SMALL, "%s: workspace %zu < %zu bytes", fn, ws_bytes, L.total);
+  if (L.total > 0) CHECK_PTR(ws);
+  return hip_status(fn, qnf4::launch_adapters_fwd(view(W), static_cast<const uint16_t*>(X), M, view(adapters),
+                                                  plan_of(plan, M, adapters->count), Y, y_dtype == QLORA_BF16,
+                                                  T_save, static_cast<char*>(ws), L,
+                                                  static_cast<hipStream_t>(stream)));
+}
+
+qlora_status qlora_adapters_bwd(const qlora_nf4_t* W, const void* X, const void* dY, int64_t M,
+                                const qlora_adapters_t* adapters, const void* plan, size_t plan_bytes,
+                                const float* T_saved, void* dX, qlora_dtype dx_dtype, float* dA, float* dB, void* ws,
+                                size_t ws_bytes, void* stream) {
+  const char* fn = "qlora_adapters_bwd";
+  qlora_status st = check_adapter_args(fn, W, X, M, adapters, plan, plan_bytes);
+  if (st != QLORA_OK) return st;
+  if (dx_dtype != QLORA_F32 && dx_dtype != QLORA_BF16)
+    return fail(QLORA_ERR_UNSUPPORTED_DTYPE, "%s: dx_dtype=%d (F32 or BF16)", fn, dx_dtype);
+  CHECK_PTR(dA);
+  CHECK_PTR(dB);
+  if (M > 0) {
+    CHECK_PTR(dY);
+    CHECK_PTR(dX);
+  }
+  CHECK_OPT_PTR(T_saved);
+  const qnf4::AdaptersBwdLayout L =
+      qnf4::adapters_bwd_layout(M, W->n_rows, W->n_cols, adapters->r, adapters->count);
+  if (ws_bytes < L.total)
+    return fail(QLORA_ERR_WORKSPACE_TOO_SMALL, "%s: workspace %zu < %zu bytes", fn, ws_bytes, L.total);
+  if (L.total > 0) CHECK_PTR(ws);
+  return hip_status(fn, qnf4::launch_adapters_bwd(view(W), static_cast<const uint16_t*>(X),
+                                                  static_cast<const uint16_t*>(dY), M, view(adapters),
+                                                  plan_of(plan, M, adapters->count), T_saved, dX,
+                                                  dx_dtype == QLORA_BF16, dA, dB, static_cast<char*>(ws), L,
+                                                  static_cast<hipStream_t>(stream)));
+}
+
+namespace {
+
+bool is_float_dtype(qlora_dtype d) { return d == QLORA_F32 || d == QLORA_BF16 || d == QLORA_F16; }
+
+// Arguments that both passes of the distillation loss share.
+qlora_status check_distill(const char* fn, const void* Z, qlora_dtype z_dtype, int64_t M, int64_t V, int64_t ldz,
+                           const void* top, qlora_dtype top_dtype, const int32_t* top_index, int32_t k, float tau,
+                           const float* weight, const void* dZ) {
+  if (!is_float_dtype(z_dtype) || !is_float_dtype(top_dtype))
+    return fail(QLORA_ERR_UNSUPPORTED_DTYPE, "%s: z_dtype=%d, top_dtype=%d (F32, BF16 or F16)", fn, z_dtype, top_dtype);
+  if (M < 0 || M >= (int64_t(1) << 31))
+    return fail(QLORA_ERR_INVALID_ARG, "%s: M=%lld outside [0, 2^31)", fn, (long long)M);
+  if (V < 1 || ldz < V)
+    return fail(QLORA_ERR_INVALID_ARG, "%s: V=%lld, ldz=%lld (1 <= V <= ldz)", fn, (long long)V, (long long)ldz);
+  if (ldz >= (int64_t(1) << 30) || (M > 0 && ldz > (int64_t(1) << 40) / M))
+    return fail(QLORA_ERR_INVALID_ARG, "%s: ldz or M*ldz too large", fn);
+  if (k < 1 || k > qnf4::kMaxTop) return fail(QLORA_ERR_INVALID_ARG, "%s: k=%d outside [1, %d]", fn, k, qnf4::kMaxTop);
+  if (!(tau >= 1e-6f && tau <= 1e6f)) return fail(QLORA_ERR_INVALID_ARG, "%s: tau=%g outside [1e-6, 1e6]", fn, tau);
+  if (M > 0) {
+    CHECK_PTR(Z);
+    CHECK_PTR(top);
+    CHECK_PTR(top_index);
+  }
+  CHECK_OPT_PTR(weight);
+  CHECK_OPT_PTR(dZ);
+  return QLORA_OK;
+}
+
+}  // namespace
+
+qlora_status qlora_distill_fwd(const void* Z, qlora_dtype z_dtype, int64_t M, int64_t V, int64_t ldz, const void* top,
+                               qlora_dtype top_dtype, const int32_t* top_index, int32_t k, float tau,
+                               const float* weight, float* loss, float* lse, void* dZ, void* stream) {
+  const char* fn = "qlora_distill_fwd";
+  qlora_status st = check_distill(fn, Z, z_dtype, M, V, ldz, top, top_dtype, top_index, k, tau, weight, dZ);
+  if (st != QLORA_OK) return st;
+  if (M > 0) CHECK_PTR(loss);
+  CHECK_OPT_PTR(lse);
+  const qnf4::DistillArgs a{Z, top, top_index, weight, nullptr, loss, lse, dZ, M, V, ldz, k, tau};
+  return hip_status(fn, qnf4::launch_distill(a, z_dtype, top_dtype, static_cast<hipStream_t>(stream)));
+}
+
+qlora_status qlora_distill_bwd(const void* Z, qlora_dtype z_dtype, int64_t M, int64_t V, int64_t ldz, const void* top,
+                               qlora_dtype top_dtype, const int32_t* top_index, int32_t k, float tau, const float* lse,
+                               const float* weight, void* dZ, void* stream) {
+  const char* fn = "qlora_distill_bwd";
+  qlora_status st = check_distill(fn, Z, z_dtype, M, V, ldz, top, top_dtype, top_index, k, tau, weight, dZ);
+  if (st != QLORA_OK) return st;
+  if (M > 0) {
+    CHECK_PTR(lse);
+    CHECK_PTR(dZ);
+  }
+  const qnf4::DistillArgs a{Z, top, top_index, weight, lse, nullptr, nullptr, dZ, M, V, ldz, k, tau};
+  return hip_status(fn, qnf4::launch_distill(a, z_dtype, top_dtype, static_cast<hipStream_t>(stream)));
+}
+
+namespace {
+
 qlora_status check_qtensor(const char* fn, const qlora_qtensor_t* q) {
   if (q == nullptr) return fail(QLORA_ERR_INVALID_ARG, "%s: tensor descriptor is NULL", fn);
   qlora_status st = check_shape(fn, q->n_rows, q->n_cols);

@@ -517,6 +517,7 @@ hipError_t launch_dx_gemm(const Nf4View& W, const uint16_t* dY, int64_t M, const
                               (const uint16_t*)sU, (const uint16_t*)AT2, Rp, dX, db, tm, tk, splits, P, codebook()) \
                : timed_launch(kKernDxGemm, dx_gemm_kernel<LS, false>, dim3(grid), dim3(kThreads), st, W, dY, M, \
                               (const uint16_t*)sU, (const uint16_t*)AT2, Rp, dX, db, tm, tk, splits, P, codebook());
+    QNF4_DX_CASE(0)
     QNF4_DX_CASE(1)
     QNF4_DX_CASE(2)
     QNF4_DX_CASE(3)

@@ -428,6 +428,7 @@ hipError_t launch_fwd_gemm(const Nf4View& W, const uint16_t* X, int64_t M, const
     if (tall) return f16 ? QNF4_FWD_LAUNCH(LS, true, 512) : QNF4_FWD_LAUNCH(LS, false, 512);                 \
     return f16 ? QNF4_FWD_LAUNCH(LS, true, 256) : QNF4_FWD_LAUNCH(LS, false, 256);
   switch (2 * Rp / KSTEP) {
+    QNF4_FWD_CASE(0)
     QNF4_FWD_CASE(1)
     QNF4_FWD_CASE(2)
     QNF4_FWD_CASE(3)

@@ -207,6 +207,70 @@ hipError_t launch_format_dequantize(const uint8_t* codes, const float* absmax, i
 hipError_t launch_format_gemv(const uint8_t* codes, const float* absmax, int fmt, int64_t N, int64_t K,
                               const uint16_t* X, int64_t M, void* Y, bool y_bf16, hipStream_t st);
 
+// Many adapters beside one weight ----------------------------------------------
+constexpr int kMaxAdapters = 1024;
+// A pool of `count` adapters of the same width r: A [count, r, K], B
+// [count, N, r], s [count].
+struct AdapterView {
+  const uint16_t* A;
+  const uint16_t* B;
+  const float* s;
+  int count, r;
+};
+// The plan of one batch (int32 words): which adapter each token carries, and
+// the tokens sorted by adapter.  Written by adapters_plan_kernel; every kernel
+// that reads an index from it checks it against its own bounds.
+struct PlanView {
+  int32_t* head;   // [0] used adapters, [1] tokens with an adapter
+  int32_t* owner;  // [M] adapter of token m, -1: none
+  int32_t* perm;   // [M] sorted position -> token (tokens without an adapter last)
+  int32_t* group;  // [M] sorted position -> number of its used adapter (head[0]: none)
+  int32_t* id;     // [count] used adapter -> adapter
+  int32_t* start;  // [count + 1] its first sorted position
+  int32_t* slot;   // [count] adapter -> used adapter, -1: no token carries it
+};
+size_t plan_bytes(int64_t M, int count);
+PlanView plan_view(void* plan, int64_t M, int count);
+hipError_t launch_adapters_plan(const int32_t* index, int64_t M, int count, const PlanView& pl, hipStream_t st);
+
+struct AdaptersFwdLayout {
+  size_t off_T, off_P, total;
+  int splits;
+};
+struct AdaptersBwdLayout {
+  size_t off_T, off_U, off_P, total;
+  int splits;
+};
+AdaptersFwdLayout adapters_fwd_layout(int64_t M, int64_t N, int64_t K, int r, int count);
+AdaptersBwdLayout adapters_bwd_layout(int64_t M, int64_t N, int64_t K, int r, int count);
+// The largest layout totals over M in [0, M_max].
+size_t adapters_fwd_ws_max(int64_t M_max, int64_t N, int64_t K, int r, int count);
+size_t adapters_bwd_ws_max(int64_t M_max, int64_t N, int64_t K, int r, int count);
+hipError_t launch_adapters_fwd(const Nf4View& W, const uint16_t* X, int64_t M, const AdapterView& ad,
+                               const PlanView& pl, void* Y, bool y16, float* T_save, char* ws,
+                               const AdaptersFwdLayout& L, hipStream_t st);
+hipError_t launch_adapters_bwd(const Nf4View& W, const uint16_t* X, const uint16_t* dY, int64_t M,
+                               const AdapterView& ad, const PlanView& pl, const float* T_saved, void* dX, bool dx16,
+                               float* dA, float* dB, char* ws, const AdaptersBwdLayout& L, hipStream_t st);
+
+// Distillation from a teacher's top logits ---------------------------------------
+constexpr int kMaxTop = 512;
+struct DistillArgs {
+  const void* Z;       // logits [M, ldz]
+  const void* top;     // the teacher's top logits [M, k]
+  const int32_t* at;   // their columns [M, k]; outside [0, V): no entry
+  const float* weight; // [M] or null (1)
+  const float* lse_in; // [M]: the saved log-sum-exp (backward), or null
+  float* loss;         // [M] or null
+  float* lse;          // [M] or null
+  void* dZ;            // [M, ldz] or null
+  int64_t M, V, ldz;
+  int k;
+  float tau;
+};
+// z_type, t_type: 0 fp32, 1 bf16, 2 fp16
+hipError_t launch_distill(const DistillArgs& a, int z_type, int t_type, hipStream_t st);
+
 // Benchmark instrumentation -------------------------------------------------
 constexpr int kPeakWorkgroups = 2048;  // 8 waves per compute unit of an MI355X
 int64_t mfma_peak_flop(int64_t iters);
