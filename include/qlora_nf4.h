@@ -296,7 +296,7 @@ qlora_status qlora_adapters_plan(const int32_t* index, int64_t M, int32_t count,
  *   plan    of this M and of the pool's count (qlora_adapters_plan);
  *   T_save  device fp32 [M, r] receiving T[m] = X[m]·A_aᵀ (zeros for a token
  *           without an adapter), or NULL.
- * Limits as for qlora_linear_fwd, r·max(N, K) < 2^30 and 6·M·round_up(r, 32) < 2^31.
+ * Limits as for qlora_linear_fwd, r·max(N, K) < 2^30 and M·round_up(3r, 64) < 2^30.
  * An adapter that no token carries is not read.  A NaN or infinity in a
  * token's X reaches no other token's outputs. */
 qlora_status qlora_adapters_fwd(const qlora_nf4_t* W, const void* X, int64_t M,

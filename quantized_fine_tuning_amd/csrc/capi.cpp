@@ -407,7 +407,7 @@ qlora_status check_adapter_limits(const char* fn, int64_t M, int64_t N, int64_t 
   const int64_t wide = N > K ? N : K;
   if (r * wide >= (int64_t(1) << 30))
     return fail(QLORA_ERR_INVALID_ARG, "%s: r*max(N, K) = %lld elements (limit 2^30)", fn, (long long)(r * wide));
-  if (6 * M * ((r + 31) / 32 * 32) >= (int64_t(1) << 31))
+  if (2 * M * qnf4::adapter_cols(r) >= (int64_t(1) << 31))
     return fail(QLORA_ERR_INVALID_ARG, "%s: M=%lld too large for rank %d", fn, (long long)M, r);
   return QLORA_OK;
 }

@@ -82,14 +82,20 @@ __device__ __forceinline__ int wswz(int row, int chunk) {
 __device__ __forceinline__ int dq_rg(int l) { return ((l >> 1) & 3) | ((l >> 3) & 4); }
 __device__ __forceinline__ int dq_cg(int l) { return (l & 1) | ((l >> 2) & 6); }
 
-template <int LSTEPS, bool F16>
+// MULTI: the tokens carry different adapters (AdapterGemmArgs): tile rows are
+// sorted positions, dY rows are gathered and output rows scattered through
+// the plan, and the LoRA steps run over the used adapters whose tokens the
+// tile holds, 3r/64 steps each, rounded up (rows of other adapters read as
+// zero; the split reductions share these steps out as they do the n steps).
+template <int LSTEPS, bool F16, bool MULTI = false>
 __global__ __launch_bounds__(kThreads, 1) void dx_gemm_kernel(Nf4View W, const uint16_t* __restrict__ dY,
                                                               int64_t M, const uint16_t* __restrict__ sU,
                                                               const uint16_t* __restrict__ AT2,
                                                               int64_t Rp, void* __restrict__ dX,
                                                               int dx_bf16, int tiles_m, int tiles_k,
                                                               int splits, float* __restrict__ P,
-                                                              Codebook cb) {
+                                                              Codebook cb,
+                                                              std::conditional_t<MULTI, AdapterGemmArgs, NoAdapters> ma) {
   __shared__ __attribute__((aligned(16))) char sa0[TM * 128], sa1[TM * 128];  // A tiles: dY, then sU
   __shared__ __attribute__((aligned(16))) char sw[2][TK * 128];  // B tiles: Ŵᵀ, then AT2
   // per step slot: the row tables of each block column (row 8rg + i at
@@ -112,7 +118,29 @@ __global__ __launch_bounds__(kThreads, 1) void dx_gemm_kernel(Nf4View W, const u
   const int nall = (int)((N + NSTEP - 1) / NSTEP);
   const int nfirst = split_first(sp, splits, nall);
   const int nsteps = split_first(sp + 1, splits, nall) - nfirst;
-  const int lsteps = sp == splits - 1 ? LSTEPS : 0;
+  int lsteps = sp == splits - 1 ? LSTEPS : 0;
+  // MULTI: this workgroup's LoRA steps [lfirst, lfirst + lsteps) of the
+  // tile's; step i belongs to used adapter gfirst + i / lper, chunk i % lper
+  int lfirst = 0, gfirst = 0, lper = 1;
+  if constexpr (MULTI) {
+    const int64_t held = std::min<int64_t>(ma.pl.head[1], M);
+    lper = ma.C / 64;
+    if (m0 < held) {
+      gfirst = ma.pl.group[m0];
+      const int glast = std::min(ma.pl.group[std::min<int64_t>(m0 + TM, held) - 1], ma.count - 1);
+      const int all = gfirst >= 0 && glast >= gfirst ? std::min(glast - gfirst + 1, TM) * lper : 0;
+      lfirst = split_first(sp, splits, all);
+      lsteps = split_first(sp + 1, splits, all) - lfirst;
+    }
+  }
+  // the sorted positions [p0, p1) of LoRA step l's adapter, relative to m0
+  auto rows_of = [&](int l, int& p0, int& p1) __attribute__((always_inline)) {
+    if constexpr (MULTI) {
+      const int g = gfirst + (lfirst + l) / lper;
+      p0 = (int)(ma.pl.start[g] - m0);
+      p1 = (int)(std::min<int64_t>(ma.pl.start[g + 1], M) - m0);
+    }
+  };
   auto sab = [&](int i) { return i ? sa1 : sa0; };
 
   // Slice sigma (columns [32 sigma, +32)) of step t into Ŵᵀ(t): lane (rg, cg)
@@ -278,17 +306,59 @@ __global__ __launch_bounds__(kThreads, 1) void dx_gemm_kernel(Nf4View W, const u
       if (dq) dequant_slice(std::false_type(), s + 1, 2 * wave, read_codes_mfma(s + 1), no_issue);
       __syncthreads();
     }
+    if constexpr (!MULTI) {
 #pragma unroll 1
-    for (int s = nsteps - 1; s < nsteps + lsteps; ++s) {
-      mfma_step(sab(s & 1), sw[s & 1]);
+      for (int s = nsteps - 1; s < nsteps + lsteps; ++s) {
+        mfma_step(sab(s & 1), sw[s & 1]);
+        __syncthreads();
+      }
+    } else {
+      mfma_step(sab((nsteps - 1) & 1), sw[(nsteps - 1) & 1]);
       __syncthreads();
+#pragma unroll 1
+      for (int l = 0; l < lsteps; ++l) {
+        const int s = nsteps + l;
+        int p0, p1;
+        rows_of(l, p0, p1);  // (waves whose rows hold none of the adapter's tokens skip its steps)
+        if (p0 < 128 * wm + 128 && p1 > 128 * wm) mfma_step(sab(s & 1), sw[s & 1]);
+        __syncthreads();
+      }
     }
 
     // epilogue: lane holds rows 128wm + 16i + 4kq + v of column k0 + 64wk + 16j + lr
     int row0 = 128 * wm + 4 * kq, col0 = 64 * wk + lr;
     asm volatile("" : "+v"(row0), "+v"(col0));
     const bool full = (m0 + TM <= M) && (k0 + TK <= K);
-    if (splits > 1) {
+    if constexpr (MULTI) {
+      // rows back to their tokens
+      auto scatter = [&](auto&& put) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int64_t pos = m0 + row0 + 16 * i;
+          if (pos >= M) continue;
+          const int4 tok = *reinterpret_cast<const int4*>(ma.pl.perm + pos);
+          const int t4[4] = {tok.x, tok.y, tok.z, tok.w};
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            if (pos + v < M && (uint64_t)(int64_t)t4[v] < (uint64_t)M) {
+              const int64_t o = (int64_t)t4[v] * K + k0 + col0;
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                if (full || k0 + col0 + 16 * j < K) put(o + 16 * j, acc[i][j][v]);
+            }
+        }
+      };
+      if (splits > 1) {
+        float* const Ps = P + (int64_t)sp * M * K;
+        scatter([&](int64_t o, float v) { Ps[o] = v; });
+      } else if (dx_bf16) {
+        scatter([&](int64_t o, float v) {
+          static_cast<uint16_t*>(dX)[o] = (uint16_t)(pack16<F16>(v, 0.0f) & 0xffffu);
+        });
+      } else {
+        scatter([&](int64_t o, float v) { static_cast<float*>(dX)[o] = v; });
+      }
+    } else if (splits > 1) {
       float* Pp = P + ((int64_t)sp * M + m0 + row0) * K + k0 + col0;
 #pragma unroll
       for (int i = 0; i < 8; ++i)
@@ -347,9 +417,22 @@ __global__ __launch_bounds__(kThreads, 1) void dx_gemm_kernel(Nf4View W, const u
   const int ylch = (lane & 7) ^ rsw(lane >> 3);
   const uint32_t vy = (uint32_t)(((64 * p + (lane >> 3)) * N + 8 * ylch) * 2);
   const uint32_t y_gstride = (uint32_t)(8 * N * 2);
-  const i32x4_t ryw = rsrc_words(dY + m0 * N, (M - m0) * N * 2);
+  const i32x4_t ryw = MULTI ? rsrc_words(dY, M * N * 2) : rsrc_words(dY + m0 * N, (M - m0) * N * 2);
+  // MULTI: the byte offset of each row's token (past every buffer for none);
+  // chunks past a row's end read as zero (they are the next token's)
+  uint32_t vtok[MULTI ? 8 : 1];
+  if constexpr (MULTI) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      const int64_t pos = m0 + 64 * p + 8 * c + (lane >> 3);
+      const int64_t tok = pos < M ? ma.pl.perm[pos] : -1;
+      vtok[c] = (uint64_t)tok < (uint64_t)M ? (uint32_t)((tok * N + 8 * ylch) * 2) : 0x7fffffffu;
+    }
+  }
   auto copy_y_part = [&](char* t, int s, int c) __attribute__((always_inline)) {
-    dma_lds16(ryw, t + (64 * p + 8 * c) * 128, vy + c * y_gstride, (uint32_t)(nfirst + s) * 128u);
+    uint32_t vo = vy + c * y_gstride;
+    if constexpr (MULTI) vo = (int64_t)(nfirst + s) * NSTEP + 8 * ylch < N ? vtok[c] : 0x7fffffffu;
+    dma_lds16(ryw, t + (64 * p + 8 * c) * 128, vo, (uint32_t)(nfirst + s) * 128u);
   };
   auto copy_y = [&](char* t, int s) __attribute__((always_inline)) {
 #pragma unroll
@@ -369,6 +452,36 @@ __global__ __launch_bounds__(kThreads, 1) void dx_gemm_kernel(Nf4View W, const u
       const int lch = (lane & 7) ^ wsw(row);
       buf_load_lds16(rat, t + (64 * p + 8 * c) * 128, (uint32_t)((row * 2 * Rp + 8 * lch) * 2),
                      (uint32_t)l * 128u);
+    }
+  };
+
+  // MULTI: the LoRA step's tiles straight from S and the adapter's transposed
+  // A, each 16-byte chunk from column (64l + 8 chunk) mod r of its part; rows
+  // of other adapters, columns past 3r and rows past K read as zero
+  auto copy_multi = [&](char* ts, char* tf, int l) __attribute__((always_inline)) {
+    if constexpr (MULTI) {
+      const int i = lfirst + l, g = gfirst + i / lper, col0l = 64 * (i % lper);
+      int p0, p1;
+      rows_of(l, p0, p1);
+      const rsrc_t ru3 = make_rsrc(ma.S, M * ma.C * 2);
+      const int colu = col0l + 8 * ylch;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const int row = 64 * p + 8 * c + (lane >> 3);
+        const uint32_t o = (uint32_t)(((m0 + row) * ma.C + colu) * 2);
+        buf_load_lds16(ru3, ts + (64 * p + 8 * c) * 128,
+                       colu < 3 * ma.r && row >= p0 && row < p1 ? o : 0x7fffffffu, 0u);
+      }
+      const int a = ma.by_id ? ma.pl.id[g] : g;
+      const bool ok = (unsigned)a < (unsigned)ma.count;
+      const rsrc_t rf = make_rsrc(ma.F + (int64_t)(ok ? a : 0) * K * ma.r, ok ? K * ma.r * 2 : 0);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const int row = 64 * p + 8 * c + (lane >> 3);
+        const int col = col0l + 8 * ((lane & 7) ^ wsw(row));
+        buf_load_lds16(rf, tf + (64 * p + 8 * c) * 128,
+                       col < 3 * ma.r ? (uint32_t)(((k0 + row) * ma.r + col % ma.r) * 2) : 0x7fffffffu, 0u);
+      }
     }
   };
 
@@ -480,8 +593,12 @@ __global__ __launch_bounds__(kThreads, 1) void dx_gemm_kernel(Nf4View W, const u
   // last reduction step: copy LoRA step 0 (sU and AT2 tiles) into the other
   // buffers; then the LoRA steps
   if (lsteps > 0) {
-    copy_su(sab(nsteps & 1), 0);
-    copy_at(sw[nsteps & 1], 0);
+    if constexpr (MULTI) {
+      copy_multi(sab(nsteps & 1), sw[nsteps & 1], 0);
+    } else {
+      copy_su(sab(nsteps & 1), 0);
+      copy_at(sw[nsteps & 1], 0);
+    }
   }
   wait_vmem();
   __syncthreads();
@@ -489,8 +606,12 @@ __global__ __launch_bounds__(kThreads, 1) void dx_gemm_kernel(Nf4View W, const u
   for (int l = 0; l < lsteps; ++l) {
     const int s = nsteps + l;
     if (l + 1 < lsteps) {
-      copy_su(sab((s + 1) & 1), l + 1);
-      copy_at(sw[(s + 1) & 1], l + 1);
+      if constexpr (MULTI) {
+        copy_multi(sab((s + 1) & 1), sw[(s + 1) & 1], l + 1);
+      } else {
+        copy_su(sab((s + 1) & 1), l + 1);
+        copy_at(sw[(s + 1) & 1], l + 1);
+      }
     }
     wait_vmem();
     __syncthreads();
@@ -514,10 +635,9 @@ hipError_t launch_dx_gemm(const Nf4View& W, const uint16_t* dY, int64_t M, const
 #define QNF4_DX_CASE(LS)                                                                      \
   case LS:                                                                                    \
     return f16 ? timed_launch(kKernDxGemm, dx_gemm_kernel<LS, true>, dim3(grid), dim3(kThreads), st, W, dY, M, \
-                              (const uint16_t*)sU, (const uint16_t*)AT2, Rp, dX, db, tm, tk, splits, P, codebook()) \
+                              (const uint16_t*)sU, (const uint16_t*)AT2, Rp, dX, db, tm, tk, splits, P, codebook(), NoAdapters{}) \
                : timed_launch(kKernDxGemm, dx_gemm_kernel<LS, false>, dim3(grid), dim3(kThreads), st, W, dY, M, \
-                              (const uint16_t*)sU, (const uint16_t*)AT2, Rp, dX, db, tm, tk, splits, P, codebook());
-    QNF4_DX_CASE(0)
+                              (const uint16_t*)sU, (const uint16_t*)AT2, Rp, dX, db, tm, tk, splits, P, codebook(), NoAdapters{});
     QNF4_DX_CASE(1)
     QNF4_DX_CASE(2)
     QNF4_DX_CASE(3)
@@ -530,6 +650,16 @@ hipError_t launch_dx_gemm(const Nf4View& W, const uint16_t* dY, int64_t M, const
     default:
       return hipErrorInvalidValue;
   }
+  return hipGetLastError();
+}
+
+hipError_t launch_dx_gemm_adapters(const Nf4View& W, const uint16_t* dY, int64_t M, const AdapterGemmArgs& ma, void* dX,
+                                   bool dx16, int splits, float* P, hipStream_t st) {
+  const int tm = (int)((M + TM - 1) / TM), tk = (int)((W.K + TK - 1) / TK);
+  const unsigned grid = tile_grid(tm, tk, splits);
+  const uint16_t* none = nullptr;
+  hipLaunchKernelGGL((dx_gemm_kernel<0, false, true>), dim3(grid), dim3(kThreads), 0, st, W, dY, M, none, none,
+                     (int64_t)0, dX, dx16 ? 1 : 0, tm, tk, splits, P, codebook(), ma);
   return hipGetLastError();
 }
 

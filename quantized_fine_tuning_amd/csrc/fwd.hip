@@ -88,14 +88,20 @@ __device__ __forceinline__ int xswz(int row, int chunk) {
 // TMV x (65536 / TMV) output tiles: 256 x 256, or 512 x 128 (the weight
 // rows of a step decoded once for twice the tokens: half the producers'
 // decode per MFMA, twice their X copy).
-template <int LSTEPS, bool F16, int TMV>
+// MULTI: the tokens carry different adapters (AdapterGemmArgs): tile rows are
+// sorted positions, X rows are gathered and output rows scattered through
+// the plan, and the LoRA steps run over the used adapters whose tokens the
+// tile holds, 3r/64 steps each, rounded up (rows of other adapters read as
+// zero; the split reductions share these steps out as they do the K steps).
+template <int LSTEPS, bool F16, int TMV, bool MULTI = false>
 __global__ __launch_bounds__(kThreads, 1) void fwd_gemm_kernel(Nf4View W, const uint16_t* __restrict__ X,
                                                                int64_t M, const uint16_t* __restrict__ sT,
                                                                const uint16_t* __restrict__ B2,
                                                                int64_t Rp, void* __restrict__ Y,
                                                                int y_bf16, int tiles_m, int tiles_n,
                                                                int splits, float* __restrict__ P,
-                                                               Codebook cb) {
+                                                               Codebook cb,
+                                                               std::conditional_t<MULTI, AdapterGemmArgs, NoAdapters> ma) {
   constexpr int TM = TMV, TN = 65536 / TMV;
   constexpr int WGN = TN / 64;           // MFMA waves along N (4 or 2), each 128 x 64
   constexpr int XR = TM / kProdWaves;    // X rows copied per producer and step (64 or 128)
@@ -117,7 +123,29 @@ __global__ __launch_bounds__(kThreads, 1) void fwd_gemm_kernel(Nf4View W, const 
   const int kall = (int)(K / KSTEP);
   const int kfirst = split_first(sp, splits, kall);
   const int ksteps = split_first(sp + 1, splits, kall) - kfirst;
-  const int lsteps = sp == splits - 1 ? LSTEPS : 0;
+  int lsteps = sp == splits - 1 ? LSTEPS : 0;
+  // MULTI: this workgroup's LoRA steps [lfirst, lfirst + lsteps) of the
+  // tile's; step i belongs to used adapter gfirst + i / lper, chunk i % lper
+  int lfirst = 0, gfirst = 0, lper = 1;
+  if constexpr (MULTI) {
+    const int64_t held = std::min<int64_t>(ma.pl.head[1], M);
+    lper = ma.C / 64;
+    if (m0 < held) {
+      gfirst = ma.pl.group[m0];
+      const int glast = std::min(ma.pl.group[std::min<int64_t>(m0 + TM, held) - 1], ma.count - 1);
+      const int all = gfirst >= 0 && glast >= gfirst ? std::min(glast - gfirst + 1, TM) * lper : 0;
+      lfirst = split_first(sp, splits, all);
+      lsteps = split_first(sp + 1, splits, all) - lfirst;
+    }
+  }
+  // the sorted positions [p0, p1) of LoRA step l's adapter, relative to m0
+  auto rows_of = [&](int l, int& p0, int& p1) __attribute__((always_inline)) {
+    if constexpr (MULTI) {
+      const int g = gfirst + (lfirst + l) / lper;
+      p0 = (int)(ma.pl.start[g] - m0);
+      p1 = (int)(std::min<int64_t>(ma.pl.start[g + 1], M) - m0);
+    }
+  };
   auto sxb = [&](int i) { return i ? sx1 : sx0; };
 
   // Resources start at this tile's first row and end at the tensor's last
@@ -181,10 +209,23 @@ __global__ __launch_bounds__(kThreads, 1) void fwd_gemm_kernel(Nf4View W, const 
       mfma_step(sxb(s & 1), sw[s & 1]);
       __syncthreads();
     }
+    if constexpr (!MULTI) {
 #pragma unroll 1
-    for (int s = ksteps - 1; s < ksteps + lsteps; ++s) {
-      mfma_step(sxb(s & 1), sw[s & 1]);
+      for (int s = ksteps - 1; s < ksteps + lsteps; ++s) {
+        mfma_step(sxb(s & 1), sw[s & 1]);
+        __syncthreads();
+      }
+    } else {
+      mfma_step(sxb((ksteps - 1) & 1), sw[(ksteps - 1) & 1]);
       __syncthreads();
+#pragma unroll 1
+      for (int l = 0; l < lsteps; ++l) {
+        const int s = ksteps + l;
+        int p0, p1;
+        rows_of(l, p0, p1);  // (waves whose rows hold none of the adapter's tokens skip its steps)
+        if (p0 < 128 * wm + 128 && p1 > 128 * wm) mfma_step(sxb(s & 1), sw[s & 1]);
+        __syncthreads();
+      }
     }
 
     // epilogue: lane holds rows 128wm + 16i + 4kq + v of column 64wn + 16j + lr.
@@ -193,7 +234,36 @@ __global__ __launch_bounds__(kThreads, 1) void fwd_gemm_kernel(Nf4View W, const 
     int row0 = 128 * wm + 4 * kq, col0 = 64 * wn + lr;
     asm volatile("" : "+v"(row0), "+v"(col0));
     const bool full = (m0 + TM <= M) && (n0 + TN <= N);
-    if (splits > 1) {
+    if constexpr (MULTI) {
+      // rows back to their tokens
+      auto scatter = [&](auto&& put) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int64_t pos = m0 + row0 + 16 * i;
+          if (pos >= M) continue;
+          const int4 tok = *reinterpret_cast<const int4*>(ma.pl.perm + pos);
+          const int t4[4] = {tok.x, tok.y, tok.z, tok.w};
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            if (pos + v < M && (uint64_t)(int64_t)t4[v] < (uint64_t)M) {
+              const int64_t o = (int64_t)t4[v] * N + n0 + col0;
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                if (full || n0 + col0 + 16 * j < N) put(o + 16 * j, acc[i][j][v]);
+            }
+        }
+      };
+      if (splits > 1) {
+        float* const Ps = P + (int64_t)sp * M * N;
+        scatter([&](int64_t o, float v) { Ps[o] = v; });
+      } else if (y_bf16) {
+        scatter([&](int64_t o, float v) {
+          static_cast<uint16_t*>(Y)[o] = (uint16_t)(pack16<F16>(v, 0.0f) & 0xffffu);
+        });
+      } else {
+        scatter([&](int64_t o, float v) { static_cast<float*>(Y)[o] = v; });
+      }
+    } else if (splits > 1) {
       float* Pp = P + ((int64_t)sp * M + m0 + row0) * N + n0 + col0;
 #pragma unroll
       for (int i = 0; i < 8; ++i)
@@ -253,9 +323,19 @@ __global__ __launch_bounds__(kThreads, 1) void fwd_gemm_kernel(Nf4View W, const 
   const int xlch = (lane & 7) ^ rsw(lane >> 3);
   const uint32_t vx = (uint32_t)(((XR * p + (lane >> 3)) * K + 8 * xlch) * 2);
   const uint32_t x_gstride = (uint32_t)(8 * K * 2);
-  const i32x4_t rxw = rsrc_words(X + m0 * K, (M - m0) * K * 2);
+  const i32x4_t rxw = MULTI ? rsrc_words(X, M * K * 2) : rsrc_words(X + m0 * K, (M - m0) * K * 2);
+  // MULTI: the byte offset of each row's token (past every buffer for none)
+  uint32_t vtok[MULTI ? XR / 8 : 1];
+  if constexpr (MULTI) {
+#pragma unroll
+    for (int c = 0; c < XR / 8; ++c) {
+      const int64_t pos = m0 + XR * p + 8 * c + (lane >> 3);
+      const int64_t tok = pos < M ? ma.pl.perm[pos] : -1;
+      vtok[c] = (uint64_t)tok < (uint64_t)M ? (uint32_t)((tok * K + 8 * xlch) * 2) : 0x7fffffffu;
+    }
+  }
   auto copy_x_part = [&](char* t, int s, int c) __attribute__((always_inline)) {
-    dma_lds16(rxw, t + (XR * p + 8 * c) * 128, vx + c * x_gstride, (uint32_t)(kfirst + s) * 128u);
+    dma_lds16(rxw, t + (XR * p + 8 * c) * 128, MULTI ? vtok[c] : vx + c * x_gstride, (uint32_t)(kfirst + s) * 128u);
   };
   auto copy_x = [&](char* t, int s) __attribute__((always_inline)) {
 #pragma unroll
@@ -269,6 +349,33 @@ __global__ __launch_bounds__(kThreads, 1) void fwd_gemm_kernel(Nf4View W, const 
 #pragma unroll
     for (int c = 0; c < RR / 8; ++c)
       buf_load_lds16(r, t + (RR * p + 8 * c) * 128, vl, c * l_gstride + (uint32_t)l * 128u);
+  };
+  // MULTI: the LoRA step's tiles straight from S and the adapter's factor, each
+  // 16-byte chunk from column (64l + 8 chunk) mod r of its part; rows of other
+  // adapters, columns past 3r and rows past N read as zero
+  auto copy_multi = [&](char* ts, char* tf, int l) __attribute__((always_inline)) {
+    if constexpr (MULTI) {
+      const int i = lfirst + l, g = gfirst + i / lper, col = 64 * (i % lper) + 8 * xlch;
+      const bool in = col < 3 * ma.r;
+      int p0, p1;
+      rows_of(l, p0, p1);
+      const rsrc_t rt3 = make_rsrc(ma.S, M * ma.C * 2);
+#pragma unroll
+      for (int c = 0; c < XR / 8; ++c) {
+        const int row = XR * p + 8 * c + (lane >> 3);
+        const uint32_t o = (uint32_t)(((m0 + row) * ma.C + col) * 2);
+        buf_load_lds16(rt3, ts + (XR * p + 8 * c) * 128, in && row >= p0 && row < p1 ? o : 0x7fffffffu, 0u);
+      }
+      const int a = ma.by_id ? ma.pl.id[g] : g;
+      const bool ok = (unsigned)a < (unsigned)ma.count;
+      const rsrc_t rf = make_rsrc(ma.F + (int64_t)(ok ? a : 0) * N * ma.r, ok ? N * ma.r * 2 : 0);
+#pragma unroll
+      for (int c = 0; c < WR / 8; ++c) {
+        const int row = WR * p + 8 * c + (lane >> 3);
+        buf_load_lds16(rf, tf + (WR * p + 8 * c) * 128,
+                       in ? (uint32_t)(((n0 + row) * ma.r + col % ma.r) * 2) : 0x7fffffffu, 0u);
+      }
+    }
   };
   using XRows = std::integral_constant<int, XR>;
   using WRows = std::integral_constant<int, WR>;
@@ -386,8 +493,12 @@ __global__ __launch_bounds__(kThreads, 1) void fwd_gemm_kernel(Nf4View W, const 
   // last weight step: copy LoRA step 0 (sT and B2 tiles) into the other
   // buffers; then the LoRA steps
   if (lsteps > 0) {
-    copy_lora(rt, sxb(ksteps & 1), 0, XRows{});
-    copy_lora(rb, sw[ksteps & 1], 0, WRows{});
+    if constexpr (MULTI) {
+      copy_multi(sxb(ksteps & 1), sw[ksteps & 1], 0);
+    } else {
+      copy_lora(rt, sxb(ksteps & 1), 0, XRows{});
+      copy_lora(rb, sw[ksteps & 1], 0, WRows{});
+    }
   }
   wait_vmem();
   __syncthreads();
@@ -395,8 +506,12 @@ __global__ __launch_bounds__(kThreads, 1) void fwd_gemm_kernel(Nf4View W, const 
   for (int l = 0; l < lsteps; ++l) {
     const int s = ksteps + l;
     if (l + 1 < lsteps) {
-      copy_lora(rt, sxb((s + 1) & 1), l + 1, XRows{});
-      copy_lora(rb, sw[(s + 1) & 1], l + 1, WRows{});
+      if constexpr (MULTI) {
+        copy_multi(sxb((s + 1) & 1), sw[(s + 1) & 1], l + 1);
+      } else {
+        copy_lora(rt, sxb((s + 1) & 1), l + 1, XRows{});
+        copy_lora(rb, sw[(s + 1) & 1], l + 1, WRows{});
+      }
     }
     wait_vmem();
     __syncthreads();
@@ -422,13 +537,12 @@ hipError_t launch_fwd_gemm(const Nf4View& W, const uint16_t* X, int64_t M, const
   const int yb = y16 ? 1 : 0;
 #define QNF4_FWD_LAUNCH(LS, F16V, TMV)                                                                        \
   timed_launch(kKernFwdGemm, fwd_gemm_kernel<LS, F16V, TMV>, dim3(grid), dim3(kThreads), st, W, X, M,        \
-               (const uint16_t*)sT, (const uint16_t*)B2, Rp, Y, yb, tm, tn, splits, P, codebook())
+               (const uint16_t*)sT, (const uint16_t*)B2, Rp, Y, yb, tm, tn, splits, P, codebook(), NoAdapters{})
 #define QNF4_FWD_CASE(LS)                                                                                    \
   case LS:                                                                                                   \
     if (tall) return f16 ? QNF4_FWD_LAUNCH(LS, true, 512) : QNF4_FWD_LAUNCH(LS, false, 512);                 \
     return f16 ? QNF4_FWD_LAUNCH(LS, true, 256) : QNF4_FWD_LAUNCH(LS, false, 256);
   switch (2 * Rp / KSTEP) {
-    QNF4_FWD_CASE(0)
     QNF4_FWD_CASE(1)
     QNF4_FWD_CASE(2)
     QNF4_FWD_CASE(3)
@@ -442,6 +556,22 @@ hipError_t launch_fwd_gemm(const Nf4View& W, const uint16_t* X, int64_t M, const
   }
 #undef QNF4_FWD_CASE
 #undef QNF4_FWD_LAUNCH
+}
+
+hipError_t launch_fwd_gemm_adapters(const Nf4View& W, const uint16_t* X, int64_t M, const AdapterGemmArgs& ma, void* Y,
+                                    bool y16, int splits, float* P, hipStream_t st) {
+  const bool tall = fwd_tall(M);
+  const int tmv = tall ? 512 : 256;
+  const int tm = (int)((M + tmv - 1) / tmv), tn = (int)((W.N + 65536 / tmv - 1) / (65536 / tmv));
+  const unsigned grid = tile_grid(tm, tn, splits);
+  const uint16_t* none = nullptr;
+  if (tall)
+    hipLaunchKernelGGL((fwd_gemm_kernel<0, false, 512, true>), dim3(grid), dim3(kThreads), 0, st, W, X, M, none, none,
+                       (int64_t)0, Y, y16 ? 1 : 0, tm, tn, splits, P, codebook(), ma);
+  else
+    hipLaunchKernelGGL((fwd_gemm_kernel<0, false, 256, true>), dim3(grid), dim3(kThreads), 0, st, W, X, M, none, none,
+                       (int64_t)0, Y, y16 ? 1 : 0, tm, tn, splits, P, codebook(), ma);
+  return hipGetLastError();
 }
 
 }  // namespace qnf4

@@ -53,6 +53,7 @@
 // first barrier waits for is requested after the codes: loads complete in
 // issue order, so such a wait would also wait for them.
 #include <algorithm>
+#include <type_traits>
 
 #include "host.h"
 
@@ -158,12 +159,17 @@ static_assert(kGemvAccBytes + 32 * 1024 + kGemvEpiBytes <= 160 * 1024, "X of 32 
 // every wave loads its fragments from global memory (the same few bytes
 // requested by every wave of every workgroup at once cost ~1.6 us at M = 1
 // on the q_proj weight, ~2 us at M = 16, measured).
-template <bool F16, int XV, int WV>
+// MULTI: the tokens carry different adapters (GemvAdapters): T comes finished
+// (one slice) and each output's thread reads its own token's adapter row of
+// the pool, the first kPreB chunks of it requested right behind the codes.
+constexpr int kPreB = 4;
+template <bool F16, int XV, int WV, bool MULTI = false>
 __global__ __launch_bounds__(64 * WV) void gemv_kernel(Nf4View W, const uint16_t* __restrict__ X,
                                                             int M, const float* __restrict__ P, int S, int JT,
                                                             const uint16_t* __restrict__ B, int r,
                                                             float scale, void* __restrict__ Y,
-                                                            int y_bf16, float* __restrict__ T_out, Codebook cb) {
+                                                            int y_bf16, float* __restrict__ T_out, Codebook cb,
+                                                            std::conditional_t<MULTI, GemvAdapters, NoAdapters> ga_) {
   constexpr int NW = WV, NT = 64 * WV;  // waves and threads of the workgroup
   static_assert(NT >= 16 * GEMV_ROWS, "one thread per output of a 16-token x 16-row tile");
   constexpr bool XL = XV > 0;  // X staged: XV 16-byte pieces per thread
@@ -247,8 +253,14 @@ __global__ __launch_bounds__(64 * WV) void gemv_kernel(Nf4View W, const uint16_t
   // Requested first, so that waiting for them does not wait for the codes
   // (loads complete in issue order): 8 values of the workgroup's B rows
   // (16·r contiguous bf16), and X when staged.
-  const rsrc_t rbr = make_rsrc(B + n0 * r, (N - n0) * r * 2);
-  const u32x4_t braw = buf_load16(rbr, tid < 2 * r ? (uint32_t)(16 * tid) : 0x7fffffffu, 0u);
+  u32x4_t braw;
+  int own = -1;  // MULTI: the adapter of token tid / 16
+  if constexpr (MULTI) {
+    if (tid < 16 * M) own = ga_.owner[tid >> 4];
+  } else {
+    const rsrc_t rbr = make_rsrc(B + n0 * r, (N - n0) * r * 2);
+    braw = buf_load16(rbr, tid < 2 * r ? (uint32_t)(16 * tid) : 0x7fffffffu, 0u);
+  }
   u32x4_t xs[XL ? XV : 1];
   if constexpr (XL) {
     const int nvec = (M * (int)K * 2) / 16;
@@ -281,6 +293,21 @@ __global__ __launch_bounds__(64 * WV) void gemv_kernel(Nf4View W, const uint16_t
           buf_load4(rp, tid < M * r && i < S ? po + (uint32_t)(i * JT * 256 * 4) : 0x7fffffffu, 0u));
   }
   __builtin_amdgcn_sched_barrier(0);
+  // MULTI: thread (token tid / 16, weight row n0 + tid % 16)'s row of its
+  // adapter's B
+  const uint16_t* brow = nullptr;
+  float own_scale = 0.f;
+  u32x4_t bpre[MULTI ? kPreB : 1];
+  if constexpr (MULTI) {
+    if ((unsigned)own < (unsigned)ga_.count && n0 + (tid & 15) < N) {
+      brow = B + ((int64_t)own * N + n0 + (tid & 15)) * r;
+      own_scale = ga_.s[own];
+#pragma unroll
+      for (int i = 0; i < kPreB; ++i)
+        bpre[i] = 8 * i < r ? *reinterpret_cast<const u32x4_t*>(brow + 8 * i) : u32x4_t{0u, 0u, 0u, 0u};
+    }
+  }
+  __builtin_amdgcn_sched_barrier(0);
   if constexpr (XL) {
     const int nvec = (M * (int)K * 2) / 16;
 #pragma unroll
@@ -301,7 +328,7 @@ __global__ __launch_bounds__(64 * WV) void gemv_kernel(Nf4View W, const uint16_t
       }
     }
   };
-  if (!epi_late) stage_b();
+  if (!epi_late && !MULTI) stage_b();
   __syncthreads();  // codebook, X, B rows
 
   // two groups per iteration, alternating buffers: the loads of the next
@@ -319,7 +346,7 @@ __global__ __launch_bounds__(64 * WV) void gemv_kernel(Nf4View W, const uint16_t
   s_acc[wave][lane] = acc;
   if (epi_late) {
     __syncthreads();  // X read by every wave: its region takes t_fin and s_b
-    stage_b();
+    if constexpr (!MULTI) stage_b();
   }
   if (t_pre) {
     if (tid < M * r) {
@@ -344,8 +371,33 @@ __global__ __launch_bounds__(64 * WV) void gemv_kernel(Nf4View W, const uint16_t
 #pragma unroll
       for (int w = 1; w < NW; ++w) y = __fadd_rn(y, s_acc[w][16 * (m >> 2) + c][m & 3]);
       float dot = 0.0f;
-      for (int j = 0; j < r; ++j) dot = __fadd_rn(dot, __fmul_rn(t_fin[m * 257 + j], s_b[c * r + j]));
-      y = __fadd_rn(y, __fmul_rn(scale, dot));
+      if constexpr (MULTI) {
+        if (brow) {
+          auto add8 = [&](int j, const u32x4_t& v) __attribute__((always_inline)) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              dot = __builtin_fmaf(t_fin[m * 257 + j + 2 * i], bf16lo(v[i]), dot);
+              dot = __builtin_fmaf(t_fin[m * 257 + j + 2 * i + 1], bf16hi(v[i]), dot);
+            }
+          };
+#pragma unroll
+          for (int i = 0; i < kPreB; ++i)
+            if (8 * i < r) add8(8 * i, bpre[i]);
+          for (int j = 8 * kPreB; j < r; j += 8 * kPreB) {
+            u32x4_t v[kPreB];
+#pragma unroll
+            for (int i = 0; i < kPreB; ++i)
+              v[i] = *reinterpret_cast<const u32x4_t*>(brow + (j + 8 * i < r ? j + 8 * i : j));
+#pragma unroll
+            for (int i = 0; i < kPreB; ++i)
+              if (j + 8 * i < r) add8(j + 8 * i, v[i]);
+          }
+          y = __builtin_fmaf(own_scale, dot, y);
+        }
+      } else {
+        for (int j = 0; j < r; ++j) dot = __fadd_rn(dot, __fmul_rn(t_fin[m * 257 + j], s_b[c * r + j]));
+        y = __fadd_rn(y, __fmul_rn(scale, dot));
+      }
       if (y_bf16)
         static_cast<uint16_t*>(Y)[(int64_t)m * N + nn] = (uint16_t)(pack16<F16>(y, 0.0f) & 0xffffu);
       else
@@ -397,9 +449,9 @@ hipError_t launch_gemv(const Nf4View& W, const uint16_t* X, int64_t M, const uin
   const bool four = narrow && xb <= 8 * 1024 && 2 * r <= 64 * 4;
 #define QNF4_GEMV_LAUNCH(XV, WV)                                                                                \
   return f16 ? timed_launch_shm(kKernGemv, gemv_kernel<true, XV, WV>, dim3(grid), dim3(64 * WV), shm, st, W, X, \
-                                (int)M, (const float*)P, S, JT, B, r, scale, Y, yb, T, codebook())      \
+                                (int)M, (const float*)P, S, JT, B, r, scale, Y, yb, T, codebook(), NoAdapters{})      \
              : timed_launch_shm(kKernGemv, gemv_kernel<false, XV, WV>, dim3(grid), dim3(64 * WV), shm, st, W, X, \
-                                (int)M, (const float*)P, S, JT, B, r, scale, Y, yb, T, codebook())
+                                (int)M, (const float*)P, S, JT, B, r, scale, Y, yb, T, codebook(), NoAdapters{})
   // X staged with 2 or 8 pieces of 16 bytes per thread (up to 32 or 128 KB)
   if (four) QNF4_GEMV_LAUNCH(2, 4);
   if (narrow) QNF4_GEMV_LAUNCH(4, 8);
@@ -407,6 +459,35 @@ hipError_t launch_gemv(const Nf4View& W, const uint16_t* X, int64_t M, const uin
   if (xl) QNF4_GEMV_LAUNCH(8, 16);
   QNF4_GEMV_LAUNCH(0, 16);
 #undef QNF4_GEMV_LAUNCH
+}
+
+// T: the finished low-rank factor in the split kernel's tile layout, one slice.
+hipError_t launch_gemv_adapters(const Nf4View& W, const uint16_t* X, int64_t M, const AdapterView& ad,
+                                const int32_t* owner, void* Y, bool y16, const float* T, hipStream_t st) {
+  const int JT = (ad.r + 15) / 16;
+  const unsigned grid = (unsigned)((W.N + GEMV_ROWS - 1) / GEMV_ROWS);
+  const size_t xb = (size_t)M * W.K * 2;
+  const bool xl = xb <= (size_t)kGemvXLdsBytes, x2 = xb <= 32 * 1024;
+  const size_t shm = x2 ? xb : (xl ? std::max(xb, kGemvEpiBytes) : 0);
+  // the workgroup shapes of the one-adapter form
+  const bool narrow = grid > 256 && xb <= 32 * 1024;
+  const bool four = narrow && xb <= 8 * 1024;
+  float* const no_out = nullptr;
+#define QNF4_GEMV_LAUNCH(XV, WV)                                                                                  \
+  hipLaunchKernelGGL((gemv_kernel<false, XV, WV, true>), dim3(grid), dim3(64 * WV), shm, st, W, X, (int)M, T, 1, JT, \
+                     ad.B, ad.r, 1.0f, Y, y16 ? 1 : 0, no_out, codebook(), GemvAdapters{owner, ad.s, ad.count})
+  if (four)
+    QNF4_GEMV_LAUNCH(2, 4);
+  else if (narrow)
+    QNF4_GEMV_LAUNCH(4, 8);
+  else if (x2)
+    QNF4_GEMV_LAUNCH(2, 16);
+  else if (xl)
+    QNF4_GEMV_LAUNCH(8, 16);
+  else
+    QNF4_GEMV_LAUNCH(0, 16);
+#undef QNF4_GEMV_LAUNCH
+  return hipGetLastError();
 }
 
 }  // namespace qnf4

@@ -233,13 +233,40 @@ size_t plan_bytes(int64_t M, int count);
 PlanView plan_view(void* plan, int64_t M, int count);
 hipError_t launch_adapters_plan(const int32_t* index, int64_t M, int count, const PlanView& pl, hipStream_t st);
 
+// The adapters' share of a dequant-in-tile GEMM over tokens in plan order:
+// output row p belongs to token perm[p] and takes, beside the base product,
+// S[p]·F_aᵀ, S [M, C] the three-part bf16 split of the scaled low-rank factor
+// (columns [0, r), [r, 2r), [2r, 3r)) and F_a [rows, r] the used adapter's
+// factor of F (its adapter number where `by_id`, its number among the used
+// ones otherwise).
+struct AdapterGemmArgs {
+  PlanView pl;
+  const uint16_t* S;
+  const uint16_t* F;
+  int r, C, count, by_id;
+};
+// The adapters of the dequant-GEMV's tokens.
+struct GemvAdapters {
+  const int32_t* owner;
+  const float* s;
+  int count;
+};
+struct NoAdapters {};
+constexpr int64_t adapter_cols(int64_t r) { return round_up(3 * r, 64); }
+
 struct AdaptersFwdLayout {
-  size_t off_T, off_P, total;
+  // M <= 16: fp32 T in tiles; else bf16 S [M, C] of s·T; the GEMM's split
+  // partials (splits > 1)
+  size_t off_S, off_P, total;
   int splits;
 };
 struct AdaptersBwdLayout {
-  size_t off_T, off_U, off_P, total;
-  int splits;
+  // bf16 sU [M, C]; its transpose sUT and sTT [3r, Mp]; the used adapters'
+  // transposed copies AT [used, K, r] and BT [used, r, N]; the gradient
+  // units' table; one fp32 area: the dX GEMM's split partials, then the
+  // gradients' partials [slots, r·(K + N)]
+  size_t off_U, off_UT, off_TT, off_AT, off_BT, off_units, off_P, total;
+  int splits, unit, units, slots;
 };
 AdaptersFwdLayout adapters_fwd_layout(int64_t M, int64_t N, int64_t K, int r, int count);
 AdaptersBwdLayout adapters_bwd_layout(int64_t M, int64_t N, int64_t K, int r, int count);

@@ -210,10 +210,10 @@ def test_adapters_without_tokens_are_not_read():
 def test_a_tokens_infinities_stay_its_own():
     import torch as t
     for M in (12, 200):
-        c = Case(M, 256, 320, 16, 3, "each")
+        c = Case(M, 264, 320, 16, 3, "each")
         bad = [1, 7]             # adapters 1 and 1: adapters 0 and 2 keep their gradients
         c.X[1, 3], c.dY[1, 5], c.X[7, 0] = float("inf"), float("nan"), float("nan")
-        clean = Case(M, 256, 320, 16, 3, "each")
+        clean = Case(M, 264, 320, 16, 3, "each")
         rest = [m for m in range(M) if m not in bad]
         assert t.equal(c.forward(t.float32)[0][rest], clean.forward(t.float32)[0][rest])
         got, want = c.backward(t.float32, None), clean.backward(t.float32, None)
