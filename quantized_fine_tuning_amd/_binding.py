@@ -259,6 +259,16 @@ class Nf4Tensor:
                            _ptr(self.dq_mean, "dq_mean"))
 
 
+def _weight_on(W: Nf4Tensor, dev: int) -> qlora_nf4_t:
+    torch = _torch()
+    n, k = W.n_rows, W.n_cols
+    nb = n * k // 64
+    return qlora_nf4_t(n, k, _address_1d(W.codes, "codes", 32 * nb, torch.uint8, dev),
+                       _address_1d(W.absmax_e4m3, "absmax_e4m3", nb, torch.uint8, dev),
+                       _address_1d(W.dq_scale, "dq_scale", (nb + 255) // 256, torch.float32, dev),
+                       _address_1d(W.dq_mean, "dq_mean", 1, torch.float32, dev))
+
+
 def workspace(nbytes: int, device="cuda"):
     torch = _torch()
     return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
@@ -457,19 +467,50 @@ def qlora_merge_lora(W: Nf4Tensor, A, B, r: int, alpha: float, out, stream=None)
                                 _ptr(out, "out"), _dtype(out, "out"), _stream(stream)))
 
 
-def _one_device(stream, **tensors):
-    """Every tensor, and the stream, on the current device: the library
-    launches there."""
+# The entry points below are called once per layer and token by serving loops,
+# so their checks are written for the case that passes: one comparison each,
+# the message built only when one fails.
+
+def _launch_stream(stream, dev: int) -> int:
+    """The given stream, or torch's current one, as a raw pointer; the tensors'
+    device has to be the current one and the stream's."""
     torch = _torch()
-    for name, t in tensors.items():
-        if t is not None and not t.is_cuda:
-            raise ValueError(f"{name} must be a GPU tensor")
-    want = torch.device("cuda", torch.cuda.current_device())
-    if getattr(stream, "device", want) != want:
-        raise ValueError(f"stream is on {stream.device}, the current device is {want}")
-    for name, t in tensors.items():
-        if t is not None and t.device != want:
-            raise ValueError(f"{name} is on {t.device}, the current device is {want}")
+    if dev < 0:
+        raise ValueError("the tensors must be GPU tensors")
+    if torch.cuda.current_device() != dev:
+        raise ValueError(f"the tensors are on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    on = getattr(stream, "device", None)
+    if on is not None and on.index != dev:
+        raise ValueError(f"stream is on {on}, the tensors on cuda:{dev}")
+    return stream.cuda_stream
+
+
+def _address(t, name: str, shape, dtypes, dev: int) -> int:
+    """data_ptr of a contiguous tensor of this shape and one of these dtypes on
+    this device."""
+    if t is None or t.shape != shape or t.dtype not in dtypes:
+        _expect(t, name, shape, dtypes)
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, " + (f"others on cuda:{dev}" if dev >= 0 else "others on the CPU"))
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _address_1d(t, name: str, n: int, dtype, dev: int) -> int:
+    """The same for a 1-d tensor of at least n elements."""
+    if t is None or t.dtype != dtype or t.dim() != 1 or t.numel() < n:
+        _expect_numel(t, name, n, dtype)
+    return _address(t, name, t.shape, (dtype,), dev)
+
+
+def _scratch(t, name: str, dev: int):
+    """(address, bytes) of a workspace or plan buffer."""
+    if t is None:
+        raise ValueError(f"{name} is None")
+    return _address(t, name, t.shape, (t.dtype,), dev), t.numel() * t.element_size()
 
 
 class AdapterPool:
@@ -489,8 +530,12 @@ class AdapterPool:
         _expect(scale, "scale", (self.count,), (torch.float32,))
         self.A, self.B, self.scale = A, B, scale
 
-    def c_struct(self) -> qlora_adapters_t:
-        return qlora_adapters_t(_ptr(self.A, "A"), _ptr(self.B, "B"), _ptr(self.scale, "scale"), self.count, self.r)
+    def _struct_on(self, dev: int) -> qlora_adapters_t:
+        torch = _torch()
+        c, r, n, k = self.count, self.r, self.n_rows, self.n_cols
+        return qlora_adapters_t(_address(self.A, "A", (c, r, k), (torch.bfloat16,), dev),
+                                _address(self.B, "B", (c, n, r), (torch.bfloat16,), dev),
+                                _address(self.scale, "scale", (c,), (torch.float32,), dev), c, r)
 
 
 class AdapterPlan:
@@ -516,103 +561,99 @@ def qlora_adapters_sizes(N: int, K: int, M_max: int, r: int, count: int) -> dict
 
 def qlora_adapters_plan(index, plan: AdapterPlan, stream=None) -> None:
     """index int32 [M]: the adapter of every token; outside [0, count): none."""
-    torch = _torch()
-    _expect(index, "index", (plan.M,), (torch.int32,))
-    _one_device(stream, index=index, plan=plan.buffer)
-    _check(lib.qlora_adapters_plan(_ptr(index, "index"), plan.M, plan.count, _ptr(plan.buffer, "plan"),
-                                   _bytes(plan.buffer, "plan"), _stream(stream)))
+    dev = plan.buffer.get_device()
+    at = _address(index, "index", (plan.M,), (_torch().int32,), dev)
+    buf, size = _scratch(plan.buffer, "plan", dev)
+    raw = _launch_stream(stream, dev)
+    _check(lib.qlora_adapters_plan(at, plan.M, plan.count, buf, size, raw))
 
 
 def _check_adapters(W: Nf4Tensor, X, pool: AdapterPool, plan: AdapterPlan):
-    torch = _torch()
     if X is None or X.dim() != 2:
         raise ValueError("X must be [M, K]")
-    _expect(X, "X", (X.shape[0], W.n_cols), (torch.bfloat16,))
-    if (pool.n_rows, pool.n_cols) != (W.n_rows, W.n_cols):
+    if pool.n_rows != W.n_rows or pool.n_cols != W.n_cols:
         raise ValueError(f"the adapters are for a [{pool.n_rows}, {pool.n_cols}] weight, W is "
                          f"[{W.n_rows}, {W.n_cols}]")
-    if plan.M != X.shape[0] or plan.count != pool.count:
-        raise ValueError(f"the plan is for {plan.M} tokens and {plan.count} adapters, the call has {X.shape[0]} and "
+    M = X.shape[0]
+    if plan.M != M or plan.count != pool.count:
+        raise ValueError(f"the plan is for {plan.M} tokens and {plan.count} adapters, the call has {M} and "
                          f"{pool.count}")
-    return X.shape[0]
+    return M
 
 
 def qlora_adapters_fwd(W: Nf4Tensor, X, pool: AdapterPool, plan: AdapterPlan, Y, T_save, ws, stream=None) -> None:
     """Y[m] = X[m]·Ŵᵀ + s_a·(X[m]·A_aᵀ)·B_aᵀ, a the adapter of token m in the plan."""
     torch = _torch()
+    f32, bf16 = torch.float32, torch.bfloat16
     M = _check_adapters(W, X, pool, plan)
-    _expect(Y, "Y", (M, W.n_rows), (torch.float32, torch.bfloat16))
-    if T_save is not None:
-        _expect(T_save, "T_save", (M, pool.r), (torch.float32,))
-    _one_device(stream, W=W.codes, X=X, A=pool.A, B=pool.B, scale=pool.scale, plan=plan.buffer, Y=Y, T_save=T_save,
-                ws=ws)
-    st, ad = W.c_struct(), pool.c_struct()
-    _check(lib.qlora_adapters_fwd(ctypes.byref(st), _ptr(X, "X"), M, ctypes.byref(ad), _ptr(plan.buffer, "plan"),
-                                  _bytes(plan.buffer, "plan"), _ptr(Y, "Y"), _dtype(Y, "Y"), _ptr(T_save, "T_save"),
-                                  _ptr(ws, "ws"), _bytes(ws, "ws"), _stream(stream)))
+    dev = X.get_device()
+    x = _address(X, "X", (M, W.n_cols), (bf16,), dev)
+    y = _address(Y, "Y", (M, W.n_rows), (f32, bf16), dev)
+    t = None if T_save is None else _address(T_save, "T_save", (M, pool.r), (f32,), dev)
+    buf, size = _scratch(plan.buffer, "plan", dev)
+    w, nbytes = _scratch(ws, "ws", dev)
+    wd, ad = _weight_on(W, dev), pool._struct_on(dev)
+    _check(lib.qlora_adapters_fwd(ctypes.byref(wd), x, M, ctypes.byref(ad), buf, size, y,
+                                  QLORA_BF16 if Y.dtype == bf16 else QLORA_F32, t, w, nbytes,
+                                  _launch_stream(stream, dev)))
 
 
 def qlora_adapters_bwd(W: Nf4Tensor, X, dY, pool: AdapterPool, plan: AdapterPlan, T_saved, dX, dA, dB, ws,
                        stream=None) -> None:
     """dX, and dA, dB of every adapter of the pool (zeros without tokens)."""
     torch = _torch()
+    f32, bf16 = torch.float32, torch.bfloat16
     M = _check_adapters(W, X, pool, plan)
-    _expect(dY, "dY", (M, W.n_rows), (torch.bfloat16,))
-    if T_saved is not None:
-        _expect(T_saved, "T_saved", (M, pool.r), (torch.float32,))
-    _expect(dX, "dX", (M, W.n_cols), (torch.float32, torch.bfloat16))
-    _expect(dA, "dA", (pool.count, pool.r, W.n_cols), (torch.float32,))
-    _expect(dB, "dB", (pool.count, W.n_rows, pool.r), (torch.float32,))
-    _one_device(stream, W=W.codes, X=X, dY=dY, A=pool.A, B=pool.B, scale=pool.scale, plan=plan.buffer,
-                T_saved=T_saved, dX=dX, dA=dA, dB=dB, ws=ws)
-    st, ad = W.c_struct(), pool.c_struct()
-    _check(lib.qlora_adapters_bwd(ctypes.byref(st), _ptr(X, "X"), _ptr(dY, "dY"), M, ctypes.byref(ad),
-                                  _ptr(plan.buffer, "plan"), _bytes(plan.buffer, "plan"), _ptr(T_saved, "T_saved"),
-                                  _ptr(dX, "dX"), _dtype(dX, "dX"), _ptr(dA, "dA"), _ptr(dB, "dB"), _ptr(ws, "ws"),
-                                  _bytes(ws, "ws"), _stream(stream)))
+    N, K, r, count = W.n_rows, W.n_cols, pool.r, pool.count
+    dev = X.get_device()
+    x, dy = _address(X, "X", (M, K), (bf16,), dev), _address(dY, "dY", (M, N), (bf16,), dev)
+    t = None if T_saved is None else _address(T_saved, "T_saved", (M, r), (f32,), dev)
+    dx = _address(dX, "dX", (M, K), (f32, bf16), dev)
+    da, db = _address(dA, "dA", (count, r, K), (f32,), dev), _address(dB, "dB", (count, N, r), (f32,), dev)
+    buf, size = _scratch(plan.buffer, "plan", dev)
+    w, nbytes = _scratch(ws, "ws", dev)
+    wd, ad = _weight_on(W, dev), pool._struct_on(dev)
+    _check(lib.qlora_adapters_bwd(ctypes.byref(wd), x, dy, M, ctypes.byref(ad), buf, size, t, dx,
+                                  QLORA_BF16 if dX.dtype == bf16 else QLORA_F32, da, db, w, nbytes,
+                                  _launch_stream(stream, dev)))
 
 
-def _check_distill(Z, top, top_index, weight, vocab):
+def _distill_args(Z, top, top_index, weight, dZ, vocab):
+    """(device, the C arguments from Z to k, the weight's and the gradient's
+    address)."""
     torch = _torch()
     floats = (torch.float32, torch.bfloat16, torch.float16)
     if Z is None or Z.dim() != 2 or top is None or top.dim() != 2:
         raise ValueError("Z must be [M, ldz] and top [M, k]")
-    M, ldz = Z.shape
-    _expect(Z, "Z", (M, ldz), floats)
-    _expect(top, "top", (M, top.shape[1]), floats)
-    _expect(top_index, "top_index", (M, top.shape[1]), (torch.int32,))
-    if weight is not None:
-        _expect(weight, "weight", (M,), (torch.float32,))
-    return M, ldz, ldz if vocab is None else int(vocab), top.shape[1]
+    M, ldz = shape = Z.shape
+    dev = Z.get_device()
+    k = top.shape[1]
+    z = _address(Z, "Z", shape, floats, dev)
+    t = _address(top, "top", (M, k), floats, dev)
+    at = _address(top_index, "top_index", (M, k), (torch.int32,), dev)
+    w = None if weight is None else _address(weight, "weight", (M,), (torch.float32,), dev)
+    d = None if dZ is None else _address(dZ, "dZ", shape, (Z.dtype,), dev)
+    return dev, (z, _dtype(Z, "Z"), M, ldz if vocab is None else int(vocab), ldz, t, _dtype(top, "top"), at, k), w, d
 
 
 def qlora_distill_fwd(Z, top, top_index, tau: float, weight, loss, lse=None, dZ=None, vocab=None, stream=None) -> None:
     """loss[m] = w·tau²·KL(softmax(top / tau) || softmax(Z / tau)) per token,
     its log-sum-exp and, if dZ is given (it may be Z), the gradient of their
     sum.  vocab: the columns of Z that count (all of them by default)."""
-    torch = _torch()
-    M, ldz, V, k = _check_distill(Z, top, top_index, weight, vocab)
-    _expect(loss, "loss", (M,), (torch.float32,))
-    if lse is not None:
-        _expect(lse, "lse", (M,), (torch.float32,))
-    if dZ is not None:
-        _expect(dZ, "dZ", (M, ldz), (Z.dtype,))
-    _one_device(stream, Z=Z, top=top, top_index=top_index, weight=weight, loss=loss, lse=lse, dZ=dZ)
-    _check(lib.qlora_distill_fwd(_ptr(Z, "Z"), _dtype(Z, "Z"), M, V, ldz, _ptr(top, "top"), _dtype(top, "top"),
-                                 _ptr(top_index, "top_index"), k, float(tau), _ptr(weight, "weight"),
-                                 _ptr(loss, "loss"), _ptr(lse, "lse"), _ptr(dZ, "dZ"), _stream(stream)))
+    dev, args, w, d = _distill_args(Z, top, top_index, weight, dZ, vocab)
+    f32 = (_torch().float32,)
+    out = _address(loss, "loss", (args[2],), f32, dev)
+    norm = None if lse is None else _address(lse, "lse", (args[2],), f32, dev)
+    _check(lib.qlora_distill_fwd(*args, tau, w, out, norm, d, _launch_stream(stream, dev)))
 
 
 def qlora_distill_bwd(Z, top, top_index, tau: float, lse, weight, dZ, vocab=None, stream=None) -> None:
     """The gradient alone, from the lse of qlora_distill_fwd; dZ may be Z."""
-    torch = _torch()
-    M, ldz, V, k = _check_distill(Z, top, top_index, weight, vocab)
-    _expect(lse, "lse", (M,), (torch.float32,))
-    _expect(dZ, "dZ", (M, ldz), (Z.dtype,))
-    _one_device(stream, Z=Z, top=top, top_index=top_index, weight=weight, lse=lse, dZ=dZ)
-    _check(lib.qlora_distill_bwd(_ptr(Z, "Z"), _dtype(Z, "Z"), M, V, ldz, _ptr(top, "top"), _dtype(top, "top"),
-                                 _ptr(top_index, "top_index"), k, float(tau), _ptr(lse, "lse"),
-                                 _ptr(weight, "weight"), _ptr(dZ, "dZ"), _stream(stream)))
+    if dZ is None:
+        raise ValueError("dZ is None")
+    dev, args, w, d = _distill_args(Z, top, top_index, weight, dZ, vocab)
+    norm = _address(lse, "lse", (args[2],), (_torch().float32,), dev)
+    _check(lib.qlora_distill_bwd(*args, tau, norm, w, d, _launch_stream(stream, dev)))
 
 
 class QTensor:

@@ -269,6 +269,83 @@ __global__ __launch_bounds__(64 * kDownWaves) void adapters_down_kernel(const ui
   }
 }
 
+// The same for few tokens: a workgroup per (position, kFewRanks ranks), its 4
+// waves sharing the reduction, 8 elements per lane and step; each token reads
+// its own adapter (tokens of one adapter share it in L2).  Fewer dependent
+// loads before the data than with tiles, and the adapters' rows spread over
+// many workgroups.  Up to 16 tokens positions are tokens (the plan's order
+// does not matter to the dequant-GEMV).
+constexpr int kFewTokens = 64, kFewRanks = 4;
+__device__ __forceinline__ float dot8(const u32x4_t a, const u32x4_t b, float acc) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    acc = __builtin_fmaf(bf16lo(a[i]), bf16lo(b[i]), acc);
+    acc = __builtin_fmaf(bf16hi(a[i]), bf16hi(b[i]), acc);
+  }
+  return acc;
+}
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
+  return v;
+}
+template <bool TOKENS>
+__global__ __launch_bounds__(256) void adapters_few_down_kernel(const uint16_t* __restrict__ L, int64_t M, int64_t Kred,
+                                                                const uint16_t* __restrict__ R, int by_id,
+                                                                AdapterView ad, PlanView pl, DownOut out) {
+  constexpr int UN = 3;
+  __shared__ float s_part[4][kFewRanks];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int64_t pos = blockIdx.x;
+  const int j0 = kFewRanks * (int)blockIdx.y, r = ad.r;
+  const int tok = TOKENS ? (int)pos : pl.perm[pos];
+  if ((uint32_t)tok >= (uint32_t)M) return;
+  const int id = pl.owner[tok];
+  const bool has = (unsigned)id < (unsigned)ad.count;
+  float acc[kFewRanks] = {};
+  if (has) {
+    const int g = by_id ? id : std::max(pl.slot[id], 0);
+    const rsrc_t rl = make_rsrc(L + (int64_t)tok * Kred, Kred * 2);
+    const rsrc_t rr = make_rsrc(R + ((int64_t)g * r + j0) * Kred, (int64_t)kFewRanks * Kred * 2);
+    for (int64_t k0 = 8 * tid; k0 < Kred; k0 += 2048 * UN) {
+      u32x4_t x[UN], w[UN][kFewRanks];
+#pragma unroll
+      for (int u = 0; u < UN; ++u) {
+        const int64_t k = k0 + 2048 * u;
+        const bool in = k < Kred;
+        x[u] = buf_load16(rl, in ? (uint32_t)(k * 2) : 0x7fffffffu, 0u);
+#pragma unroll
+        for (int j = 0; j < kFewRanks; ++j)
+          w[u][j] = buf_load16(rr, in ? (uint32_t)((j * Kred + k) * 2) : 0x7fffffffu, 0u);
+      }
+#pragma unroll
+      for (int u = 0; u < UN; ++u)
+#pragma unroll
+        for (int j = 0; j < kFewRanks; ++j) acc[j] = dot8(x[u], w[u][j], acc[j]);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kFewRanks; ++j) {
+    acc[j] = wave_sum(acc[j]);
+    if (lane == 0) s_part[wave][j] = acc[j];
+  }
+  __syncthreads();
+  if (tid >= kFewRanks) return;
+  const int j = j0 + tid;
+  const float t = ((s_part[0][tid] + s_part[1][tid]) + s_part[2][tid]) + s_part[3][tid];
+  if (out.T) out.T[(int64_t)tok * r + j] = t;
+  if (out.Tt) out.Tt[(j >> 4) * 256 + 16 * tok + (j & 15)] = t;
+  if (has && (out.S || out.ST)) {
+    uint16_t v[3];
+    split3(__fmul_rn(ad.s[id], t), v);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      if (out.S) out.S[pos * adapter_cols(r) + i * r + j] = v[i];
+      if (out.ST) out.ST[(int64_t)(i * r + j) * out.Mp + pos] = v[i];
+    }
+  }
+}
+
 // ---------------------------------------------------------------------------
 // Operand copies of the backward pass, one launch: block 0 cuts every used
 // adapter's positions into units of at most `unit` (the gradients' work
@@ -338,17 +415,26 @@ __global__ __launch_bounds__(256) void adapters_prep_kernel(const float* __restr
     // positions p, ranks j of s·T
     const int64_t q0 = (int64_t)(b / jb) * 64;
     const int j0 = (int)(b % jb) * 64, j = j0 + col;
-#pragma unroll 4
+    // (unconditional loads of clamped addresses: each step's 16 go out together)
+    int tok[16], id[16];
+    float sv[16], tv[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) tok[i] = pl.perm[std::min<int64_t>(q0 + 4 * i + row, M - 1)];
+#pragma unroll
     for (int i = 0; i < 16; ++i) {
-      const int64_t pos = q0 + 4 * i + row;
-      uint16_t v[3] = {0, 0, 0};
-      if (pos < held && j < r) {
-        const int64_t tok = pl.perm[pos];
-        const int g = pl.group[pos];
-        const int id = (unsigned)g < (unsigned)used ? pl.id[g] : -1;
-        if ((uint64_t)tok < (uint64_t)M && (unsigned)id < (unsigned)ad.count)
-          split3(__fmul_rn(ad.s[id], T[tok * r + j]), v);
-      }
+      if (q0 + 4 * i + row >= held || j >= r || (uint32_t)tok[i] >= (uint32_t)M) tok[i] = -1;
+      id[i] = pl.owner[std::max(tok[i], 0)];
+      tv[i] = T[(int64_t)std::max(tok[i], 0) * r + std::min(j, r - 1)];
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      if ((unsigned)id[i] >= (unsigned)ad.count) tok[i] = -1;
+      sv[i] = ad.s[tok[i] < 0 ? 0 : id[i]];
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      uint16_t v[3];
+      split3(tok[i] < 0 ? 0.f : __fmul_rn(sv[i], tv[i]), v);
 #pragma unroll
       for (int t = 0; t < 3; ++t) sh[t][col][4 * i + row] = v[t];
     }
@@ -569,11 +655,6 @@ __global__ __launch_bounds__(256) void adapters_gradient_finish_kernel(float* __
 // Host
 // ---------------------------------------------------------------------------
 
-namespace {
-constexpr int64_t kPlanHead = 16;  // words
-int64_t plan_pad(int64_t n) { return round_up(n, 16); }
-}  // namespace
-
 size_t plan_bytes(int64_t M, int count) {
   return (size_t)(kPlanHead + 3 * plan_pad(M) + 3 * plan_pad(count + 1)) * 4;
 }
@@ -602,6 +683,14 @@ int rank_blocks(int r) { return r <= 16 ? 1 : r <= 32 ? 2 : 4; }
 
 hipError_t launch_down(const uint16_t* L, int64_t M, int64_t Kred, const uint16_t* R, int by_id, const AdapterView& ad,
                        const PlanView& pl, const DownOut& out, hipStream_t st) {
+  if (M <= kFewTokens) {
+    const dim3 grid((unsigned)M, (unsigned)(ad.r / kFewRanks));
+    if (M <= 16 && out.S == nullptr && out.ST == nullptr)
+      adapters_few_down_kernel<true><<<grid, 256, 0, st>>>(L, M, Kred, R, by_id, ad, pl, out);
+    else
+      adapters_few_down_kernel<false><<<grid, 256, 0, st>>>(L, M, Kred, R, by_id, ad, pl, out);
+    return hipGetLastError();
+  }
   const unsigned tiles = cdiv(M, 16);
   // few tokens: one workgroup per 16 ranks, so that each reads less of the
   // adapter; then as many workgroups per tile as fill the chip once
@@ -705,7 +794,8 @@ hipError_t launch_adapters_fwd(const Nf4View& W, const uint16_t* X, int64_t M, c
   float* P = reinterpret_cast<float*>(ws + L.off_P);
   hipError_t e = launch_down(X, M, W.K, ad.A, 1, ad, pl, DownOut{T_save, nullptr, S, nullptr, 0}, st);
   if (e != hipSuccess) return e;
-  const AdapterGemmArgs ma{pl, S, ad.B, ad.r, (int)adapter_cols(ad.r), ad.count, 1};
+  const AdapterGemmArgs ma{pl.head, (int)plan_pad(M), (int)plan_pad(ad.count + 1), S, ad.B, ad.r,
+                           (int)adapter_cols(ad.r), ad.count, 1};
   e = launch_fwd_gemm_adapters(W, X, M, ma, Y, y16, L.splits, P, st);
   if (e != hipSuccess || L.splits == 1) return e;
   return launch_splitk_reduce(P, L.splits, M * W.N, Y, y16, false, st);
@@ -741,7 +831,8 @@ hipError_t launch_adapters_bwd(const Nf4View& W, const uint16_t* X, const uint16
     e = launch_down(X, M, K, ad.A, 1, ad, pl, DownOut{nullptr, nullptr, nullptr, TT, Mp}, st);
   if (e == hipSuccess) e = launch_down(dY, M, N, BT, 0, ad, pl, DownOut{nullptr, nullptr, U, UT, Mp}, st);
   if (e != hipSuccess) return e;
-  const AdapterGemmArgs ma{pl, U, AT, ad.r, (int)adapter_cols(r), ad.count, 0};
+  const AdapterGemmArgs ma{pl.head, (int)plan_pad(M), (int)plan_pad(ad.count + 1), U, AT, ad.r,
+                           (int)adapter_cols(r), ad.count, 0};
   e = launch_dx_gemm_adapters(W, dY, M, ma, dX, dx16, L.splits, P, st);
   if (e == hipSuccess && L.splits > 1) e = launch_splitk_reduce(P, L.splits, M * K, dX, dx16, false, st);
   if (e != hipSuccess) return e;

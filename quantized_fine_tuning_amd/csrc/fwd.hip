@@ -128,11 +128,11 @@ __global__ __launch_bounds__(kThreads, 1) void fwd_gemm_kernel(Nf4View W, const 
   // tile's; step i belongs to used adapter gfirst + i / lper, chunk i % lper
   int lfirst = 0, gfirst = 0, lper = 1;
   if constexpr (MULTI) {
-    const int64_t held = std::min<int64_t>(ma.pl.head[1], M);
+    const int held = std::min(ma.held(), (int)M);
     lper = ma.C / 64;
-    if (m0 < held) {
-      gfirst = ma.pl.group[m0];
-      const int glast = std::min(ma.pl.group[std::min<int64_t>(m0 + TM, held) - 1], ma.count - 1);
+    if ((int)m0 < held) {
+      gfirst = ma.group((int)m0);
+      const int glast = std::min(ma.group(std::min((int)m0 + TM, held) - 1), ma.count - 1);
       const int all = gfirst >= 0 && glast >= gfirst ? std::min(glast - gfirst + 1, TM) * lper : 0;
       lfirst = split_first(sp, splits, all);
       lsteps = split_first(sp + 1, splits, all) - lfirst;
@@ -142,8 +142,8 @@ __global__ __launch_bounds__(kThreads, 1) void fwd_gemm_kernel(Nf4View W, const 
   auto rows_of = [&](int l, int& p0, int& p1) __attribute__((always_inline)) {
     if constexpr (MULTI) {
       const int g = gfirst + (lfirst + l) / lper;
-      p0 = (int)(ma.pl.start[g] - m0);
-      p1 = (int)(std::min<int64_t>(ma.pl.start[g + 1], M) - m0);
+      p0 = ma.start(g) - (int)m0;
+      p1 = std::min(ma.start(g + 1), (int)M) - (int)m0;
     }
   };
   auto sxb = [&](int i) { return i ? sx1 : sx0; };
@@ -235,33 +235,55 @@ __global__ __launch_bounds__(kThreads, 1) void fwd_gemm_kernel(Nf4View W, const 
     asm volatile("" : "+v"(row0), "+v"(col0));
     const bool full = (m0 + TM <= M) && (n0 + TN <= N);
     if constexpr (MULTI) {
-      // rows back to their tokens
-      auto scatter = [&](auto&& put) __attribute__((always_inline)) {
+      // rows back to their tokens, as buffer stores: a row or column past the
+      // output's end gets an offset past the buffer's (no branches; the 16-bit
+      // output and the partials of a split are below 2^31 bytes)
+      auto scatter = [&](auto size, auto&& put) __attribute__((always_inline)) {
+        constexpr uint32_t SZ = decltype(size)::value;
+        const bool whole = n0 + TN <= N;
+        const uint32_t colb = ((uint32_t)n0 + (uint32_t)col0) * SZ;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const int64_t pos = m0 + row0 + 16 * i;
-          if (pos >= M) continue;
-          const int4 tok = *reinterpret_cast<const int4*>(ma.pl.perm + pos);
+          const int pos = (int)m0 + row0 + 16 * i;
+          const int4 tok = *reinterpret_cast<const int4*>(ma.perm() + std::min(pos, ((int)M - 1) & ~3));
           const int t4[4] = {tok.x, tok.y, tok.z, tok.w};
 #pragma unroll
-          for (int v = 0; v < 4; ++v)
-            if (pos + v < M && (uint64_t)(int64_t)t4[v] < (uint64_t)M) {
-              const int64_t o = (int64_t)t4[v] * N + n0 + col0;
+          for (int v = 0; v < 4; ++v) {
+            const bool row_ok = pos + v < (int)M && (uint32_t)t4[v] < (uint32_t)M;
+            const uint32_t o = row_ok ? (uint32_t)t4[v] * (uint32_t)N * SZ : 0x80000000u;
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
-                if (full || n0 + col0 + 16 * j < N) put(o + 16 * j, acc[i][j][v]);
+            for (int j = 0; j < 4; ++j) {
+              uint32_t at = o + colb + 16 * SZ * j;
+              if (!whole) at = n0 + col0 + 16 * j < N ? at : 0xffffffffu;
+              put(at, acc[i][j][v]);
             }
+          }
         }
       };
       if (splits > 1) {
-        float* const Ps = P + (int64_t)sp * M * N;
-        scatter([&](int64_t o, float v) { Ps[o] = v; });
+        const rsrc_t rp = make_rsrc(P + (int64_t)sp * M * N, M * N * 4);
+        scatter(std::integral_constant<uint32_t, 4>(),
+                [&](uint32_t at, float v) { __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), rp, at, 0, 0); });
       } else if (y_bf16) {
-        scatter([&](int64_t o, float v) {
-          static_cast<uint16_t*>(Y)[o] = (uint16_t)(pack16<F16>(v, 0.0f) & 0xffffu);
+        const rsrc_t ry = make_rsrc(Y, M * N * 2);
+        scatter(std::integral_constant<uint32_t, 2>(), [&](uint32_t at, float v) {
+          __builtin_amdgcn_raw_buffer_store_b16((short)(pack16<F16>(v, 0.0f) & 0xffffu), ry, at, 0, 0);
         });
       } else {
-        scatter([&](int64_t o, float v) { static_cast<float*>(Y)[o] = v; });
+        float* const D = static_cast<float*>(Y);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int pos = (int)m0 + row0 + 16 * i;
+#pragma unroll 1
+          for (int v = 0; v < 4; ++v) {
+            const int tok = pos + v < (int)M ? ma.perm()[pos + v] : -1;
+            if ((uint32_t)tok >= (uint32_t)M) continue;
+            float* const Dr = D + (int64_t)tok * N + n0 + col0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (n0 + col0 + 16 * j < N) Dr[16 * j] = v == 0 ? acc[i][j][0] : v == 1 ? acc[i][j][1] : v == 2 ? acc[i][j][2] : acc[i][j][3];
+          }
+        }
       }
     } else if (splits > 1) {
       float* Pp = P + ((int64_t)sp * M + m0 + row0) * N + n0 + col0;
@@ -327,11 +349,15 @@ __global__ __launch_bounds__(kThreads, 1) void fwd_gemm_kernel(Nf4View W, const 
   // MULTI: the byte offset of each row's token (past every buffer for none)
   uint32_t vtok[MULTI ? XR / 8 : 1];
   if constexpr (MULTI) {
+    // (unconditional loads, all in flight together)
+    int tok[XR / 8];
+#pragma unroll
+    for (int c = 0; c < XR / 8; ++c)
+      tok[c] = ma.perm()[std::min((int)m0 + XR * p + 8 * c + (lane >> 3), (int)M - 1)];
 #pragma unroll
     for (int c = 0; c < XR / 8; ++c) {
-      const int64_t pos = m0 + XR * p + 8 * c + (lane >> 3);
-      const int64_t tok = pos < M ? ma.pl.perm[pos] : -1;
-      vtok[c] = (uint64_t)tok < (uint64_t)M ? (uint32_t)((tok * K + 8 * xlch) * 2) : 0x7fffffffu;
+      const bool ok = (int)m0 + XR * p + 8 * c + (lane >> 3) < (int)M && (uint32_t)tok[c] < (uint32_t)M;
+      vtok[c] = ok ? ((uint32_t)tok[c] * (uint32_t)K + 8 * xlch) * 2u : 0x7fffffffu;
     }
   }
   auto copy_x_part = [&](char* t, int s, int c) __attribute__((always_inline)) {
@@ -366,7 +392,7 @@ __global__ __launch_bounds__(kThreads, 1) void fwd_gemm_kernel(Nf4View W, const 
         const uint32_t o = (uint32_t)(((m0 + row) * ma.C + col) * 2);
         buf_load_lds16(rt3, ts + (XR * p + 8 * c) * 128, in && row >= p0 && row < p1 ? o : 0x7fffffffu, 0u);
       }
-      const int a = ma.by_id ? ma.pl.id[g] : g;
+      const int a = ma.by_id ? ma.id(g) : g;
       const bool ok = (unsigned)a < (unsigned)ma.count;
       const rsrc_t rf = make_rsrc(ma.F + (int64_t)(ok ? a : 0) * N * ma.r, ok ? N * ma.r * 2 : 0);
 #pragma unroll

@@ -229,6 +229,8 @@ struct PlanView {
   int32_t* start;  // [count + 1] its first sorted position
   int32_t* slot;   // [count] adapter -> used adapter, -1: no token carries it
 };
+constexpr int kPlanHead = 16;  // words
+inline int64_t plan_pad(int64_t n) { return round_up(n, 16); }
 size_t plan_bytes(int64_t M, int count);
 PlanView plan_view(void* plan, int64_t M, int count);
 hipError_t launch_adapters_plan(const int32_t* index, int64_t M, int count, const PlanView& pl, hipStream_t st);
@@ -240,10 +242,18 @@ hipError_t launch_adapters_plan(const int32_t* index, int64_t M, int count, cons
 // factor of F (its adapter number where `by_id`, its number among the used
 // ones otherwise).
 struct AdapterGemmArgs {
-  PlanView pl;
+  // (the plan as one address and two strides: the kernels are short of scalar
+  // registers)
+  const int32_t* plan;
+  int m_pad, c_pad;
   const uint16_t* S;
   const uint16_t* F;
   int r, C, count, by_id;
+  __device__ __forceinline__ int held() const { return plan[1]; }
+  __device__ __forceinline__ const int32_t* perm() const { return plan + kPlanHead + m_pad; }
+  __device__ __forceinline__ int group(int p) const { return plan[kPlanHead + 2 * m_pad + p]; }
+  __device__ __forceinline__ int id(int g) const { return plan[kPlanHead + 3 * m_pad + g]; }
+  __device__ __forceinline__ int start(int g) const { return plan[kPlanHead + 3 * m_pad + c_pad + g]; }
 };
 // The adapters of the dequant-GEMV's tokens.
 struct GemvAdapters {
