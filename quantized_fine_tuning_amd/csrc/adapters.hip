@@ -10,9 +10,9 @@
 // that Y and dX are written once; the adapters' gradients are reductions over
 // runs of positions.
 #include <algorithm>
-#include <type_traits>
 
 #include "host.h"
+#include "tiling.h"
 
 namespace qnf4 {
 
@@ -43,7 +43,7 @@ constexpr int kPlanWaves = 16;
 __global__ __launch_bounds__(64 * kPlanWaves) void adapters_plan_kernel(const int32_t* __restrict__ index, int64_t M,
                                                                         int count, PlanView pl) {
   extern __shared__ int32_t hist[];  // [16][count + 1]; column `count`: no adapter
-  __shared__ int32_t s_wave[2][kPlanWaves];
+  __shared__ int32_t s_wave[3][kPlanWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int cols = count + 1;
   for (int i = tid; i < kPlanWaves * cols; i += 64 * kPlanWaves) hist[i] = 0;
@@ -59,41 +59,48 @@ __global__ __launch_bounds__(64 * kPlanWaves) void adapters_plan_kernel(const in
   }
   __syncthreads();
   // thread a: adapter a's tokens, then exclusive sums over the adapters of
-  // the tokens and of "carries any token"
+  // the tokens, of "carries any token" and of the 64-position tiles
   int total = 0;
   if (tid < count)
     for (int w = 0; w < kPlanWaves; ++w) total += hist[w * cols + tid];
   const int used = total > 0 ? 1 : 0;
-  int st = total, su = used;
+  const int tiles = (total + 63) / 64;
+  int st = total, su = used, sx = tiles;
   for (int o = 1; o < 64; o <<= 1) {
-    const int a = __shfl_up(st, o, 64), b = __shfl_up(su, o, 64);
+    const int a = __shfl_up(st, o, 64), b = __shfl_up(su, o, 64), c = __shfl_up(sx, o, 64);
     if (lane >= o) {
       st += a;
       su += b;
+      sx += c;
     }
   }
   if (lane == 63) {
     s_wave[0][wave] = st;
     s_wave[1][wave] = su;
+    s_wave[2][wave] = sx;
   }
   __syncthreads();
-  int bt = 0, bu = 0, all = 0, nact = 0;
+  int all = 0, nact = 0, all_tiles = 0;
+  st -= total;
+  su -= used;
+  sx -= tiles;
   for (int w = 0; w < kPlanWaves; ++w) {
     if (w < wave) {
-      bt += s_wave[0][w];
-      bu += s_wave[1][w];
+      st += s_wave[0][w];
+      su += s_wave[1][w];
+      sx += s_wave[2][w];
     }
     all += s_wave[0][w];
     nact += s_wave[1][w];
+    all_tiles += s_wave[2][w];
   }
-  st += bt - total;
-  su += bu - used;
   __syncthreads();
   if (tid < count) {
     pl.slot[tid] = used ? su : -1;
     if (used) {
       pl.id[su] = tid;
       pl.start[su] = st;
+      for (int i = 0; i < tiles; ++i) pl.tile[sx + i] = int2{su, st + 64 * i};
     }
     int run = st;
     for (int w = 0; w < kPlanWaves; ++w) {
@@ -105,6 +112,7 @@ __global__ __launch_bounds__(64 * kPlanWaves) void adapters_plan_kernel(const in
   if (tid == 0) {
     pl.head[0] = nact;
     pl.head[1] = all;
+    pl.head[2] = all_tiles;
     pl.start[nact] = all;
     int run = all;
     for (int w = 0; w < kPlanWaves; ++w) {
@@ -150,27 +158,9 @@ __global__ __launch_bounds__(64 * kPlanWaves) void adapters_plan_kernel(const in
 }
 
 // ---------------------------------------------------------------------------
-// Low-rank factors.  For the 16 sorted positions of a tile and one of the used
-// adapters among them (blockIdx.y, its stride gridDim.y): D[p][j] =
-// Σ_k L[token(p)][k]·R_a[j][k] over NJ blocks of 16 ranks, 16 waves taking
-// 64-element runs of the reduction in turn, each lane whole 32-byte pieces of
-// its row (L read straight from memory: every byte is used once), the waves'
-// sums added in wave order.  Only the positions of that adapter are written:
-//   T   [M, r] fp32 by token (zeros for a token without an adapter), or
-//   Tt  the same in the dequant-GEMV's tiles (M <= 16),
-//   S   [M, C] by position, v = s_a·D as hi + mid + lo in bf16 (24 bits: the
-//       products with it are as exact as fp32 ones),
-//   ST  its transpose [3r, Mp].
+// Low-rank factors, three-part: v = s_a·D as hi + mid + lo in bf16 (24 bits:
+// products with it are as exact as fp32 ones).
 // ---------------------------------------------------------------------------
-constexpr int kDownWaves = 16;
-struct DownOut {
-  float* T;
-  float* Tt;
-  uint16_t* S;
-  uint16_t* ST;
-  int64_t Mp;
-};
-
 __device__ __forceinline__ void split3(float v, uint16_t* o) {
 #pragma unroll
   for (int i = 0; i < 3; ++i) {
@@ -180,96 +170,254 @@ __device__ __forceinline__ void split3(float v, uint16_t* o) {
   }
 }
 
-template <int NJ>
-__global__ __launch_bounds__(64 * kDownWaves) void adapters_down_kernel(const uint16_t* __restrict__ L, int64_t M,
-                                                                        int64_t Kred, const uint16_t* __restrict__ R,
-                                                                        int by_id, AdapterView ad, PlanView pl,
-                                                                        DownOut out) {
-  __shared__ f32x4_t s_acc[kDownWaves][NJ][64];
-  constexpr int UN = NJ == 1 ? 4 : NJ == 2 ? 3 : 2;  // runs in flight per wave
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int lr = lane & 15, kq = lane >> 4;
-  const int64_t pos0 = 16 * (int64_t)blockIdx.x;
-  const int jb0 = NJ * (int)blockIdx.z, r = ad.r, C = (int)adapter_cols(r);
-  const int64_t held = std::min<int64_t>(pl.head[1], M);
-  // (the row loaded by lanes lr, and the output row of thread tid / 16 % 16)
-  const int64_t lpos = pos0 + lr, opos = pos0 + ((tid >> 4) & 15);
-  const int64_t ltok = lpos < held ? pl.perm[lpos] : -1;
-  const int64_t otok = opos < M ? pl.perm[opos] : -1;
-  const bool otok_ok = (uint64_t)otok < (uint64_t)M;
-  if (blockIdx.y == 0 && opos >= held && otok_ok) {
-    for (int o = tid; o < 256 * NJ; o += 64 * kDownWaves) {
-      const int j = 16 * (jb0 + (o >> 8)) + (o & 15);
-      if (j < r && out.T) out.T[otok * r + j] = 0.f;
-      if (j < r && out.Tt) out.Tt[(j >> 4) * 256 + 16 * otok + (j & 15)] = 0.f;
-    }
-  }
-  if (pos0 >= held) return;
-  const int g0 = std::max(pl.group[pos0], 0);
-  const int g1 = std::min(pl.group[std::min(pos0 + 16, held) - 1], ad.count - 1);
-  const int ogroup = opos < held ? pl.group[opos] : -1;
-  const rsrc_t rl = make_rsrc(L, M * Kred * 2);
-  const bool lok = (uint64_t)ltok < (uint64_t)M;
-  const uint32_t loff = lok ? (uint32_t)(ltok * Kred * 2) : 0u;
-  const int runs = (int)((Kred + 63) / 64);
-  for (int g = g0 + (int)blockIdx.y; g <= g1; g += (int)gridDim.y) {
-    const int id = pl.id[g];
-    if ((unsigned)id >= (unsigned)ad.count) break;
-    const rsrc_t rr = make_rsrc(R + (int64_t)(by_id ? id : g) * r * Kred, (int64_t)r * Kred * 2);
-    f32x4_t acc[NJ];
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) acc[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    for (int run = wave; run < runs; run += UN * kDownWaves) {
-      u32x4_t x[UN][2], w[UN][NJ][2];
-#pragma unroll
-      for (int u = 0; u < UN; ++u)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int64_t k = 64 * (int64_t)(run + u * kDownWaves) + 16 * kq + 8 * h;
-          const bool in = k < Kred;
-          x[u][h] = buf_load16(rl, in && lok ? loff + (uint32_t)(k * 2) : 0x7fffffffu, 0u);
-#pragma unroll
-          for (int j = 0; j < NJ; ++j) {
-            const int row = 16 * (jb0 + j) + lr;
-            w[u][j][h] = buf_load16(rr, in && row < r ? (uint32_t)((row * Kred + k) * 2) : 0x7fffffffu, 0u);
-          }
-        }
-#pragma unroll
-      for (int u = 0; u < UN; ++u)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int j = 0; j < NJ; ++j) acc[j] = mfma_16x16x32(x[u][h], w[u][j][h], acc[j]);
-    }
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) s_acc[wave][j][lane] = acc[j];
-    __syncthreads();
-    if (ogroup == g && otok_ok) {
-      const float s = ad.s[id];
-      for (int o = tid; o < 256 * NJ; o += 64 * kDownWaves) {
-        const int jb = o >> 8, row = (o >> 4) & 15, jj = o & 15, j = 16 * (jb0 + jb) + jj;
-        if (j >= r) continue;
-        float t = 0.f;
-#pragma unroll
-        for (int w = 0; w < kDownWaves; ++w) t += s_acc[w][jb][16 * (row >> 2) + jj][row & 3];
-        if (out.T) out.T[otok * r + j] = t;
-        if (out.Tt) out.Tt[(j >> 4) * 256 + 16 * otok + (j & 15)] = t;
-        if (out.S || out.ST) {
-          uint16_t v[3];
-          split3(__fmul_rn(s, t), v);
-#pragma unroll
-          for (int i = 0; i < 3; ++i) {
-            if (out.S) out.S[opos * C + i * r + j] = v[i];
-            if (out.ST) out.ST[(int64_t)(i * r + j) * out.Mp + opos] = v[i];
-          }
-        }
-      }
-    }
-    __syncthreads();
-  }
+// Opens a ring stage to the workgroup: this wave's copies but the newest N are
+// done, and so are its LDS reads of the stage that is refilled next.
+template <int N>
+__device__ __forceinline__ void open_stage() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0070 | (N & 15) | ((N >> 4) << 14));  // vmcnt(N) lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
 }
 
-// The same for few tokens: a workgroup per (position, kFewRanks ranks), its 4
+// D[p][j] = Σ_k L[token(p)][k]·R_a(j, k) for the positions of one plan tile (up
+// to 64 of one adapter), 16·NJ ranks and one slice of the reduction, as fp32
+// partial sums P[slice][p][j].  R_a is A_a [r, Kred] (T = X·A_aᵀ) or, NATURAL,
+// B_a [Kred, r] (U = dY·B_a), whose operand fragments are transposing reads.
+// Bound by reading L once: both operands are copied straight into a ring of
+// LDS stages (64 reduction elements; L rows gathered through the plan), all
+// but one in flight, and the slices give every compute unit a part of the
+// ring's traffic (64 positions per tile read R a quarter as often as 16).  4
+// waves: NJ across the ranks, 4/NJ across the rows.
+constexpr int kDownRing = 4;
+struct DownJob {
+  const uint16_t* L;
+  int64_t Kred;
+  const uint16_t* R;
+  float* P;
+  int slices;
+};
+// NATURAL: the 16-byte chunks of a reduction row (2·NJ of them) XORed by bits
+// of the row, so that the 4 rows of a transposing read lie on different banks.
+template <int NJ>
+__device__ __forceinline__ int rank_swz(int row) {
+  return NJ == 4 ? (row & 3) << 1 : NJ == 2 ? row & 2 : 0;
+}
+__device__ __forceinline__ int dswz(int row, int chunk) { return row * 128 + ((chunk ^ (row & 7)) << 4); }
+
+template <int NJ, bool NATURAL>
+__device__ __forceinline__ void down_tile(const DownJob& J, int tile, int slice, int j0, int64_t M,
+                                          const AdapterView& ad, const PlanView& pl, char* sl, char* sr) {
+  constexpr int RI = NJ == 4 ? 2 : 1;                  // R copies per wave and stage
+  constexpr int LB = 64 * 128, RB = 4 * RI * 1024;     // stage bytes
+  const int2 tl = pl.tile[tile];
+  const int g = std::min(std::max(tl.x, 0), ad.count - 1), r = ad.r;
+  const int p0 = std::max(tl.y, 0), p1 = (int)std::min<int64_t>(std::min(p0 + 64, pl.start[g + 1]), M);
+  const int id = pl.id[g];
+  if ((unsigned)id >= (unsigned)ad.count || p0 >= p1) return;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lr = lane & 15, kq = lane >> 4;
+  const int64_t Kred = J.Kred;
+  const int all = (int)((Kred + 63) / 64);
+  const int s0 = split_first(slice, J.slices, all), s1 = split_first(slice + 1, J.slices, all);
+  const i32x4_t rl = rsrc_words(J.L, M * Kred * 2);
+  const i32x4_t rr = rsrc_words(J.R + (int64_t)id * r * Kred, (int64_t)r * Kred * 2);
+  // L: wave w copies rows 16w + 8c + (lane >> 3), lane i physical chunk i & 7
+  const int lch = (lane & 7) ^ (lane >> 3);
+  uint32_t vl[2];
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    const int pos = p0 + 16 * wave + 8 * c + (lane >> 3);
+    const int tok = pl.perm[std::min(pos, p1 - 1)];
+    vl[c] = pos < p1 && (uint32_t)tok < (uint32_t)M ? (uint32_t)tok * (uint32_t)Kred * 2u + 16u * lch : 0x7fffffffu;
+  }
+  auto issue = [&](int b, int s) __attribute__((always_inline)) {
+    const int64_t k0 = 64 * (int64_t)s;
+    const bool in = s < s1 && k0 + 8 * lch < Kred;
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+      dma_lds16(rl, sl + b * LB + (16 * wave + 8 * c) * 128, in ? vl[c] + (uint32_t)(k0 * 2) : 0x7fffffffu, 0u);
+#pragma unroll
+    for (int c = 0; c < RI; ++c) {
+      uint32_t o = 0x7fffffffu;
+      if constexpr (NATURAL) {
+        // rows of the reduction, 2·NJ chunks of 8 ranks each
+        const int idx = 64 * (RI * wave + c) + lane, row = idx / (2 * NJ);
+        const int j = j0 + 8 * ((idx % (2 * NJ)) ^ rank_swz<NJ>(row));
+        if (row < 64 && s < s1 && k0 + row < Kred && j < r) o = (uint32_t)(((k0 + row) * r + j) * 2);
+      } else {
+        const int row = 8 * (RI * wave + c) + (lane >> 3), j = j0 + row;
+        const int64_t k = k0 + 8 * ((lane & 7) ^ (row & 7));
+        if (row < 16 * NJ && j < r && s < s1 && k < Kred) o = (uint32_t)((j * Kred + k) * 2);
+      }
+      dma_lds16(rr, sr + b * RB + (RI * wave + c) * 1024, o, 0u);
+    }
+  };
+  const int wj = wave % NJ, wr = wave / NJ;  // this wave's rank block, and its NJ row blocks
+  f32x4_t acc[NJ];
+#pragma unroll
+  for (int i = 0; i < NJ; ++i) acc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i + 1 < kDownRing; ++i) issue(i, s0 + i);
+  for (int s = s0; s < s1; ++s) {
+    const int b = (s - s0) % kDownRing;
+    open_stage<(kDownRing - 2) * (2 + RI)>();
+    issue((s - s0 + kDownRing - 1) % kDownRing, s + kDownRing - 1);
+    const char* const lt = sl + b * LB;
+    const char* const rt = sr + b * RB;
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      u32x4_t w;
+      if constexpr (NATURAL) {
+        u32x2_t h[2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const int row = 32 * ks + 8 * kq + 4 * q + (lr >> 2), col = 16 * wj + 4 * (lr & 3);
+          h[q] = lds_read_tr(rt + row * 32 * NJ + (((col >> 3) ^ rank_swz<NJ>(row)) << 4) + 2 * (col & 7));
+        }
+        w = u32x4_t{h[0][0], h[0][1], h[1][0], h[1][1]};
+      } else {
+        w = *reinterpret_cast<const u32x4_t*>(rt + dswz(16 * wj + lr, 4 * ks + kq));
+      }
+#pragma unroll
+      for (int i = 0; i < NJ; ++i) {
+        const u32x4_t x = *reinterpret_cast<const u32x4_t*>(lt + dswz(16 * (NJ * wr + i) + lr, 4 * ks + kq));
+        acc[i] = mfma_16x16x32(x, w, acc[i]);
+      }
+    }
+  }
+  wait_vmem();  // no copy may land in LDS after the workgroup ends
+  const int j = j0 + 16 * wj + lr;
+  if (j >= r) return;
+#pragma unroll
+  for (int i = 0; i < NJ; ++i)
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const int pos = p0 + 16 * (NJ * wr + i) + 4 * kq + v;
+      if (pos < p1) J.P[((int64_t)slice * M + pos) * r + j] = acc[i][v];
+    }
+}
+
+// Job t (T = X·A_aᵀ; no slices: not asked for) and job u (U = dY·B_a) in one
+// launch: blockIdx.x = tile, y = slice of t, then of u, z = block of 16·NJ ranks.
+template <int NJ>
+__global__ __launch_bounds__(256) void adapters_down_kernel(DownJob t, DownJob u, int64_t M, AdapterView ad,
+                                                            PlanView pl) {
+  __shared__ __attribute__((aligned(1024))) char sl[kDownRing * 64 * 128];
+  __shared__ __attribute__((aligned(1024))) char sr[kDownRing * 4 * (NJ == 4 ? 2 : 1) * 1024];
+  const int tile = (int)blockIdx.x, y = (int)blockIdx.y, j0 = 16 * NJ * (int)blockIdx.z;
+  if (tile >= pl.head[2]) return;
+  if (y < t.slices)
+    down_tile<NJ, false>(t, tile, y, j0, M, ad, pl, sl, sr);
+  else
+    down_tile<NJ, true>(u, tile, y - t.slices, j0, M, ad, pl, sl, sr);
+}
+
+// The slices added in order, for 16 positions x 16 ranks per workgroup (one
+// value a thread): S [M, C] by position, and T [M, r] fp32 by token (zeros for
+// a token without an adapter).  A job without slices splits the T it is given.
+// One workgroup more (blockIdx.x == 0, if the table is asked for) cuts every
+// used adapter's positions into units of at most `unit`, the gradients' work
+// items.
+struct FactorJob {
+  const float* P;
+  int slices;
+  const float* T_in;
+  float* T_out;
+  uint16_t* S;
+};
+// {used adapter, first position, end, partial slot or -1: written directly}
+struct UnitTable {
+  int32_t* head;   // [0] units
+  int4* unit;      // [units]
+  int4* of_group;  // [count] {first slot or -1, units, 0, 0}
+};
+__device__ __forceinline__ int block_scan256(int v, int* s, int& total) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int x = v;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int y = __shfl_up(x, o, 64);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();
+  if (lane == 63) s[wave] = x;
+  __syncthreads();
+  total = 0;
+  for (int w = 0; w < 4; ++w) {
+    if (w < wave) x += s[w];
+    total += s[w];
+  }
+  return x - v;
+}
+__device__ __forceinline__ void cut_units(const AdapterView& ad, const PlanView& pl, const UnitTable& ut, int64_t M,
+                                          int unit, int max_units, int max_slots) {
+  __shared__ int s_scan[4];
+  const int used = std::min(std::max(pl.head[0], 0), ad.count);
+  const int64_t held = std::min<int64_t>(pl.head[1], M);
+  int u0 = 0, s0 = 0;
+  for (int b = 0; b < used; b += 256) {
+    const int g = b + (int)threadIdx.x;
+    int p0 = 0, p1 = 0;
+    if (g < used) {
+      p0 = std::max(pl.start[g], 0);
+      p1 = (int)std::min<int64_t>(pl.start[g + 1], held);
+    }
+    const int n = p1 > p0 ? (p1 - p0 + unit - 1) / unit : 0;
+    int tu, ts;
+    const int u = u0 + block_scan256(n, s_scan, tu), s = s0 + block_scan256(n > 1 ? n : 0, s_scan, ts);
+    if (g < used) ut.of_group[g] = int4{n > 1 ? s : -1, n, 0, 0};
+    for (int i = 0; i < n; ++i)
+      if (u + i < max_units && (n == 1 || s + i < max_slots))
+        ut.unit[u + i] = int4{g, p0 + i * unit, std::min(p0 + (i + 1) * unit, p1), n > 1 ? s + i : -1};
+    u0 += tu;
+    s0 += ts;
+  }
+  if (threadIdx.x == 0) ut.head[0] = std::min(u0, max_units);
+}
+
+__global__ __launch_bounds__(256) void adapters_factor_kernel(FactorJob t, FactorJob u, int64_t M, AdapterView ad,
+                                                              PlanView pl, unsigned first, UnitTable ut, int unit,
+                                                              int max_units, int max_slots) {
+  if (blockIdx.x < first) {
+    if (blockIdx.y == 0 && blockIdx.z == 0) cut_units(ad, pl, ut, M, unit, max_units, max_slots);
+    return;
+  }
+  const FactorJob J = blockIdx.z ? u : t;
+  const int64_t pos = 16 * (int64_t)(blockIdx.x - first) + (threadIdx.x >> 4);
+  const int r = ad.r, j = 16 * (int)blockIdx.y + (threadIdx.x & 15);
+  if (pos >= M || j >= r) return;
+  const int tok = pl.perm[pos];
+  if ((uint32_t)tok >= (uint32_t)M) return;
+  const bool has = pos < std::min<int64_t>(pl.head[1], M);
+  float v = 0.f;
+  if (has) {
+    if (J.slices == 0) {
+      v = J.T_in[(int64_t)tok * r + j];
+    } else {
+      const float* const p = J.P + pos * r + j;
+      // (the loads of eight slices, of existing ones whatever their number, before their adds)
+      for (int s = 0; s < J.slices; s += 8) {
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = p[(int64_t)std::min(s + i, J.slices - 1) * M * r];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (s + i < J.slices) v += x[i];
+      }
+    }
+  }
+  if (J.T_out) J.T_out[(int64_t)tok * r + j] = v;
+  if (!has || !J.S) return;
+  const int id = pl.owner[tok];
+  if ((unsigned)id >= (unsigned)ad.count) return;
+  uint16_t o[3];
+  split3(__fmul_rn(ad.s[id], v), o);
+#pragma unroll
+  for (int i = 0; i < 3; ++i) J.S[pos * adapter_cols(r) + i * r + j] = o[i];
+}
+
+// T for few tokens, in one launch: a workgroup per (position, kFewRanks ranks), its 4
 // waves sharing the reduction, 8 elements per lane and step; each token reads
 // its own adapter (tokens of one adapter share it in L2).  Fewer dependent
 // loads before the data than with tiles, and the adapters' rows spread over
@@ -291,8 +439,8 @@ __device__ __forceinline__ float wave_sum(float v) {
 }
 template <bool TOKENS>
 __global__ __launch_bounds__(256) void adapters_few_down_kernel(const uint16_t* __restrict__ L, int64_t M, int64_t Kred,
-                                                                const uint16_t* __restrict__ R, int by_id,
-                                                                AdapterView ad, PlanView pl, DownOut out) {
+                                                                AdapterView ad, PlanView pl, float* __restrict__ T,
+                                                                float* __restrict__ Tt, uint16_t* __restrict__ S) {
   constexpr int UN = 3;
   __shared__ float s_part[4][kFewRanks];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -304,9 +452,8 @@ __global__ __launch_bounds__(256) void adapters_few_down_kernel(const uint16_t* 
   const bool has = (unsigned)id < (unsigned)ad.count;
   float acc[kFewRanks] = {};
   if (has) {
-    const int g = by_id ? id : std::max(pl.slot[id], 0);
     const rsrc_t rl = make_rsrc(L + (int64_t)tok * Kred, Kred * 2);
-    const rsrc_t rr = make_rsrc(R + ((int64_t)g * r + j0) * Kred, (int64_t)kFewRanks * Kred * 2);
+    const rsrc_t rr = make_rsrc(ad.A + ((int64_t)id * r + j0) * Kred, (int64_t)kFewRanks * Kred * 2);
     for (int64_t k0 = 8 * tid; k0 < Kred; k0 += 2048 * UN) {
       u32x4_t x[UN], w[UN][kFewRanks];
 #pragma unroll
@@ -333,217 +480,79 @@ __global__ __launch_bounds__(256) void adapters_few_down_kernel(const uint16_t* 
   if (tid >= kFewRanks) return;
   const int j = j0 + tid;
   const float t = ((s_part[0][tid] + s_part[1][tid]) + s_part[2][tid]) + s_part[3][tid];
-  if (out.T) out.T[(int64_t)tok * r + j] = t;
-  if (out.Tt) out.Tt[(j >> 4) * 256 + 16 * tok + (j & 15)] = t;
-  if (has && (out.S || out.ST)) {
+  if (T) T[(int64_t)tok * r + j] = t;
+  if (Tt) Tt[(j >> 4) * 256 + 16 * tok + (j & 15)] = t;
+  if (has && S) {
     uint16_t v[3];
     split3(__fmul_rn(ad.s[id], t), v);
 #pragma unroll
-    for (int i = 0; i < 3; ++i) {
-      if (out.S) out.S[pos * adapter_cols(r) + i * r + j] = v[i];
-      if (out.ST) out.ST[(int64_t)(i * r + j) * out.Mp + pos] = v[i];
-    }
-  }
-}
-
-// ---------------------------------------------------------------------------
-// Operand copies of the backward pass, one launch: block 0 cuts every used
-// adapter's positions into units of at most `unit` (the gradients' work
-// items); the next bt blocks split a saved T into ST [3r, Mp]; the rest
-// transpose the used adapters: BT [used, r, N], AT [used, K, r], in 64 x 64
-// tiles through LDS.
-// ---------------------------------------------------------------------------
-// {used adapter, first position, end, partial slot or -1: written directly}
-struct UnitTable {
-  int32_t* head;   // [0] units
-  int4* unit;      // [units]
-  int4* of_group;  // [count] {first slot or -1, units, 0, 0}
-};
-__device__ __forceinline__ int block_scan256(int v, int* s, int& total) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  int x = v;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int y = __shfl_up(x, o, 64);
-    if (lane >= o) x += y;
-  }
-  __syncthreads();
-  if (lane == 63) s[wave] = x;
-  __syncthreads();
-  total = 0;
-  for (int w = 0; w < 4; ++w) {
-    if (w < wave) x += s[w];
-    total += s[w];
-  }
-  return x - v;
-}
-__global__ __launch_bounds__(256) void adapters_prep_kernel(const float* __restrict__ T, int64_t M, int64_t Mp,
-                                                            uint16_t* __restrict__ ST, uint16_t* __restrict__ BT,
-                                                            int64_t N, uint16_t* __restrict__ AT, int64_t K,
-                                                            AdapterView ad, PlanView pl, UnitTable ut, int unit,
-                                                            int max_units, int max_slots, unsigned bt, unsigned nb,
-                                                            unsigned na, unsigned jb) {
-  __shared__ uint16_t sh[3][64][66];
-  __shared__ int s_scan[4];
-  const int col = threadIdx.x & 63, row = threadIdx.x >> 6, r = ad.r;
-  const int used = std::min(std::max(pl.head[0], 0), ad.count);
-  const int64_t held = std::min<int64_t>(pl.head[1], M);
-  if (blockIdx.x == 0) {
-    int u0 = 0, s0 = 0;
-    for (int b = 0; b < used; b += 256) {
-      const int g = b + (int)threadIdx.x;
-      int p0 = 0, p1 = 0;
-      if (g < used) {
-        p0 = std::max(pl.start[g], 0);
-        p1 = (int)std::min<int64_t>(pl.start[g + 1], held);
-      }
-      const int n = p1 > p0 ? (p1 - p0 + unit - 1) / unit : 0;
-      int tu, ts;
-      const int u = u0 + block_scan256(n, s_scan, tu), s = s0 + block_scan256(n > 1 ? n : 0, s_scan, ts);
-      if (g < used) ut.of_group[g] = int4{n > 1 ? s : -1, n, 0, 0};
-      for (int i = 0; i < n; ++i)
-        if (u + i < max_units && (n == 1 || s + i < max_slots))
-          ut.unit[u + i] = int4{g, p0 + i * unit, std::min(p0 + (i + 1) * unit, p1), n > 1 ? s + i : -1};
-      u0 += tu;
-      s0 += ts;
-    }
-    if (threadIdx.x == 0) ut.head[0] = std::min(u0, max_units);
-    return;
-  }
-  unsigned b = blockIdx.x - 1;
-  if (b < bt) {
-    // positions p, ranks j of s·T
-    const int64_t q0 = (int64_t)(b / jb) * 64;
-    const int j0 = (int)(b % jb) * 64, j = j0 + col;
-    // (unconditional loads of clamped addresses: each step's 16 go out together)
-    int tok[16], id[16];
-    float sv[16], tv[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) tok[i] = pl.perm[std::min<int64_t>(q0 + 4 * i + row, M - 1)];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      if (q0 + 4 * i + row >= held || j >= r || (uint32_t)tok[i] >= (uint32_t)M) tok[i] = -1;
-      id[i] = pl.owner[std::max(tok[i], 0)];
-      tv[i] = T[(int64_t)std::max(tok[i], 0) * r + std::min(j, r - 1)];
-    }
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      if ((unsigned)id[i] >= (unsigned)ad.count) tok[i] = -1;
-      sv[i] = ad.s[tok[i] < 0 ? 0 : id[i]];
-    }
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      uint16_t v[3];
-      split3(tok[i] < 0 ? 0.f : __fmul_rn(sv[i], tv[i]), v);
-#pragma unroll
-      for (int t = 0; t < 3; ++t) sh[t][col][4 * i + row] = v[t];
-    }
-    __syncthreads();
-    for (int i = 0; i < 16; ++i) {
-      const int jj = 4 * i + row;
-      const int64_t pos = q0 + col;
-      if (j0 + jj < r && pos < Mp)
-#pragma unroll
-        for (int t = 0; t < 3; ++t) ST[(int64_t)(t * r + j0 + jj) * Mp + pos] = sh[t][jj][col];
-    }
-    return;
-  }
-  b -= bt;
-  const int g = (int)(b / (nb + na));
-  if (g >= used) return;
-  const int id = pl.id[g];
-  if ((unsigned)id >= (unsigned)ad.count) return;
-  unsigned t = b % (nb + na);
-  // in [rows, cols] -> out [cols, rows]
-  const bool isb = t < nb;
-  if (!isb) t -= nb;
-  const int64_t rows = isb ? N : r, cols = isb ? r : K;
-  const uint16_t* in = isb ? ad.B + (int64_t)id * N * r : ad.A + (int64_t)id * r * K;
-  uint16_t* o = isb ? BT + (int64_t)g * N * r : AT + (int64_t)g * K * r;
-  const int64_t r0 = 64 * (int64_t)(isb ? t / jb : t % jb), c0 = 64 * (int64_t)(isb ? t % jb : t / jb);
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int64_t rr = r0 + 4 * i + row, cc = c0 + col;
-    const bool ok = rr < rows && cc < cols;
-    const uint16_t v = in[ok ? rr * cols + cc : 0];
-    sh[0][col][4 * i + row] = ok ? v : 0;
-  }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int64_t cc = c0 + 4 * i + row, rr = r0 + col;
-    if (cc < cols && rr < rows) o[cc * rows + rr] = sh[0][4 * i + row][col];
+    for (int i = 0; i < 3; ++i) S[pos * adapter_cols(r) + i * r + j] = v[i];
   }
 }
 
 // ---------------------------------------------------------------------------
 // The adapters' gradients: for one unit (positions [p0, p1) of one used
 // adapter), 128 columns of L (X for dA, dY for dB) and up to 16·NJ ranks,
-//   D[c][j] = Σ_p L[token(p)][c]·(ST[j][p] + ST[r + j][p] + ST[2r + j][p]).
-// Stages of 64 positions, both operands copied straight into LDS, one stage
-// ahead; L rows are gathered through the plan and kept in their natural
-// layout, an MFMA operand (8 consecutive positions of one column) gathered
-// with 2-byte reads.  Positions outside the unit read as zero on both sides.
-// A unit that is its adapter's only one writes the gradient itself, the
-// others partial sums, added in unit order by the finishing kernel.
+//   D[c][j] = Σ_p L[token(p)][c]·(S[p][j] + S[p][r + j] + S[p][2r + j]).
+// Stages of 32 positions, both operands copied straight into a ring of LDS
+// stages in their own layouts (L rows gathered through the plan); the MFMA
+// operands, 8 consecutive positions of one column, are transposing reads.
+// Positions outside the unit read as zero on both sides.  A unit that is its
+// adapter's only one writes the gradient itself, the others partial sums,
+// added in unit order by the finishing kernel.
 // ---------------------------------------------------------------------------
-constexpr int kMaxUnit = 1024;
+constexpr int kMaxUnit = 1024, kGradRing = 3;
 struct GradientJob {
   const uint16_t* L;
   int64_t cols;
-  const uint16_t* ST;
-  float* out;       // [count][r·cols]
-  int64_t part_off; // of this job within a partial slot
-  int along;        // out [cols][r] (dB), else [r][cols] (dA)
+  const uint16_t* S;
+  float* out;        // [count][r·cols]
+  int64_t part_off;  // of this job within a partial slot
 };
-__device__ __forceinline__ int lswz(int row, int chunk) {
-  return row * 256 + ((chunk ^ (((row >> 3) & 7) << 1)) << 4);
+// 16-byte chunk c of L row p at c ^ ((p & 3) << 1): the 4 rows of a transposing
+// read on different banks
+__device__ __forceinline__ int lswz(int row, int col) {
+  return row * 256 + (((col >> 3) ^ ((row & 3) << 1)) << 4) + 2 * (col & 7);
 }
-__device__ __forceinline__ int sswz(int row, int chunk) { return row * 128 + ((chunk ^ (row & 7)) << 4); }
-
+// The same for S rows of 6·NJ chunks (three parts of 2·NJ).
 template <int NJ>
-__global__ __launch_bounds__(256) void adapters_gradient_kernel(GradientJob ja, GradientJob jb, unsigned tiles_a,
-                                                                int64_t M, int64_t Mp, AdapterView ad, PlanView pl,
-                                                                UnitTable ut, float* __restrict__ P,
-                                                                int64_t slot_floats) {
-  constexpr int SI = NJ == 1 ? 2 : NJ == 2 ? 3 : 6;  // S copies per wave and stage (8 rows each)
-  __shared__ __attribute__((aligned(1024))) char sl[2][64 * 256];
-  __shared__ __attribute__((aligned(1024))) char ss[2][4 * SI * 8 * 128];
-  __shared__ int s_tok[kMaxUnit + 128];
-  if ((int)blockIdx.y >= ut.head[0]) return;
-  const bool second = blockIdx.x >= tiles_a;
-  const GradientJob J = second ? jb : ja;
-  const int4 u = ut.unit[blockIdx.y];
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int lr = lane & 15, kq = lane >> 4, r = ad.r;
-  const int64_t c0 = 128 * (int64_t)(second ? blockIdx.x - tiles_a : blockIdx.x);
-  const int j0 = 16 * NJ * (int)blockIdx.z;
-  const int p0 = u.y, p1 = std::min(u.z, u.y + kMaxUnit), base = p0 & ~7;
-  const int stages = (p1 - base + 63) / 64;
-  for (int i = tid; i < 64 * stages; i += 256) {
-    const int pos = base + i;
-    s_tok[i] = pos >= p0 && pos < p1 ? pl.perm[pos] : -1;
-  }
-  __syncthreads();
+__device__ __forceinline__ int factor_swz(int row) {
+  return NJ == 4 ? (row & 3) << 1 : NJ == 2 ? row & 2 : 0;
+}
 
-  const i32x4_t rl = rsrc_words(J.L, M * J.cols * 2), rs = rsrc_words(J.ST, (int64_t)3 * r * Mp * 2);
+// ALONG: out [cols][r] (dB), else [r][cols] (dA).
+template <int NJ, bool ALONG>
+__device__ __forceinline__ void gradient_unit(const GradientJob& J, int64_t c0, int j0, const int4 u, int64_t M,
+                                              const AdapterView& ad, const PlanView& pl, float* __restrict__ P,
+                                              int64_t slot_floats, char* sl, char* ss, int* s_tok) {
+  constexpr int SI = NJ == 4 ? 3 : NJ == 2 ? 2 : 1;  // S copies per wave and stage
+  constexpr int LB = 32 * 256, SB = 4 * SI * 1024, SROW = 96 * NJ;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lr = lane & 15, kq = lane >> 4, r = ad.r, C = (int)adapter_cols(r);
+  const int p0 = u.y, p1 = std::min(u.z, u.y + kMaxUnit);
+  const int stages = (p1 - p0 + 31) / 32;
+  for (int i = tid; i < 32 * stages; i += 256) s_tok[i] = p0 + i < p1 ? pl.perm[p0 + i] : -1;
+  __syncthreads();
+  const i32x4_t rl = rsrc_words(J.L, M * J.cols * 2), rs = rsrc_words(J.S, M * C * 2);
   auto issue = [&](int b, int s) __attribute__((always_inline)) {
+    // L: wave w copies rows 8w + 4c + (lane >> 4), lane i physical chunk i & 15
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const int row = 16 * wave + 4 * c + (lane >> 4);
-      const int64_t col = c0 + 8 * ((lane & 15) ^ (((row >> 3) & 7) << 1));
-      const int tok = s_tok[64 * s + row];
-      const bool in = (uint64_t)(int64_t)tok < (uint64_t)M && col < J.cols;
-      dma_lds16(rl, sl[b] + (16 * wave + 4 * c) * 256, in ? (uint32_t)((tok * J.cols + col) * 2) : 0x7fffffffu, 0u);
+    for (int c = 0; c < 2; ++c) {
+      const int row = 8 * wave + 4 * c + (lane >> 4);
+      const int64_t col = c0 + 8 * ((lane & 15) ^ ((row & 3) << 1));
+      const int tok = s < stages ? s_tok[32 * s + row] : -1;
+      const bool in = (uint32_t)tok < (uint32_t)M && col < J.cols;
+      dma_lds16(rl, sl + b * LB + (8 * wave + 4 * c) * 256,
+                in ? ((uint32_t)tok * (uint32_t)J.cols + (uint32_t)col) * 2u : 0x7fffffffu, 0u);
     }
 #pragma unroll
     for (int c = 0; c < SI; ++c) {
-      const int row = 8 * (SI * wave + c) + (lane >> 3);
-      const int part = row / (16 * NJ), j = j0 + row % (16 * NJ);
-      const int64_t pos = base + 64 * s + 8 * ((lane & 7) ^ (row & 7));
-      const bool in = part < 3 && j < r && pos < Mp;
-      dma_lds16(rs, ss[b] + 8 * (SI * wave + c) * 128, in ? (uint32_t)(((part * r + j) * Mp + pos) * 2) : 0x7fffffffu,
-                0u);
+      const int idx = 64 * (SI * wave + c) + lane, row = idx / (6 * NJ);
+      const int ch = (idx % (6 * NJ)) ^ factor_swz<NJ>(row), part = ch / (2 * NJ), j = j0 + 8 * (ch % (2 * NJ));
+      const int pos = p0 + 32 * s + row;
+      const bool in = row < 32 && pos < p1 && j < r;
+      dma_lds16(rs, ss + b * SB + (SI * wave + c) * 1024,
+                in ? ((uint32_t)pos * (uint32_t)C + (uint32_t)(part * r + j)) * 2u : 0x7fffffffu, 0u);
     }
   };
   f32x4_t acc[2][NJ];
@@ -551,62 +560,39 @@ __global__ __launch_bounds__(256) void adapters_gradient_kernel(GradientJob ja, 
   for (int i = 0; i < 2; ++i)
 #pragma unroll
     for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  auto compute = [&](auto along, int b, int s) __attribute__((always_inline)) {
-    const char* const lt = sl[b];
-    const char* const st = ss[b];
-    const bool inside = base + 64 * s >= p0 && base + 64 * s + 64 <= p1;
 #pragma unroll
-    for (int mh = 0; mh < 2; ++mh) {
-      u32x4_t a[2];
-#pragma unroll
-      for (int pf = 0; pf < 2; ++pf) {
-        const int c = 32 * wave + 16 * pf + lr;
-        uint32_t h[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          h[i] = *reinterpret_cast<const uint16_t*>(lt + lswz(32 * mh + 8 * kq + i, c >> 3) + 2 * (c & 7));
-#pragma unroll
-        for (int t = 0; t < 4; ++t) a[pf][t] = h[2 * t] | (h[2 * t + 1] << 16);
-      }
-      u32x4_t mask = {~0u, ~0u, ~0u, ~0u};
-      if (!inside) {
-        const int q = base + 64 * s + 32 * mh + 8 * kq;
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-          mask[t] = (q + 2 * t >= p0 && q + 2 * t < p1 ? 0xffffu : 0u) |
-                    (q + 2 * t + 1 >= p0 && q + 2 * t + 1 < p1 ? 0xffff0000u : 0u);
-      }
-#pragma unroll
-      for (int part = 0; part < 3; ++part)
-#pragma unroll
-        for (int jf = 0; jf < NJ; ++jf) {
-          u32x4_t f = *reinterpret_cast<const u32x4_t*>(st + sswz(16 * NJ * part + 16 * jf + lr, 4 * mh + kq));
-          if (!inside)
-#pragma unroll
-            for (int t = 0; t < 4; ++t) f[t] &= mask[t];
-#pragma unroll
-          for (int pf = 0; pf < 2; ++pf)
-            acc[pf][jf] = decltype(along)::value ? mfma_16x16x32(a[pf], f, acc[pf][jf])
-                                                 : mfma_16x16x32(f, a[pf], acc[pf][jf]);
-        }
-    }
-  };
-  issue(0, 0);
+  for (int i = 0; i + 1 < kGradRing; ++i) issue(i, i);
   for (int s = 0; s < stages; ++s) {
-    if (s + 1 < stages) {
-      issue((s + 1) & 1, s + 1);
-      wait_vmem_le<4 + SI>();
-    } else {
-      wait_vmem();
+    open_stage<(kGradRing - 2) * (2 + SI)>();
+    issue((s + kGradRing - 1) % kGradRing, s + kGradRing - 1);
+    const char* const lt = sl + (s % kGradRing) * LB;
+    const char* const st = ss + (s % kGradRing) * SB;
+    const int trow = 8 * kq + (lr >> 2), tcol = 4 * (lr & 3);  // this lane's part of a transposing read
+    u32x4_t a[2];
+#pragma unroll
+    for (int pf = 0; pf < 2; ++pf) {
+      const u32x2_t h0 = lds_read_tr(lt + lswz(trow, 32 * wave + 16 * pf + tcol));
+      const u32x2_t h1 = lds_read_tr(lt + lswz(trow + 4, 32 * wave + 16 * pf + tcol));
+      a[pf] = u32x4_t{h0[0], h0[1], h1[0], h1[1]};
     }
-    asm volatile("" ::: "memory");
-    __syncthreads();
-    if (J.along)
-      compute(std::true_type(), s & 1, s);
-    else
-      compute(std::false_type(), s & 1, s);
-    __syncthreads();
+#pragma unroll
+    for (int part = 0; part < 3; ++part)
+#pragma unroll
+      for (int jf = 0; jf < NJ; ++jf) {
+        const int col = 16 * (NJ * part + jf) + tcol;
+        u32x2_t h[2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const int row = trow + 4 * q;
+          h[q] = lds_read_tr(st + row * SROW + (((col >> 3) ^ factor_swz<NJ>(row)) << 4) + 2 * (col & 7));
+        }
+        const u32x4_t f = {h[0][0], h[0][1], h[1][0], h[1][1]};
+#pragma unroll
+        for (int pf = 0; pf < 2; ++pf)
+          acc[pf][jf] = ALONG ? mfma_16x16x32(a[pf], f, acc[pf][jf]) : mfma_16x16x32(f, a[pf], acc[pf][jf]);
+      }
   }
+  wait_vmem();  // no copy may land in LDS after the workgroup ends
   const int id = pl.id[u.x];
   if ((unsigned)id >= (unsigned)ad.count) return;
   float* const o = u.w < 0 ? J.out + (int64_t)id * r * J.cols : P + (int64_t)u.w * slot_floats + J.part_off;
@@ -618,10 +604,26 @@ __global__ __launch_bounds__(256) void adapters_gradient_kernel(GradientJob ja, 
       for (int v = 0; v < 4; ++v) {
         const int64_t cb = c0 + 32 * wave + 16 * pf;
         const int jbase = j0 + 16 * jf;
-        const int64_t c = J.along ? cb + 4 * kq + v : cb + lr;
-        const int j = J.along ? jbase + lr : jbase + 4 * kq + v;
-        if (c < J.cols && j < r) o[J.along ? c * r + j : j * J.cols + c] = acc[pf][jf][v];
+        const int64_t c = ALONG ? cb + 4 * kq + v : cb + lr;
+        const int j = ALONG ? jbase + lr : jbase + 4 * kq + v;
+        if (c < J.cols && j < r) o[ALONG ? c * r + j : j * J.cols + c] = acc[pf][jf][v];
       }
+}
+
+template <int NJ>
+__global__ __launch_bounds__(256) void adapters_gradient_kernel(GradientJob ja, GradientJob jb, unsigned tiles_a,
+                                                                int64_t M, AdapterView ad, PlanView pl, UnitTable ut,
+                                                                float* __restrict__ P, int64_t slot_floats) {
+  __shared__ __attribute__((aligned(1024))) char sl[kGradRing * 32 * 256];
+  __shared__ __attribute__((aligned(1024))) char ss[kGradRing * 4 * (NJ == 4 ? 3 : NJ == 2 ? 2 : 1) * 1024];
+  __shared__ int s_tok[kMaxUnit];
+  if ((int)blockIdx.y >= ut.head[0]) return;
+  const int4 u = ut.unit[blockIdx.y];
+  const int j0 = 16 * NJ * (int)blockIdx.z;
+  if (blockIdx.x < tiles_a)
+    gradient_unit<NJ, false>(ja, 128 * (int64_t)blockIdx.x, j0, u, M, ad, pl, P, slot_floats, sl, ss, s_tok);
+  else
+    gradient_unit<NJ, true>(jb, 128 * (int64_t)(blockIdx.x - tiles_a), j0, u, M, ad, pl, P, slot_floats, sl, ss, s_tok);
 }
 
 // Partial sums added in unit order; zeros for an adapter without tokens.
@@ -656,7 +658,7 @@ __global__ __launch_bounds__(256) void adapters_gradient_finish_kernel(float* __
 // ---------------------------------------------------------------------------
 
 size_t plan_bytes(int64_t M, int count) {
-  return (size_t)(kPlanHead + 3 * plan_pad(M) + 3 * plan_pad(count + 1)) * 4;
+  return (size_t)(kPlanHead + 3 * plan_pad(M) + 3 * plan_pad(count + 1) + plan_pad(2 * plan_tiles(M, count))) * 4;
 }
 PlanView plan_view(void* plan, int64_t M, int count) {
   PlanView v;
@@ -667,6 +669,7 @@ PlanView plan_view(void* plan, int64_t M, int count) {
   v.id = v.group + plan_pad(M);
   v.start = v.id + plan_pad(count + 1);
   v.slot = v.start + plan_pad(count + 1);
+  v.tile = reinterpret_cast<int2*>(v.slot + plan_pad(count + 1));
   return v;
 }
 hipError_t launch_adapters_plan(const int32_t* index, int64_t M, int count, const PlanView& pl, hipStream_t st) {
@@ -676,35 +679,26 @@ hipError_t launch_adapters_plan(const int32_t* index, int64_t M, int count, cons
 
 namespace {
 
-int64_t position_stride(int64_t M) { return round_up(std::max<int64_t>(M, 1), 64); }
-
 // NJ blocks of 16 ranks per workgroup
 int rank_blocks(int r) { return r <= 16 ? 1 : r <= 32 ? 2 : 4; }
 
-hipError_t launch_down(const uint16_t* L, int64_t M, int64_t Kred, const uint16_t* R, int by_id, const AdapterView& ad,
-                       const PlanView& pl, const DownOut& out, hipStream_t st) {
-  if (M <= kFewTokens) {
-    const dim3 grid((unsigned)M, (unsigned)(ad.r / kFewRanks));
-    if (M <= 16 && out.S == nullptr && out.ST == nullptr)
-      adapters_few_down_kernel<true><<<grid, 256, 0, st>>>(L, M, Kred, R, by_id, ad, pl, out);
-    else
-      adapters_few_down_kernel<false><<<grid, 256, 0, st>>>(L, M, Kred, R, by_id, ad, pl, out);
-    return hipGetLastError();
-  }
-  const unsigned tiles = cdiv(M, 16);
-  // few tokens: one workgroup per 16 ranks, so that each reads less of the
-  // adapter; then as many workgroups per tile as fill the chip once
-  const int nj = tiles < 64 ? 1 : rank_blocks(ad.r);
-  const unsigned z = cdiv(ad.r, 16 * nj);
-  const unsigned want = 512 / (tiles * z) + 1;
-  const unsigned y = std::min<unsigned>({want, 16u, (unsigned)ad.count});
-  const dim3 grid(tiles, y, z), block(64 * kDownWaves);
+// Slices of a low-rank factor's reduction: about 512 workgroups over the
+// tiles that M tokens make at least, of 4 stages each or more, 16 at most.
+int down_slices(int64_t M, int64_t Kred, int r) {
+  const int64_t work = std::max<int64_t>(1, M / 64) * cdiv(r, 16 * rank_blocks(r));
+  return (int)std::max<int64_t>(1, std::min<int64_t>({512 / work, (int64_t)cdiv(Kred, 256), 16}));
+}
+
+hipError_t launch_down(const DownJob& t, const DownJob& u, int64_t M, const AdapterView& ad, const PlanView& pl,
+                       hipStream_t st) {
+  const int nj = rank_blocks(ad.r);
+  const dim3 grid((unsigned)plan_tiles(M, ad.count), (unsigned)(t.slices + u.slices), cdiv(ad.r, 16 * nj));
   if (nj == 1)
-    adapters_down_kernel<1><<<grid, block, 0, st>>>(L, M, Kred, R, by_id, ad, pl, out);
+    adapters_down_kernel<1><<<grid, 256, 0, st>>>(t, u, M, ad, pl);
   else if (nj == 2)
-    adapters_down_kernel<2><<<grid, block, 0, st>>>(L, M, Kred, R, by_id, ad, pl, out);
+    adapters_down_kernel<2><<<grid, 256, 0, st>>>(t, u, M, ad, pl);
   else
-    adapters_down_kernel<4><<<grid, block, 0, st>>>(L, M, Kred, R, by_id, ad, pl, out);
+    adapters_down_kernel<4><<<grid, 256, 0, st>>>(t, u, M, ad, pl);
   return hipGetLastError();
 }
 
@@ -713,89 +707,111 @@ hipError_t launch_down(const uint16_t* L, int64_t M, int64_t Kred, const uint16_
 AdaptersFwdLayout adapters_fwd_layout(int64_t M, int64_t N, int64_t K, int r, int count) {
   AdaptersFwdLayout L{};
   L.splits = M > 16 ? fwd_gemm_splits(M, N, K, SIZE_MAX) : 1;
+  L.slices = M > kFewTokens ? down_slices(M, K, r) : 0;
   L.off_S = 0;
   L.off_P = M > 16 ? round_up(M * adapter_cols(r) * 2, 256) : M > 0 ? round_up((int64_t)cdiv(r, 16) * 1024, 256) : 0;
-  L.total = L.off_P + (L.splits > 1 ? round_up((int64_t)L.splits * M * N * 4, 256) : 0);
+  const int64_t gemm = L.splits > 1 ? (int64_t)L.splits * M * N * 4 : 0;
+  L.total = L.off_P + round_up(std::max(gemm, (int64_t)L.slices * M * r * 4), 256);
   return L;
 }
+namespace {
+// Column tiles times rank blocks of the gradients, and the units they need to
+// fill the chip about twice over.
+int64_t gradient_parts(int64_t N, int64_t K, int r) {
+  const int64_t work = (int64_t)(cdiv(K, 128) + cdiv(N, 128)) * cdiv(r, 16 * rank_blocks(r));
+  return std::max<int64_t>(1, (512 + work - 1) / work);
+}
+int64_t unit_table_bytes(int64_t units, int count) { return round_up(256 + (units + count) * 16, 256); }
+}  // namespace
 AdaptersBwdLayout adapters_bwd_layout(int64_t M, int64_t N, int64_t K, int r, int count) {
   AdaptersBwdLayout L{};
   L.splits = M > 0 ? dx_gemm_splits(M, N, K, SIZE_MAX) : 1;
   if (M == 0) return L;
-  const int64_t Mp = position_stride(M), used = std::min<int64_t>(count, M);
-  // about 512 workgroups or more: units of 64 to 1,024 positions
-  const int64_t work = (int64_t)(cdiv(K, 128) + cdiv(N, 128)) * cdiv(r, 16 * rank_blocks(r));
-  const int64_t parts = std::max<int64_t>(1, (512 + work - 1) / work);
+  L.slices_U = down_slices(M, N, r);
+  L.slices_T = down_slices(M, K, r);
+  const int64_t parts = gradient_parts(N, K, r);
   L.unit = (int)std::min<int64_t>(kMaxUnit, round_up((M + parts - 1) / parts, 64));
-  L.units = (int)(M / L.unit + used);
+  L.units = (int)(M / L.unit + std::min<int64_t>(count, M));
   L.slots = (int)(2 * M / L.unit);  // (an adapter of n > 1 units has more than (n - 1)·unit tokens)
   size_t off = 0;
   L.off_U = off;
   off += round_up(M * adapter_cols(r) * 2, 256);
-  L.off_UT = off;
-  off += round_up(3 * r * Mp * 2, 256);
-  L.off_TT = off;
-  off += round_up(3 * r * Mp * 2, 256);
-  L.off_AT = off;
-  off += round_up(used * K * r * 2, 256);
-  L.off_BT = off;
-  off += round_up(used * N * r * 2, 256);
+  L.off_T = off;
+  off += round_up(M * adapter_cols(r) * 2, 256);
   L.off_units = off;
-  off += round_up(256 + (int64_t)(L.units + count) * 16, 256);
+  off += unit_table_bytes(L.units, count);
   L.off_P = off;
   const int64_t gemm = L.splits > 1 ? (int64_t)L.splits * M * K * 4 : 0;
-  off += round_up(std::max<int64_t>(gemm, (int64_t)L.slots * r * (K + N) * 4), 256);
+  const int64_t factors = (int64_t)(L.slices_U + L.slices_T) * M * r * 4;
+  off += round_up(std::max({gemm, factors, (int64_t)L.slots * r * (K + N) * 4}), 256);
   L.total = off;
   return L;
 }
 
+// Within a band of 256 tokens the GEMM's split count is constant and its
+// partials grow with M; a factor's slices only fall with M, by less than M
+// grows from one multiple of 64 to the next, so the largest M of every 64 is
+// taken.
 size_t adapters_fwd_ws_max(int64_t M_max, int64_t N, int64_t K, int r, int count) {
   size_t most = adapters_fwd_layout(std::min<int64_t>(M_max, 16), N, K, r, count).total;
-  // the split count depends on M through the number of 256-row tiles alone
-  // and the bytes grow with M within such a band: each band's largest M
-  for (int64_t top = 256; M_max > 16; top += 256) {
+  for (int64_t top = 63; M_max > 16; top += 64) {
     most = std::max(most, adapters_fwd_layout(std::min(top, M_max), N, K, r, count).total);
     if (top >= M_max) break;
+    most = std::max(most, adapters_fwd_layout(std::min(top + 1, M_max), N, K, r, count).total);
   }
   return most;
 }
 size_t adapters_bwd_ws_max(int64_t M_max, int64_t N, int64_t K, int r, int count) {
-  // every part but the shared area grows with M; that one is bounded band by
-  // band for the GEMM's partials, and for the gradients by 2M/unit slots:
-  // units of at least M/parts give 2·parts, units of 1,024 at most 2M/1,024
+  // the factors grow with M; the shared area is bounded band by band for the
+  // GEMM's and the factors' partials, and for the gradients' by 2M/unit
+  // slots: units of at least M/parts give 2·parts, units of 1,024 2M/1,024
   const AdaptersBwdLayout L = adapters_bwd_layout(M_max, N, K, r, count);
   if (M_max == 0) return L.total;
   int64_t area = 0;
-  for (int64_t top = 256;; top += 256) {
-    const int64_t M = std::min(top, M_max);
-    const int splits = dx_gemm_splits(M, N, K, SIZE_MAX);
-    if (splits > 1) area = std::max(area, splits * M * K * 4);
+  for (int64_t top = 63;; top += 64) {
+    for (int64_t M : {std::min(top, M_max), std::min(top + 1, M_max)}) {
+      const AdaptersBwdLayout l = adapters_bwd_layout(M, N, K, r, count);
+      if (l.splits > 1) area = std::max(area, l.splits * M * K * 4);
+      area = std::max(area, (int64_t)(l.slices_U + l.slices_T) * M * r * 4);
+    }
     if (top >= M_max) break;
   }
-  const int64_t work = (int64_t)(cdiv(K, 128) + cdiv(N, 128)) * cdiv(r, 16 * rank_blocks(r));
-  const int64_t parts = std::max<int64_t>(1, (512 + work - 1) / work);
+  const int64_t parts = gradient_parts(N, K, r);
   const int64_t slots = std::min(std::max<int64_t>(2 * parts, 2 * M_max / kMaxUnit), 2 * M_max / 64);
   area = std::max(area, slots * r * (K + N) * 4);
-  // the units' table: M / unit is at most parts or M / 1,024
   const int64_t units = std::max(parts, M_max / kMaxUnit) + std::min<int64_t>(count, M_max);
-  return L.off_units + round_up(256 + (units + count) * 16, 256) + round_up(area, 256);
+  return L.off_units + unit_table_bytes(units, count) + round_up(area, 256);
 }
 
 hipError_t launch_adapters_fwd(const Nf4View& W, const uint16_t* X, int64_t M, const AdapterView& ad,
                                const PlanView& pl, void* Y, bool y16, float* T_save, char* ws,
                                const AdaptersFwdLayout& L, hipStream_t st) {
   if (M == 0) return hipSuccess;
+  const dim3 few((unsigned)M, (unsigned)(ad.r / kFewRanks));
+  uint16_t* const none = nullptr;
   if (M <= 16) {
     float* Tt = reinterpret_cast<float*>(ws + L.off_S);
-    const hipError_t e = launch_down(X, M, W.K, ad.A, 1, ad, pl, DownOut{T_save, Tt, nullptr, nullptr, 0}, st);
+    adapters_few_down_kernel<true><<<few, 256, 0, st>>>(X, M, W.K, ad, pl, T_save, Tt, none);
+    const hipError_t e = hipGetLastError();
     return e != hipSuccess ? e : launch_gemv_adapters(W, X, M, ad, pl.owner, Y, y16, Tt, st);
   }
   uint16_t* S = reinterpret_cast<uint16_t*>(ws + L.off_S);
   float* P = reinterpret_cast<float*>(ws + L.off_P);
-  hipError_t e = launch_down(X, M, W.K, ad.A, 1, ad, pl, DownOut{T_save, nullptr, S, nullptr, 0}, st);
+  hipError_t e;
+  if (M <= kFewTokens) {
+    adapters_few_down_kernel<false><<<few, 256, 0, st>>>(X, M, W.K, ad, pl, T_save, (float*)nullptr, S);
+    e = hipGetLastError();
+  } else {
+    e = launch_down(DownJob{X, W.K, ad.A, P, L.slices}, DownJob{}, M, ad, pl, st);
+    if (e != hipSuccess) return e;
+    const FactorJob t{P, L.slices, nullptr, T_save, S};
+    adapters_factor_kernel<<<dim3(cdiv(M, 16), cdiv(ad.r, 16)), 256, 0, st>>>(t, t, M, ad, pl, 0u, UnitTable{}, 1, 0, 0);
+    e = hipGetLastError();
+  }
   if (e != hipSuccess) return e;
+  // (the partial sums of T have been consumed: P now takes the split partials)
   const AdapterGemmArgs ma{pl.head, (int)plan_pad(M), (int)plan_pad(ad.count + 1), S, ad.B, ad.r,
-                           (int)adapter_cols(ad.r), ad.count, 1};
+                           (int)adapter_cols(ad.r), ad.count};
   e = launch_fwd_gemm_adapters(W, X, M, ma, Y, y16, L.splits, P, st);
   if (e != hipSuccess || L.splits == 1) return e;
   return launch_splitk_reduce(P, L.splits, M * W.N, Y, y16, false, st);
@@ -810,43 +826,39 @@ hipError_t launch_adapters_bwd(const Nf4View& W, const uint16_t* X, const uint16
     e = launch_zero(dA, ad.count * r * K, st);
     return e != hipSuccess ? e : launch_zero(dB, ad.count * r * N, st);
   }
-  const int64_t Mp = position_stride(M);
   uint16_t* U = reinterpret_cast<uint16_t*>(ws + L.off_U);
-  uint16_t* UT = reinterpret_cast<uint16_t*>(ws + L.off_UT);
-  uint16_t* TT = reinterpret_cast<uint16_t*>(ws + L.off_TT);
-  uint16_t* AT = reinterpret_cast<uint16_t*>(ws + L.off_AT);
-  uint16_t* BT = reinterpret_cast<uint16_t*>(ws + L.off_BT);
+  uint16_t* T = reinterpret_cast<uint16_t*>(ws + L.off_T);
   float* P = reinterpret_cast<float*>(ws + L.off_P);
   UnitTable ut;
   ut.head = reinterpret_cast<int32_t*>(ws + L.off_units);
   ut.unit = reinterpret_cast<int4*>(ws + L.off_units + 256);
   ut.of_group = ut.unit + L.units;
-  const unsigned jb = cdiv(r, 64), bt = T_saved ? cdiv(Mp, 64) * jb : 0u;
-  const unsigned nb = cdiv(N, 64) * jb, na = cdiv(K, 64) * jb;
-  const unsigned used = (unsigned)std::min<int64_t>(ad.count, M);
-  adapters_prep_kernel<<<1 + bt + used * (nb + na), 256, 0, st>>>(T_saved, M, Mp, TT, BT, N, AT, K, ad, pl, ut, L.unit,
-                                                                  L.units, L.slots, bt, nb, na, jb);
-  e = hipGetLastError();
-  if (e == hipSuccess && !T_saved)
-    e = launch_down(X, M, K, ad.A, 1, ad, pl, DownOut{nullptr, nullptr, nullptr, TT, Mp}, st);
-  if (e == hipSuccess) e = launch_down(dY, M, N, BT, 0, ad, pl, DownOut{nullptr, nullptr, U, UT, Mp}, st);
+  // U, and T unless it was saved
+  float* const PU = P + (T_saved ? 0 : (int64_t)L.slices_T * M * r);
+  const DownJob dt{X, K, ad.A, P, T_saved ? 0 : L.slices_T}, du{dY, N, ad.B, PU, L.slices_U};
+  e = launch_down(dt, du, M, ad, pl, st);
   if (e != hipSuccess) return e;
-  const AdapterGemmArgs ma{pl.head, (int)plan_pad(M), (int)plan_pad(ad.count + 1), U, AT, ad.r,
-                           (int)adapter_cols(r), ad.count, 0};
+  const FactorJob ft{P, dt.slices, T_saved, nullptr, T}, fu{PU, L.slices_U, nullptr, nullptr, U};
+  adapters_factor_kernel<<<dim3(1 + cdiv(M, 16), cdiv(r, 16), 2), 256, 0, st>>>(ft, fu, M, ad, pl, 1u, ut, L.unit,
+                                                                               L.units, L.slots);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const AdapterGemmArgs ma{pl.head, (int)plan_pad(M), (int)plan_pad(ad.count + 1), U, ad.A, ad.r,
+                           (int)adapter_cols(r), ad.count};
   e = launch_dx_gemm_adapters(W, dY, M, ma, dX, dx16, L.splits, P, st);
   if (e == hipSuccess && L.splits > 1) e = launch_splitk_reduce(P, L.splits, M * K, dX, dx16, false, st);
   if (e != hipSuccess) return e;
   const int64_t slot = r * (K + N);
-  const GradientJob ja{X, K, UT, dA, 0, 0}, jo{dY, N, TT, dB, r * K, 1};
+  const GradientJob ja{X, K, U, dA, 0}, jo{dY, N, T, dB, r * K};
   const int nj = rank_blocks(ad.r);
   const unsigned ta = cdiv(K, 128);
   const dim3 grid(ta + cdiv(N, 128), (unsigned)L.units, cdiv(r, 16 * nj));
   if (nj == 1)
-    adapters_gradient_kernel<1><<<grid, 256, 0, st>>>(ja, jo, ta, M, Mp, ad, pl, ut, P, slot);
+    adapters_gradient_kernel<1><<<grid, 256, 0, st>>>(ja, jo, ta, M, ad, pl, ut, P, slot);
   else if (nj == 2)
-    adapters_gradient_kernel<2><<<grid, 256, 0, st>>>(ja, jo, ta, M, Mp, ad, pl, ut, P, slot);
+    adapters_gradient_kernel<2><<<grid, 256, 0, st>>>(ja, jo, ta, M, ad, pl, ut, P, slot);
   else
-    adapters_gradient_kernel<4><<<grid, 256, 0, st>>>(ja, jo, ta, M, Mp, ad, pl, ut, P, slot);
+    adapters_gradient_kernel<4><<<grid, 256, 0, st>>>(ja, jo, ta, M, ad, pl, ut, P, slot);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   adapters_gradient_finish_kernel<<<dim3(std::min(cdiv(slot, 1024), 256u), (unsigned)ad.count), 256, 0, st>>>(

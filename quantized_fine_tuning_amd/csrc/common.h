@@ -193,6 +193,14 @@ __device__ __forceinline__ uint32_t lds_offset(const void* p) {
 __device__ __forceinline__ uint16_t lds_read_u16(uint32_t a) {
   return *(const lds_u16_t*)(uintptr_t)a;
 }
+// Transposing LDS read of 8 bytes per lane (ds_read_b64_tr_b16): within each 16
+// lanes, lanes 4i .. 4i + 3 address the 16 values (32 bytes) of row i, and lane
+// c receives column c of the 4 rows.
+typedef short i16x4_t __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ u32x2_t lds_read_tr(const char* p) {
+  return __builtin_bit_cast(
+      u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) i16x4_t*)(p)));
+}
 // v = hi + lo with hi = RNE_bf16(v) and lo = RNE_bf16(v - hi): the pair
 // carries about 16 significant bits of an fp32 value into bf16 products.
 __device__ __forceinline__ void split_hilo(float v, uint16_t& hi, uint16_t& lo) {

@@ -79,6 +79,12 @@ __device__ __forceinline__ int wswz(int row, int chunk) {
 // lane bits 0..5 are cg0, rg0, rg1, cg1, cg2, rg2.  Each half-wave then
 // reads the tables of 4 row groups (32 banks once), and each 8 consecutive
 // lanes store their 16-byte chunks to 8 distinct chunk positions.
+// MULTI's A tile (64 three-part ranks of 256 columns): the 16-byte chunks of a
+// row XORed by its low bits, so that the 4 rows of a transposing read lie on
+// different banks; byte of column col (a multiple of 4).
+__device__ __forceinline__ int atswz(int row, int col) {
+  return row * 512 + (((col >> 3) ^ ((row & 3) << 1)) << 4) + 2 * (col & 7);
+}
 __device__ __forceinline__ int dq_rg(int l) { return ((l >> 1) & 3) | ((l >> 3) & 4); }
 __device__ __forceinline__ int dq_cg(int l) { return (l & 1) | ((l >> 2) & 6); }
 
@@ -292,6 +298,33 @@ __global__ __launch_bounds__(kThreads, 1) void dx_gemm_kernel(Nf4View W, const u
       }
     };
 
+    // MULTI, a LoRA step: the B tile is 64 rows (three-part ranks) of 256
+    // columns k in the adapter's own layout; a fragment (8 consecutive ranks of
+    // one column) is two transposing reads, lane i of each 16 supplying 8 bytes
+    // of row i / 4 and receiving column i.
+    auto read_bt = [&](const char* wb, int ks, u32x4_t* b) __attribute__((always_inline)) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        u32x2_t h[2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+          h[q] = lds_read_tr(wb + atswz(8 * (2 * kq + ks) + 4 * q + (lr >> 2), 64 * wk + 16 * j + 4 * (lr & 3)));
+        b[j] = u32x4_t{h[0][0], h[0][1], h[1][0], h[1][1]};
+      }
+    };
+    auto lora_step = [&](const char* ya, const char* wb) __attribute__((always_inline)) {
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        read_bt(wb, ks, bfr);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const u32x4_t a = read_a(ya, 8 * ks + i);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[i][j] = mfma16<F16>(a, bfr[j], acc[i][j]);
+        }
+      }
+    };
+
     const bool dq = wave < 4;  // dequantizes slice 2w of every step
     __syncthreads();  // codes and tables of steps 0 and 1 in place
     auto read_codes_mfma = [&](int t) __attribute__((always_inline)) {
@@ -320,7 +353,7 @@ __global__ __launch_bounds__(kThreads, 1) void dx_gemm_kernel(Nf4View W, const u
         const int s = nsteps + l;
         int p0, p1;
         rows_of(l, p0, p1);  // (waves whose rows hold none of the adapter's tokens skip its steps)
-        if (p0 < 128 * wm + 128 && p1 > 128 * wm) mfma_step(sab(s & 1), sw[s & 1]);
+        if (p0 < 128 * wm + 128 && p1 > 128 * wm) lora_step(sab(s & 1), sw[s & 1]);
         __syncthreads();
       }
     }
@@ -480,9 +513,10 @@ __global__ __launch_bounds__(kThreads, 1) void dx_gemm_kernel(Nf4View W, const u
     }
   };
 
-  // MULTI: the LoRA step's tiles straight from S and the adapter's transposed
-  // A, each 16-byte chunk from column (64l + 8 chunk) mod r of its part; rows
-  // of other adapters, columns past 3r and rows past K read as zero
+  // MULTI: the LoRA step's tiles straight from S (each 16-byte chunk from
+  // column 64l + 8 chunk) and the adapter's A (tile row t from its row
+  // (64l + t) mod r); rows of other adapters, three-part ranks past 3r and
+  // columns past K read as zero
   auto copy_multi = [&](char* ts, char* tf, int l) __attribute__((always_inline)) {
     if constexpr (MULTI) {
       const int i = lfirst + l, g = gfirst + i / lper, col0l = 64 * (i % lper);
@@ -497,15 +531,17 @@ __global__ __launch_bounds__(kThreads, 1) void dx_gemm_kernel(Nf4View W, const u
         buf_load_lds16(ru3, ts + (64 * p + 8 * c) * 128,
                        colu < 3 * ma.r && row >= p0 && row < p1 ? o : 0x7fffffffu, 0u);
       }
-      const int a = ma.by_id ? ma.id(g) : g;
+      const int a = ma.id(g);
       const bool ok = (unsigned)a < (unsigned)ma.count;
       const rsrc_t rf = make_rsrc(ma.F + (int64_t)(ok ? a : 0) * K * ma.r, ok ? K * ma.r * 2 : 0);
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
-        const int row = 64 * p + 8 * c + (lane >> 3);
-        const int col = col0l + 8 * ((lane & 7) ^ wsw(row));
-        buf_load_lds16(rf, tf + (64 * p + 8 * c) * 128,
-                       col < 3 * ma.r ? (uint32_t)(((k0 + row) * ma.r + col % ma.r) * 2) : 0x7fffffffu, 0u);
+        // rows 16p + 2c, +1; lane l fills physical chunk l % 32 of row l / 32
+        const int row = 16 * p + 2 * c + (lane >> 5);
+        const int64_t k = k0 + 8 * ((lane & 31) ^ ((row & 3) << 1));
+        const int t = col0l + row;
+        buf_load_lds16(rf, tf + (16 * p + 2 * c) * 512,
+                       t < 3 * ma.r && k < K ? (uint32_t)(((int64_t)(t % ma.r) * K + k) * 2) : 0x7fffffffu, 0u);
       }
     }
   };

@@ -392,7 +392,7 @@ __global__ __launch_bounds__(kThreads, 1) void fwd_gemm_kernel(Nf4View W, const 
         const uint32_t o = (uint32_t)(((m0 + row) * ma.C + col) * 2);
         buf_load_lds16(rt3, ts + (XR * p + 8 * c) * 128, in && row >= p0 && row < p1 ? o : 0x7fffffffu, 0u);
       }
-      const int a = ma.by_id ? ma.id(g) : g;
+      const int a = ma.id(g);
       const bool ok = (unsigned)a < (unsigned)ma.count;
       const rsrc_t rf = make_rsrc(ma.F + (int64_t)(ok ? a : 0) * N * ma.r, ok ? N * ma.r * 2 : 0);
 #pragma unroll

@@ -221,13 +221,14 @@ struct AdapterView {
 // the tokens sorted by adapter.  Written by adapters_plan_kernel; every kernel
 // that reads an index from it checks it against its own bounds.
 struct PlanView {
-  int32_t* head;   // [0] used adapters, [1] tokens with an adapter
+  int32_t* head;   // [0] used adapters, [1] tokens with an adapter, [2] tiles
   int32_t* owner;  // [M] adapter of token m, -1: none
   int32_t* perm;   // [M] sorted position -> token (tokens without an adapter last)
   int32_t* group;  // [M] sorted position -> number of its used adapter (head[0]: none)
   int32_t* id;     // [count] used adapter -> adapter
   int32_t* start;  // [count + 1] its first sorted position
   int32_t* slot;   // [count] adapter -> used adapter, -1: no token carries it
+  int2* tile;      // runs of up to 64 positions of one used adapter: {its number, first position}
 };
 constexpr int kPlanHead = 16;  // words
 inline int64_t plan_pad(int64_t n) { return round_up(n, 16); }
@@ -238,9 +239,8 @@ hipError_t launch_adapters_plan(const int32_t* index, int64_t M, int count, cons
 // The adapters' share of a dequant-in-tile GEMM over tokens in plan order:
 // output row p belongs to token perm[p] and takes, beside the base product,
 // S[p]·F_aᵀ, S [M, C] the three-part bf16 split of the scaled low-rank factor
-// (columns [0, r), [r, 2r), [2r, 3r)) and F_a [rows, r] the used adapter's
-// factor of F (its adapter number where `by_id`, its number among the used
-// ones otherwise).
+// (columns [0, r), [r, 2r), [2r, 3r)) and F_a the adapter's
+// factor of F: B [count, N, r] (forward) or A [count, r, K] (dX).
 struct AdapterGemmArgs {
   // (the plan as one address and two strides: the kernels are short of scalar
   // registers)
@@ -248,7 +248,7 @@ struct AdapterGemmArgs {
   int m_pad, c_pad;
   const uint16_t* S;
   const uint16_t* F;
-  int r, C, count, by_id;
+  int r, C, count;
   __device__ __forceinline__ int held() const { return plan[1]; }
   __device__ __forceinline__ const int32_t* perm() const { return plan + kPlanHead + m_pad; }
   __device__ __forceinline__ int group(int p) const { return plan[kPlanHead + 2 * m_pad + p]; }
@@ -264,19 +264,21 @@ struct GemvAdapters {
 struct NoAdapters {};
 constexpr int64_t adapter_cols(int64_t r) { return round_up(3 * r, 64); }
 
+// Tiles of a plan: one per 64 tokens and one per used adapter at most.
+inline int64_t plan_tiles(int64_t M, int count) { return M / 64 + (count < M ? count : M); }
+
 struct AdaptersFwdLayout {
-  // M <= 16: fp32 T in tiles; else bf16 S [M, C] of s·T; the GEMM's split
-  // partials (splits > 1)
+  // M <= 16: fp32 T in tiles; else bf16 S [M, C] of s·T; an fp32 area: the
+  // partial sums of T [slices, M, r], then the GEMM's (splits > 1)
   size_t off_S, off_P, total;
-  int splits;
+  int splits, slices;
 };
 struct AdaptersBwdLayout {
-  // bf16 sU [M, C]; its transpose sUT and sTT [3r, Mp]; the used adapters'
-  // transposed copies AT [used, K, r] and BT [used, r, N]; the gradient
-  // units' table; one fp32 area: the dX GEMM's split partials, then the
-  // gradients' partials [slots, r·(K + N)]
-  size_t off_U, off_UT, off_TT, off_AT, off_BT, off_units, off_P, total;
-  int splits, unit, units, slots;
+  // bf16 sU, sT [M, C]; the gradient units' table; one fp32 area: the partial
+  // sums of U and T, the dX GEMM's split partials, then the gradients'
+  // partials [slots, r·(K + N)]
+  size_t off_U, off_T, off_units, off_P, total;
+  int splits, unit, units, slots, slices_U, slices_T;
 };
 AdaptersFwdLayout adapters_fwd_layout(int64_t M, int64_t N, int64_t K, int r, int count);
 AdaptersBwdLayout adapters_bwd_layout(int64_t M, int64_t N, int64_t K, int r, int count);
