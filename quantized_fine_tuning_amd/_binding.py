@@ -503,7 +503,9 @@ def _address_1d(t, name: str, n: int, dtype, dev: int) -> int:
     """The same for a 1-d tensor of at least n elements."""
     if t is None or t.dtype != dtype or t.dim() != 1 or t.numel() < n:
         _expect_numel(t, name, n, dtype)
-    return _address(t, name, t.shape, (dtype,), dev)
+    if t.get_device() != dev or not t.is_contiguous():
+        _address(t, name, t.shape, (dtype,), dev)
+    return t.data_ptr()
 
 
 def _scratch(t, name: str, dev: int):

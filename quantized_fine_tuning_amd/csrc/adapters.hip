@@ -811,7 +811,7 @@ hipError_t launch_adapters_fwd(const Nf4View& W, const uint16_t* X, int64_t M, c
   if (e != hipSuccess) return e;
   // (the partial sums of T have been consumed: P now takes the split partials)
   const AdapterGemmArgs ma{pl.head, (int)plan_pad(M), (int)plan_pad(ad.count + 1), S, ad.B, ad.r,
-                           (int)adapter_cols(ad.r), ad.count};
+                           (int)adapter_cols(ad.r), ad.count, (y16 ? 2 : 3) * ad.r};
   e = launch_fwd_gemm_adapters(W, X, M, ma, Y, y16, L.splits, P, st);
   if (e != hipSuccess || L.splits == 1) return e;
   return launch_splitk_reduce(P, L.splits, M * W.N, Y, y16, false, st);
@@ -844,7 +844,7 @@ hipError_t launch_adapters_bwd(const Nf4View& W, const uint16_t* X, const uint16
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   const AdapterGemmArgs ma{pl.head, (int)plan_pad(M), (int)plan_pad(ad.count + 1), U, ad.A, ad.r,
-                           (int)adapter_cols(r), ad.count};
+                           (int)adapter_cols(r), ad.count, (dx16 ? 2 : 3) * ad.r};
   e = launch_dx_gemm_adapters(W, dY, M, ma, dX, dx16, L.splits, P, st);
   if (e == hipSuccess && L.splits > 1) e = launch_splitk_reduce(P, L.splits, M * K, dX, dx16, false, st);
   if (e != hipSuccess) return e;

@@ -79,7 +79,7 @@ __device__ __forceinline__ int wswz(int row, int chunk) {
 // lane bits 0..5 are cg0, rg0, rg1, cg1, cg2, rg2.  Each half-wave then
 // reads the tables of 4 row groups (32 banks once), and each 8 consecutive
 // lanes store their 16-byte chunks to 8 distinct chunk positions.
-// MULTI's A tile (64 three-part ranks of 256 columns): the 16-byte chunks of a
+// MULTI's A tile (64 split ranks of 256 columns): the 16-byte chunks of a
 // row XORed by its low bits, so that the 4 rows of a transposing read lie on
 // different banks; byte of column col (a multiple of 4).
 __device__ __forceinline__ int atswz(int row, int col) {
@@ -91,7 +91,7 @@ __device__ __forceinline__ int dq_cg(int l) { return (l & 1) | ((l >> 2) & 6); }
 // MULTI: the tokens carry different adapters (AdapterGemmArgs): tile rows are
 // sorted positions, dY rows are gathered and output rows scattered through
 // the plan, and the LoRA steps run over the used adapters whose tokens the
-// tile holds, 3r/64 steps each, rounded up (rows of other adapters read as
+// tile holds, cols/64 steps each, rounded up (rows of other adapters read as
 // zero; the split reductions share these steps out as they do the n steps).
 template <int LSTEPS, bool F16, bool MULTI = false>
 __global__ __launch_bounds__(kThreads, 1) void dx_gemm_kernel(Nf4View W, const uint16_t* __restrict__ dY,
@@ -130,7 +130,7 @@ __global__ __launch_bounds__(kThreads, 1) void dx_gemm_kernel(Nf4View W, const u
   int lfirst = 0, gfirst = 0, lper = 1;
   if constexpr (MULTI) {
     const int held = std::min(ma.held(), (int)M);
-    lper = ma.C / 64;
+    lper = (ma.cols + 63) / 64;
     if ((int)m0 < held) {
       gfirst = ma.group((int)m0);
       const int glast = std::min(ma.group(std::min((int)m0 + TM, held) - 1), ma.count - 1);
@@ -298,7 +298,7 @@ __global__ __launch_bounds__(kThreads, 1) void dx_gemm_kernel(Nf4View W, const u
       }
     };
 
-    // MULTI, a LoRA step: the B tile is 64 rows (three-part ranks) of 256
+    // MULTI, a LoRA step: the B tile is 64 rows (split ranks) of 256
     // columns k in the adapter's own layout; a fragment (8 consecutive ranks of
     // one column) is two transposing reads, lane i of each 16 supplying 8 bytes
     // of row i / 4 and receiving column i.
@@ -515,7 +515,7 @@ __global__ __launch_bounds__(kThreads, 1) void dx_gemm_kernel(Nf4View W, const u
 
   // MULTI: the LoRA step's tiles straight from S (each 16-byte chunk from
   // column 64l + 8 chunk) and the adapter's A (tile row t from its row
-  // (64l + t) mod r); rows of other adapters, three-part ranks past 3r and
+  // (64l + t) mod r); rows of other adapters, split ranks past `cols` and
   // columns past K read as zero
   auto copy_multi = [&](char* ts, char* tf, int l) __attribute__((always_inline)) {
     if constexpr (MULTI) {
@@ -529,7 +529,7 @@ __global__ __launch_bounds__(kThreads, 1) void dx_gemm_kernel(Nf4View W, const u
         const int row = 64 * p + 8 * c + (lane >> 3);
         const uint32_t o = (uint32_t)(((m0 + row) * ma.C + colu) * 2);
         buf_load_lds16(ru3, ts + (64 * p + 8 * c) * 128,
-                       colu < 3 * ma.r && row >= p0 && row < p1 ? o : 0x7fffffffu, 0u);
+                       colu < ma.cols && row >= p0 && row < p1 ? o : 0x7fffffffu, 0u);
       }
       const int a = ma.id(g);
       const bool ok = (unsigned)a < (unsigned)ma.count;
@@ -541,7 +541,7 @@ __global__ __launch_bounds__(kThreads, 1) void dx_gemm_kernel(Nf4View W, const u
         const int64_t k = k0 + 8 * ((lane & 31) ^ ((row & 3) << 1));
         const int t = col0l + row;
         buf_load_lds16(rf, tf + (16 * p + 2 * c) * 512,
-                       t < 3 * ma.r && k < K ? (uint32_t)(((int64_t)(t % ma.r) * K + k) * 2) : 0x7fffffffu, 0u);
+                       t < ma.cols && k < K ? (uint32_t)(((int64_t)(t % ma.r) * K + k) * 2) : 0x7fffffffu, 0u);
       }
     }
   };

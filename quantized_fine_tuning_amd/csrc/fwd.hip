@@ -91,7 +91,7 @@ __device__ __forceinline__ int xswz(int row, int chunk) {
 // MULTI: the tokens carry different adapters (AdapterGemmArgs): tile rows are
 // sorted positions, X rows are gathered and output rows scattered through
 // the plan, and the LoRA steps run over the used adapters whose tokens the
-// tile holds, 3r/64 steps each, rounded up (rows of other adapters read as
+// tile holds, cols/64 steps each, rounded up (rows of other adapters read as
 // zero; the split reductions share these steps out as they do the K steps).
 template <int LSTEPS, bool F16, int TMV, bool MULTI = false>
 __global__ __launch_bounds__(kThreads, 1) void fwd_gemm_kernel(Nf4View W, const uint16_t* __restrict__ X,
@@ -129,7 +129,7 @@ __global__ __launch_bounds__(kThreads, 1) void fwd_gemm_kernel(Nf4View W, const 
   int lfirst = 0, gfirst = 0, lper = 1;
   if constexpr (MULTI) {
     const int held = std::min(ma.held(), (int)M);
-    lper = ma.C / 64;
+    lper = (ma.cols + 63) / 64;
     if ((int)m0 < held) {
       gfirst = ma.group((int)m0);
       const int glast = std::min(ma.group(std::min((int)m0 + TM, held) - 1), ma.count - 1);
@@ -378,11 +378,11 @@ __global__ __launch_bounds__(kThreads, 1) void fwd_gemm_kernel(Nf4View W, const 
   };
   // MULTI: the LoRA step's tiles straight from S and the adapter's factor, each
   // 16-byte chunk from column (64l + 8 chunk) mod r of its part; rows of other
-  // adapters, columns past 3r and rows past N read as zero
+  // adapters, columns past `cols` and rows past N read as zero
   auto copy_multi = [&](char* ts, char* tf, int l) __attribute__((always_inline)) {
     if constexpr (MULTI) {
       const int i = lfirst + l, g = gfirst + i / lper, col = 64 * (i % lper) + 8 * xlch;
-      const bool in = col < 3 * ma.r;
+      const bool in = col < ma.cols;
       int p0, p1;
       rows_of(l, p0, p1);
       const rsrc_t rt3 = make_rsrc(ma.S, M * ma.C * 2);

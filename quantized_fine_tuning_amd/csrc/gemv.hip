@@ -160,9 +160,12 @@ static_assert(kGemvAccBytes + 32 * 1024 + kGemvEpiBytes <= 160 * 1024, "X of 32 
 // requested by every wave of every workgroup at once cost ~1.6 us at M = 1
 // on the q_proj weight, ~2 us at M = 16, measured).
 // MULTI: the tokens carry different adapters (GemvAdapters): T comes finished
-// (one slice) and each output's thread reads its own token's adapter row of
-// the pool, the first kPreB chunks of it requested right behind the codes.
-constexpr int kPreB = 4;
+// (one slice) and NT / 256 neighbouring threads per output read its token's
+// adapter row of the pool, 16-byte chunks in turn, the first kPreB of each
+// requested right behind the codes; their sums are added pairwise.  (One
+// thread per output took 34.5 us on the 11008 x 4096 gate with 16 adapters of
+// rank 64, its loads in the epilogue of four waves out of sixteen.)
+constexpr int kPreB = 2;
 template <bool F16, int XV, int WV, bool MULTI = false>
 __global__ __launch_bounds__(64 * WV) void gemv_kernel(Nf4View W, const uint16_t* __restrict__ X,
                                                             int M, const float* __restrict__ P, int S, int JT,
@@ -254,9 +257,12 @@ __global__ __launch_bounds__(64 * WV) void gemv_kernel(Nf4View W, const uint16_t
   // (loads complete in issue order): 8 values of the workgroup's B rows
   // (16·r contiguous bf16), and X when staged.
   u32x4_t braw;
-  int own = -1;  // MULTI: the adapter of token tid / 16
+  // MULTI: output tid / OT = (token o / 16, weight row n0 + o % 16), part tid % OT
+  constexpr int OT = NT / 256;
+  const int o_out = tid / OT, o_part = tid % OT;
+  int own = -1;  // the adapter of its token
   if constexpr (MULTI) {
-    if (tid < 16 * M) own = ga_.owner[tid >> 4];
+    if (o_out < 16 * M) own = ga_.owner[o_out >> 4];
   } else {
     const rsrc_t rbr = make_rsrc(B + n0 * r, (N - n0) * r * 2);
     braw = buf_load16(rbr, tid < 2 * r ? (uint32_t)(16 * tid) : 0x7fffffffu, 0u);
@@ -293,18 +299,18 @@ __global__ __launch_bounds__(64 * WV) void gemv_kernel(Nf4View W, const uint16_t
           buf_load4(rp, tid < M * r && i < S ? po + (uint32_t)(i * JT * 256 * 4) : 0x7fffffffu, 0u));
   }
   __builtin_amdgcn_sched_barrier(0);
-  // MULTI: thread (token tid / 16, weight row n0 + tid % 16)'s row of its
-  // adapter's B
   const uint16_t* brow = nullptr;
   float own_scale = 0.f;
   u32x4_t bpre[MULTI ? kPreB : 1];
   if constexpr (MULTI) {
-    if ((unsigned)own < (unsigned)ga_.count && n0 + (tid & 15) < N) {
-      brow = B + ((int64_t)own * N + n0 + (tid & 15)) * r;
+    if ((unsigned)own < (unsigned)ga_.count && n0 + (o_out & 15) < N) {
+      brow = B + ((int64_t)own * N + n0 + (o_out & 15)) * r;
       own_scale = ga_.s[own];
 #pragma unroll
-      for (int i = 0; i < kPreB; ++i)
-        bpre[i] = 8 * i < r ? *reinterpret_cast<const u32x4_t*>(brow + 8 * i) : u32x4_t{0u, 0u, 0u, 0u};
+      for (int i = 0; i < kPreB; ++i) {
+        const int j = 8 * (o_part + i * OT);
+        bpre[i] = *reinterpret_cast<const u32x4_t*>(brow + (j < r ? j : 0));
+      }
     }
   }
   __builtin_amdgcn_sched_barrier(0);
@@ -360,6 +366,39 @@ __global__ __launch_bounds__(64 * WV) void gemv_kernel(Nf4View W, const uint16_t
     gemv_t_reduce(NT, M, r, P, S, JT, t_fin, T_out);
   }
   __syncthreads();
+  if constexpr (MULTI) {
+    const int m = o_out >> 4, c = o_out & 15;
+    float y = 0.f, dot = 0.f;
+    for (int w = o_part; w < NW; w += OT) y += s_acc[w][16 * (m >> 2) + c][m & 3];
+    if (brow) {
+      const float* const tm = t_fin + m * 257;
+      auto add8 = [&](int j, const u32x4_t& v) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          dot = __builtin_fmaf(tm[j + 2 * i], bf16lo(v[i]), dot);
+          dot = __builtin_fmaf(tm[j + 2 * i + 1], bf16hi(v[i]), dot);
+        }
+      };
+#pragma unroll
+      for (int i = 0; i < kPreB; ++i) {
+        const int j = 8 * (o_part + i * OT);
+        if (j < r) add8(j, bpre[i]);
+      }
+      for (int j = 8 * (o_part + kPreB * OT); j < r; j += 8 * OT)
+        add8(j, *reinterpret_cast<const u32x4_t*>(brow + j));
+    }
+    y = __builtin_fmaf(own_scale, dot, y);
+#pragma unroll
+    for (int o = 1; o < OT; o <<= 1) y += __shfl_xor(y, o, 64);
+    const int64_t nn = n0 + c;
+    if (o_part == 0 && m < M && nn < N) {
+      if (y_bf16)
+        static_cast<uint16_t*>(Y)[(int64_t)m * N + nn] = (uint16_t)(pack16<F16>(y, 0.0f) & 0xffffu);
+      else
+        static_cast<float*>(Y)[(int64_t)m * N + nn] = y;
+    }
+    return;
+  }
   // one thread per output (token m, weight row n0 + c): the 16 partial
   // tiles in a fixed order, then the adapter term
   // fl32(s · Σ_j T[m][j]·B[n0 + c][j]) in fp32, j in order
@@ -371,33 +410,8 @@ __global__ __launch_bounds__(64 * WV) void gemv_kernel(Nf4View W, const uint16_t
 #pragma unroll
       for (int w = 1; w < NW; ++w) y = __fadd_rn(y, s_acc[w][16 * (m >> 2) + c][m & 3]);
       float dot = 0.0f;
-      if constexpr (MULTI) {
-        if (brow) {
-          auto add8 = [&](int j, const u32x4_t& v) __attribute__((always_inline)) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              dot = __builtin_fmaf(t_fin[m * 257 + j + 2 * i], bf16lo(v[i]), dot);
-              dot = __builtin_fmaf(t_fin[m * 257 + j + 2 * i + 1], bf16hi(v[i]), dot);
-            }
-          };
-#pragma unroll
-          for (int i = 0; i < kPreB; ++i)
-            if (8 * i < r) add8(8 * i, bpre[i]);
-          for (int j = 8 * kPreB; j < r; j += 8 * kPreB) {
-            u32x4_t v[kPreB];
-#pragma unroll
-            for (int i = 0; i < kPreB; ++i)
-              v[i] = *reinterpret_cast<const u32x4_t*>(brow + (j + 8 * i < r ? j + 8 * i : j));
-#pragma unroll
-            for (int i = 0; i < kPreB; ++i)
-              if (j + 8 * i < r) add8(j + 8 * i, v[i]);
-          }
-          y = __builtin_fmaf(own_scale, dot, y);
-        }
-      } else {
-        for (int j = 0; j < r; ++j) dot = __fadd_rn(dot, __fmul_rn(t_fin[m * 257 + j], s_b[c * r + j]));
-        y = __fadd_rn(y, __fmul_rn(scale, dot));
-      }
+      for (int j = 0; j < r; ++j) dot = __fadd_rn(dot, __fmul_rn(t_fin[m * 257 + j], s_b[c * r + j]));
+      y = __fadd_rn(y, __fmul_rn(scale, dot));
       if (y_bf16)
         static_cast<uint16_t*>(Y)[(int64_t)m * N + nn] = (uint16_t)(pack16<F16>(y, 0.0f) & 0xffffu);
       else

@@ -239,6 +239,8 @@ hipError_t launch_adapters_plan(const int32_t* index, int64_t M, int count, cons
 // The adapters' share of a dequant-in-tile GEMM over tokens in plan order:
 // output row p belongs to token perm[p] and takes, beside the base product,
 // S[p]·F_aᵀ, S [M, C] the three-part bf16 split of the scaled low-rank factor
+// (fp32 output; for a bf16 one the first two parts, 16 bits of it, whose
+// rounding is 2^-8 of the output's half step or less)
 // (columns [0, r), [r, 2r), [2r, 3r)) and F_a the adapter's
 // factor of F: B [count, N, r] (forward) or A [count, r, K] (dX).
 struct AdapterGemmArgs {
@@ -248,7 +250,7 @@ struct AdapterGemmArgs {
   int m_pad, c_pad;
   const uint16_t* S;
   const uint16_t* F;
-  int r, C, count;
+  int r, C, count, cols;  // cols: the columns of S that enter, 2r or 3r
   __device__ __forceinline__ int held() const { return plan[1]; }
   __device__ __forceinline__ const int32_t* perm() const { return plan + kPlanHead + m_pad; }
   __device__ __forceinline__ int group(int p) const { return plan[kPlanHead + 2 * m_pad + p]; }
