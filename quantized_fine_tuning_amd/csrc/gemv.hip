@@ -53,7 +53,6 @@
 // first barrier waits for is requested after the codes: loads complete in
 // issue order, so such a wait would also wait for them.
 #include <algorithm>
-#include <type_traits>
 
 #include "host.h"
 
@@ -159,20 +158,12 @@ static_assert(kGemvAccBytes + 32 * 1024 + kGemvEpiBytes <= 160 * 1024, "X of 32 
 // every wave loads its fragments from global memory (the same few bytes
 // requested by every wave of every workgroup at once cost ~1.6 us at M = 1
 // on the q_proj weight, ~2 us at M = 16, measured).
-// MULTI: the tokens carry different adapters (GemvAdapters): T comes finished
-// (one slice) and NT / 256 neighbouring threads per output read its token's
-// adapter row of the pool, 16-byte chunks in turn, the first kPreB of each
-// requested right behind the codes; their sums are added pairwise.  (One
-// thread per output took 34.5 us on the 11008 x 4096 gate with 16 adapters of
-// rank 64, its loads in the epilogue of four waves out of sixteen.)
-constexpr int kPreB = 2;
-template <bool F16, int XV, int WV, bool MULTI = false>
+template <bool F16, int XV, int WV>
 __global__ __launch_bounds__(64 * WV) void gemv_kernel(Nf4View W, const uint16_t* __restrict__ X,
                                                             int M, const float* __restrict__ P, int S, int JT,
                                                             const uint16_t* __restrict__ B, int r,
                                                             float scale, void* __restrict__ Y,
-                                                            int y_bf16, float* __restrict__ T_out, Codebook cb,
-                                                            std::conditional_t<MULTI, GemvAdapters, NoAdapters> ga_) {
+                                                            int y_bf16, float* __restrict__ T_out, Codebook cb) {
   constexpr int NW = WV, NT = 64 * WV;  // waves and threads of the workgroup
   static_assert(NT >= 16 * GEMV_ROWS, "one thread per output of a 16-token x 16-row tile");
   constexpr bool XL = XV > 0;  // X staged: XV 16-byte pieces per thread
@@ -256,17 +247,8 @@ __global__ __launch_bounds__(64 * WV) void gemv_kernel(Nf4View W, const uint16_t
   // Requested first, so that waiting for them does not wait for the codes
   // (loads complete in issue order): 8 values of the workgroup's B rows
   // (16·r contiguous bf16), and X when staged.
-  u32x4_t braw;
-  // MULTI: output tid / OT = (token o / 16, weight row n0 + o % 16), part tid % OT
-  constexpr int OT = NT / 256;
-  const int o_out = tid / OT, o_part = tid % OT;
-  int own = -1;  // the adapter of its token
-  if constexpr (MULTI) {
-    if (o_out < 16 * M) own = ga_.owner[o_out >> 4];
-  } else {
-    const rsrc_t rbr = make_rsrc(B + n0 * r, (N - n0) * r * 2);
-    braw = buf_load16(rbr, tid < 2 * r ? (uint32_t)(16 * tid) : 0x7fffffffu, 0u);
-  }
+  const rsrc_t rbr = make_rsrc(B + n0 * r, (N - n0) * r * 2);
+  const u32x4_t braw = buf_load16(rbr, tid < 2 * r ? (uint32_t)(16 * tid) : 0x7fffffffu, 0u);
   u32x4_t xs[XL ? XV : 1];
   if constexpr (XL) {
     const int nvec = (M * (int)K * 2) / 16;
@@ -299,21 +281,6 @@ __global__ __launch_bounds__(64 * WV) void gemv_kernel(Nf4View W, const uint16_t
           buf_load4(rp, tid < M * r && i < S ? po + (uint32_t)(i * JT * 256 * 4) : 0x7fffffffu, 0u));
   }
   __builtin_amdgcn_sched_barrier(0);
-  const uint16_t* brow = nullptr;
-  float own_scale = 0.f;
-  u32x4_t bpre[MULTI ? kPreB : 1];
-  if constexpr (MULTI) {
-    if ((unsigned)own < (unsigned)ga_.count && n0 + (o_out & 15) < N) {
-      brow = B + ((int64_t)own * N + n0 + (o_out & 15)) * r;
-      own_scale = ga_.s[own];
-#pragma unroll
-      for (int i = 0; i < kPreB; ++i) {
-        const int j = 8 * (o_part + i * OT);
-        bpre[i] = *reinterpret_cast<const u32x4_t*>(brow + (j < r ? j : 0));
-      }
-    }
-  }
-  __builtin_amdgcn_sched_barrier(0);
   if constexpr (XL) {
     const int nvec = (M * (int)K * 2) / 16;
 #pragma unroll
@@ -334,7 +301,7 @@ __global__ __launch_bounds__(64 * WV) void gemv_kernel(Nf4View W, const uint16_t
       }
     }
   };
-  if (!epi_late && !MULTI) stage_b();
+  if (!epi_late) stage_b();
   __syncthreads();  // codebook, X, B rows
 
   // two groups per iteration, alternating buffers: the loads of the next
@@ -352,7 +319,7 @@ __global__ __launch_bounds__(64 * WV) void gemv_kernel(Nf4View W, const uint16_t
   s_acc[wave][lane] = acc;
   if (epi_late) {
     __syncthreads();  // X read by every wave: its region takes t_fin and s_b
-    if constexpr (!MULTI) stage_b();
+    stage_b();
   }
   if (t_pre) {
     if (tid < M * r) {
@@ -366,39 +333,6 @@ __global__ __launch_bounds__(64 * WV) void gemv_kernel(Nf4View W, const uint16_t
     gemv_t_reduce(NT, M, r, P, S, JT, t_fin, T_out);
   }
   __syncthreads();
-  if constexpr (MULTI) {
-    const int m = o_out >> 4, c = o_out & 15;
-    float y = 0.f, dot = 0.f;
-    for (int w = o_part; w < NW; w += OT) y += s_acc[w][16 * (m >> 2) + c][m & 3];
-    if (brow) {
-      const float* const tm = t_fin + m * 257;
-      auto add8 = [&](int j, const u32x4_t& v) __attribute__((always_inline)) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          dot = __builtin_fmaf(tm[j + 2 * i], bf16lo(v[i]), dot);
-          dot = __builtin_fmaf(tm[j + 2 * i + 1], bf16hi(v[i]), dot);
-        }
-      };
-#pragma unroll
-      for (int i = 0; i < kPreB; ++i) {
-        const int j = 8 * (o_part + i * OT);
-        if (j < r) add8(j, bpre[i]);
-      }
-      for (int j = 8 * (o_part + kPreB * OT); j < r; j += 8 * OT)
-        add8(j, *reinterpret_cast<const u32x4_t*>(brow + j));
-    }
-    y = __builtin_fmaf(own_scale, dot, y);
-#pragma unroll
-    for (int o = 1; o < OT; o <<= 1) y += __shfl_xor(y, o, 64);
-    const int64_t nn = n0 + c;
-    if (o_part == 0 && m < M && nn < N) {
-      if (y_bf16)
-        static_cast<uint16_t*>(Y)[(int64_t)m * N + nn] = (uint16_t)(pack16<F16>(y, 0.0f) & 0xffffu);
-      else
-        static_cast<float*>(Y)[(int64_t)m * N + nn] = y;
-    }
-    return;
-  }
   // one thread per output (token m, weight row n0 + c): the 16 partial
   // tiles in a fixed order, then the adapter term
   // fl32(s · Σ_j T[m][j]·B[n0 + c][j]) in fp32, j in order
@@ -417,6 +351,200 @@ __global__ __launch_bounds__(64 * WV) void gemv_kernel(Nf4View W, const uint16_t
       else
         static_cast<float*>(Y)[(int64_t)m * N + nn] = y;
     }
+  }
+}
+
+// The same product for tokens that carry different adapters (GemvAdapters; T
+// comes finished, in the split kernel's tile layout).  Workgroups walk over the
+// row groups, X staged once for all of theirs: a wave requests the codes of
+// its next block group, of this row group or the next, before it decodes the
+// current one.  NT / 256 neighbouring threads share an output: each adds its
+// part of the waves' tiles and, of its token's adapter row, every OT-th 16-byte
+// chunk times T, requested before the next codes so that waiting for them does
+// not wait for those; the parts are added pairwise.  (The 11008 x 4096 gate, 16
+// tokens with adapters of rank 64: one thread per output with its loads in the
+// epilogue 34.5 us, shared outputs 31.7, row
+// groups walked over 18.4.)
+constexpr int kPreB = 2;
+template <int XV, int WV>
+__global__ __launch_bounds__(64 * WV) void gemv_adapters_kernel(Nf4View W, const uint16_t* __restrict__ X, int M,
+                                                                const float* __restrict__ T,
+                                                                const uint16_t* __restrict__ B, int r, GemvAdapters ad,
+                                                                void* __restrict__ Y, int y_bf16, int row_groups,
+                                                                Codebook cb) {
+  constexpr int NW = WV, NT = 64 * WV, OT = NT / 256;
+  constexpr bool XL = XV > 0;
+  extern __shared__ __attribute__((aligned(16))) char sx[];  // X [M][K] bf16 (XL)
+  __shared__ __attribute__((aligned(256))) float sq[16];
+  __shared__ f32x4_t s_acc[NW][64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lr = lane & 15, kq = lane >> 4;
+  const int64_t K = W.K, N = W.N;
+  const int nb = (int)(K / kBlock), ngroups = (nb + 3) / 4, per = (ngroups + NW - 1) / NW;
+  const uint32_t kpr = (uint32_t)nb;
+  const float mu = *W.mu;
+  const rsrc_t rs = make_rsrc(W.s, ((N * kpr + kDqBlock - 1) / kDqBlock) * 4);
+  const rsrc_t rx = make_rsrc(X, (int64_t)M * K * 2);
+  const bool x_row = lr < M;
+  // output o = (token o / 16, row o % 16 of the group), part of it
+  const int o_m = tid / OT >> 4, o_c = tid / OT & 15, o_part = tid % OT;
+  int own = -1;
+  if (o_m < M) own = ad.owner[o_m];
+
+  struct Group {
+    u32x4_t c[2];  // the lane's 64 codes
+    uint32_t e;    // e4m3 byte
+    float s;       // group scale
+    u32x4_t x[XL ? 1 : 8];  // X fragments when X is not staged
+  };
+  // block group `step` of this wave in row group rg (zeros past the end)
+  auto load = [&](Group& g, int rg, int step) __attribute__((always_inline)) {
+    const int64_t n0 = (int64_t)rg * GEMV_ROWS;
+    const rsrc_t rc = make_rsrc(W.codes + n0 * (K / 2), (N - n0) * (K / 2));
+    const rsrc_t re = make_rsrc(W.e + n0 * kpr, (N - n0) * kpr);
+    const int grp = wave + NW * step, b = 4 * grp + kq;
+    const bool ok = rg < row_groups && grp < ngroups && b < nb;
+    const uint32_t off = ok ? (uint32_t)(lr * (K / 2) + b * 32) : 0x7fffffffu;
+    g.c[0] = buf_load16(rc, off, 0u);
+    g.c[1] = buf_load16(rc, off, 16u);
+    const uint32_t blk = (uint32_t)(lr * kpr + b);
+    g.e = buf_load1(re, ok ? blk : 0x7fffffffu, 0u);
+    g.s = __uint_as_float(buf_load4(rs, ok ? (((uint32_t)n0 * kpr + blk) / kDqBlock) * 4u : 0x7fffffffu, 0u));
+    if constexpr (!XL) {
+      const uint32_t xo = ok && x_row ? (uint32_t)((lr * K + b * kBlock) * 2) : 0x7fffffffu;
+#pragma unroll
+      for (int t = 0; t < 8; ++t) g.x[t] = buf_load16(rx, xo, 16u * t);
+    }
+  };
+  f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+  auto consume = [&](const Group& g, int step) __attribute__((always_inline)) {
+    const float cp = decode_constant(g.e, g.s, mu);
+    const int grp = wave + NW * step, b = 4 * grp + kq;
+    const bool use_x = x_row && grp < ngroups && b < nb;
+    const char* xrow = sx + (size_t)(lr * K + (use_x ? b : 0) * kBlock) * 2;
+    const uint32_t sqb = lds_offset(sq);
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+      const uint32_t w = g.c[t >> 2][t & 3];  // codes 8t .. 8t+7
+      const uint32_t we = (w << 2) & 0x3C3C3C3Cu, wo = (w >> 2) & 0x3C3C3C3Cu;
+      u32x4_t bfrag;
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        const float qe = *(const __attribute__((address_space(3))) float*)(uintptr_t)__builtin_amdgcn_perm(
+            sqb, we, 0x07060500u | (uint32_t)p);
+        const float qo = *(const __attribute__((address_space(3))) float*)(uintptr_t)__builtin_amdgcn_perm(
+            sqb, wo, 0x07060500u | (uint32_t)p);
+        bfrag[p] = pack_bf16x2(__fmul_rn(qe, cp), __fmul_rn(qo, cp));
+      }
+      u32x4_t xa;
+      if constexpr (XL)
+        xa = use_x ? *reinterpret_cast<const u32x4_t*>(xrow + 16 * t) : u32x4_t{0u, 0u, 0u, 0u};
+      else
+        xa = g.x[t];
+      acc = mfma_16x16x32(xa, bfrag, acc);
+    }
+  };
+  auto barrier = [&]() __attribute__((always_inline)) {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): loads in flight stay there
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
+
+  u32x4_t xs[XL ? XV : 1];
+  const int nvec = (M * (int)K * 2) / 16;
+  if constexpr (XL) {
+#pragma unroll
+    for (int i = 0; i < XV; ++i) {
+      const int v = tid + i * NT;
+      xs[i] = buf_load16(rx, v < nvec ? (uint32_t)(16 * v) : 0x7fffffffu, 0u);
+    }
+  }
+  const float cbq = cb.q[tid & 15];
+  __builtin_amdgcn_sched_barrier(0);
+  Group ga, gb;
+  int rg = (int)blockIdx.x, step = 0;
+  load(ga, rg, 0);
+  __builtin_amdgcn_sched_barrier(0);
+  const bool has = (unsigned)own < (unsigned)ad.count;
+  const float own_scale = has ? ad.s[own] : 0.f;
+  if constexpr (XL) {
+#pragma unroll
+    for (int i = 0; i < XV; ++i) {
+      const int v = tid + i * NT;
+      if (v < nvec) *reinterpret_cast<u32x4_t*>(sx + 16 * v) = xs[i];
+    }
+  }
+  if (tid < 16) sq[tid] = cbq;
+  barrier();
+
+  // one block group: the next one's codes requested, this one decoded; at the
+  // row group's end the outputs.  False after the last.
+  auto turn = [&](const Group& cur, Group& nxt) __attribute__((always_inline)) {
+    const bool last = step + 1 == per;
+    const int64_t nn = (int64_t)rg * GEMV_ROWS + o_c;
+    const uint16_t* brow = nullptr;
+    u32x4_t bv[kPreB];
+    f32x4_t tv[kPreB][2];
+    auto t_at = [&](int j, f32x4_t* t) __attribute__((always_inline)) {
+      const f32x4_t* const p = reinterpret_cast<const f32x4_t*>(T + (j >> 4) * 256 + 16 * o_m + (j & 15));
+      t[0] = p[0];
+      t[1] = p[1];
+    };
+    if (last && has && nn < N) {
+      brow = B + ((int64_t)own * N + nn) * r;
+#pragma unroll
+      for (int i = 0; i < kPreB; ++i) {
+        const int j = 8 * (o_part + i * OT), jc = j < r ? j : 0;
+        bv[i] = *reinterpret_cast<const u32x4_t*>(brow + jc);
+        t_at(jc, tv[i]);
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    const int nrg = last ? rg + (int)gridDim.x : rg, nstep = last ? 0 : step + 1;
+    load(nxt, nrg, nstep);
+    __builtin_amdgcn_sched_barrier(0);
+    consume(cur, step);
+    if (last) {
+      s_acc[wave][lane] = acc;
+      acc = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      barrier();
+      float y = 0.f, dot = 0.f;
+#pragma unroll
+      for (int w = 0; w < NW; w += OT) y += s_acc[w + o_part][16 * (o_m >> 2) + o_c][o_m & 3];
+      if (brow) {
+        auto add8 = [&](const f32x4_t* t, const u32x4_t& v) __attribute__((always_inline)) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            dot = __builtin_fmaf(t[i >> 1][2 * (i & 1)], bf16lo(v[i]), dot);
+            dot = __builtin_fmaf(t[i >> 1][2 * (i & 1) + 1], bf16hi(v[i]), dot);
+          }
+        };
+#pragma unroll
+        for (int i = 0; i < kPreB; ++i)
+          if (8 * (o_part + i * OT) < r) add8(tv[i], bv[i]);
+        for (int j = 8 * (o_part + kPreB * OT); j < r; j += 8 * OT) {
+          f32x4_t t[2];
+          t_at(j, t);
+          add8(t, *reinterpret_cast<const u32x4_t*>(brow + j));
+        }
+      }
+      y = __builtin_fmaf(own_scale, dot, y);
+#pragma unroll
+      for (int o = 1; o < OT; o <<= 1) y += __shfl_xor(y, o, 64);
+      if (o_part == 0 && o_m < M && nn < N) {
+        if (y_bf16)
+          static_cast<uint16_t*>(Y)[(int64_t)o_m * N + nn] = (uint16_t)(pack_bf16x2(y, 0.0f) & 0xffffu);
+        else
+          static_cast<float*>(Y)[(int64_t)o_m * N + nn] = y;
+      }
+      barrier();  // the tiles are read: the next row group may write its own
+    }
+    rg = nrg;
+    step = nstep;
+    return rg < row_groups;
+  };
+  while (turn(ga, gb) && turn(gb, ga)) {
   }
 }
 
@@ -463,9 +591,9 @@ hipError_t launch_gemv(const Nf4View& W, const uint16_t* X, int64_t M, const uin
   const bool four = narrow && xb <= 8 * 1024 && 2 * r <= 64 * 4;
 #define QNF4_GEMV_LAUNCH(XV, WV)                                                                                \
   return f16 ? timed_launch_shm(kKernGemv, gemv_kernel<true, XV, WV>, dim3(grid), dim3(64 * WV), shm, st, W, X, \
-                                (int)M, (const float*)P, S, JT, B, r, scale, Y, yb, T, codebook(), NoAdapters{})      \
+                                (int)M, (const float*)P, S, JT, B, r, scale, Y, yb, T, codebook())      \
              : timed_launch_shm(kKernGemv, gemv_kernel<false, XV, WV>, dim3(grid), dim3(64 * WV), shm, st, W, X, \
-                                (int)M, (const float*)P, S, JT, B, r, scale, Y, yb, T, codebook(), NoAdapters{})
+                                (int)M, (const float*)P, S, JT, B, r, scale, Y, yb, T, codebook())
   // X staged with 2 or 8 pieces of 16 bytes per thread (up to 32 or 128 KB)
   if (four) QNF4_GEMV_LAUNCH(2, 4);
   if (narrow) QNF4_GEMV_LAUNCH(4, 8);
@@ -478,28 +606,27 @@ hipError_t launch_gemv(const Nf4View& W, const uint16_t* X, int64_t M, const uin
 // T: the finished low-rank factor in the split kernel's tile layout, one slice.
 hipError_t launch_gemv_adapters(const Nf4View& W, const uint16_t* X, int64_t M, const AdapterView& ad,
                                 const int32_t* owner, void* Y, bool y16, const float* T, hipStream_t st) {
-  const int JT = (ad.r + 15) / 16;
-  const unsigned grid = (unsigned)((W.N + GEMV_ROWS - 1) / GEMV_ROWS);
+  const int groups = (int)((W.N + GEMV_ROWS - 1) / GEMV_ROWS);
   const size_t xb = (size_t)M * W.K * 2;
   const bool xl = xb <= (size_t)kGemvXLdsBytes, x2 = xb <= 32 * 1024;
-  const size_t shm = x2 ? xb : (xl ? std::max(xb, kGemvEpiBytes) : 0);
-  // the workgroup shapes of the one-adapter form
-  const bool narrow = grid > 256 && xb <= 32 * 1024;
-  const bool four = narrow && xb <= 8 * 1024;
-  float* const no_out = nullptr;
-#define QNF4_GEMV_LAUNCH(XV, WV)                                                                                  \
-  hipLaunchKernelGGL((gemv_kernel<false, XV, WV, true>), dim3(grid), dim3(64 * WV), shm, st, W, X, (int)M, T, 1, JT, \
-                     ad.B, ad.r, 1.0f, Y, y16 ? 1 : 0, no_out, codebook(), GemvAdapters{owner, ad.s, ad.count})
+  const size_t shm = xl ? xb : 0;
+  // the workgroup shapes of the one-adapter form, as many of each as are
+  // resident at once
+  const bool narrow = groups > 256 && x2, four = narrow && xb <= 8 * 1024;
+#define QNF4_GEMV_LAUNCH(XV, WV, RES)                                                                          \
+  hipLaunchKernelGGL((gemv_adapters_kernel<XV, WV>), dim3((unsigned)std::min(groups, 256 * RES)), dim3(64 * WV), \
+                     shm, st, W, X, (int)M, T, ad.B, ad.r, GemvAdapters{owner, ad.s, ad.count}, Y, y16 ? 1 : 0,  \
+                     groups, codebook())
   if (four)
-    QNF4_GEMV_LAUNCH(2, 4);
+    QNF4_GEMV_LAUNCH(2, 4, 4);
   else if (narrow)
-    QNF4_GEMV_LAUNCH(4, 8);
+    QNF4_GEMV_LAUNCH(4, 8, 2);
   else if (x2)
-    QNF4_GEMV_LAUNCH(2, 16);
+    QNF4_GEMV_LAUNCH(2, 16, 1);
   else if (xl)
-    QNF4_GEMV_LAUNCH(8, 16);
+    QNF4_GEMV_LAUNCH(8, 16, 1);
   else
-    QNF4_GEMV_LAUNCH(0, 16);
+    QNF4_GEMV_LAUNCH(0, 8, 1);  // (two block groups' X fragments take more registers than 16 waves leave)
 #undef QNF4_GEMV_LAUNCH
   return hipGetLastError();
 }
