@@ -706,7 +706,7 @@ hipError_t launch_down(const DownJob& t, const DownJob& u, int64_t M, const Adap
 
 AdaptersFwdLayout adapters_fwd_layout(int64_t M, int64_t N, int64_t K, int r, int count) {
   AdaptersFwdLayout L{};
-  L.splits = M > 16 ? fwd_gemm_splits(M, N, K, SIZE_MAX) : 1;
+  L.splits = M > kMidTokens ? fwd_gemm_splits(M, N, K, SIZE_MAX) : M > 16 ? mid_fwd_splits(M, N, K) : 1;
   L.slices = M > kFewTokens ? down_slices(M, K, r) : 0;
   L.off_S = 0;
   L.off_P = M > 16 ? round_up(M * adapter_cols(r) * 2, 256) : M > 0 ? round_up((int64_t)cdiv(r, 16) * 1024, 256) : 0;
@@ -748,12 +748,13 @@ AdaptersBwdLayout adapters_bwd_layout(int64_t M, int64_t N, int64_t K, int r, in
   return L;
 }
 
-// Within a band of 256 tokens the GEMM's split count is constant and its
+// Within a band of 256 tokens (up to kMidTokens of 32, 64 and 128) the GEMM's split count is constant and its
 // partials grow with M; a factor's slices only fall with M, by less than M
 // grows from one multiple of 64 to the next, so the largest M of every 64 is
 // taken.
 size_t adapters_fwd_ws_max(int64_t M_max, int64_t N, int64_t K, int r, int count) {
   size_t most = adapters_fwd_layout(std::min<int64_t>(M_max, 16), N, K, r, count).total;
+  most = std::max(most, adapters_fwd_layout(std::min<int64_t>(M_max, 32), N, K, r, count).total);
   for (int64_t top = 63; M_max > 16; top += 64) {
     most = std::max(most, adapters_fwd_layout(std::min(top, M_max), N, K, r, count).total);
     if (top >= M_max) break;
@@ -812,7 +813,8 @@ hipError_t launch_adapters_fwd(const Nf4View& W, const uint16_t* X, int64_t M, c
   // (the partial sums of T have been consumed: P now takes the split partials)
   const AdapterGemmArgs ma{pl.head, (int)plan_pad(M), (int)plan_pad(ad.count + 1), S, ad.B, ad.r,
                            (int)adapter_cols(ad.r), ad.count, (y16 ? 2 : 3) * ad.r};
-  e = launch_fwd_gemm_adapters(W, X, M, ma, Y, y16, L.splits, P, st);
+  e = M <= kMidTokens ? launch_mid_fwd(W, X, M, ma, Y, y16, L.splits, P, st)
+                      : launch_fwd_gemm_adapters(W, X, M, ma, Y, y16, L.splits, P, st);
   if (e != hipSuccess || L.splits == 1) return e;
   return launch_splitk_reduce(P, L.splits, M * W.N, Y, y16, false, st);
 }

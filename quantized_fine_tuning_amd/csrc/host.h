@@ -269,6 +269,12 @@ constexpr int64_t adapter_cols(int64_t r) { return round_up(3 * r, 64); }
 // Tiles of a plan: one per 64 tokens and one per used adapter at most.
 inline int64_t plan_tiles(int64_t M, int count) { return M / 64 + (count < M ? count : M); }
 
+// The base products of 17 to kMidTokens tokens (mid.hip).
+constexpr int64_t kMidTokens = 64;
+int mid_fwd_splits(int64_t M, int64_t N, int64_t K);
+hipError_t launch_mid_fwd(const Nf4View& W, const uint16_t* X, int64_t M, const AdapterGemmArgs& ma, void* Y, bool y16,
+                          int splits, float* P, hipStream_t st);
+
 struct AdaptersFwdLayout {
   // M <= 16: fp32 T in tiles; else bf16 S [M, C] of s·T; an fp32 area: the
   // partial sums of T [slices, M, r], then the GEMM's (splits > 1)
