@@ -350,9 +350,13 @@ __global__ __launch_bounds__(kPartThreads) void distill_gradient_kernel(DistillA
 #pragma unroll
   for (int j = 0; j < kPartVecs; ++j) z[j] = R.load(i0 + j * kPartThreads);
   const float lse = a.lse_in[m], w = a.weight ? a.weight[m] : 1.0f;
-  if (tid < 64) load_entries<ZT, TT>(s, a, m, R.row, tid);
-  __syncthreads();  // (the entries' logits are read: dZ may be Z)
-  if (tid < 64) entry_softmax(s, a.k, tid);
+  const bool in_place = a.dZ == a.Z;
+  // (in place the entries' logits have to be read before any is overwritten;
+  // otherwise the first wave sees to the entries while the others write)
+  if (in_place) {
+    if (tid < 64) load_entries<ZT, TT>(s, a, m, R.row, tid);
+    __syncthreads();
+  }
   bool live = lse > -INFINITY && w != 0.f;
   const float g = w * a.tau;
   // lse·log2(e) in two parts
@@ -371,6 +375,10 @@ __global__ __launch_bounds__(kPartThreads) void distill_gradient_kernel(DistillA
     }
   // (the exponentials are written before the entries are waited for; a row
   // without entries gets its zeros now)
+  if (tid < 64) {
+    if (!in_place) load_entries<ZT, TT>(s, a, m, R.row, tid);
+    entry_softmax(s, a.k, tid);
+  }
   __syncthreads();
   if (live && !(s.t_max > -INFINITY)) {
     live = false;
