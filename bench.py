@@ -44,6 +44,8 @@ Extra objects on the JSON line:
                  65B parameters); only the quantize kernels are timed;
   adamw, merge, formats, f16_step   the next rows (AdamW step, LoRA merge,
                  comparison formats, fp16 compute);
+  adapters       many adapters on one weight (forward, backward, 16 tokens)
+                 beside one adapter's calls, and top-logit distillation;
   cpu_baseline   the oracle (numpy, fp64) on a bounded sample: one whole step
                  of the 7B MLP workload; breadth: quantize params/s on
                  several shapes and fp64 fwd+bwd of one linear of each
@@ -57,7 +59,7 @@ reported only while the kernel's sources are byte-identical to the ones
 profiled; otherwise null.
 
 Usage: python bench.py [--gpus 1] [--steps K] [--warmup W] [--settle S] [--no-cpu-baseline]
-                       [--no-gemv] [--no-adamw] [--no-merge] [--no-formats] [--no-f16]
+                       [--no-gemv] [--no-adamw] [--no-merge] [--no-formats] [--no-adapters] [--no-f16]
                        [--no-workloads] [--no-sweep] [--no-bulk] [--bulk-sample]
 """
 
@@ -609,6 +611,64 @@ def run_merge(torch, q, args):
     return out
 
 
+def run_adapters(torch, q, args):
+    """Many adapters on one weight, and the loss that trains them: the 7B gate
+    (11008x4096, r = 64) with 8 adapters over 4096 tokens in uneven runs
+    (forward, backward; the same with one adapter beside it) and 16 tokens of
+    16 adapters; distillation of 4096 x 32000 bf16 logits from 64 teacher
+    logits, loss with gradient.  Mean time of a call among others."""
+    N, K, r, out = 11008, 4096, 64, {}
+    g = torch.Generator(device="cuda").manual_seed(11)
+
+    def draw(*shape, scale=1.0):
+        return (torch.randn(*shape, device="cuda", generator=g) * scale).to(torch.bfloat16)
+
+    def timed(fn, n=30):
+        for _ in range(3):
+            fn()
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        for _ in range(n):
+            fn()
+        b.record()
+        torch.cuda.synchronize()
+        return a.elapsed_time(b) / n * 1e3
+
+    W = q.Nf4Tensor.empty(N, K)
+    q.qlora_nf4_quantize(draw(N, K, scale=0.02), W, q.workspace(q.qlora_nf4_sizes(N, K, 0, r)["quantize_ws_bytes"]))
+    for name, M, count in (("gate_M4096_8_adapters", 4096, 8), ("gate_M16_16_adapters", 16, 16)):
+        pool = q.AdapterPool(draw(count, r, K, scale=0.02), draw(count, N, r, scale=0.01),
+                             torch.full((count,), 0.25, device="cuda"))
+        index = torch.arange(M, device="cuda", dtype=torch.int32) * count // M
+        plan = q.AdapterPlan.empty(M, count)
+        q.qlora_adapters_plan(index, plan)
+        X, dY = draw(M, K), draw(M, N)
+        Y, T = torch.empty_like(dY), torch.empty(M, r, device="cuda")
+        dX, dA, dB = torch.empty_like(X), torch.empty(count, r, K, device="cuda"), torch.empty(count, N, r, device="cuda")
+        sz, one = q.qlora_adapters_sizes(N, K, M, r, count), q.qlora_nf4_sizes(N, K, M, r)
+        wf, wb = q.workspace(max(sz["fwd_ws_bytes"], one["fwd_ws_bytes"])), q.workspace(max(sz["bwd_ws_bytes"], one["bwd_ws_bytes"]))
+        A, B = pool.A[0].contiguous(), pool.B[0].contiguous()
+        rec = {"plan_us": timed(lambda: q.qlora_adapters_plan(index, plan)),
+               "fwd_us": timed(lambda: q.qlora_adapters_fwd(W, X, pool, plan, Y, T, wf)),
+               "one_adapter_fwd_us": timed(lambda: q.qlora_linear_fwd(W, X, A, B, r, 16.0, Y, T, wf))}
+        if M > 16:
+            q.qlora_adapters_fwd(W, X, pool, plan, Y, T, wf)
+            rec["bwd_us"] = timed(lambda: q.qlora_adapters_bwd(W, X, dY, pool, plan, T, dX, dA, dB, wb))
+            rec["one_adapter_bwd_us"] = timed(lambda: q.qlora_linear_bwd(W, X, dY, A, B, r, 16.0, T, dX, dA[0], dB[0], wb))
+        out[name] = {k: round(v, 2) for k, v in rec.items()}
+        log(f"[bench] adapters {name}: {out[name]}")
+        del pool, X, dY, Y, T, dX, dA, dB, wf, wb
+    M, V, k = 4096, 32000, 64
+    Z = draw(M, V, scale=2.5)
+    top, at = Z.topk(k, dim=1)
+    at, loss, dZ = at.to(torch.int32).contiguous(), torch.empty(M, device="cuda"), torch.empty_like(Z)
+    us = timed(lambda: q.qlora_distill_fwd(Z, top.contiguous(), at, 2.0, None, loss, None, dZ))
+    nbytes = 4 * M * V + 6 * M * k
+    out["distill_4096x32000"] = {"us": round(us, 2), "bytes": nbytes, "GB/s": round(nbytes / us / 1e3, 1)}
+    log(f"[bench] distillation: {out['distill_4096x32000']}")
+    return out
+
+
 def format_gemv_bytes(fmt, N, K, M):
     """Bytes the comparison-format GEMV must move: codes, fp32 block
     constants and X in; Y (bf16) out."""
@@ -864,6 +924,7 @@ def main():
     ap.add_argument("--no-adamw", action="store_true")
     ap.add_argument("--no-merge", action="store_true")
     ap.add_argument("--no-formats", action="store_true")
+    ap.add_argument("--no-adapters", action="store_true")
     ap.add_argument("--no-f16", action="store_true")
     ap.add_argument("--no-workloads", action="store_true")
     ap.add_argument("--no-sweep", action="store_true")
@@ -895,6 +956,7 @@ def main():
     adamw = None if args.no_adamw else run_adamw(torch, q, args)
     merge = None if args.no_merge else run_merge(torch, q, args)
     formats = None if args.no_formats else run_formats(torch, q, args)
+    adapters = None if args.no_adapters else run_adapters(torch, q, args)
     f16_step = None
     if not args.no_f16:
         m16 = run_step(torch, q, args, f16=True, steps=5, warmup=2, with_quantize=False)
@@ -947,6 +1009,7 @@ def main():
         "adamw": adamw,
         "merge": merge,
         "formats": formats,
+        "adapters": adapters,
         "f16_step": f16_step,
         "kernels": {k: {kk: (round(vv, 4) if isinstance(vv, float) else vv) for kk, vv in v.items()}
                     for k, v in mlp["per_kernel"].items()},
