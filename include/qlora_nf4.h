@@ -298,7 +298,8 @@ qlora_status qlora_adapters_plan(const int32_t* index, int64_t M, int32_t count,
  *           without an adapter), or NULL.
  * Limits as for qlora_linear_fwd, r·max(N, K) < 2^30 and M·round_up(3r, 64) < 2^30.
  * An adapter that no token carries is not read.  A NaN or infinity in a
- * token's X reaches no other token's outputs. */
+ * token's X reaches no other token's outputs; one in a used adapter may reach
+ * tokens of the same batch that do not carry it. */
 qlora_status qlora_adapters_fwd(const qlora_nf4_t* W, const void* X, int64_t M,
                                 const qlora_adapters_t* adapters, const void* plan,
                                 size_t plan_bytes, void* Y, qlora_dtype y_dtype,
@@ -337,7 +338,7 @@ qlora_status qlora_adapters_bwd(const qlora_nf4_t* W, const void* X, const void*
  *   dZ         device [M, ldz] in z_dtype, the gradient of Σ_m loss[m], with
  *              zeros in the padding columns; it may be Z itself; NULL: the
  *              loss alone.
- * 1 <= k <= 512, 1 <= V <= ldz < 2^29, 1e-6 <= tau <= 1e6, M·ldz <= 2^40, M < 2^31.
+ * 1 <= k <= 512, 1 <= V <= ldz < 2^28, 1e-6 <= tau <= 1e6, M·ldz <= 2^40, M < 2^31.
  * A token of weight 0 or without entries has loss 0 and a zero gradient
  * whatever its logits are.  A logit of −infinity is a masked column (q = 0);
  * a row whose largest logit is below -1e30 has no columns: loss 0, zero

@@ -637,7 +637,7 @@ __global__ __launch_bounds__(256) void adapters_gradient_finish_kernel(float* __
     const int4 t = ut.of_group[g];
     first = t.x;
     n = t.y;
-    if (n == 1 || first + n > max_slots) return;
+    if (n == 1 || (n > 0 && (first < 0 || first + n > max_slots))) return;
   }
   for (int64_t i = 4 * ((int64_t)blockIdx.x * 256 + threadIdx.x); i < na + nb; i += 1024 * (int64_t)gridDim.x) {
     f32x4_t v = {0.f, 0.f, 0.f, 0.f};
@@ -725,7 +725,7 @@ int64_t unit_table_bytes(int64_t units, int count) { return round_up(256 + (unit
 }  // namespace
 AdaptersBwdLayout adapters_bwd_layout(int64_t M, int64_t N, int64_t K, int r, int count) {
   AdaptersBwdLayout L{};
-  L.splits = M > 0 ? dx_gemm_splits(M, N, K, SIZE_MAX) : 1;
+  L.splits = M > kMidTokens ? dx_gemm_splits(M, N, K, SIZE_MAX) : M > 0 ? mid_dx_splits(M, N, K) : 1;
   if (M == 0) return L;
   L.slices_U = down_slices(M, N, r);
   L.slices_T = down_slices(M, K, r);
@@ -748,35 +748,38 @@ AdaptersBwdLayout adapters_bwd_layout(int64_t M, int64_t N, int64_t K, int r, in
   return L;
 }
 
-// Within a band of 256 tokens (up to kMidTokens of 32, 64 and 128) the GEMM's split count is constant and its
-// partials grow with M; a factor's slices only fall with M, by less than M
-// grows from one multiple of 64 to the next, so the largest M of every 64 is
-// taken.
-size_t adapters_fwd_ws_max(int64_t M_max, int64_t N, int64_t K, int r, int count) {
-  size_t most = adapters_fwd_layout(std::min<int64_t>(M_max, 16), N, K, r, count).total;
-  most = std::max(most, adapters_fwd_layout(std::min<int64_t>(M_max, 32), N, K, r, count).total);
-  for (int64_t top = 63; M_max > 16; top += 64) {
-    most = std::max(most, adapters_fwd_layout(std::min(top, M_max), N, K, r, count).total);
+// Up to kMidTokens tokens the split count may change at any of them, so each is
+// taken; above, it is constant within a band of 256 tokens (the GEMMs' tiles)
+// and the partials grow with M, and so are a factor's slices between multiples
+// of 64: the last of every 64 and the first of the next are taken.
+namespace {
+template <typename F>
+void each_worst(int64_t M_max, F&& take) {
+  for (int64_t M = 1; M <= std::min(M_max, kMidTokens); ++M) take(M);
+  for (int64_t top = kMidTokens + 63; M_max > kMidTokens; top += 64) {
+    take(std::min(top, M_max));
     if (top >= M_max) break;
-    most = std::max(most, adapters_fwd_layout(std::min(top + 1, M_max), N, K, r, count).total);
+    take(top + 1);
   }
+}
+}  // namespace
+size_t adapters_fwd_ws_max(int64_t M_max, int64_t N, int64_t K, int r, int count) {
+  size_t most = 0;
+  each_worst(M_max, [&](int64_t M) { most = std::max(most, adapters_fwd_layout(M, N, K, r, count).total); });
   return most;
 }
 size_t adapters_bwd_ws_max(int64_t M_max, int64_t N, int64_t K, int r, int count) {
-  // the factors grow with M; the shared area is bounded band by band for the
-  // GEMM's and the factors' partials, and for the gradients' by 2M/unit
-  // slots: units of at least M/parts give 2·parts, units of 1,024 2M/1,024
+  // the factors grow with M; the shared area is bounded by the products' and
+  // the factors' partials as above, and for the gradients' by 2M/unit slots:
+  // units of at least M/parts give 2·parts, units of 1,024 2M/1,024
   const AdaptersBwdLayout L = adapters_bwd_layout(M_max, N, K, r, count);
   if (M_max == 0) return L.total;
   int64_t area = 0;
-  for (int64_t top = 63;; top += 64) {
-    for (int64_t M : {std::min(top, M_max), std::min(top + 1, M_max)}) {
-      const AdaptersBwdLayout l = adapters_bwd_layout(M, N, K, r, count);
-      if (l.splits > 1) area = std::max(area, l.splits * M * K * 4);
-      area = std::max(area, (int64_t)(l.slices_U + l.slices_T) * M * r * 4);
-    }
-    if (top >= M_max) break;
-  }
+  each_worst(M_max, [&](int64_t M) {
+    const AdaptersBwdLayout l = adapters_bwd_layout(M, N, K, r, count);
+    if (l.splits > 1) area = std::max(area, l.splits * M * K * 4);
+    area = std::max(area, (int64_t)(l.slices_U + l.slices_T) * M * r * 4);
+  });
   const int64_t parts = gradient_parts(N, K, r);
   const int64_t slots = std::min(std::max<int64_t>(2 * parts, 2 * M_max / kMaxUnit), 2 * M_max / 64);
   area = std::max(area, slots * r * (K + N) * 4);
@@ -847,7 +850,8 @@ hipError_t launch_adapters_bwd(const Nf4View& W, const uint16_t* X, const uint16
   if (e != hipSuccess) return e;
   const AdapterGemmArgs ma{pl.head, (int)plan_pad(M), (int)plan_pad(ad.count + 1), U, ad.A, ad.r,
                            (int)adapter_cols(r), ad.count, (dx16 ? 2 : 3) * ad.r};
-  e = launch_dx_gemm_adapters(W, dY, M, ma, dX, dx16, L.splits, P, st);
+  e = M <= kMidTokens ? launch_mid_dx(W, dY, M, ma, dX, dx16, L.splits, P, st)
+                      : launch_dx_gemm_adapters(W, dY, M, ma, dX, dx16, L.splits, P, st);
   if (e == hipSuccess && L.splits > 1) e = launch_splitk_reduce(P, L.splits, M * K, dX, dx16, false, st);
   if (e != hipSuccess) return e;
   const int64_t slot = r * (K + N);

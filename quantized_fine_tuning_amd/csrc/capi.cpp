@@ -540,7 +540,7 @@ qlora_status check_distill(const char* fn, const void* Z, qlora_dtype z_dtype, i
     return fail(QLORA_ERR_INVALID_ARG, "%s: M=%lld outside [0, 2^31)", fn, (long long)M);
   if (V < 1 || ldz < V)
     return fail(QLORA_ERR_INVALID_ARG, "%s: V=%lld, ldz=%lld (1 <= V <= ldz)", fn, (long long)V, (long long)ldz);
-  if (ldz >= (int64_t(1) << 29) || (M > 0 && ldz > (int64_t(1) << 40) / M))
+  if (ldz >= (int64_t(1) << 28) || (M > 0 && ldz > (int64_t(1) << 40) / M))
     return fail(QLORA_ERR_INVALID_ARG, "%s: ldz or M*ldz too large", fn);
   if (k < 1 || k > qnf4::kMaxTop) return fail(QLORA_ERR_INVALID_ARG, "%s: k=%d outside [1, %d]", fn, k, qnf4::kMaxTop);
   if (!(tau >= 1e-6f && tau <= 1e6f)) return fail(QLORA_ERR_INVALID_ARG, "%s: tau=%g outside [1e-6, 1e6]", fn, tau);

@@ -58,7 +58,7 @@ struct RowTokens {
   }
 };
 
-// The adapters' share as more reduction stages of 256 columns: the `cols` split
+// The adapters' share as more reduction stages of `width` columns: the `cols` split
 // ranks of each used adapter among positions [p0, p0 + rows), one adapter after
 // another (column c belongs to used adapter gfirst + c / cols); `all` columns,
 // this split's stages [first, last).
@@ -66,14 +66,14 @@ struct LoraShare {
   int gfirst, all, first, last;
 };
 __device__ __forceinline__ LoraShare lora_share(const AdapterGemmArgs& ma, int p0, int rows, int64_t M, int sp,
-                                                int splits) {
+                                                int splits, int width) {
   LoraShare s{0, 0, 0, 0};
   const int held = std::min(ma.held(), (int)M);
   if (p0 < held) {
     s.gfirst = ma.group(p0);
     const int glast = std::min(ma.group(std::min(p0 + rows, held) - 1), ma.count - 1);
     s.all = s.gfirst >= 0 && glast >= s.gfirst ? std::min(glast - s.gfirst + 1, rows) * ma.cols : 0;
-    const int stages = (s.all + 255) / 256;
+    const int stages = (s.all + width - 1) / width;
     s.first = split_first(sp, splits, stages);
     s.last = split_first(sp + 1, splits, stages);
   }
@@ -189,7 +189,7 @@ __global__ __launch_bounds__(kMidThreads) void mid_fwd_kernel(Nf4View W, const u
 
   // the adapters, while the first stages are on their way, through the ring's
   // free stage
-  const LoraShare L = lora_share(ma, p0, TM, M, sp, splits);
+  const LoraShare L = lora_share(ma, p0, TM, M, sp, splits, 256);
   if (L.first < L.last) {
     const i32x4_t rS = rsrc_words(ma.S, M * ma.C * 2);
     const float inv_cols = 1.0f / (float)ma.cols;
@@ -261,19 +261,220 @@ __global__ __launch_bounds__(kMidThreads) void mid_fwd_kernel(Nf4View W, const u
   }
 }
 
+// ---------------------------------------------------------------------------
+// dX = dY·Ŵ + S·A for 16·NT positions and 128 columns k, 32 per wave.  The
+// reduction runs over weight rows while a row's codes run along k, so a stage
+// of 64 rows is decoded into a bf16 tile [row][k] (thread: 32 codes of a row)
+// and the MFMA operands, 8 rows of one column, are transposing reads of it.
+// dY rows, codes and constants are copied into LDS two stages ahead; within a
+// stage the products come first and the next stage's decode after them.  The
+// adapters come first of all, as stages of 64 split ranks (LoraShare): rows of
+// A_a in the tile's place.  Two workgroups share a compute unit.  (61 tokens,
+// 4096 x 4096: 17.7 us against 25.3 with the GEMM.)
+// ---------------------------------------------------------------------------
+constexpr int kDxThreads = 256;
+// byte of column `col` (a multiple of 4) of tile row `row`: 16-byte chunk c at
+// c ^ ((row & 3) << 1), the 4 rows of a transposing read on different banks
+__device__ __forceinline__ int tswz(int row, int col) {
+  return row * 256 + (((col >> 3) ^ ((row & 3) << 1)) << 4) + 2 * (col & 7);
+}
+template <int NT>
+__global__ __launch_bounds__(kDxThreads) void mid_dx_kernel(Nf4View W, const uint16_t* __restrict__ dY, int64_t M,
+                                                            void* __restrict__ dX, int dx_bf16, int tiles_k, int splits,
+                                                            float* __restrict__ P, Codebook cb, AdapterGemmArgs ma) {
+  constexpr int TM = 16 * NT, D = 3, YI = NT / 2;  // dY copies per wave and stage (8 rows each)
+  __shared__ __attribute__((aligned(1024))) char sy[D][TM * 128];
+  __shared__ __attribute__((aligned(1024))) char sc[D][4 * 1536];  // per wave: codes 1 KB, e4m3 dwords, scales
+  __shared__ __attribute__((aligned(1024))) char sw[2][64 * 256];
+  __shared__ __attribute__((aligned(256))) float sq[16];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lr = lane & 15, kq = lane >> 4;
+  const int64_t K = W.K, N = W.N;
+  const int tk = (int)blockIdx.x % tiles_k, tm = (int)blockIdx.x / tiles_k, sp = (int)blockIdx.y;
+  const int p0 = TM * tm;
+  const int64_t k0 = 128 * (int64_t)tk;
+  const uint32_t kpr = (uint32_t)(K / kBlock);
+  const int all = (int)((N + 63) / 64);
+  const int s0 = split_first(sp, splits, all), s1 = split_first(sp + 1, splits, all);
+  const float mu = *W.mu;
+  const i32x4_t ry = rsrc_words(dY, M * N * 2), rc = rsrc_words(W.codes, N * (K / 2)), re = rsrc_words(W.e, N * kpr);
+  const i32x4_t rs = rsrc_words(W.s, ((N * kpr + kDqBlock - 1) / kDqBlock) * 4);
+  const RowTokens<NT> rows(ma, p0, M, kq);
+
+  // dY: wave w copies rows 8(YI·w + c) + (lane >> 3), lane l physical chunk l % 8
+  const int ych = (lane & 7) ^ (lane >> 3);
+  uint32_t vy[YI];
+  {
+    int tok[YI];
+#pragma unroll
+    for (int c = 0; c < YI; ++c) tok[c] = ma.perm()[std::min(p0 + 8 * (YI * wave + c) + (lane >> 3), (int)M - 1)];
+#pragma unroll
+    for (int c = 0; c < YI; ++c)
+      vy[c] = p0 + 8 * (YI * wave + c) + (lane >> 3) < (int)M && (uint32_t)tok[c] < (uint32_t)M
+                  ? (uint32_t)tok[c] * (uint32_t)N * 2u + 16u * ych
+                  : 0x7fffffffu;
+  }
+  // this thread's codes: row drow of a stage, columns [32·dq, +32) of the tile
+  const int drow = tid >> 2, dq = tid & 3;
+  const bool dcol = k0 + 32 * dq < K;
+  const uint32_t vcode = (uint32_t)(drow * (K / 2)) + (uint32_t)(k0 / 2) + 16u * dq;
+  const uint32_t blk0 = (uint32_t)drow * kpr + (uint32_t)(k0 / kBlock) + (dq >> 1);
+  auto issue = [&](int b, int s) __attribute__((always_inline)) {
+    const bool in = s < s1 && 64 * (int64_t)s + 8 * ych < N;
+#pragma unroll
+    for (int c = 0; c < YI; ++c)
+      dma_lds16(ry, sy[b] + (YI * wave + c) * 1024, in ? vy[c] : 0x7fffffffu, (uint32_t)s * 128u);
+    const bool ok = s < s1 && dcol && 64 * (int64_t)s + drow < N;
+    char* const w = sc[b] + wave * 1536;
+    const uint32_t blk = blk0 + 64 * (uint32_t)s * kpr;
+    dma_lds16(rc, w, ok ? vcode + (uint32_t)(32 * (int64_t)s * K) : 0x7fffffffu, 0u);
+    dma_lds4(re, w + 1024, ok ? blk & ~3u : 0x7fffffffu, 0u);
+    dma_lds4(rs, w + 1280, ok ? (blk / kDqBlock) * 4u : 0x7fffffffu, 0u);
+  };
+  const uint32_t sqb = lds_offset(sq);
+  // this thread's 32 values of stage s into the tile (zeros past N: with no
+  // scale and no code they would be level 0 times the mean)
+  auto decode = [&](const char* w, char* t, int s) __attribute__((always_inline)) {
+    const u32x4_t c = *reinterpret_cast<const u32x4_t*>(w + 16 * lane);
+    const uint32_t e4 = *reinterpret_cast<const uint32_t*>(w + 1024 + 4 * lane);
+    const float sg = *reinterpret_cast<const float*>(w + 1280 + 4 * lane);
+    const uint32_t blk = blk0 + 64 * (uint32_t)s * kpr;
+    const bool ok = dcol && 64 * (int64_t)s + drow < N;
+    const float cp = ok ? decode_constant((e4 >> (8 * (blk & 3u))) & 0xffu, sg, mu) : 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t we = (c[i] << 2) & 0x3C3C3C3Cu, wo = (c[i] >> 2) & 0x3C3C3C3Cu;
+      u32x4_t o;
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        const float qe = *(const __attribute__((address_space(3))) float*)(uintptr_t)__builtin_amdgcn_perm(
+            sqb, we, 0x07060500u | (uint32_t)p);
+        const float qo = *(const __attribute__((address_space(3))) float*)(uintptr_t)__builtin_amdgcn_perm(
+            sqb, wo, 0x07060500u | (uint32_t)p);
+        o[p] = pack_bf16x2(__fmul_rn(qe, cp), __fmul_rn(qo, cp));
+      }
+      *reinterpret_cast<u32x4_t*>(t + tswz(drow, 32 * dq + 8 * i)) = o;
+    }
+  };
+  f32x4_t acc[2][NT];
+#pragma unroll
+  for (int f = 0; f < 2; ++f)
+#pragma unroll
+    for (int i = 0; i < NT; ++i) acc[f][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  auto multiply = [&](const char* y, const char* t) __attribute__((always_inline)) {
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      u32x4_t b[2];
+#pragma unroll
+      for (int f = 0; f < 2; ++f) {
+        const int row = 32 * ks + 8 * kq + (lr >> 2), col = 32 * wave + 16 * f + 4 * (lr & 3);
+        const u32x2_t h0 = lds_read_tr(t + tswz(row, col)), h1 = lds_read_tr(t + tswz(row + 4, col));
+        b[f] = u32x4_t{h0[0], h0[1], h1[0], h1[1]};
+      }
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        const u32x4_t a =
+            *reinterpret_cast<const u32x4_t*>(y + (16 * i + lr) * 128 + (((4 * ks + kq) ^ (lr & 7)) << 4));
+#pragma unroll
+        for (int f = 0; f < 2; ++f) acc[f][i] = mfma_16x16x32(a, b[f], acc[f][i]);
+      }
+    }
+  };
+  constexpr int PER = YI + 3;  // copies per wave and stage
+  const float cbq = cb.q[tid & 15];
+  issue(0, s0);
+  issue(1, s0 + 1);
+  if (tid < 16) sq[tid] = cbq;
+
+  // the adapters, through the ring's free stage and the second tile
+  const LoraShare L = lora_share(ma, p0, TM, M, sp, splits, 64);
+  if (L.first < L.last) {
+    const i32x4_t rS = rsrc_words(ma.S, M * ma.C * 2);
+    const float inv_cols = 1.0f / (float)ma.cols;
+    auto adapter_of = [&](int c) __attribute__((always_inline)) { return (int)(((float)c + 0.5f) * inv_cols); };
+    for (int ls = L.first; ls < L.last; ++ls) {
+      if (ls > L.first) open_stage<0>();  // (stage and tile are read)
+      const int c = 64 * ls + 8 * ych, cc = std::min(c, L.all - 8), g = adapter_of(cc);
+      const int lo = ma.start(L.gfirst + g) - p0, hi = std::min(ma.start(L.gfirst + g + 1), (int)M) - p0;
+#pragma unroll
+      for (int i = 0; i < YI; ++i) {
+        const int row = 8 * (YI * wave + i) + (lane >> 3);
+        const bool in = c < L.all && row >= lo && row < hi;
+        dma_lds16(rS, sy[2] + (YI * wave + i) * 1024,
+                  in ? (uint32_t)(((p0 + row) * ma.C + cc - g * ma.cols) * 2) : 0x7fffffffu, 0u);
+      }
+      // tile rows 16w + 4i + (lane >> 4), physical chunk lane % 16
+      int id[4], at[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int t = 64 * ls + 16 * wave + 4 * i + (lane >> 4), tc = std::min(t, L.all - 1), ga = adapter_of(tc);
+        at[i] = t < L.all ? (tc - ga * ma.cols) % ma.r : -1;
+        id[i] = ma.id(L.gfirst + ga);
+      }
+      u32x4_t v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = 16 * wave + 4 * i + (lane >> 4);
+        const int64_t k = k0 + 8 * ((lane & 15) ^ ((row & 3) << 1));
+        const bool ok = at[i] >= 0 && (unsigned)id[i] < (unsigned)ma.count && k < K;
+        v[i] = *reinterpret_cast<const u32x4_t*>(ma.F + (ok ? ((int64_t)id[i] * ma.r + at[i]) * K + k : 0));
+        if (!ok) v[i] = u32x4_t{0u, 0u, 0u, 0u};
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<u32x4_t*>(sw[1] + (16 * wave + 4 * i) * 256 + 16 * lane) = v[i];
+      open_stage<0>();
+      multiply(sy[2], sw[1]);
+    }
+  }
+
+  // stage s0 decoded; then per stage: its products, the next one's decode
+  open_stage<PER>();  // (the levels are in LDS, and this wave's copies of stage s0)
+  if (s0 < s1) decode(sc[0] + wave * 1536, sw[0], s0);
+  int b = 0;
+  for (int s = s0; s < s1; ++s) {
+    const int b1 = b + 1 == D ? 0 : b + 1, b2 = b1 + 1 == D ? 0 : b1 + 1;
+    // tile s is written, and every wave has waited for its copies of stage s
+    open_stage<PER>();
+    issue(b2, s + 2);
+    multiply(sy[b], sw[(s - s0) & 1]);
+    wait_vmem_le<PER>();  // this wave's copies of stage s + 1
+    asm volatile("" ::: "memory");
+    if (s + 1 < s1) decode(sc[b1] + wave * 1536, sw[(s + 1 - s0) & 1], s + 1);
+    b = b1;
+  }
+  wait_vmem();  // no copy may land in LDS after the workgroup ends
+
+#pragma unroll
+  for (int f = 0; f < 2; ++f) {
+    const int64_t k = k0 + 32 * wave + 16 * f + lr;
+    if (k >= K) continue;
+    if (splits > 1) {
+      float* const D0 = P + (int64_t)sp * M * K + k;
+      rows.scatter(acc[f], [&](int tok, float v) { D0[(int64_t)tok * K] = v; });
+    } else if (dx_bf16) {
+      uint16_t* const D0 = static_cast<uint16_t*>(dX) + k;
+      rows.scatter(acc[f], [&](int tok, float v) { D0[(int64_t)tok * K] = (uint16_t)(pack_bf16x2(v, 0.f) & 0xffffu); });
+    } else {
+      float* const D0 = static_cast<float*>(dX) + k;
+      rows.scatter(acc[f], [&](int tok, float v) { D0[(int64_t)tok * K] = v; });
+    }
+  }
+}
+
 // Positions per workgroup, in tiles of 16.
 int mid_tiles(int64_t M) { return M <= 32 ? 2 : 4; }
 
 }  // namespace
 
 // The split count with the least estimated time, in microseconds: rounds of
-// workgroups over the 256 compute units at 2.3 us a stage and 7.7 around them,
-// and the fp32 partials written and read at 4 TB/s.
-int mid_splits(int64_t tiles, int64_t stages, int64_t elements) {
+// `slots` workgroups at `stage` us a stage and `around` all of them, and the
+// fp32 partials written and read at 4 TB/s.
+int mid_splits(int64_t tiles, int64_t stages, int64_t elements, int64_t slots, double stage, double around) {
   int best = 1;
   double least = 0;
   for (int64_t s = 1; s <= 16 && 2 * s <= std::max<int64_t>(stages, 2); ++s) {
-    const double t = (double)((tiles * s + 255) / 256) * ((double)((stages + s - 1) / s) * 2.3 + 7.7) +
+    const double t = (double)((tiles * s + slots - 1) / slots) * ((double)((stages + s - 1) / s) * stage + around) +
                      (s > 1 ? (double)s * (double)elements * 8 / 4e6 : 0.0);
     if (s == 1 || t < least) {
       least = t;
@@ -282,9 +483,15 @@ int mid_splits(int64_t tiles, int64_t stages, int64_t elements) {
   }
   return best;
 }
+// One workgroup per compute unit (its LDS), 2.3 us a stage.
 int mid_fwd_splits(int64_t M, int64_t N, int64_t K) {
   const int64_t tm = 16 * mid_tiles(M);
-  return mid_splits(((M + tm - 1) / tm) * ((N + 127) / 128), (K + 255) / 256, M * N);
+  return mid_splits(((M + tm - 1) / tm) * ((N + 127) / 128), (K + 255) / 256, M * N, 256, 2.3, 7.7);
+}
+// Two workgroups per compute unit.
+int mid_dx_splits(int64_t M, int64_t N, int64_t K) {
+  const int64_t tm = 16 * mid_tiles(M);
+  return mid_splits(((M + tm - 1) / tm) * ((K + 127) / 128), (N + 63) / 64, M * K, 512, 1.0, 6.0);
 }
 
 hipError_t launch_mid_fwd(const Nf4View& W, const uint16_t* X, int64_t M, const AdapterGemmArgs& ma, void* Y, bool y16,
@@ -293,6 +500,20 @@ hipError_t launch_mid_fwd(const Nf4View& W, const uint16_t* X, int64_t M, const 
   const dim3 grid((unsigned)(tiles_n * ((M + tm - 1) / tm)), (unsigned)splits);
 #define QNF4_MID(NT) \
   mid_fwd_kernel<NT><<<grid, kMidThreads, 0, st>>>(W, X, M, Y, y16 ? 1 : 0, tiles_n, splits, P, codebook(), ma)
+  if (nt == 2)
+    QNF4_MID(2);
+  else
+    QNF4_MID(4);
+#undef QNF4_MID
+  return hipGetLastError();
+}
+
+hipError_t launch_mid_dx(const Nf4View& W, const uint16_t* dY, int64_t M, const AdapterGemmArgs& ma, void* dX, bool dx16,
+                         int splits, float* P, hipStream_t st) {
+  const int nt = mid_tiles(M), tm = 16 * nt, tiles_k = (int)((W.K + 127) / 128);
+  const dim3 grid((unsigned)(tiles_k * ((M + tm - 1) / tm)), (unsigned)splits);
+#define QNF4_MID(NT) \
+  mid_dx_kernel<NT><<<grid, kDxThreads, 0, st>>>(W, dY, M, dX, dx16 ? 1 : 0, tiles_k, splits, P, codebook(), ma)
   if (nt == 2)
     QNF4_MID(2);
   else

@@ -47,9 +47,9 @@ def test_workspaces_cover_every_smaller_batch(n, k, r, count):
     """Sizes of M_max hold for each M below it: a call with exactly that many
     bytes passes the check (it then stops at the next one, a NULL workspace)."""
     d, ad = weight(n, k), pool(count=count, r=r)
-    for m_max in (1, 16, 17, 200, 777, 1025, 2049):
+    for m_max in (1, 16, 17, 50, 64, 200, 777, 1025, 2049):
         sizes = q.qlora_adapters_sizes(n, k, m_max, r, count)
-        for m in sorted({1, 8, 16, 17, 63, 64, 65, 129, 255, 256, 257, 511, 600, 777, 1024, 1025, 2048, 2049}):
+        for m in sorted({*range(1, 66), 63, 64, 65, 129, 255, 256, 257, 511, 600, 777, 1024, 1025, 2048, 2049}):
             if m > m_max:
                 break
             assert q.lib.qlora_adapters_fwd(ctypes.byref(d), FAKE, m, ctypes.byref(ad), FAKE, BIG, FAKE, q.QLORA_BF16,
@@ -151,6 +151,8 @@ def test_binding_refuses_wrong_tensors_on_the_host():
     X, Y, ws = torch.zeros(5, 64, dtype=bf), torch.zeros(5, 16, dtype=bf), torch.zeros(1 << 12, dtype=torch.uint8)
     with pytest.raises(ValueError, match="GPU"):
         q.qlora_adapters_fwd(W, X, p, plan, Y, None, ws)
+    with pytest.raises(ValueError, match="contiguous"):
+        q.qlora_adapters_fwd(W, torch.zeros(64, 5, dtype=bf).t(), p, plan, Y, None, ws)
     with pytest.raises(ValueError, match="plan"):
         q.qlora_adapters_fwd(W, X[:4], p, plan, Y[:4], None, ws)
     with pytest.raises(ValueError, match="plan"):
