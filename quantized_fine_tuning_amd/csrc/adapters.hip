@@ -706,7 +706,7 @@ hipError_t launch_down(const DownJob& t, const DownJob& u, int64_t M, const Adap
 
 AdaptersFwdLayout adapters_fwd_layout(int64_t M, int64_t N, int64_t K, int r, int count) {
   AdaptersFwdLayout L{};
-  L.splits = M > kMidTokens ? fwd_gemm_splits(M, N, K, SIZE_MAX) : M > 16 ? mid_fwd_splits(M, N, K) : 1;
+  L.splits = M > kMidTokens ? fwd_gemm_splits(M, N, K, SIZE_MAX) : M > 16 ? mid_fwd_plan(M, N, K).splits : 1;
   L.slices = M > kFewTokens ? down_slices(M, K, r) : 0;
   L.off_S = 0;
   L.off_P = M > 16 ? round_up(M * adapter_cols(r) * 2, 256) : M > 0 ? round_up((int64_t)cdiv(r, 16) * 1024, 256) : 0;
@@ -816,7 +816,7 @@ hipError_t launch_adapters_fwd(const Nf4View& W, const uint16_t* X, int64_t M, c
   // (the partial sums of T have been consumed: P now takes the split partials)
   const AdapterGemmArgs ma{pl.head, (int)plan_pad(M), (int)plan_pad(ad.count + 1), S, ad.B, ad.r,
                            (int)adapter_cols(ad.r), ad.count, (y16 ? 2 : 3) * ad.r};
-  e = M <= kMidTokens ? launch_mid_fwd(W, X, M, ma, Y, y16, L.splits, P, st)
+  e = M <= kMidTokens ? launch_mid_fwd(W, X, M, ma, Y, y16, mid_fwd_plan(M, W.N, W.K), P, st)
                       : launch_fwd_gemm_adapters(W, X, M, ma, Y, y16, L.splits, P, st);
   if (e != hipSuccess || L.splits == 1) return e;
   return launch_splitk_reduce(P, L.splits, M * W.N, Y, y16, false, st);

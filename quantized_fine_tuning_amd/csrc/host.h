@@ -272,9 +272,13 @@ inline int64_t plan_tiles(int64_t M, int count) { return M / 64 + (count < M ? c
 // The base products of few tokens (mid.hip): the forward one of 17 to
 // kMidTokens, dX of 1 to kMidTokens.
 constexpr int64_t kMidTokens = 64;
-int mid_fwd_splits(int64_t M, int64_t N, int64_t K);
+struct MidPlan {
+  int splits, waves;
+  double us;  // estimated
+};
+MidPlan mid_fwd_plan(int64_t M, int64_t N, int64_t K);
 hipError_t launch_mid_fwd(const Nf4View& W, const uint16_t* X, int64_t M, const AdapterGemmArgs& ma, void* Y, bool y16,
-                          int splits, float* P, hipStream_t st);
+                          const MidPlan& plan, float* P, hipStream_t st);
 int mid_dx_splits(int64_t M, int64_t N, int64_t K);
 hipError_t launch_mid_dx(const Nf4View& W, const uint16_t* dY, int64_t M, const AdapterGemmArgs& ma, void* dX, bool dx16,
                          int splits, float* P, hipStream_t st);

@@ -18,8 +18,6 @@
 namespace qnf4 {
 namespace {
 
-constexpr int kMidThreads = 512, kMidWaves = kMidThreads / 64;
-
 // Waits for this wave's copies but the newest N and for its LDS reads, then
 // for the workgroup.
 template <int N>
@@ -81,7 +79,7 @@ __device__ __forceinline__ LoraShare lora_share(const AdapterGemmArgs& ma, int p
 }
 
 // ---------------------------------------------------------------------------
-// Y = X·Ŵᵀ + S·Bᵀ for 16·NT positions and 128 weight rows, 16 per wave.  A
+// Y = X·Ŵᵀ + S·Bᵀ for 16·NT positions and 16 weight rows per wave.  A
 // stage is 256 reduction elements: four NF4 blocks of each row, lane (row l % 16,
 // q = l / 16) owning block q with its one constant.  The lane decodes 8 codes
 // at a time straight into an MFMA operand (levels from a 16-entry LDS table;
@@ -92,21 +90,24 @@ __device__ __forceinline__ LoraShare lora_share(const AdapterGemmArgs& ma, int p
 // shape (LoraShare): S rows into a free stage of the ring, every 8-rank piece of
 // B_a[n] straight into its operand register.
 // ---------------------------------------------------------------------------
-template <int NT>
-__global__ __launch_bounds__(kMidThreads) void mid_fwd_kernel(Nf4View W, const uint16_t* __restrict__ X, int64_t M,
+// WV waves: 8, or 16 with twice the weight rows (four waves on a SIMD cover each
+// other's lookups better, 2.9 us for a stage of twice the weights, but the
+// tiles are fewer: mid_fwd_plan).
+template <int NT, int WV>
+__global__ __launch_bounds__(64 * WV) void mid_fwd_kernel(Nf4View W, const uint16_t* __restrict__ X, int64_t M,
                                                               void* __restrict__ Y, int y_bf16, int tiles_n, int splits,
                                                               float* __restrict__ P, Codebook cb, AdapterGemmArgs ma) {
   constexpr int TM = 16 * NT, ROW = 512, XB = TM * ROW, WB = 2560;  // bytes: X of a stage, one wave's codes and constants
-  constexpr int D = NT == 2 ? 4 : 3;                                // ring depth
+  constexpr int D = WV == 16 ? 2 : NT == 2 ? 4 : 3, XI = 8 * NT / WV;                                // ring depth
   __shared__ __attribute__((aligned(1024))) char sx[D][XB];
-  __shared__ __attribute__((aligned(1024))) char sc[D][kMidWaves * WB];
+  __shared__ __attribute__((aligned(1024))) char sc[D][WV * WB];
   __shared__ __attribute__((aligned(256))) float sq[16];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lr = lane & 15, kq = lane >> 4;
   const int64_t K = W.K, N = W.N;
   const int tn = (int)blockIdx.x % tiles_n, tm = (int)blockIdx.x / tiles_n, sp = (int)blockIdx.y;
   const int p0 = TM * tm;
-  const int64_t n0 = 128 * (int64_t)tn + 16 * wave;  // this wave's rows
+  const int64_t n0 = 16 * WV * (int64_t)tn + 16 * wave;  // this wave's rows
   const uint32_t kpr = (uint32_t)(K / kBlock);
   const int all = (int)((K + 255) / 256);
   const int s0 = split_first(sp, splits, all), s1 = split_first(sp + 1, splits, all);
@@ -116,16 +117,16 @@ __global__ __launch_bounds__(kMidThreads) void mid_fwd_kernel(Nf4View W, const u
   const i32x4_t rs = rsrc_words(W.s, ((N * kpr + kDqBlock - 1) / kDqBlock) * 4);
   const i32x4_t rx = rsrc_words(X, M * K * 2);
 
-  // X: wave w copies rows 2(NT·w + c), +1; lane l physical chunk l % 32
-  uint32_t vx[NT];
-  int ch[NT];
+  // X: wave w copies rows 2(XI·w + c), +1; lane l physical chunk l % 32
+  uint32_t vx[XI];
+  int ch[XI];
   {
-    int tok[NT];
+    int tok[XI];
 #pragma unroll
-    for (int c = 0; c < NT; ++c) tok[c] = ma.perm()[std::min(p0 + 2 * (NT * wave + c) + (lane >> 5), (int)M - 1)];
+    for (int c = 0; c < XI; ++c) tok[c] = ma.perm()[std::min(p0 + 2 * (XI * wave + c) + (lane >> 5), (int)M - 1)];
 #pragma unroll
-    for (int c = 0; c < NT; ++c) {
-      const int row = 2 * (NT * wave + c) + (lane >> 5);
+    for (int c = 0; c < XI; ++c) {
+      const int row = 2 * (XI * wave + c) + (lane >> 5);
       ch[c] = (lane & 31) ^ (row & 15);
       vx[c] = p0 + row < (int)M && (uint32_t)tok[c] < (uint32_t)M ? (uint32_t)tok[c] * (uint32_t)K * 2u + 16u * ch[c]
                                                                   : 0x7fffffffu;
@@ -138,8 +139,8 @@ __global__ __launch_bounds__(kMidThreads) void mid_fwd_kernel(Nf4View W, const u
   const bool row_ok = n0 + lr < N;
   auto issue = [&](int b, int s) __attribute__((always_inline)) {
 #pragma unroll
-    for (int c = 0; c < NT; ++c)
-      dma_lds16(rx, sx[b] + (NT * wave + c) * 1024,
+    for (int c = 0; c < XI; ++c)
+      dma_lds16(rx, sx[b] + (XI * wave + c) * 1024,
                 s < s1 && 256 * (int64_t)s + 8 * ch[c] < K ? vx[c] : 0x7fffffffu, (uint32_t)s * 512u);
     const bool ok = s < s1 && row_ok && 4 * (uint32_t)s + kq < kpr;
     char* const w = sc[b] + wave * WB;
@@ -196,7 +197,7 @@ __global__ __launch_bounds__(kMidThreads) void mid_fwd_kernel(Nf4View W, const u
     // (c + 0.5) / cols is never nearer than 0.5 / cols to a whole number
     auto adapter_of = [&](int c) __attribute__((always_inline)) { return (int)(((float)c + 0.5f) * inv_cols); };
     for (int ls = L.first; ls < L.last; ++ls) {
-      int id[8], at[8], lo[NT], hi[NT], col[NT];
+      int id[8], at[8], lo[XI], hi[XI], col[XI];
 #pragma unroll
       for (int t = 0; t < 8; ++t) {
         const int c = 256 * ls + 64 * kq + 8 * t, cc = std::min(c, L.all - 8), g = adapter_of(cc);
@@ -204,7 +205,7 @@ __global__ __launch_bounds__(kMidThreads) void mid_fwd_kernel(Nf4View W, const u
         id[t] = ma.id(L.gfirst + g);
       }
 #pragma unroll
-      for (int i = 0; i < NT; ++i) {
+      for (int i = 0; i < XI; ++i) {
         const int c = 256 * ls + 8 * ch[i], cc = std::min(c, L.all - 8), g = adapter_of(cc);
         col[i] = c < L.all ? cc - g * ma.cols : -1;
         lo[i] = ma.start(L.gfirst + g) - p0;
@@ -212,10 +213,10 @@ __global__ __launch_bounds__(kMidThreads) void mid_fwd_kernel(Nf4View W, const u
       }
       if (ls > L.first) open_stage<0>();  // (the free stage is read)
 #pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        const int row = 2 * (NT * wave + i) + (lane >> 5);
+      for (int i = 0; i < XI; ++i) {
+        const int row = 2 * (XI * wave + i) + (lane >> 5);
         const bool in = col[i] >= 0 && row >= lo[i] && row < hi[i];
-        dma_lds16(rS, sx[D - 1] + (NT * wave + i) * 1024,
+        dma_lds16(rS, sx[D - 1] + (XI * wave + i) * 1024,
                   in ? (uint32_t)(((p0 + row) * ma.C + col[i]) * 2) : 0x7fffffffu, 0u);
       }
       u32x4_t bf[8];
@@ -240,7 +241,7 @@ __global__ __launch_bounds__(kMidThreads) void mid_fwd_kernel(Nf4View W, const u
 
   int b = 0;
   for (int s = s0; s < s1; ++s) {
-    open_stage<(D - 2) * (NT + 4)>();
+    open_stage<(D - 2) * (XI + 4)>();
     issue(b == 0 ? D - 1 : b - 1, s + D - 1);
     consume(sx[b], sc[b] + wave * WB, s);
     b = b + 1 == D ? 0 : b + 1;
@@ -470,40 +471,49 @@ int mid_tiles(int64_t M) { return M <= 32 ? 2 : 4; }
 // The split count with the least estimated time, in microseconds: rounds of
 // `slots` workgroups at `stage` us a stage and `around` all of them, and the
 // fp32 partials written and read at 4 TB/s.
-int mid_splits(int64_t tiles, int64_t stages, int64_t elements, int64_t slots, double stage, double around) {
-  int best = 1;
-  double least = 0;
+MidPlan mid_splits(int64_t tiles, int64_t stages, int64_t elements, int64_t slots, double stage, double around) {
+  MidPlan best{1, 8, 0.0};
   for (int64_t s = 1; s <= 16 && 2 * s <= std::max<int64_t>(stages, 2); ++s) {
     const double t = (double)((tiles * s + slots - 1) / slots) * ((double)((stages + s - 1) / s) * stage + around) +
                      (s > 1 ? (double)s * (double)elements * 8 / 4e6 : 0.0);
-    if (s == 1 || t < least) {
-      least = t;
-      best = (int)s;
-    }
+    if (s == 1 || t < best.us) best = MidPlan{(int)s, 8, t};
   }
   return best;
 }
-// One workgroup per compute unit (its LDS), 2.3 us a stage.
-int mid_fwd_splits(int64_t M, int64_t N, int64_t K) {
-  const int64_t tm = 16 * mid_tiles(M);
-  return mid_splits(((M + tm - 1) / tm) * ((N + 127) / 128), (K + 255) / 256, M * N, 256, 2.3, 7.7);
+// One workgroup per compute unit (its LDS), 2.3 us a stage with 8 waves and 2.9
+// with 16: 64 tokens, 4096 x 4096, 24 us in all with 8 and 27 with 16; 11008 x
+// 4096, 41 and 36.
+MidPlan mid_fwd_plan(int64_t M, int64_t N, int64_t K) {
+  const int64_t tm = 16 * mid_tiles(M), mt = (M + tm - 1) / tm, stages = (K + 255) / 256;
+  const MidPlan narrow = mid_splits(mt * ((N + 127) / 128), stages, M * N, 256, 2.3, 7.7);
+  MidPlan wide = mid_splits(mt * ((N + 255) / 256), stages, M * N, 256, 2.9, 7.5);
+  wide.waves = 16;
+  return wide.us < narrow.us ? wide : narrow;
 }
 // Two workgroups per compute unit.
 int mid_dx_splits(int64_t M, int64_t N, int64_t K) {
   const int64_t tm = 16 * mid_tiles(M);
-  return mid_splits(((M + tm - 1) / tm) * ((K + 127) / 128), (N + 63) / 64, M * K, 512, 1.0, 6.0);
+  return mid_splits(((M + tm - 1) / tm) * ((K + 127) / 128), (N + 63) / 64, M * K, 512, 1.0, 6.0).splits;
 }
 
 hipError_t launch_mid_fwd(const Nf4View& W, const uint16_t* X, int64_t M, const AdapterGemmArgs& ma, void* Y, bool y16,
-                          int splits, float* P, hipStream_t st) {
-  const int nt = mid_tiles(M), tm = 16 * nt, tiles_n = (int)((W.N + 127) / 128);
-  const dim3 grid((unsigned)(tiles_n * ((M + tm - 1) / tm)), (unsigned)splits);
-#define QNF4_MID(NT) \
-  mid_fwd_kernel<NT><<<grid, kMidThreads, 0, st>>>(W, X, M, Y, y16 ? 1 : 0, tiles_n, splits, P, codebook(), ma)
-  if (nt == 2)
-    QNF4_MID(2);
-  else
-    QNF4_MID(4);
+                          const MidPlan& plan, float* P, hipStream_t st) {
+  const int nt = mid_tiles(M), tm = 16 * nt, rows = 16 * plan.waves, tiles_n = (int)((W.N + rows - 1) / rows);
+  const dim3 grid((unsigned)(tiles_n * ((M + tm - 1) / tm)), (unsigned)plan.splits);
+#define QNF4_MID(NT, WV)                                                                                        \
+  mid_fwd_kernel<NT, WV><<<grid, 64 * WV, 0, st>>>(W, X, M, Y, y16 ? 1 : 0, tiles_n, plan.splits, P, codebook(), \
+                                                   ma)
+  if (plan.waves == 16) {
+    if (nt == 2)
+      QNF4_MID(2, 16);
+    else
+      QNF4_MID(4, 16);
+  } else {
+    if (nt == 2)
+      QNF4_MID(2, 8);
+    else
+      QNF4_MID(4, 8);
+  }
 #undef QNF4_MID
   return hipGetLastError();
 }
