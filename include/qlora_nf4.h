@@ -298,8 +298,8 @@ qlora_status qlora_adapters_plan(const int32_t* index, int64_t M, int32_t count,
  *           without an adapter), or NULL.
  * Limits as for qlora_linear_fwd, r·max(N, K) < 2^30 and M·round_up(3r, 64) < 2^30.
  * An adapter that no token carries is not read.  A NaN or infinity in a
- * token's X reaches no other token's outputs; one in a used adapter may reach
- * tokens of the same batch that do not carry it. */
+ * token's X reaches no other token's outputs, and one in an adapter no token's
+ * that does not carry it. */
 qlora_status qlora_adapters_fwd(const qlora_nf4_t* W, const void* X, int64_t M,
                                 const qlora_adapters_t* adapters, const void* plan,
                                 size_t plan_bytes, void* Y, qlora_dtype y_dtype,

@@ -140,6 +140,23 @@ __device__ __forceinline__ f32x4_t mfma16(const u32x4_t a, const u32x4_t b, f32x
     return mfma_16x16x32(a, b, c);
   }
 }
+// d += a·b for the rows of a block that `in` marks (4kq + v: row v of the lane)
+// alone: the others keep their sums whatever a and b hold.
+template <bool F16>
+__device__ __forceinline__ void mfma_rows(const u32x4_t a, const u32x4_t b, f32x4_t& d, const bool (&in)[4]) {
+  const f32x4_t t = mfma16<F16>(a, b, d);
+#pragma unroll
+  for (int v = 0; v < 4; ++v) d[v] = in[v] ? t[v] : d[v];
+}
+// Whether n operands hold a NaN or an infinity: zero times it is NaN, which one
+// matrix instruction per operand finds for all of its values.
+template <bool F16>
+__device__ __forceinline__ bool any_not_finite(const u32x4_t* b, int n) {
+  f32x4_t t = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < n; ++i) t = mfma16<F16>(u32x4_t{0u, 0u, 0u, 0u}, b[i], t);
+  return __builtin_amdgcn_ballot_w64(t[0] != t[0]) != 0;  // (uniform for the compiler too)
+}
 
 // ---------------------------------------------------------------------------
 // Buffer loads: a scalar resource (base, size in bytes) plus a per-lane 32-bit

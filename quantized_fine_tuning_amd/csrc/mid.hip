@@ -56,21 +56,33 @@ struct RowTokens {
   }
 };
 
-// The adapters' share as more reduction stages of `width` columns: the `cols` split
+// The adapters' share as more reduction stages of `width` columns: the split
 // ranks of each used adapter among positions [p0, p0 + rows), one adapter after
-// another (column c belongs to used adapter gfirst + c / cols); `all` columns,
-// this split's stages [first, last).
+// another, `each` columns (`cols` and zeros up to a multiple of 32, so that the
+// 32 columns of one matrix instruction are one adapter's and its result can be
+// kept to that adapter's rows where the adapter holds an infinity or NaN, which
+// times another row's zeros is NaN); `all` columns, this split's stages [first, last).
 struct LoraShare {
-  int gfirst, all, first, last;
+  int gfirst, each, all, first, last;
+  float inv_each;
+  // ((c + 0.5) / each is never nearer than 0.5 / each to a whole number)
+  __device__ __forceinline__ int adapter_of(int c) const { return (int)(((float)c + 0.5f) * inv_each); }
+  // the rows, from p0 on, of the adapter that columns [c, c + 32) belong to
+  __device__ __forceinline__ void rows(const AdapterGemmArgs& ma, int c, int p0, int64_t M, int& lo, int& hi) const {
+    const int g = adapter_of(std::min(c, all - 32));
+    lo = c < all ? ma.start(gfirst + g) - p0 : 0;
+    hi = c < all ? std::min(ma.start(gfirst + g + 1), (int)M) - p0 : 0;
+  }
 };
 __device__ __forceinline__ LoraShare lora_share(const AdapterGemmArgs& ma, int p0, int rows, int64_t M, int sp,
                                                 int splits, int width) {
-  LoraShare s{0, 0, 0, 0};
+  const int each = (ma.cols + 31) & ~31;
+  LoraShare s{0, each, 0, 0, 0, 1.0f / (float)each};
   const int held = std::min(ma.held(), (int)M);
   if (p0 < held) {
     s.gfirst = ma.group(p0);
     const int glast = std::min(ma.group(std::min(p0 + rows, held) - 1), ma.count - 1);
-    s.all = s.gfirst >= 0 && glast >= s.gfirst ? std::min(glast - s.gfirst + 1, rows) * ma.cols : 0;
+    s.all = s.gfirst >= 0 && glast >= s.gfirst ? std::min(glast - s.gfirst + 1, rows) * each : 0;
     const int stages = (s.all + width - 1) / width;
     s.first = split_first(sp, splits, stages);
     s.last = split_first(sp + 1, splits, stages);
@@ -193,21 +205,26 @@ __global__ __launch_bounds__(64 * WV) void mid_fwd_kernel(Nf4View W, const uint1
   const LoraShare L = lora_share(ma, p0, TM, M, sp, splits, 256);
   if (L.first < L.last) {
     const i32x4_t rS = rsrc_words(ma.S, M * ma.C * 2);
-    const float inv_cols = 1.0f / (float)ma.cols;
-    // (c + 0.5) / cols is never nearer than 0.5 / cols to a whole number
-    auto adapter_of = [&](int c) __attribute__((always_inline)) { return (int)(((float)c + 0.5f) * inv_cols); };
     for (int ls = L.first; ls < L.last; ++ls) {
+      // matrix instruction t: columns [32t, +32) of the stage, 8 per lane
       int id[8], at[8], lo[XI], hi[XI], col[XI];
+      auto piece = [&](int t, int& a, int& rank) __attribute__((always_inline)) {
+        const int c = 256 * ls + 32 * t, cc = std::min(c, L.all - 32), g = L.adapter_of(cc), j = cc - g * L.each + 8 * kq;
+        rank = c < L.all && j < ma.cols && row_ok ? j % ma.r : -1;
+        a = ma.id(L.gfirst + g);
+      };
+      auto load_piece = [&](int a, int rank) __attribute__((always_inline)) {
+        const bool ok = rank >= 0 && (unsigned)a < (unsigned)ma.count;
+        const u32x4_t v =
+            *reinterpret_cast<const u32x4_t*>(ma.F + (ok ? ((int64_t)a * N + n0 + lr) * ma.r + rank : 0));
+        return ok ? v : u32x4_t{0u, 0u, 0u, 0u};
+      };
 #pragma unroll
-      for (int t = 0; t < 8; ++t) {
-        const int c = 256 * ls + 64 * kq + 8 * t, cc = std::min(c, L.all - 8), g = adapter_of(cc);
-        at[t] = c < L.all && row_ok ? (cc - g * ma.cols) % ma.r : -1;
-        id[t] = ma.id(L.gfirst + g);
-      }
+      for (int t = 0; t < 8; ++t) piece(t, id[t], at[t]);
 #pragma unroll
       for (int i = 0; i < XI; ++i) {
-        const int c = 256 * ls + 8 * ch[i], cc = std::min(c, L.all - 8), g = adapter_of(cc);
-        col[i] = c < L.all ? cc - g * ma.cols : -1;
+        const int c = 256 * ls + 8 * ch[i], cc = std::min(c, L.all - 8), g = L.adapter_of(cc);
+        col[i] = c < L.all && cc - g * L.each < ma.cols ? cc - g * L.each : -1;
         lo[i] = ma.start(L.gfirst + g) - p0;
         hi[i] = std::min(ma.start(L.gfirst + g + 1), (int)M) - p0;
       }
@@ -221,21 +238,37 @@ __global__ __launch_bounds__(64 * WV) void mid_fwd_kernel(Nf4View W, const uint1
       }
       u32x4_t bf[8];
 #pragma unroll
-      for (int t = 0; t < 8; ++t) {
-        const bool ok = at[t] >= 0 && (unsigned)id[t] < (unsigned)ma.count;
-        bf[t] = *reinterpret_cast<const u32x4_t*>(
-            ma.F + (ok ? ((int64_t)id[t] * N + n0 + lr) * ma.r + at[t] : 0));
-        if (!ok) bf[t] = u32x4_t{0u, 0u, 0u, 0u};
-      }
+      for (int t = 0; t < 8; ++t) bf[t] = load_piece(id[t], at[t]);
       open_stage<0>();
+      const bool apart = any_not_finite<false>(bf, 8);
+      auto operand = [&](int i, int t) __attribute__((always_inline)) {
+        return *reinterpret_cast<const u32x4_t*>(sx[D - 1] + (16 * i + lr) * ROW + (((4 * t + kq) ^ lr) << 4));
+      };
+      if (!apart) {
 #pragma unroll
-      for (int t = 0; t < 8; ++t)
+        for (int t = 0; t < 8; ++t) {
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-          const u32x4_t a = *reinterpret_cast<const u32x4_t*>(sx[D - 1] + (16 * i + lr) * ROW +
-                                                              (((8 * kq + t) ^ lr) << 4));
-          acc[i] = mfma_16x16x32(a, bf[t], acc[i]);
+          for (int i = 0; i < NT; ++i) acc[i] = mfma_16x16x32(operand(i, t), bf[t], acc[i]);
+          if (t % 2) __builtin_amdgcn_sched_barrier(0);  // (not every operand's registers at once)
         }
+      }
+      asm volatile("" ::: "memory");
+      if (apart) {
+#pragma unroll 1
+        for (int t = 0; t < 8; ++t) {
+          int first, end, a, rank;
+          L.rows(ma, 256 * ls + 32 * t, p0, M, first, end);
+          piece(t, a, rank);
+          const u32x4_t f = load_piece(a, rank);
+#pragma unroll
+          for (int i = 0; i < NT; ++i) {
+            bool in[4];
+#pragma unroll
+            for (int v = 0; v < 4; ++v) in[v] = 16 * i + 4 * kq + v >= first && 16 * i + 4 * kq + v < end;
+            mfma_rows<false>(operand(i, t), f, acc[i], in);
+          }
+        }
+      }
     }
   }
 
@@ -362,7 +395,7 @@ __global__ __launch_bounds__(kDxThreads) void mid_dx_kernel(Nf4View W, const uin
   for (int f = 0; f < 2; ++f)
 #pragma unroll
     for (int i = 0; i < NT; ++i) acc[f][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  auto multiply = [&](const char* y, const char* t) __attribute__((always_inline)) {
+  auto multiply = [&](const char* y, const char* t, auto&& add) __attribute__((always_inline)) {
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
       u32x4_t b[2];
@@ -372,13 +405,17 @@ __global__ __launch_bounds__(kDxThreads) void mid_dx_kernel(Nf4View W, const uin
         const u32x2_t h0 = lds_read_tr(t + tswz(row, col)), h1 = lds_read_tr(t + tswz(row + 4, col));
         b[f] = u32x4_t{h0[0], h0[1], h1[0], h1[1]};
       }
+      add(ks, b, [&](int i) __attribute__((always_inline)) {
+        return *reinterpret_cast<const u32x4_t*>(y + (16 * i + lr) * 128 + (((4 * ks + kq) ^ (lr & 7)) << 4));
+      });
+    }
+  };
+  auto all_rows = [&](int, const u32x4_t* w, auto&& y) __attribute__((always_inline)) {
 #pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        const u32x4_t a =
-            *reinterpret_cast<const u32x4_t*>(y + (16 * i + lr) * 128 + (((4 * ks + kq) ^ (lr & 7)) << 4));
+    for (int i = 0; i < NT; ++i) {
+      const u32x4_t a = y(i);
 #pragma unroll
-        for (int f = 0; f < 2; ++f) acc[f][i] = mfma_16x16x32(a, b[f], acc[f][i]);
-      }
+      for (int f = 0; f < 2; ++f) acc[f][i] = mfma_16x16x32(a, w[f], acc[f][i]);
     }
   };
   constexpr int PER = YI + 3;  // copies per wave and stage
@@ -391,25 +428,23 @@ __global__ __launch_bounds__(kDxThreads) void mid_dx_kernel(Nf4View W, const uin
   const LoraShare L = lora_share(ma, p0, TM, M, sp, splits, 64);
   if (L.first < L.last) {
     const i32x4_t rS = rsrc_words(ma.S, M * ma.C * 2);
-    const float inv_cols = 1.0f / (float)ma.cols;
-    auto adapter_of = [&](int c) __attribute__((always_inline)) { return (int)(((float)c + 0.5f) * inv_cols); };
     for (int ls = L.first; ls < L.last; ++ls) {
       if (ls > L.first) open_stage<0>();  // (stage and tile are read)
-      const int c = 64 * ls + 8 * ych, cc = std::min(c, L.all - 8), g = adapter_of(cc);
+      const int c = 64 * ls + 8 * ych, cc = std::min(c, L.all - 8), g = L.adapter_of(cc);
       const int lo = ma.start(L.gfirst + g) - p0, hi = std::min(ma.start(L.gfirst + g + 1), (int)M) - p0;
 #pragma unroll
       for (int i = 0; i < YI; ++i) {
         const int row = 8 * (YI * wave + i) + (lane >> 3);
-        const bool in = c < L.all && row >= lo && row < hi;
+        const bool in = c < L.all && cc - g * L.each < ma.cols && row >= lo && row < hi;
         dma_lds16(rS, sy[2] + (YI * wave + i) * 1024,
-                  in ? (uint32_t)(((p0 + row) * ma.C + cc - g * ma.cols) * 2) : 0x7fffffffu, 0u);
+                  in ? (uint32_t)(((p0 + row) * ma.C + cc - g * L.each) * 2) : 0x7fffffffu, 0u);
       }
       // tile rows 16w + 4i + (lane >> 4), physical chunk lane % 16
       int id[4], at[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int t = 64 * ls + 16 * wave + 4 * i + (lane >> 4), tc = std::min(t, L.all - 1), ga = adapter_of(tc);
-        at[i] = t < L.all ? (tc - ga * ma.cols) % ma.r : -1;
+        const int t = 64 * ls + 16 * wave + 4 * i + (lane >> 4), tc = std::min(t, L.all - 1), ga = L.adapter_of(tc);
+        at[i] = t < L.all && tc - ga * L.each < ma.cols ? (tc - ga * L.each) % ma.r : -1;
         id[i] = ma.id(L.gfirst + ga);
       }
       u32x4_t v[4];
@@ -425,7 +460,24 @@ __global__ __launch_bounds__(kDxThreads) void mid_dx_kernel(Nf4View W, const uin
       for (int i = 0; i < 4; ++i)
         *reinterpret_cast<u32x4_t*>(sw[1] + (16 * wave + 4 * i) * 256 + 16 * lane) = v[i];
       open_stage<0>();
-      multiply(sy[2], sw[1]);
+      multiply(sy[2], sw[1], [&](int ks, const u32x4_t* w, auto&& y) __attribute__((always_inline)) {
+        const bool apart = any_not_finite<false>(w, 2);
+        if (!apart) all_rows(ks, w, y);
+        asm volatile("" ::: "memory");
+        asm volatile("" ::: "memory");
+      if (apart) {
+          int lo, hi;
+          L.rows(ma, 64 * ls + 32 * ks, p0, M, lo, hi);
+#pragma unroll
+          for (int i = 0; i < NT; ++i) {
+            bool in[4];
+#pragma unroll
+            for (int v = 0; v < 4; ++v) in[v] = 16 * i + 4 * kq + v >= lo && 16 * i + 4 * kq + v < hi;
+#pragma unroll
+            for (int f = 0; f < 2; ++f) mfma_rows<false>(y(i), w[f], acc[f][i], in);
+          }
+        }
+      });
     }
   }
 
@@ -438,7 +490,7 @@ __global__ __launch_bounds__(kDxThreads) void mid_dx_kernel(Nf4View W, const uin
     // tile s is written, and every wave has waited for its copies of stage s
     open_stage<PER>();
     issue(b2, s + 2);
-    multiply(sy[b], sw[(s - s0) & 1]);
+    multiply(sy[b], sw[(s - s0) & 1], all_rows);
     wait_vmem_le<PER>();  // this wave's copies of stage s + 1
     asm volatile("" ::: "memory");
     if (s + 1 < s1) decode(sc[b1] + wave * 1536, sw[(s + 1 - s0) & 1], s + 1);

@@ -72,3 +72,38 @@ def test_many_tokens(M, N, K, r, count, kind, out, saved):
     c = Case(M, N, K, r, count, kind)
     _, T = A.check_forward(c, dtype)
     A.check_backward(c, dtype, T if saved else None)
+
+
+@pytest.mark.parametrize("M,N,K,r,count,kind", [
+    (7, 264, 320, 16, 3, "each"),
+    (24, 264, 320, 8, 3, "each"),       # a split rank block of 16 and 16 zeros
+    (32, 8328, 1856, 24, 4, "mixed"),
+    (61, 264, 320, 24, 7, "each"),
+    (64, 520, 1088, 64, 5, "runs"),
+    (200, 264, 320, 16, 5, "each"),
+    (300, 520, 1088, 40, 3, "runs"),
+    (1100, 136, 320, 16, 6, "runs"),
+])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_an_adapters_infinities_stay_its_tokens_own(M, N, K, r, count, kind, out):
+    """One adapter's factors hold NaN and infinities: every token of another
+    one, or of none, has the same bits as without them, and so have the other
+    adapters' gradients."""
+    import torch as t
+    print(f"adapters with infinities {M} x {N} x {K} r={r} count={count} {kind} {out}", flush=True)
+    dtype = t.bfloat16 if out == "bf16" else t.float32
+    c = Case(M, N, K, r, count, kind)
+    bad = int(c.index[M // 2]) if 0 <= c.index[M // 2] < count else 1
+    own = t.from_numpy(np.flatnonzero(c.index == bad)).cuda()
+    rest = t.from_numpy(np.flatnonzero(c.index != bad)).cuda()
+    others = [a for a in range(count) if a != bad]
+    Y, T = c.forward(dtype)
+    want = c.backward(dtype, T)
+    c.A[bad, r - 1, 3:9], c.B[bad, 5, :] = float("inf"), float("nan")
+    c.B[bad, N - 1, 0], c.A[bad, :, K - 1] = float("-inf"), float("nan")
+    bad_Y, bad_T = c.forward(dtype)
+    got = c.backward(dtype, bad_T)
+    assert t.equal(bad_Y[rest], Y[rest]) and t.equal(bad_T[rest], T[rest]) and t.equal(got[0][rest], want[0][rest])
+    for a in others:
+        assert t.equal(got[1][a], want[1][a]) and t.equal(got[2][a], want[2][a])
+    assert len(own) == 0 or (bad_Y[own].isnan().any(1).all() and got[0][own].isnan().any(1).all())
