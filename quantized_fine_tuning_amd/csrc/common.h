@@ -141,12 +141,19 @@ __device__ __forceinline__ f32x4_t mfma16(const u32x4_t a, const u32x4_t b, f32x
   }
 }
 // d += a·b for the rows of a block that `in` marks (4kq + v: row v of the lane)
-// alone: the others keep their sums whatever a and b hold.
-template <bool F16>
+// alone: the others keep their sums whatever a and b hold.  APART: a·b is
+// summed by itself and added (other bits, fewer registers).
+template <bool F16, bool APART>
 __device__ __forceinline__ void mfma_rows(const u32x4_t a, const u32x4_t b, f32x4_t& d, const bool (&in)[4]) {
-  const f32x4_t t = mfma16<F16>(a, b, d);
+  if constexpr (APART) {
+    const f32x4_t t = mfma16<F16>(a, b, f32x4_t{0.f, 0.f, 0.f, 0.f});
 #pragma unroll
-  for (int v = 0; v < 4; ++v) d[v] = in[v] ? t[v] : d[v];
+    for (int v = 0; v < 4; ++v) d[v] += in[v] ? t[v] : 0.f;
+  } else {
+    const f32x4_t t = mfma16<F16>(a, b, d);
+#pragma unroll
+    for (int v = 0; v < 4; ++v) d[v] = in[v] ? t[v] : d[v];
+  }
 }
 // Whether n operands hold a NaN or an infinity: zero times it is NaN, which one
 // matrix instruction per operand finds for all of its values.

@@ -326,10 +326,10 @@ __global__ __launch_bounds__(kThreads, 1) void dx_gemm_kernel(Nf4View W, const u
     };
     // MULTI, a LoRA step of an adapter that has some of the wave's rows: those of
     // other adapters read as zero, but zero times an infinity or NaN is NaN.  A
-    // B tile that holds one is multiplied by lora_step_rows, where rows [lo, hi)
-    // alone take the sums, with the same bits (8 matrix instructions against 64 to find out: 363 us for the whole pass of
-    // 2045 tokens of 40 adapters, r = 64, 8192 x 8192, against 373 always adding by
-    // rows and 355 with neither).
+    // B tile that holds one goes through lora_step_rows, where rows [lo, hi)
+    // alone take the sums (8 matrix instructions against 64 to find out: 361 us
+    // for the whole pass of 2045 tokens of 40 adapters, r = 64, 8192 x 8192,
+    // against 373 always adding by rows and 355 with neither).
     auto not_finite = [&](const char* wb) __attribute__((always_inline)) {
       bool bad = false;
 #pragma unroll
@@ -340,7 +340,7 @@ __global__ __launch_bounds__(kThreads, 1) void dx_gemm_kernel(Nf4View W, const u
       return bad;
     };
     auto lora_step_rows = [&](const char* ya, const char* wb, int lo, int hi) __attribute__((always_inline)) {
-#pragma unroll 1
+#pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
         read_bt(wb, ks, bfr);
 #pragma unroll
@@ -350,7 +350,7 @@ __global__ __launch_bounds__(kThreads, 1) void dx_gemm_kernel(Nf4View W, const u
           for (int v = 0; v < 4; ++v) in[v] = 16 * i + 4 * kq + v >= lo && 16 * i + 4 * kq + v < hi;
           const u32x4_t a = read_a(ya, 8 * ks + i);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) mfma_rows<F16>(a, bfr[j], acc[i][j], in);
+          for (int j = 0; j < 4; ++j) mfma_rows<F16, true>(a, bfr[j], acc[i][j], in);
         }
       }
     };

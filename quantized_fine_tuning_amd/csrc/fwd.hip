@@ -203,31 +203,37 @@ __global__ __launch_bounds__(kThreads, 1) void fwd_gemm_kernel(Nf4View W, const 
     };
     // MULTI, a LoRA step of an adapter that has some of the wave's rows: those of
     // other adapters read as zero, but zero times an infinity or NaN is NaN.  A
-    // B tile that holds one is multiplied by lora_step_rows, where rows [lo, hi)
-    // alone take the sums, with the same bits (8 matrix instructions against 64 to find out: 368 us for 4096 tokens of 8
-    // requests, r = 64, 11008 x 4096, against 382 always adding by rows and 357
-    // with neither).
-    auto not_finite = [&](const char* wb) __attribute__((always_inline)) {
+    // B tile that holds one goes through lora_step_rows, where rows [lo, hi)
+    // alone take the sums (8 matrix instructions against 64 to find out: 362 us
+    // for 4096 tokens of 8 requests, r = 64, 11008 x 4096, against 382 always
+    // adding by rows and 357 with neither).
+    using LdsTile = const __attribute__((address_space(3))) char*;
+    auto read_tile = [&](LdsTile t, int row, int ks) __attribute__((always_inline)) {
+      return *(const __attribute__((address_space(3))) u32x4_t*)(t + xswz(row, 2 * kq + ks));
+    };
+    auto not_finite = [&](LdsTile wb) __attribute__((always_inline)) {
       bool bad = false;
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
-        read_b(wb, ks, bfr);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) bfr[j] = read_tile(wb, brow + 16 * j, ks);
         bad |= any_not_finite<F16>(bfr, 4);
       }
       return bad;
     };
-    auto lora_step_rows = [&](const char* xa, const char* wb, int lo, int hi) __attribute__((always_inline)) {
-#pragma unroll 1
+    auto lora_step_rows = [&](LdsTile xa, LdsTile wb, int lo, int hi) __attribute__((always_inline)) {
+#pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
-        read_b(wb, ks, bfr);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) bfr[j] = read_tile(wb, brow + 16 * j, ks);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           bool in[4];
 #pragma unroll
           for (int v = 0; v < 4; ++v) in[v] = 16 * i + 4 * kq + v >= lo && 16 * i + 4 * kq + v < hi;
-          const u32x4_t a = read_a(xa, 8 * ks + i);
+          const u32x4_t a = read_tile(xa, arow + 16 * i, ks);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) mfma_rows<F16>(a, bfr[j], acc[i][j], in);
+          for (int j = 0; j < 4; ++j) mfma_rows<F16, true>(a, bfr[j], acc[i][j], in);
         }
       }
     };
@@ -256,10 +262,13 @@ __global__ __launch_bounds__(kThreads, 1) void fwd_gemm_kernel(Nf4View W, const 
         p0 = __builtin_amdgcn_readfirstlane(p0);
         p1 = __builtin_amdgcn_readfirstlane(p1);
         const bool some = p0 < 128 * wm + 128 && p1 > 128 * wm, whole = p0 <= 128 * wm && p1 >= 128 * wm + 128;
-        const bool apart = some && !whole && not_finite(sw[s & 1]);
+        const bool apart = some && !whole && not_finite((LdsTile)sw[0] + (s & 1) * sizeof(sw[0]));
         if (some && !apart) mfma_step(sxb(s & 1), sw[s & 1]);
         asm volatile("" ::: "memory");  // (two branches, not one of two arms, whose sums would not stay in place)
-        if (apart) lora_step_rows(sxb(s & 1), sw[s & 1], p0 - 128 * wm, p1 - 128 * wm);
+        if (apart) {
+          const LdsTile xa = s & 1 ? (LdsTile)sx1 : (LdsTile)sx0;
+          lora_step_rows(xa, (LdsTile)sw[0] + (s & 1) * sizeof(sw[0]), p0 - 128 * wm, p1 - 128 * wm);
+        }
         __syncthreads();
       }
     }

@@ -265,7 +265,7 @@ __global__ __launch_bounds__(64 * WV) void mid_fwd_kernel(Nf4View W, const uint1
             bool in[4];
 #pragma unroll
             for (int v = 0; v < 4; ++v) in[v] = 16 * i + 4 * kq + v >= first && 16 * i + 4 * kq + v < end;
-            mfma_rows<false>(operand(i, t), f, acc[i], in);
+            mfma_rows<false, false>(operand(i, t), f, acc[i], in);
           }
         }
       }
@@ -474,7 +474,7 @@ __global__ __launch_bounds__(kDxThreads) void mid_dx_kernel(Nf4View W, const uin
 #pragma unroll
             for (int v = 0; v < 4; ++v) in[v] = 16 * i + 4 * kq + v >= lo && 16 * i + 4 * kq + v < hi;
 #pragma unroll
-            for (int f = 0; f < 2; ++f) mfma_rows<false>(y(i), w[f], acc[f][i], in);
+            for (int f = 0; f < 2; ++f) mfma_rows<false, false>(y(i), w[f], acc[f][i], in);
           }
         }
       });
