@@ -22,12 +22,15 @@
 // for its gradient).  Chunks are those of the tensor's own 16-byte grid, so
 // that rows of any alignment load and store whole chunks except at their two
 // ends.  The entries are wave 0's work, beside the row's loads, so a row
-// costs three barriers.
+// costs three barriers.  (4096 x 32000 bf16, k = 64: 120 us, 4.4 TB/s, a large
+// copy reaching 4.6; 509 x 32003 fp32: 33 us; the loss alone of 1024 x 128000
+// bf16: 48 us.  A row of 32000 bf16 alone takes 8 us: one workgroup's three
+// passes of latency.)
 //
 // Gradient from a saved log-sum-exp: no sums over the row, so rows are cut
 // into parts of 2,048 chunks, a workgroup each.  Its exponent z·c − lse·log2(e)
 // takes both products in two parts: rounded ones would be off by an ulp of
-// z/tau.
+// z/tau.  (777 x 50001 fp16, k = 128: 51 us; the kernel 44, 4.7 TB/s.)
 #include <algorithm>
 
 #include "host.h"
