@@ -338,7 +338,7 @@ qlora_status qlora_adapters_bwd(const qlora_nf4_t* W, const void* X, const void*
  *   dZ         device [M, ldz] in z_dtype, the gradient of Σ_m loss[m], with
  *              zeros in the padding columns; it may be Z itself; NULL: the
  *              loss alone.
- * 1 <= k <= 512, 1 <= V <= ldz < 2^28, 1e-6 <= tau <= 1e6, M·ldz <= 2^40, M < 2^31.
+ * 1 <= k <= 512, 1 <= V <= ldz < 2^28, 1e-6 <= tau <= 1e6, M·ldz <= 2^40, M < 2^22.
  * A token of weight 0 or without entries has loss 0 and a zero gradient
  * whatever its logits are.  A logit of −infinity is a masked column (q = 0);
  * a row whose largest logit is below -1e30 has no columns: loss 0, zero

@@ -536,8 +536,9 @@ qlora_status check_distill(const char* fn, const void* Z, qlora_dtype z_dtype, i
                            const float* weight, const void* dZ) {
   if (!is_float_dtype(z_dtype) || !is_float_dtype(top_dtype))
     return fail(QLORA_ERR_UNSUPPORTED_DTYPE, "%s: z_dtype=%d, top_dtype=%d (F32, BF16 or F16)", fn, z_dtype, top_dtype);
-  if (M < 0 || M >= (int64_t(1) << 31))
-    return fail(QLORA_ERR_INVALID_ARG, "%s: M=%lld outside [0, 2^31)", fn, (long long)M);
+  // (a launch holds fewer than 2^32 threads, up to 1,024 of them per token)
+  if (M < 0 || M >= (int64_t(1) << 22))
+    return fail(QLORA_ERR_INVALID_ARG, "%s: M=%lld outside [0, 2^22)", fn, (long long)M);
   if (V < 1 || ldz < V)
     return fail(QLORA_ERR_INVALID_ARG, "%s: V=%lld, ldz=%lld (1 <= V <= ldz)", fn, (long long)V, (long long)ldz);
   if (ldz >= (int64_t(1) << 28) || (M > 0 && ldz > (int64_t(1) << 40) / M))

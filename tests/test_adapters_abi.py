@@ -137,6 +137,14 @@ def test_distillation_refusals():
     assert bwd(m=0, Z=None, top=None, at=None, lse=None, dZ=None) == q.QLORA_OK
 
 
+def test_distillation_refuses_more_tokens_than_one_launch_holds():
+    for m in (1 << 22, (1 << 31) - 1, 1 << 31):
+        assert q.lib.qlora_distill_fwd(FAKE, q.QLORA_BF16, m, 1, 1, FAKE, q.QLORA_F32, FAKE, 1, 1.0, None, FAKE, None,
+                                       None, None) == INVALID
+        assert q.lib.qlora_distill_bwd(FAKE, q.QLORA_BF16, m, 1, 1, FAKE, q.QLORA_F32, FAKE, 1, 1.0, FAKE, None, FAKE,
+                                       None) == INVALID
+
+
 def test_binding_refuses_wrong_tensors_on_the_host():
     torch = pytest.importorskip("torch")
     bf = torch.bfloat16
