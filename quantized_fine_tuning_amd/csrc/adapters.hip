@@ -444,11 +444,31 @@ __device__ __forceinline__ float wave_sum(float v) {
   for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
   return v;
 }
+// This thread's part of kFewRanks ranks of one token: x·R[j], rows of Kred.
+__device__ __forceinline__ void few_rows(const uint16_t* x_row, const uint16_t* R, int64_t Kred, int tid, float* acc) {
+  constexpr int UN = 3;
+  const rsrc_t rl = make_rsrc(x_row, Kred * 2), rr = make_rsrc(R, (int64_t)kFewRanks * Kred * 2);
+  for (int64_t k0 = 8 * tid; k0 < Kred; k0 += 2048 * UN) {
+    u32x4_t x[UN], w[UN][kFewRanks];
+#pragma unroll
+    for (int u = 0; u < UN; ++u) {
+      const int64_t k = k0 + 2048 * u;
+      const bool in = k < Kred;
+      x[u] = buf_load16(rl, in ? (uint32_t)(k * 2) : 0x7fffffffu, 0u);
+#pragma unroll
+      for (int j = 0; j < kFewRanks; ++j)
+        w[u][j] = buf_load16(rr, in ? (uint32_t)((j * Kred + k) * 2) : 0x7fffffffu, 0u);
+    }
+#pragma unroll
+    for (int u = 0; u < UN; ++u)
+#pragma unroll
+      for (int j = 0; j < kFewRanks; ++j) acc[j] = dot8(x[u], w[u][j], acc[j]);
+  }
+}
 template <bool TOKENS>
 __global__ __launch_bounds__(256) void adapters_few_down_kernel(const uint16_t* __restrict__ L, int64_t M, int64_t Kred,
                                                                 AdapterView ad, PlanView pl, float* __restrict__ T,
                                                                 float* __restrict__ Tt, uint16_t* __restrict__ S) {
-  constexpr int UN = 3;
   __shared__ float s_part[4][kFewRanks];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t pos = blockIdx.x;
@@ -458,26 +478,7 @@ __global__ __launch_bounds__(256) void adapters_few_down_kernel(const uint16_t* 
   const int id = pl.owner[tok];
   const bool has = (unsigned)id < (unsigned)ad.count;
   float acc[kFewRanks] = {};
-  if (has) {
-    const rsrc_t rl = make_rsrc(L + (int64_t)tok * Kred, Kred * 2);
-    const rsrc_t rr = make_rsrc(ad.A + ((int64_t)id * r + j0) * Kred, (int64_t)kFewRanks * Kred * 2);
-    for (int64_t k0 = 8 * tid; k0 < Kred; k0 += 2048 * UN) {
-      u32x4_t x[UN], w[UN][kFewRanks];
-#pragma unroll
-      for (int u = 0; u < UN; ++u) {
-        const int64_t k = k0 + 2048 * u;
-        const bool in = k < Kred;
-        x[u] = buf_load16(rl, in ? (uint32_t)(k * 2) : 0x7fffffffu, 0u);
-#pragma unroll
-        for (int j = 0; j < kFewRanks; ++j)
-          w[u][j] = buf_load16(rr, in ? (uint32_t)((j * Kred + k) * 2) : 0x7fffffffu, 0u);
-      }
-#pragma unroll
-      for (int u = 0; u < UN; ++u)
-#pragma unroll
-        for (int j = 0; j < kFewRanks; ++j) acc[j] = dot8(x[u], w[u][j], acc[j]);
-    }
-  }
+  if (has) few_rows(L + (int64_t)tok * Kred, ad.A + ((int64_t)id * r + j0) * Kred, Kred, tid, acc);
 #pragma unroll
   for (int j = 0; j < kFewRanks; ++j) {
     acc[j] = wave_sum(acc[j]);
@@ -495,6 +496,80 @@ __global__ __launch_bounds__(256) void adapters_few_down_kernel(const uint16_t* 
 #pragma unroll
     for (int i = 0; i < 3; ++i) S[pos * adapter_cols(r) + i * r + j] = v[i];
   }
+}
+
+// Both factors of a backward pass over few tokens, and its unit table, in one
+// launch in place of adapters_down_kernel and adapters_factor_kernel: a workgroup
+// per (position, 8 ranks of U), one per (position, kFewRanks of T; blockIdx.z
+// = 1) and one for the table (blockIdx.x == 0).  U[m][j] = Σ_n dY[m][n]·B_a[n][j]:
+// a thread takes two rows of B_a a step, 16 bytes of each.
+__global__ __launch_bounds__(256) void adapters_few_factors_kernel(const uint16_t* __restrict__ X,
+                                                                   const uint16_t* __restrict__ dY, int64_t M,
+                                                                   int64_t N, int64_t K, AdapterView ad, PlanView pl,
+                                                                   const float* __restrict__ T_in,
+                                                                   uint16_t* __restrict__ ST, uint16_t* __restrict__ SU,
+                                                                   UnitTable ut, int unit, int max_units,
+                                                                   int max_slots) {
+  if (blockIdx.x == 0) {
+    if (blockIdx.y == 0 && blockIdx.z == 0) cut_units(ad, pl, ut, M, unit, max_units, max_slots);
+    return;
+  }
+  __shared__ float s_part[4][8];
+  const bool is_u = blockIdx.z == 0;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = ad.r;
+  const int ranks = is_u ? 8 : kFewRanks, j0 = ranks * (int)blockIdx.y;
+  const int64_t pos = blockIdx.x - 1;
+  if (j0 >= r) return;
+  const int tok = pl.perm[pos];
+  if ((uint32_t)tok >= (uint32_t)M) return;
+  const int id = pl.owner[tok];
+  if ((unsigned)id >= (unsigned)ad.count) return;
+  float acc[8] = {};
+  if (is_u) {
+    constexpr int UN = 4;
+    const rsrc_t rl = make_rsrc(dY + (int64_t)tok * N, N * 2), rr = make_rsrc(ad.B + (int64_t)id * N * r, N * r * 2);
+    for (int64_t n0 = 2 * tid; n0 < N; n0 += 512 * UN) {
+      uint32_t y[UN];
+      u32x4_t w[UN][2];
+#pragma unroll
+      for (int u = 0; u < UN; ++u) {
+        const int64_t n = n0 + 512 * u;  // (N is even)
+        const bool in = n < N;
+        y[u] = buf_load4(rl, in ? (uint32_t)(n * 2) : 0x7fffffffu, 0u);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          w[u][i] = buf_load16(rr, in ? (uint32_t)(((n + i) * r + j0) * 2) : 0x7fffffffu, 0u);
+      }
+#pragma unroll
+      for (int u = 0; u < UN; ++u)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float v = i ? bf16hi(y[u]) : bf16lo(y[u]);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            acc[2 * q] = __builtin_fmaf(v, bf16lo(w[u][i][q]), acc[2 * q]);
+            acc[2 * q + 1] = __builtin_fmaf(v, bf16hi(w[u][i][q]), acc[2 * q + 1]);
+          }
+        }
+    }
+  } else if (!T_in) {
+    few_rows(X + (int64_t)tok * K, ad.A + ((int64_t)id * r + j0) * K, K, tid, acc);
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    acc[j] = wave_sum(acc[j]);
+    if (lane == 0) s_part[wave][j] = acc[j];
+  }
+  __syncthreads();
+  if (tid >= ranks) return;
+  const int j = j0 + tid;
+  const float t = !is_u && T_in ? T_in[(int64_t)tok * r + j]
+                                : ((s_part[0][tid] + s_part[1][tid]) + s_part[2][tid]) + s_part[3][tid];
+  uint16_t* const S = is_u ? SU : ST;
+  uint16_t v[3];
+  split3(__fmul_rn(ad.s[id], t), v);
+#pragma unroll
+  for (int i = 0; i < 3; ++i) S[pos * adapter_cols(r) + i * r + j] = v[i];
 }
 
 // ---------------------------------------------------------------------------
@@ -733,12 +808,19 @@ int64_t gradient_parts(int64_t N, int64_t K, int r) {
 }
 int64_t unit_table_bytes(int64_t units, int count) { return round_up(256 + (units + count) * 16, 256); }
 }  // namespace
+// Whether a backward pass takes its factors from adapters_few_factors_kernel: one
+// launch for two, but a token's 16 bytes of every row of B_a waste more of the
+// lines they come in, and are read by more tokens, the longer the rows are.  (A
+// whole pass, replayed: 61 tokens, r = 8, 4096 x 4096, 31.8 us against 34.7; 64
+// tokens, 11008 x 4096, r = 16, 52.5 against 52.4; r = 32, 70.9 against 55.4.)
+bool few_factors(int64_t M, int r) { return M <= kFewTokens && r <= 16; }
 AdaptersBwdLayout adapters_bwd_layout(int64_t M, int64_t N, int64_t K, int r, int count) {
   AdaptersBwdLayout L{};
   L.splits = M > kMidTokens ? dx_gemm_splits(M, N, K, SIZE_MAX) : M > 0 ? mid_dx_splits(M, N, K) : 1;
   if (M == 0) return L;
-  L.slices_U = down_slices(M, N, r);
-  L.slices_T = down_slices(M, K, r);
+  const bool few = few_factors(M, r);
+  L.slices_U = few ? 0 : down_slices(M, N, r);
+  L.slices_T = few ? 0 : down_slices(M, K, r);
   const int64_t parts = gradient_parts(N, K, r);
   L.unit = (int)std::min<int64_t>(kMaxUnit, round_up((M + parts - 1) / parts, 64));
   L.units = (int)(M / L.unit + std::min<int64_t>(count, M));
@@ -849,14 +931,20 @@ hipError_t launch_adapters_bwd(const Nf4View& W, const uint16_t* X, const uint16
   ut.unit = reinterpret_cast<int4*>(ws + L.off_units + 256);
   ut.of_group = ut.unit + L.units;
   // U, and T unless it was saved
-  float* const PU = P + (T_saved ? 0 : (int64_t)L.slices_T * M * r);
-  const DownJob dt{X, K, ad.A, P, T_saved ? 0 : L.slices_T}, du{dY, N, ad.B, PU, L.slices_U};
-  e = launch_down(dt, du, M, ad, pl, st);
-  if (e != hipSuccess) return e;
-  const FactorJob ft{P, dt.slices, T_saved, nullptr, T}, fu{PU, L.slices_U, nullptr, nullptr, U};
-  adapters_factor_kernel<<<dim3(1 + cdiv(M, 16), cdiv(r, 16), 2), 256, 0, st>>>(ft, fu, M, ad, pl, 1u, ut, L.unit,
-                                                                               L.units, L.slots);
-  e = hipGetLastError();
+  if (L.slices_U == 0) {
+    adapters_few_factors_kernel<<<dim3((unsigned)(M + 1), (unsigned)(r / kFewRanks), 2), 256, 0, st>>>(
+        X, dY, M, N, K, ad, pl, T_saved, T, U, ut, L.unit, L.units, L.slots);
+    e = hipGetLastError();
+  } else {
+    float* const PU = P + (T_saved ? 0 : (int64_t)L.slices_T * M * r);
+    const DownJob dt{X, K, ad.A, P, T_saved ? 0 : L.slices_T}, du{dY, N, ad.B, PU, L.slices_U};
+    e = launch_down(dt, du, M, ad, pl, st);
+    if (e != hipSuccess) return e;
+    const FactorJob ft{P, dt.slices, T_saved, nullptr, T}, fu{PU, L.slices_U, nullptr, nullptr, U};
+    adapters_factor_kernel<<<dim3(1 + cdiv(M, 16), cdiv(r, 16), 2), 256, 0, st>>>(ft, fu, M, ad, pl, 1u, ut, L.unit,
+                                                                                 L.units, L.slots);
+    e = hipGetLastError();
+  }
   if (e != hipSuccess) return e;
   const AdapterGemmArgs ma{pl.head, (int)plan_pad(M), (int)plan_pad(ad.count + 1), U, ad.A, ad.r,
                            (int)adapter_cols(r), ad.count, (dx16 ? 2 : 3) * ad.r};
