@@ -695,16 +695,40 @@ __device__ __forceinline__ void gradient_unit(const GradientJob& J, int64_t c0, 
       }
 }
 
+// Zeros in the same part of an adapter without tokens.
+template <int NJ>
+__device__ __forceinline__ void zero_part(float* out, int64_t cols, int r, int64_t c0, int j0, bool along) {
+  // along: 128 rows c of 4·NJ chunks of 4 ranks; else 16·NJ rows j of 32 chunks of 4 columns
+  const int per = along ? 4 * NJ : 32;
+  for (int i = threadIdx.x; i < 512 * NJ; i += 256) {
+    const int64_t c = c0 + (along ? i / per : 4 * (i % per));
+    const int j = j0 + (along ? 4 * (i % per) : i / per);
+    if (c < cols && j < r)
+      *reinterpret_cast<f32x4_t*>(out + (along ? c * r + j : j * cols + c)) = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  }
+}
+// blockIdx.y: a unit, or from max_units on an adapter, for its zeros (launched
+// so where every adapter is one unit and nothing is left to finish).
 template <int NJ>
 __global__ __launch_bounds__(256) void adapters_gradient_kernel(GradientJob ja, GradientJob jb, unsigned tiles_a,
                                                                 int64_t M, AdapterView ad, PlanView pl, UnitTable ut,
-                                                                float* __restrict__ P, int64_t slot_floats) {
+                                                                int max_units, float* __restrict__ P,
+                                                                int64_t slot_floats) {
   __shared__ __attribute__((aligned(1024))) char sl[kGradRing * 32 * 256];
   __shared__ __attribute__((aligned(1024))) char ss[kGradRing * 4 * (NJ == 4 ? 3 : NJ == 2 ? 2 : 1) * 1024];
   __shared__ int s_tok[kMaxUnit];
+  const int j0 = 16 * NJ * (int)blockIdx.z;
+  if ((int)blockIdx.y >= max_units) {
+    const int64_t a = blockIdx.y - max_units;
+    const int g = pl.slot[a];
+    if (g >= 0 && g < ad.count) return;
+    const bool along = blockIdx.x >= tiles_a;
+    const GradientJob& J = along ? jb : ja;
+    zero_part<NJ>(J.out + a * ad.r * J.cols, J.cols, ad.r, 128 * (int64_t)(blockIdx.x - (along ? tiles_a : 0u)), j0, along);
+    return;
+  }
   if ((int)blockIdx.y >= ut.head[0]) return;
   const int4 u = ut.unit[blockIdx.y];
-  const int j0 = 16 * NJ * (int)blockIdx.z;
   if (blockIdx.x < tiles_a)
     gradient_unit<NJ, false>(ja, 128 * (int64_t)blockIdx.x, j0, u, M, ad, pl, P, slot_floats, sl, ss, s_tok);
   else
@@ -956,15 +980,19 @@ hipError_t launch_adapters_bwd(const Nf4View& W, const uint16_t* X, const uint16
   const GradientJob ja{X, K, U, dA, 0}, jo{dY, N, T, dB, r * K};
   const int nj = rank_blocks(ad.r);
   const unsigned ta = cdiv(K, 128);
-  const dim3 grid(ta + cdiv(N, 128), (unsigned)L.units, cdiv(r, 16 * nj));
+  // up to one unit of tokens no adapter has partial sums to add: its zeros, if it
+  // has no tokens, come with the gradients (61 tokens, 4096 x 4096, r = 8: 31 us
+  // the whole pass with a finishing launch, 28.8 without)
+  const bool finish = M > L.unit;
+  const dim3 grid(ta + cdiv(N, 128), (unsigned)(L.units + (finish ? 0 : ad.count)), cdiv(r, 16 * nj));
   if (nj == 1)
-    adapters_gradient_kernel<1><<<grid, 256, 0, st>>>(ja, jo, ta, M, ad, pl, ut, P, slot);
+    adapters_gradient_kernel<1><<<grid, 256, 0, st>>>(ja, jo, ta, M, ad, pl, ut, L.units, P, slot);
   else if (nj == 2)
-    adapters_gradient_kernel<2><<<grid, 256, 0, st>>>(ja, jo, ta, M, ad, pl, ut, P, slot);
+    adapters_gradient_kernel<2><<<grid, 256, 0, st>>>(ja, jo, ta, M, ad, pl, ut, L.units, P, slot);
   else
-    adapters_gradient_kernel<4><<<grid, 256, 0, st>>>(ja, jo, ta, M, ad, pl, ut, P, slot);
+    adapters_gradient_kernel<4><<<grid, 256, 0, st>>>(ja, jo, ta, M, ad, pl, ut, L.units, P, slot);
   e = hipGetLastError();
-  if (e != hipSuccess) return e;
+  if (e != hipSuccess || !finish) return e;
   adapters_gradient_finish_kernel<<<dim3(std::min(cdiv(slot, 1024), 256u), (unsigned)ad.count), 256, 0, st>>>(
       dA, dB, r * K, r * N, ad.count, pl, ut, P, L.slots);
   return hipGetLastError();
