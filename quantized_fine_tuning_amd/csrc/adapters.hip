@@ -12,6 +12,7 @@
 #include <algorithm>
 
 #include "host.h"
+#include "splitk.h"
 #include "tiling.h"
 
 namespace qnf4 {
@@ -707,19 +708,35 @@ __device__ __forceinline__ void zero_part(float* out, int64_t cols, int r, int64
       *reinterpret_cast<f32x4_t*>(out + (along ? c * r + j : j * cols + c)) = f32x4_t{0.f, 0.f, 0.f, 0.f};
   }
 }
-// blockIdx.y: a unit, or from max_units on an adapter, for its zeros (launched
-// so where every adapter is one unit and nothing is left to finish).
+// blockIdx.y: a unit, or from max_units on an adapter, for its zeros, and then a
+// part of the sum of dX's split partials (launched so where every adapter is one
+// unit: no partial sums of gradients take the partials' place, and nothing is
+// left to finish).
+struct TailJobs {
+  int adapters;      // whose zeros are looked after: all of them or none
+  const f32x4_t* P;  // dX's partials; n4 = 0: none
+  int splits;
+  int64_t n4;
+  void* out;
+  int out16;
+};
 template <int NJ>
 __global__ __launch_bounds__(256) void adapters_gradient_kernel(GradientJob ja, GradientJob jb, unsigned tiles_a,
                                                                 int64_t M, AdapterView ad, PlanView pl, UnitTable ut,
                                                                 int max_units, float* __restrict__ P,
-                                                                int64_t slot_floats) {
+                                                                int64_t slot_floats, TailJobs tail) {
   __shared__ __attribute__((aligned(1024))) char sl[kGradRing * 32 * 256];
   __shared__ __attribute__((aligned(1024))) char ss[kGradRing * 4 * (NJ == 4 ? 3 : NJ == 2 ? 2 : 1) * 1024];
   __shared__ int s_tok[kMaxUnit];
   const int j0 = 16 * NJ * (int)blockIdx.z;
   if ((int)blockIdx.y >= max_units) {
     const int64_t a = blockIdx.y - max_units;
+    if (a >= tail.adapters) {
+      const int64_t block = ((a - tail.adapters) * gridDim.z + blockIdx.z) * gridDim.x + blockIdx.x;
+      const int64_t i = 256 * block + threadIdx.x;
+      if (i < tail.n4) splitk_sum4<false>(tail.P, tail.splits, tail.n4, i, tail.out, tail.out16);
+      return;
+    }
     const int g = pl.slot[a];
     if (g >= 0 && g < ad.count) return;
     const bool along = blockIdx.x >= tiles_a;
@@ -974,23 +991,27 @@ hipError_t launch_adapters_bwd(const Nf4View& W, const uint16_t* X, const uint16
                            (int)adapter_cols(r), ad.count, (dx16 ? 2 : 3) * ad.r};
   e = M <= kMidTokens ? launch_mid_dx(W, dY, M, ma, dX, dx16, L.splits, P, st)
                       : launch_dx_gemm_adapters(W, dY, M, ma, dX, dx16, L.splits, P, st);
-  if (e == hipSuccess && L.splits > 1) e = launch_splitk_reduce(P, L.splits, M * K, dX, dx16, false, st);
+  // up to one unit of tokens no adapter has partial sums to add: the zeros of
+  // those without tokens, and the sum of dX's splits, come with the gradients
+  // (61 tokens, 4096 x 4096, r = 8: 25.9 us
+  // the whole pass, 31 with launches of their own)
+  const bool finish = M > L.unit, sum = L.splits > 1;
+  if (e == hipSuccess && sum && finish) e = launch_splitk_reduce(P, L.splits, M * K, dX, dx16, false, st);
   if (e != hipSuccess) return e;
   const int64_t slot = r * (K + N);
   const GradientJob ja{X, K, U, dA, 0}, jo{dY, N, T, dB, r * K};
   const int nj = rank_blocks(ad.r);
   const unsigned ta = cdiv(K, 128);
-  // up to one unit of tokens no adapter has partial sums to add: its zeros, if it
-  // has no tokens, come with the gradients (61 tokens, 4096 x 4096, r = 8: 31 us
-  // the whole pass with a finishing launch, 28.8 without)
-  const bool finish = M > L.unit;
-  const dim3 grid(ta + cdiv(N, 128), (unsigned)(L.units + (finish ? 0 : ad.count)), cdiv(r, 16 * nj));
+  const unsigned gx = ta + cdiv(N, 128), gz = cdiv(r, 16 * nj);
+  const TailJobs tail{finish ? 0 : ad.count, reinterpret_cast<const f32x4_t*>(P), L.splits,
+                      sum && !finish ? M * K / 4 : 0, dX, dx16 ? 1 : 0};
+  const dim3 grid(gx, (unsigned)L.units + tail.adapters + cdiv(tail.n4, (int64_t)256 * gx * gz), gz);
   if (nj == 1)
-    adapters_gradient_kernel<1><<<grid, 256, 0, st>>>(ja, jo, ta, M, ad, pl, ut, L.units, P, slot);
+    adapters_gradient_kernel<1><<<grid, 256, 0, st>>>(ja, jo, ta, M, ad, pl, ut, L.units, P, slot, tail);
   else if (nj == 2)
-    adapters_gradient_kernel<2><<<grid, 256, 0, st>>>(ja, jo, ta, M, ad, pl, ut, L.units, P, slot);
+    adapters_gradient_kernel<2><<<grid, 256, 0, st>>>(ja, jo, ta, M, ad, pl, ut, L.units, P, slot, tail);
   else
-    adapters_gradient_kernel<4><<<grid, 256, 0, st>>>(ja, jo, ta, M, ad, pl, ut, L.units, P, slot);
+    adapters_gradient_kernel<4><<<grid, 256, 0, st>>>(ja, jo, ta, M, ad, pl, ut, L.units, P, slot, tail);
   e = hipGetLastError();
   if (e != hipSuccess || !finish) return e;
   adapters_gradient_finish_kernel<<<dim3(std::min(cdiv(slot, 1024), 256u), (unsigned)ad.count), 256, 0, st>>>(

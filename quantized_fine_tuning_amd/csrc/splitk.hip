@@ -4,6 +4,7 @@
 // rounded once to the 16-bit compute format.  Streaming, four outputs per
 // lane and access.
 #include "host.h"
+#include "splitk.h"
 
 namespace qnf4 {
 namespace {
@@ -16,35 +17,8 @@ __global__ __launch_bounds__(kReduceThreads) void splitk_reduce_kernel(const f32
                                                                        int64_t n4, void* __restrict__ out,
                                                                        int out16) {
   const int64_t stride = (int64_t)gridDim.x * kReduceThreads;
-  for (int64_t i = (int64_t)blockIdx.x * kReduceThreads + threadIdx.x; i < n4; i += stride) {
-    f32x4_t a = __builtin_nontemporal_load(P + i);
-    // the loads of four partials are issued before their adds
-    for (int s = 1; s < splits; s += 4) {
-      f32x4_t b[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        // an existing partial whatever q, so that the loads are unconditional
-        const int sq = s + q < splits ? s + q : splits - 1;
-        b[q] = __builtin_nontemporal_load(P + (int64_t)sq * n4 + i);
-      }
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (s + q < splits) {
-          a[0] = a[0] + b[q][0];
-          a[1] = a[1] + b[q][1];
-          a[2] = a[2] + b[q][2];
-          a[3] = a[3] + b[q][3];
-        }
-    }
-    if (out16) {
-      u32x2_t o;
-      o[0] = pack16<F16>(a[0], a[1]);
-      o[1] = pack16<F16>(a[2], a[3]);
-      static_cast<u32x2_t*>(out)[i] = o;
-    } else {
-      static_cast<f32x4_t*>(out)[i] = a;
-    }
-  }
+  for (int64_t i = (int64_t)blockIdx.x * kReduceThreads + threadIdx.x; i < n4; i += stride)
+    splitk_sum4<F16>(P, splits, n4, i, out, out16);
 }
 
 }  // namespace
