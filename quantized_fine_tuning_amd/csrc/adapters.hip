@@ -503,7 +503,8 @@ __global__ __launch_bounds__(256) void adapters_few_down_kernel(const uint16_t* 
 // launch in place of adapters_down_kernel and adapters_factor_kernel: a workgroup
 // per (position, 8 ranks of U), one per (position, kFewRanks of T; blockIdx.z
 // = 1) and one for the table (blockIdx.x == 0).  U[m][j] = Σ_n dY[m][n]·B_a[n][j]:
-// a thread takes two rows of B_a a step, 16 bytes of each.
+// a thread takes two rows of B_a a step, 16 bytes of each.  (61 tokens of 4 adapters,
+// r = 8, 4096 x 4096: 6.0 us, latency, against 5.2 + 4.0 for the two.)
 __global__ __launch_bounds__(256) void adapters_few_factors_kernel(const uint16_t* __restrict__ X,
                                                                    const uint16_t* __restrict__ dY, int64_t M,
                                                                    int64_t N, int64_t K, AdapterView ad, PlanView pl,
