@@ -138,7 +138,8 @@ struct Row {
     }
     return v;
   }
-  // value(z) for chunk i's columns, zeros in the padding (value(−infinity))
+  // value(z) for chunk i's columns, zeros in the padding (not value(−infinity):
+  // a row that is not a number has NaN there)
   template <typename F>
   __device__ __forceinline__ void store(void* dZ, int i, const u32x4_t& v, F&& value) const {
     if (whole(i)) {
@@ -150,7 +151,7 @@ struct Row {
 #pragma unroll
       for (int k = 0; k < C::N; ++k) {
         const int col = i * C::N + k - head;
-        if (col >= 0 && col < ld) store_rounded<ZT>(dZ, row + col, value(C::get(v, k)));
+        if (col >= 0 && col < ld) store_rounded<ZT>(dZ, row + col, col < V ? value(C::get(v, k)) : 0.f);
       }
     }
   }

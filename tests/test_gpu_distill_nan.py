@@ -1,0 +1,76 @@
+"""What is not a number in the distillation loss stays visible: a NaN or an
+infinity among a row's logits, its saved log-sum-exp or its teacher's logits
+gives NaN where the fp64 oracle has it, and nothing elsewhere; other rows stay
+within the bounds of test_gpu_distill."""
+
+import numpy as np
+import pytest
+
+import quantized_fine_tuning_amd as q
+from oracle import distill as ref
+from tests import test_gpu_distill as D
+
+pytestmark = pytest.mark.gpu
+
+NAN, INF = float("nan"), float("inf")
+# one chunk a thread, eight, 1,024 threads, and rows read twice (running sums); each with padding
+LENGTHS = {"bf16": (1001, 1008), "f16": (32003, 32008), "f32": (32003, 32008), "bf16 long": (131077, 131080),
+           "f32 long": (40001, 40004)}
+
+
+def draw(form, k=12, seed=5, M=8):
+    V, ld = LENGTHS[form]
+    z = form.split()[0]
+    Z, T, at, w = D.rows(M, V, ld, k, z, "f32", seed=seed)
+    return Z, T, at, w, V, z
+
+
+def backward(Z, T, at, tau, lse, w, V, in_place=False):
+    import torch as t
+    d = [x.cuda() for x in (Z, T, at, w)]
+    dZ = d[0] if in_place else t.full_like(d[0], 7.0)
+    q.qlora_distill_bwd(d[0], d[1], d[2], tau, lse, d[3], dZ, vocab=V)
+    return dZ
+
+
+def agree(got, want, clean, limits, kind, what):
+    """NaN exactly where the oracle has it; the clean rows within their bounds."""
+    nan = np.isnan(got.double().cpu().numpy())
+    np.testing.assert_array_equal(nan, np.isnan(want), err_msg=what)
+    D.check(got[clean], want[clean], limits, kind, what)
+
+
+def both_passes(Z, T, at, w, V, z, bad, tau=1.25, backward_too=True):
+    with np.errstate(invalid="ignore", divide="ignore"):
+        want = ref.distill(Z.double().numpy(), T.double().numpy(), at.numpy(), tau, w.double().numpy(), V)
+    clean = [m for m in range(len(Z)) if m not in bad]
+    _, lim = D.bounds(Z[clean], T[clean], at[clean], tau, w[clean], V)
+    got = D.call(Z, T, at, tau, w, V)
+    for g, x, limit, kind, what in zip(got, want, lim, ("f32", "f32", z), ("loss", "lse", "dZ")):
+        agree(g, x, clean, limit, kind, what)
+    alone = D.call(Z, T, at, tau, w, V, part="loss")
+    np.testing.assert_array_equal(alone[0].cpu().numpy(), got[0].cpu().numpy())
+    np.testing.assert_array_equal(alone[1].cpu().numpy(), got[1].cpu().numpy())
+    if not backward_too:
+        return
+    lse = got[1].cpu().numpy()
+    with np.errstate(invalid="ignore", divide="ignore"):
+        _, _, dz = ref.distill(Z.double().numpy(), T.double().numpy(), at.numpy(), tau, w.double().numpy(), V, lse)
+    (_, _, _), lim = D.bounds(Z[clean], T[clean], at[clean], tau, w[clean], V, lse[clean])
+    for in_place in (False, True):
+        agree(backward(Z, T, at, tau, got[1], w, V, in_place), dz, clean, lim[2], z, "dZ from lse")
+
+
+@pytest.mark.parametrize("form", LENGTHS)
+def test_padding_is_zero_beside_a_row_that_is_not_a_number(form):
+    import torch as t
+    Z, T, at, w, V, z = draw(form)
+    print(f"distill padding {form}", flush=True)
+    Z[2, 17] = NAN
+    Z[5, V - 1] = INF
+    both_passes(Z, T, at, w, V, z, (2, 5), backward_too=False)
+    lse = t.zeros(8, device="cuda")
+    lse[3] = INF
+    for in_place in (False, True):
+        dZ = backward(Z, T, at, 1.25, lse, w, V, in_place)
+        assert not dZ[:, V:].any()
