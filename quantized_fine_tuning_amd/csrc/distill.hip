@@ -361,7 +361,7 @@ __global__ __launch_bounds__(kPartThreads) void distill_gradient_kernel(DistillA
     if (tid < 64) load_entries<ZT, TT>(s, a, m, R.row, tid);
     __syncthreads();
   }
-  bool live = lse > -INFINITY && w != 0.f;
+  bool live = lse != -INFINITY && w != 0.f;  // (a NaN lse, of a row with a NaN or an infinity, is no masked row's)
   const float g = w * a.tau;
   // lse·log2(e) in two parts
   const float rhi = __fmul_rn(lse, 1.44269502f);

@@ -74,3 +74,13 @@ def test_padding_is_zero_beside_a_row_that_is_not_a_number(form):
     for in_place in (False, True):
         dZ = backward(Z, T, at, 1.25, lse, w, V, in_place)
         assert not dZ[:, V:].any()
+
+
+@pytest.mark.parametrize("form", LENGTHS)
+def test_gradient_from_a_saved_lse_that_is_not_a_number(form):
+    Z, T, at, w, V, z = draw(form)
+    print(f"distill saved lse {form}", flush=True)
+    Z[1, V // 2] = NAN
+    Z[3, 5] = INF
+    Z[6, 0], Z[6, V - 1] = INF, NAN
+    both_passes(Z, T, at, w, V, z, (1, 3, 6))
