@@ -292,8 +292,10 @@ __global__ __launch_bounds__(T, T == 1024 && (ZT != kF32 || VECS == 0) ? 8 : 1) 
   z_max = s_max[0];
 #pragma unroll
   for (int w = 1; w < kWaves; ++w) z_max = fmaxf(z_max, s_max[w]);
-  const bool columns = z_max > kMasked;
-  rc = __fmul_rn(z_max, c);
+  // (maxima pass over NaN: where they say that every column is masked the sum
+  // has the last word, zero for masked columns, NaN where one is NaN)
+  const bool masked = !(z_max > kMasked);
+  rc = masked ? 0.f : __fmul_rn(z_max, c);
   if constexpr (VECS > 0) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) sum = chunk_sum(z[j] = opaque(z[j]), sum);
@@ -307,6 +309,7 @@ __global__ __launch_bounds__(T, T == 1024 && (ZT != kF32 || VECS == 0) ? 8 : 1) 
 #pragma unroll
   for (int w = 1; w < kWaves; ++w) sum += s_sum[w];
   const float w = a.weight ? a.weight[m] : 1.0f;
+  const bool columns = !masked || sum != 0.f;
   const bool live = columns && w != 0.f && s.t_max > -INFINITY;
   if (wave == 0) {
     const float log_sum = logf(sum) - 0.693147182f * __builtin_fmaf(z_max, c, -rc);

@@ -84,3 +84,21 @@ def test_gradient_from_a_saved_lse_that_is_not_a_number(form):
     Z[3, 5] = INF
     Z[6, 0], Z[6, V - 1] = INF, NAN
     both_passes(Z, T, at, w, V, z, (1, 3, 6))
+
+
+@pytest.mark.parametrize("form", [f for f in LENGTHS if "long" not in f])
+def test_a_row_of_nan_alone_is_not_a_masked_row(form):
+    import torch as t
+    Z, T, at, w, V, z = draw(form)
+    print(f"distill rows of NaN {form}", flush=True)
+    Z[0] = NAN
+    Z[2] = -INF                            # masked
+    Z[4] = -INF
+    Z[4, V // 3] = NAN                     # masked but for a NaN
+    Z[6] = t.finfo(Z.dtype).min if z != "f16" else -INF
+    Z[6, 1] = NAN
+    w[7] = 0.0                             # of no weight: nothing whatever it holds
+    Z[7] = NAN
+    got = D.call(Z, T, at, 1.25, w, V)
+    assert got[0][7] == 0 and not got[2][7].any() and got[1][7].isnan()
+    both_passes(Z[:7], T[:7], at[:7], w[:7], V, z, (0, 4, 6))
