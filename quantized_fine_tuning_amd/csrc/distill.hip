@@ -263,7 +263,8 @@ __global__ __launch_bounds__(T, T == 1024 && (ZT != kF32 || VECS == 0) ? 8 : 1) 
       z_max = chunk_max(z[j], z_max);
     }
   } else {
-    // running maximum and sum of this thread's chunks
+    // running maximum and sum of this thread's chunks (as long as it has met
+    // masked columns alone, rc is 0 and they add zeros, a NaN itself)
     for (int i0 = tid; i0 < R.chunks; i0 += NV * T) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) z[j] = R.load(i0 + j * T);
@@ -275,14 +276,12 @@ __global__ __launch_bounds__(T, T == 1024 && (ZT != kF32 || VECS == 0) ? 8 : 1) 
       }
       if (high > z_max) {
         const float before = rc;
-        rc = __fmul_rn(high, c);
+        rc = high > kMasked ? __fmul_rn(high, c) : 0.f;
         sum *= z_max > kMasked ? __builtin_amdgcn_exp2f(before - rc) : 0.f;
         z_max = high;
       }
-      if (z_max > kMasked) {
 #pragma unroll
-        for (int j = 0; j < NV; ++j) sum = chunk_sum(opaque(z[j]), sum);
-      }
+      for (int j = 0; j < NV; ++j) sum = chunk_sum(opaque(z[j]), sum);
     }
   }
   const float own_max = z_max, own_rc = rc;

@@ -102,3 +102,21 @@ def test_a_row_of_nan_alone_is_not_a_masked_row(form):
     got = D.call(Z, T, at, 1.25, w, V)
     assert got[0][7] == 0 and not got[2][7].any() and got[1][7].isnan()
     both_passes(Z[:7], T[:7], at[:7], w[:7], V, z, (0, 4, 6))
+
+
+@pytest.mark.parametrize("form", [f for f in LENGTHS if "long" in f])
+def test_nan_stretches_of_long_rows_reach_the_sum(form):
+    """In rows that are read for a running maximum and sum: whole rows, one
+    column, the chunks that a thread meets first or last, or all of its."""
+    Z, T, at, w, V, z = draw(form)
+    print(f"distill NaN stretches {form}", flush=True)
+    per = 4 if z == "f32" else 8           # columns of a 16-byte chunk
+    Z[0] = NAN
+    Z[1, :per] = NAN
+    Z[2, :2 * 1024 * per] = NAN            # every thread's first two chunks
+    Z[3, V - 4 * per:] = NAN
+    Z[4] = -INF                            # masked but for a NaN
+    Z[4, V // 3] = NAN
+    Z[5, :] = -INF                         # masked
+    Z[6, :V - 9] = -INF                    # nine columns left
+    both_passes(Z, T, at, w, V, z, (0, 1, 2, 3, 4))
