@@ -10,7 +10,8 @@ their columns (outside [0, V): no entry):
   dZ[v] = w·tau·(q_v − Σ_{i: c_i = v} p_i)
 
 Zero for a token of weight 0, without entries, or whose largest logit is below
--1e30 (every column masked; its lse is −infinity).
+-1e30 (every column masked; its lse is −infinity).  NaN where the formulas have
+it: a NaN or +infinity among the logits, or among the entries' logits.
 """
 
 from __future__ import annotations
@@ -36,7 +37,7 @@ def distill(Z, top, at, tau, weight=None, vocab=None, lse=None):
         out_lse[m] = high + math.log(math.fsum(np.exp(z - high)))
         use = out_lse[m] if lse is None else float(lse[m])
         entries = [(top[m, i] / tau, int(at[m, i])) for i in range(top.shape[1])
-                   if 0 <= at[m, i] < V and top[m, i] > -math.inf]
+                   if 0 <= at[m, i] < V and top[m, i] != -math.inf]
         if not entries or w == 0.0 or use == -math.inf:
             continue
         t_high = max(t for t, _ in entries)
@@ -45,7 +46,7 @@ def distill(Z, top, at, tau, weight=None, vocab=None, lse=None):
         for t, c in entries:
             log_p = (t - t_high) - t_log  # (not t - (t_high + t_log): the logits may be huge)
             p = math.exp(log_p)
-            if p > 0.0:
+            if p != 0.0:
                 loss[m] += p * (log_p - (z[c] - use))
             dZ[m, c] -= p
         loss[m] *= w * tau * tau

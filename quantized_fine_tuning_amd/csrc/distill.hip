@@ -163,6 +163,7 @@ struct Entries {
   int c[kMaxTop];
   float t[kMaxTop], z[kMaxTop], p[kMaxTop];
   float t_max, t_log;  // maximum of t, log Σ exp(t − t_max)
+  bool any;            // whether there is an entry (one of logit −infinity is none)
 };
 template <int ZT, int TT>
 __device__ __forceinline__ void load_entries(Entries& s, const DistillArgs& a, int64_t m, int64_t row, int lane) {
@@ -180,17 +181,20 @@ __device__ __forceinline__ void entry_softmax(Entries& s, int k, int lane) {
   float t_max = -INFINITY, t_sum = 0.f;
   for (int i = lane; i < k; i += 64) t_max = fmaxf(t_max, s.t[i]);
   t_max = wave_max(t_max);
-  const bool any = t_max > -INFINITY;
+  // (maxima pass over NaN, the sum does not: entries of NaN are entries)
   for (int i = lane; i < k; i += 64) {
-    s.p[i] = any ? expf(s.t[i] - t_max) : 0.f;
+    s.p[i] = s.t[i] != -INFINITY ? expf(s.t[i] - t_max) : 0.f;
     t_sum += s.p[i];
   }
   t_sum = wave_sum(t_sum);
+  const bool any = t_sum != 0.f;
   const float inv = any ? 1.0f / t_sum : 0.f;
-  for (int i = lane; i < k; i += 64) s.p[i] *= inv;
+  for (int i = lane; i < k; i += 64)
+    if (s.t[i] != -INFINITY) s.p[i] *= inv;  // (else 0, beside a NaN too)
   if (lane == 0) {
     s.t_max = t_max;
     s.t_log = any ? logf(t_sum) : 0.f;
+    s.any = any;
   }
 }
 // The teacher's share taken off the columns [v0, v1), once their exponentials
@@ -309,7 +313,7 @@ __global__ __launch_bounds__(T, T == 1024 && (ZT != kF32 || VECS == 0) ? 8 : 1) 
   for (int w = 1; w < kWaves; ++w) sum += s_sum[w];
   const float w = a.weight ? a.weight[m] : 1.0f;
   const bool columns = !masked || sum != 0.f;
-  const bool live = columns && w != 0.f && s.t_max > -INFINITY;
+  const bool live = columns && w != 0.f && s.any;
   if (wave == 0) {
     const float log_sum = logf(sum) - 0.693147182f * __builtin_fmaf(z_max, c, -rc);
     const float lse = columns ? z_max / a.tau + log_sum : -INFINITY;
@@ -317,7 +321,7 @@ __global__ __launch_bounds__(T, T == 1024 && (ZT != kF32 || VECS == 0) ? 8 : 1) 
     float loss = 0.f;
     if (live)
       for (int i = lane; i < a.k; i += 64)
-        if (s.p[i] > 0.f) loss += s.p[i] * (s.t[i] - s.t_max - s.t_log - (s.z[i] / a.tau - lse));
+        if (s.p[i] != 0.f) loss += s.p[i] * (s.t[i] - s.t_max - s.t_log - (s.z[i] / a.tau - lse));
     loss = wave_sum(loss);
     if (lane == 0) a.loss[m] = live ? w * a.tau * a.tau * loss : 0.f;
   }
@@ -386,7 +390,7 @@ __global__ __launch_bounds__(kPartThreads) void distill_gradient_kernel(DistillA
     entry_softmax(s, a.k, tid);
   }
   __syncthreads();
-  if (live && !(s.t_max > -INFINITY)) {
+  if (live && !s.any) {
     live = false;
 #pragma unroll
     for (int j = 0; j < kPartVecs; ++j)

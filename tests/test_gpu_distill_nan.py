@@ -120,3 +120,20 @@ def test_nan_stretches_of_long_rows_reach_the_sum(form):
     Z[5, :] = -INF                         # masked
     Z[6, :V - 9] = -INF                    # nine columns left
     both_passes(Z, T, at, w, V, z, (0, 1, 2, 3, 4))
+
+
+@pytest.mark.parametrize("form", LENGTHS)
+def test_teacher_logits_that_are_not_numbers(form):
+    Z, T, at, w, V, z = draw(form)
+    print(f"distill teacher {form}", flush=True)
+    T[0, 3] = NAN
+    T[1] = NAN
+    T[2, 0] = INF
+    T[3] = -INF                            # no entries
+    T[4, 1:] = -INF
+    T[4, 0] = NAN
+    T[5, 2], at[5, 2] = NAN, -1            # no entry, whatever its logit is
+    T[6], w[6] = NAN, 0.0
+    both_passes(Z, T, at, w, V, z, (0, 1, 2, 4, 6))
+    got = D.call(Z, T, at, 1.25, w, V)
+    assert got[0][6] == 0 and not got[2][6].any()
