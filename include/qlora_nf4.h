@@ -342,10 +342,11 @@ qlora_status qlora_adapters_bwd(const qlora_nf4_t* W, const void* X, const void*
  * A token of weight 0 or without entries has loss 0 and a zero gradient
  * whatever its logits are.  A logit of −infinity is a masked column (q = 0);
  * a row whose largest logit is below -1e30 has no columns: loss 0, zero
- * gradient, lse −infinity.  An entry of logit −infinity has p = 0.  For any
- * other token NaN stays NaN: a NaN or +infinity among its logits makes loss, lse
- * and its columns of dZ NaN, one among its entries' logits the loss and dZ at the
- * entries' columns. */
+ * gradient, lse −infinity.  An entry of logit −infinity has p = 0.  Entries'
+ * logits may be of any size, a row's largest logit over tau has to be a finite
+ * fp32 number.  For any other token NaN stays NaN: a NaN or +infinity among its
+ * logits makes loss, lse and its columns of dZ NaN, one among its entries' logits
+ * the loss and dZ at the entries' columns. */
 qlora_status qlora_distill_fwd(const void* Z, qlora_dtype z_dtype, int64_t M, int64_t V,
                                int64_t ldz, const void* top, qlora_dtype top_dtype,
                                const int32_t* top_index, int32_t k, float tau,

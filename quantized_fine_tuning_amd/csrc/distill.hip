@@ -157,12 +157,13 @@ struct Row {
   }
 };
 
-// The entries of one row: columns, logits (t/tau), student logits and
-// probabilities, for wave 0 to fill.
+// The entries of one row: columns, logits, student logits and probabilities,
+// for wave 0 to fill.  tau divides differences of logits: a logit's own quotient
+// may pass what fp32 holds.
 struct Entries {
   int c[kMaxTop];
   float t[kMaxTop], z[kMaxTop], p[kMaxTop];
-  float t_max, t_log;  // maximum of t, log Σ exp(t − t_max)
+  float t_max, t_log;  // maximum of t, log Σ exp((t − t_max)/tau)
   bool any;            // whether there is an entry (one of logit −infinity is none)
 };
 template <int ZT, int TT>
@@ -174,16 +175,16 @@ __device__ __forceinline__ void load_entries(Entries& s, const DistillArgs& a, i
     const float z = load_as_f32<ZT>(a.Z, row + (ok ? col : 0));
     s.c[i] = ok ? col : -1;
     s.z[i] = ok ? z : 0.f;
-    s.t[i] = ok ? t / a.tau : -INFINITY;
+    s.t[i] = ok ? t : -INFINITY;
   }
 }
-__device__ __forceinline__ void entry_softmax(Entries& s, int k, int lane) {
+__device__ __forceinline__ void entry_softmax(Entries& s, int k, float tau, int lane) {
   float t_max = -INFINITY, t_sum = 0.f;
   for (int i = lane; i < k; i += 64) t_max = fmaxf(t_max, s.t[i]);
   t_max = wave_max(t_max);
   // (maxima pass over NaN, the sum does not: entries of NaN are entries)
   for (int i = lane; i < k; i += 64) {
-    s.p[i] = s.t[i] != -INFINITY ? expf(s.t[i] - t_max) : 0.f;
+    s.p[i] = s.t[i] != -INFINITY ? expf((s.t[i] - t_max) / tau) : 0.f;
     t_sum += s.p[i];
   }
   t_sum = wave_sum(t_sum);
@@ -239,7 +240,7 @@ __global__ __launch_bounds__(T, T == 1024 && (ZT != kF32 || VECS == 0) ? 8 : 1) 
   }
   if (wave == 0) {
     load_entries<ZT, TT>(s, a, m, R.row, lane);
-    entry_softmax(s, a.k, lane);
+    entry_softmax(s, a.k, a.tau, lane);
   }
 
   // (Each pass widens the 16-bit values anew, from an opaque copy of the chunk:
@@ -321,7 +322,7 @@ __global__ __launch_bounds__(T, T == 1024 && (ZT != kF32 || VECS == 0) ? 8 : 1) 
     float loss = 0.f;
     if (live)
       for (int i = lane; i < a.k; i += 64)
-        if (s.p[i] != 0.f) loss += s.p[i] * (s.t[i] - s.t_max - s.t_log - (s.z[i] / a.tau - lse));
+        if (s.p[i] != 0.f) loss += s.p[i] * ((s.t[i] - s.t_max) / a.tau - s.t_log - (s.z[i] / a.tau - lse));
     loss = wave_sum(loss);
     if (lane == 0) a.loss[m] = live ? w * a.tau * a.tau * loss : 0.f;
   }
@@ -387,7 +388,7 @@ __global__ __launch_bounds__(kPartThreads) void distill_gradient_kernel(DistillA
   // without entries gets its zeros now)
   if (tid < 64) {
     if (!in_place) load_entries<ZT, TT>(s, a, m, R.row, tid);
-    entry_softmax(s, a.k, tid);
+    entry_softmax(s, a.k, a.tau, tid);
   }
   __syncthreads();
   if (live && !s.any) {

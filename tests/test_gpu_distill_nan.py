@@ -137,3 +137,22 @@ def test_teacher_logits_that_are_not_numbers(form):
     both_passes(Z, T, at, w, V, z, (0, 1, 2, 4, 6))
     got = D.call(Z, T, at, 1.25, w, V)
     assert got[0][6] == 0 and not got[2][6].any()
+
+
+@pytest.mark.parametrize("form", ["bf16", "f32 long"])
+@pytest.mark.parametrize("tau", [0.25, 0.01])
+def test_teacher_logits_whose_quotient_by_tau_passes_fp32(form, tau):
+    """Their differences count: equal logits of any size are a uniform teacher,
+    the far ones of a row with both have p = 0."""
+    import torch as t
+    Z, T, at, w, V, z = draw(form, M=4)
+    print(f"distill large teacher {form} tau={tau}", flush=True)
+    high, low = t.finfo(t.float32).max, t.finfo(t.float32).min
+    T[0], T[1] = low, high
+    T[2, ::2], T[2, 1::2] = high, low
+    both_passes(Z, T, at, w, V, z, (), tau=tau)
+    same = T.clone()
+    same[:2] = 0.0
+    same[2, ::2], same[2, 1::2] = 0.0, -INF
+    got, want = D.call(Z, T, at, tau, w, V), D.call(Z, same, at, tau, w, V)
+    assert all(t.equal(a, b) for a, b in zip(got, want))
