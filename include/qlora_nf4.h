@@ -291,7 +291,10 @@ qlora_status qlora_adapters_plan(const int32_t* index, int64_t M, int32_t count,
 /* The linear layer of a batch whose tokens carry different adapters, bf16
  * compute: with a the adapter of token m,
  *   Y[m] = X[m]·Ŵᵀ + s_a·(X[m]·A_aᵀ)·B_aᵀ   (no second term without one),
- * accumulated in fp32 and rounded once.
+ * accumulated in fp32 and rounded once.  s_a·T[m] enters the second product in
+ * fp32 (up to 16 tokens), to 24 bits (an fp32 Y) or, for a bf16 Y of 17 tokens and
+ * more, to 16 bits: off by 2^-16 of each |s_a·T[m][j]·B_a[n][j]|.  Where the
+ * terms cancel far below their size, ask for an fp32 Y.
  *   X, Y, y_dtype as in qlora_linear_fwd;
  *   plan    of this M and of the pool's count (qlora_adapters_plan);
  *   T_save  device fp32 [M, r] receiving T[m] = X[m]·A_aᵀ (zeros for a token
