@@ -1,0 +1,87 @@
+"""Rows of the many-adapter layer: what a token's place in the batch may change,
+whom a token's own NaN reaches, and how close a 16-bit output stays to the
+formula where its low-rank terms cancel."""
+
+import numpy as np
+import pytest
+
+import quantized_fine_tuning_amd as q
+from oracle import adapters as ref
+from tests import test_gpu_adapters as A
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("M", [11, 16, 17, 40, 61, 130, 300, 600])
+def test_tokens_in_another_order(M):
+    """The tokens permuted, and the plan made anew.  T depends on a token's own
+    row alone and keeps its bits, and so does Y up to 16 tokens.  Above, which
+    of a split reduction's parts adds an adapter's terms depends on the plan:
+    Y and dX, and the sums over tokens, are within the rounding bounds of the
+    oracle in either order."""
+    import torch as t
+    print(f"adapters permuted M={M}", flush=True)
+    c = A.Case(M, 264, 448, 32, 5, "mixed")
+    Y, T = A.check_forward(c, t.float32)
+    A.check_backward(c, t.float32, T)
+    p = np.random.default_rng(M).permutation(M)
+    c.index = c.index[p]
+    c.host = (c.host[0][p], c.host[1][p]) + c.host[2:]
+    at = t.from_numpy(p).cuda()
+    c.X, c.dY = c.X[at].contiguous(), c.dY[at].contiguous()
+    q.qlora_adapters_plan(t.from_numpy(c.index).cuda(), c.plan)
+    Y2, T2 = A.check_forward(c, t.float32)
+    A.check_backward(c, t.float32, T2)
+    assert t.equal(T2, T[at])
+    if M <= 16:
+        assert t.equal(Y2, Y[at])
+
+
+@pytest.mark.parametrize("M", [5, 16, 17, 33, 64, 65, 300])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_low_rank_terms_that_cancel(M, out):
+    """Two ranks of opposite sign, nearly equal, and inputs of two values a row:
+    an output far below its terms.  Few additions are not of zeros (2 of T and
+    of the base, r·3 of the up-projection, 2u each with u = 2^-24), so what
+    remains is the rounding of s·T or s·U: two bf16 parts, 2^-16 of each
+    |s·T_j·B_nj|, where the output is bf16 and not from the few-token product of
+    fp32 factors (Y up to 16 tokens), three parts, 2^-24, otherwise."""
+    import torch as t
+    print(f"adapters cancelling M={M} {out}", flush=True)
+    dtype = t.bfloat16 if out == "bf16" else t.float32
+    half = 2.0 ** -8 if out == "bf16" else 0.0
+    r, u = 8, 2.0 ** -24
+    c = A.Case(M, 136, 128, r, 2, "each", seed=4)
+    g = np.random.default_rng(M)
+
+    def sparse(shape):
+        x = np.zeros(shape)
+        for row in x:
+            at = g.choice(len(row), 2, replace=False)
+            row[at] = g.standard_normal(2)
+        return t.from_numpy(x).to(t.bfloat16)
+
+    X, dY = sparse((M, 128)), sparse((M, 136))
+    # dense factors in pairs: row 2i + 1 of A is row 2i but for bits near its last, its column of B the negative one
+    Af, Bf = (t.from_numpy(g.standard_normal(s)).to(t.bfloat16) for s in ((2, r, 128), (2, 136, r)))
+    Af[:, 1::2] = (Af[:, 0::2].double() * (1 + 2.0 ** -7)).to(t.bfloat16)
+    Bf[:, :, 1::2] = -Bf[:, :, 0::2]
+    for dst, src in ((c.X, X), (c.dY, dY), (c.A, Af), (c.B, Bf)):
+        dst.copy_(src)
+    s = c.host[4]
+    X, dY, Af, Bf = (x.double().numpy() for x in (X, dY, Af, Bf))
+    Y, _ = c.forward(dtype)
+    dX = c.backward(dtype, None)[0]
+    owner = c.index
+    for got, want, base, factors, split in (
+            (Y, ref.forward(X, c.W, Af, Bf, s, owner)[0], np.abs(X) @ np.abs(c.W).T,
+             [(np.abs(Af[a]) @ np.abs(X[m]), np.abs(Bf[a].T)) for m, a in enumerate(owner)], M > 16),
+            (dX, ref.backward(X, dY, c.W, Af, Bf, s, owner)[0], np.abs(dY) @ np.abs(c.W),
+             [(np.abs(dY[m]) @ np.abs(Bf[a]), np.abs(Af[a])) for m, a in enumerate(owner)], True)):
+        part = 2.0 ** -16 if out == "bf16" and split else u
+        terms = np.stack([s[a] * (f @ other) for (f, other), a in zip(factors, owner)])
+        lim = part * terms + 2 * u * (2 + 2 + 3 * r + 8) * (terms + base)
+        got = got.double().cpu().numpy()
+        far = np.abs(got - want) - lim - half * (np.abs(want) + lim)
+        at = np.unravel_index(np.argmax(far), far.shape)
+        assert far[at] <= 0, f"{got[at]} for {want[at]} at {at}, {far[at]:.3e} past its bound"
