@@ -37,6 +37,28 @@ def test_tokens_in_another_order(M):
         assert t.equal(Y2, Y[at])
 
 
+@pytest.mark.parametrize("M", [17, 24, 61, 64, 100])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_a_tokens_infinities_stay_its_own(M, out):
+    """NaN and infinities in X and dY of two tokens of one adapter: the other
+    tokens' Y, T and dX and the other adapters' gradients keep their bits."""
+    import torch as t
+    print(f"adapters with infinite tokens M={M} {out}", flush=True)
+    dtype = t.bfloat16 if out == "bf16" else t.float32
+    c = A.Case(M, 264, 320, 16, 3, "each")
+    Y, T = c.forward(dtype)
+    want = c.backward(dtype, None)
+    bad = [1, 7]
+    rest = [m for m in range(M) if m not in bad]
+    c.X[1, 3], c.dY[1, 5], c.X[7, 0], c.dY[7, 263] = float("inf"), float("nan"), float("nan"), float("-inf")
+    Y2, T2 = c.forward(dtype)
+    got = c.backward(dtype, None)
+    assert t.equal(Y2[rest], Y[rest]) and t.equal(T2[rest], T[rest]) and t.equal(got[0][rest], want[0][rest])
+    assert not Y2[bad].isfinite().all(1).any() and not got[0][bad].isfinite().all(1).any()
+    for a in (0, 2):
+        assert t.equal(got[1][a], want[1][a]) and t.equal(got[2][a], want[2][a])
+
+
 @pytest.mark.parametrize("M", [5, 16, 17, 33, 64, 65, 300])
 @pytest.mark.parametrize("out", ["bf16", "f32"])
 def test_low_rank_terms_that_cancel(M, out):
