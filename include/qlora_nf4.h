@@ -312,7 +312,8 @@ qlora_status qlora_adapters_fwd(const qlora_nf4_t* W, const void* X, int64_t M,
  *   dX[m] = dY[m]·Ŵ + s_a·U[m]·A_a,
  *   dA_a = s_a·Σ U[m]ᵀ·X[m],  dB_a = s_a·Σ dY[m]ᵀ·T[m]  over the tokens of a.
  *   T_saved  device fp32 [M, r] from qlora_adapters_fwd, or NULL to recompute;
- *   dX       device [M, K], bf16 or fp32 (dx_dtype);
+ *   dX       device [M, K], bf16 or fp32 (dx_dtype); s_a·U[m] enters a bf16 one
+ *            to 16 bits, an fp32 one to 24 (as s_a·T[m] in qlora_adapters_fwd);
  *   dA, dB   device fp32 [count, r, K] and [count, N, r], overwritten: zeros
  *            for an adapter without tokens.
  * Sums over tokens run in a fixed order: equal calls give equal bits. */
