@@ -42,6 +42,7 @@ unsigned cdiv(int64_t a, int64_t b) { return (unsigned)((a + b - 1) / b); }
 // 2,045 of 40 adapters, 12 to 15 for 4,096, once for every layer and both passes.
 // ---------------------------------------------------------------------------
 constexpr int kPlanWaves = 16;
+static_assert(kMaxAdapters <= 64 * kPlanWaves, "a thread per adapter");
 __global__ __launch_bounds__(64 * kPlanWaves) void adapters_plan_kernel(const int32_t* __restrict__ index, int64_t M,
                                                                         int count, PlanView pl) {
   extern __shared__ int32_t hist[];  // [16][count + 1]; column `count`: no adapter
@@ -170,16 +171,6 @@ __device__ __forceinline__ void split3(float v, uint16_t* o) {
     o[i] = (uint16_t)h;
     v = __fsub_rn(v, __uint_as_float(h << 16));
   }
-}
-
-// Opens a ring stage to the workgroup: this wave's copies but the newest N are
-// done, and so are its LDS reads of the stage that is refilled next.
-template <int N>
-__device__ __forceinline__ void open_stage() {
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(0x0070 | (N & 15) | ((N >> 4) << 14));  // vmcnt(N) lgkmcnt(0)
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
 }
 
 // D[p][j] = Σ_k L[token(p)][k]·R_a(j, k) for the positions of one plan tile (up
@@ -439,11 +430,6 @@ __device__ __forceinline__ float dot8(const u32x4_t a, const u32x4_t b, float ac
     acc = __builtin_fmaf(bf16hi(a[i]), bf16hi(b[i]), acc);
   }
   return acc;
-}
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
-  return v;
 }
 // This thread's part of kFewRanks ranks of one token: x·R[j], rows of Kred.
 __device__ __forceinline__ void few_rows(const uint16_t* x_row, const uint16_t* R, int64_t Kred, int tid, float* acc) {

@@ -390,6 +390,7 @@ qlora_status qlora_merge_lora(const qlora_nf4_t* W, const void* A, const void* B
 
 namespace {
 
+static_assert(QLORA_ADAPTERS_MAX == qnf4::kMaxAdapters, "one limit");
 qlora_status check_adapter_shape(const char* fn, int32_t r, int32_t count) {
   if (r < 8 || r > 256 || r % 8 != 0)
     return fail(QLORA_ERR_INVALID_ARG, "%s: r=%d is not a multiple of 8 in [8, 256]", fn, r);

@@ -54,12 +54,6 @@ __device__ __forceinline__ void store_rounded(void* p, int64_t i, float v) {
     static_cast<uint16_t*>(p)[i] = (uint16_t)(pack16<TYPE == kF16>(v, 0.f) & 0xffffu);
 }
 
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
-  return v;
-}
-
 // The elements of one 16-byte chunk.
 template <int TYPE>
 struct Chunk {

@@ -75,16 +75,17 @@ __device__ __forceinline__ int wswz(int row, int chunk) {
   return row * 128 + ((chunk ^ wsw(row)) << 4);
 }
 
-// Lane of a dequantization slice -> (row group rg, column group cg):
-// lane bits 0..5 are cg0, rg0, rg1, cg1, cg2, rg2.  Each half-wave then
-// reads the tables of 4 row groups (32 banks once), and each 8 consecutive
-// lanes store their 16-byte chunks to 8 distinct chunk positions.
 // MULTI's A tile (64 split ranks of 256 columns): the 16-byte chunks of a
 // row XORed by its low bits, so that the 4 rows of a transposing read lie on
 // different banks; byte of column col (a multiple of 4).
 __device__ __forceinline__ int atswz(int row, int col) {
   return row * 512 + (((col >> 3) ^ ((row & 3) << 1)) << 4) + 2 * (col & 7);
 }
+
+// Lane of a dequantization slice -> (row group rg, column group cg):
+// lane bits 0..5 are cg0, rg0, rg1, cg1, cg2, rg2.  Each half-wave then
+// reads the tables of 4 row groups (32 banks once), and each 8 consecutive
+// lanes store their 16-byte chunks to 8 distinct chunk positions.
 __device__ __forceinline__ int dq_rg(int l) { return ((l >> 1) & 3) | ((l >> 3) & 4); }
 __device__ __forceinline__ int dq_cg(int l) { return (l & 1) | ((l >> 2) & 6); }
 

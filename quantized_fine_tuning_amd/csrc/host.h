@@ -208,7 +208,7 @@ hipError_t launch_format_gemv(const uint8_t* codes, const float* absmax, int fmt
                               const uint16_t* X, int64_t M, void* Y, bool y_bf16, hipStream_t st);
 
 // Many adapters beside one weight ----------------------------------------------
-constexpr int kMaxAdapters = 1024;
+constexpr int kMaxAdapters = 1024;  // QLORA_ADAPTERS_MAX
 // A pool of `count` adapters of the same width r: A [count, r, K], B
 // [count, N, r], s [count].
 struct AdapterView {

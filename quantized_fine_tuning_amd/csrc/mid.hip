@@ -18,16 +18,6 @@
 namespace qnf4 {
 namespace {
 
-// Waits for this wave's copies but the newest N and for its LDS reads, then
-// for the workgroup.
-template <int N>
-__device__ __forceinline__ void open_stage() {
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(0x0070 | (N & 15) | ((N >> 4) << 14));  // vmcnt(N) lgkmcnt(0)
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-}
-
 // Output rows of an accumulator tile back to their tokens: lane holds rows
 // 4kq + v of each 16-position tile, one column; the tokens of its rows are
 // loaded at the kernel's start.
@@ -464,8 +454,7 @@ __global__ __launch_bounds__(kDxThreads) void mid_dx_kernel(Nf4View W, const uin
         const bool apart = any_not_finite<false>(w, 2);
         if (!apart) all_rows(ks, w, y);
         asm volatile("" ::: "memory");
-        asm volatile("" ::: "memory");
-      if (apart) {
+        if (apart) {
           int lo, hi;
           L.rows(ma, 64 * ls + 32 * ks, p0, M, lo, hi);
 #pragma unroll
