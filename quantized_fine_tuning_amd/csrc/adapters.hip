@@ -421,7 +421,12 @@ __global__ __launch_bounds__(256) void adapters_factor_kernel(FactorJob t, Facto
 // does not matter to the dequant-GEMV).  (16 tokens and adapters, K = 4096, r =
 // 64: 4.4 us, 2.0 TB/s of 8.5 MB; 53 tokens of 24 adapters, K = 11008, r = 32:
 // 9.2 us, 41 MB at 4.5 TB/s, each adapter read once per token that carries it,
-// mostly from L2.)
+// mostly from L2.)  At 17 to 64 tokens against the tiles of adapters_down_kernel,
+// whole forwards: r = 64, 4096 x 4096, 53 tokens of 8 adapters 26.9 us against 29.4,
+// of as many adapters 40.4 against 47.2; r = 8 23.3 against 26.8; r = 256, of as
+// many adapters 96 against 112.  Where long adapters are shared the tiles are
+// faster (r = 256, 53 tokens of 8 adapters, 44.8 against 35.2; r = 128, K = 11008,
+// 58.4 against 44.5), but how many tokens share one is known on the device alone.
 constexpr int kFewTokens = 64, kFewRanks = 4;
 __device__ __forceinline__ float dot8(const u32x4_t a, const u32x4_t b, float acc) {
 #pragma unroll

@@ -435,6 +435,9 @@ __global__ __launch_bounds__(kThreads, 1) void dx_gemm_kernel(Nf4View W, const u
           __builtin_amdgcn_raw_buffer_store_b16((short)(pack16<F16>(v, 0.0f) & 0xffffu), ry, at, 0, 0);
         });
       } else {
+        // (64-bit addresses: an fp32 output goes past the 2^31 bytes that a buffer's
+        // offsets reach.  One load of the plan a row, in a rolled loop.  4096 tokens without adapters, 11008 x 4096, the
+        // whole pass: 327 us against 319 for a bf16 dX)
         float* const D = static_cast<float*>(dX);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
