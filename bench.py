@@ -613,10 +613,12 @@ def run_merge(torch, q, args):
 
 def run_adapters(torch, q, args):
     """Many adapters on one weight, and the loss that trains them: the 7B gate
-    (11008x4096, r = 64) with 8 adapters over 4096 tokens in uneven runs
-    (forward, backward; the same with one adapter beside it) and 16 tokens of
-    16 adapters; distillation of 4096 x 32000 bf16 logits from 64 teacher
-    logits, loss with gradient.  Mean time of a call among others."""
+    (11008x4096, r = 64) with 8 adapters over 4096 tokens in equal runs
+    (forward with T saved, backward; the same with one adapter beside it) and
+    16 tokens of 16 adapters; distillation of 4096 x 32000 bf16 logits from 64
+    teacher logits, loss with gradient.  Mean time of a call among others, after
+    calls for --settle / 2 seconds: inputs are drawn in between, and the first
+    milliseconds after them run at the clocks of an idle GPU."""
     N, K, r, out = 11008, 4096, 64, {}
     g = torch.Generator(device="cuda").manual_seed(11)
 
@@ -624,8 +626,13 @@ def run_adapters(torch, q, args):
         return (torch.randn(*shape, device="cuda", generator=g) * scale).to(torch.bfloat16)
 
     def timed(fn, n=30):
-        for _ in range(3):
-            fn()
+        end = time.perf_counter() + args.settle / 2
+        while True:
+            for _ in range(3):
+                fn()
+            torch.cuda.synchronize()
+            if time.perf_counter() >= end:
+                break
         a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
         a.record()
         for _ in range(n):
