@@ -369,7 +369,7 @@ __global__ __launch_bounds__(kPartThreads) void distill_gradient_kernel(DistillA
   const float rhi = __fmul_rn(lse, 1.44269502f);
   const float rlo = __builtin_fmaf(lse, 1.92596303e-8f, __builtin_fmaf(lse, 1.44269502f, -rhi));
   auto q = [&](float x) __attribute__((always_inline)) {
-    x = fmaxf(x, kMasked);  // (−infinity·clo might be +infinity)
+    x = x < kMasked ? kMasked : x;  // (−infinity·clo might be +infinity; NaN stays)
     return __builtin_amdgcn_exp2f(__builtin_fmaf(x, chi, -rhi) + __builtin_fmaf(x, clo, -rlo));
   };
   auto grad = [&](float x) __attribute__((always_inline)) { return live ? g * q(x) : 0.f; };

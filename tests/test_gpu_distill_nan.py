@@ -86,6 +86,22 @@ def test_gradient_from_a_saved_lse_that_is_not_a_number(form):
     both_passes(Z, T, at, w, V, z, (1, 3, 6))
 
 
+@pytest.mark.parametrize("form", LENGTHS)
+def test_nan_columns_beside_a_finite_lse(form):
+    """A log-sum-exp that is a number, of another pass over the logits: the NaN
+    columns alone are NaN."""
+    Z, T, at, w, V, z = draw(form)
+    print(f"distill NaN columns {form}", flush=True)
+    lse = D.call(Z, T, at, 1.25, w, V)[1]
+    Z[2, 17], Z[4, V - 1], Z[6, V // 2:] = NAN, NAN, NAN
+    with np.errstate(invalid="ignore"):
+        _, _, want = ref.distill(Z.double().numpy(), T.double().numpy(), at.numpy(), 1.25, w.double().numpy(), V,
+                                 lse.cpu().numpy())
+    for in_place in (False, True):
+        got = backward(Z, T, at, 1.25, lse, w, V, in_place).cpu()
+        np.testing.assert_array_equal(got.isnan().numpy(), np.isnan(want))
+
+
 @pytest.mark.parametrize("form", [f for f in LENGTHS if "long" not in f])
 def test_a_row_of_nan_alone_is_not_a_masked_row(form):
     import torch as t
