@@ -19,9 +19,9 @@
 // once and its gradient written once.  The row stays in registers between
 // the two (VECS 16-byte chunks a thread, the loads of all of them in flight
 // together); a row too long for that is read once for a running maximum and
-// sum (and once more, from the caches, for its gradient).  Chunks are those of the tensor's own 16-byte grid, so
-// that rows of any alignment load and store whole chunks except at their two
-// ends.  The entries are wave 0's work, beside the row's loads, so a row
+// sum (and once more, from the caches, for its gradient).  Chunks are those of
+// the tensor's own 16-byte grid, so that rows of any alignment load and store
+// whole chunks except at their two ends.  The entries are wave 0's work, beside the row's loads, so a row
 // costs three barriers.  (4096 x 32000 bf16, k = 64: 115 us, 4.6 TB/s, a large
 // copy reaching 4.6; 509 x 32003 fp32: 33 us; the loss alone of 1024 x 128000
 // bf16: 48 us.  A row of 32000 bf16 alone takes 8 us: one workgroup's three
@@ -30,8 +30,8 @@
 // Gradient from a saved log-sum-exp: no sums over the row, so rows are cut
 // into parts of 2,048 chunks, a workgroup each.  Its exponent z·c − lse·log2(e)
 // takes both products in two parts: rounded ones would be off by an ulp of
-// z/tau.  (777 x 50001 fp16, k = 128: 43 us alone on
-// the same inputs, 50 on changing ones; the kernel 43, 4.8 TB/s.)
+// z/tau.  (777 x 50001 fp16, k = 128: 44 us on the same inputs over and over,
+// 50 on changing ones; the kernel 43, 4.8 TB/s.)
 #include <algorithm>
 
 #include "host.h"
