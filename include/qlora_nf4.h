@@ -365,6 +365,45 @@ qlora_status qlora_distill_bwd(const void* Z, qlora_dtype z_dtype, int64_t M, in
                                const float* lse, const float* weight, void* dZ,
                                void* stream);
 
+/* Log-probabilities of given tokens: the likelihood that a fine-tuning step
+ * trains, what a server reports beside its tokens, and (its top columns) what
+ * qlora_distill_fwd takes from a teacher.  Per token m, with z its logits over V
+ * columns, q = softmax(z / tau) and t = target[m]:
+ *   logp = log q_t,   entropy = -sum_v q_v log q_v,   lse = log sum_v exp(z_v / tau),
+ *   the k columns of the largest logits in falling order (equal ones by their
+ *   index), with their log q,
+ *   dZ[v] = (g ([v = t] - q_v) - h q_v (log q_v + entropy)) / tau
+ * with g and h the gradients that reach logp[m] and entropy[m].
+ *   Z          device [M, ldz], z_dtype QLORA_F32, QLORA_BF16 or QLORA_F16;
+ *              columns [V, ldz) are padding and not read;
+ *   target     device int32 [M]; a value outside [0, V) is no token: logp 0,
+ *              and g counts as 0;
+ *   logp, lse, entropy  device fp32 [M]; lse and entropy may be NULL;
+ *   top_logp, top_index device fp32 and int32 [M, k]; NULL with k = 0.  A row
+ *              with fewer columns ends in -infinity and -1;
+ *   d_logp, d_entropy   device fp32 [M], g and h; either may be NULL (0);
+ *   dZ         device [M, ldz] in z_dtype, zeros in the padding columns; it may
+ *              be Z itself; NULL: no gradient.
+ * 0 <= k <= 256; M, V, ldz and tau as for qlora_distill_fwd.
+ * A logit of -infinity is a masked column (q = 0); one below -1e30 is never
+ * among the top; a row whose largest logit is below -1e30 has no columns: logp,
+ * entropy and gradient 0, lse -infinity.  A token whose g and h are 0 has a zero
+ * gradient whatever its logits are.  A NaN or +infinity among a row's logits makes
+ * its lse, entropy, gradient and (of a given token) logp NaN; a NaN is never among
+ * the top. */
+#define QLORA_LOGPROBS_MAX_TOP 256
+qlora_status qlora_logprobs_fwd(const void* Z, qlora_dtype z_dtype, int64_t M, int64_t V, int64_t ldz,
+                                const int32_t* target, float tau, float* logp, float* lse,
+                                float* entropy, int32_t k, float* top_logp, int32_t* top_index,
+                                const float* d_logp, const float* d_entropy, void* dZ, void* stream);
+
+/* The gradient alone, from the lse (and, with d_entropy, the entropy) that
+ * qlora_logprobs_fwd saved.  dZ may be Z itself. */
+qlora_status qlora_logprobs_bwd(const void* Z, qlora_dtype z_dtype, int64_t M, int64_t V, int64_t ldz,
+                                const int32_t* target, float tau, const float* lse,
+                                const float* entropy, const float* d_logp, const float* d_entropy,
+                                void* dZ, void* stream);
+
 /* Comparison formats of the frozen weight (a second workload: P4 §三, NF4's
  * fp32 block constants before double quantization; P2 §4.1 and P4 trade-off
  * ②, uniform 4-bit integers against NF4; P3 公式导读 2, absmax INT8).  Each

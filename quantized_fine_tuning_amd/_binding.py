@@ -32,7 +32,7 @@ EXPORTS = ("qlora_nf4_sizes", "qlora_nf4_quantize", "qlora_dequantize", "qlora_l
            "qlora_linear_fwd_ex", "qlora_linear_bwd_ex", "qlora_linear_fwd_noalloc",
            "qlora_bench_mfma_peak", "qlora_bench_copy", "qlora_bench_wall_clock_khz",
            "qlora_adapters_sizes", "qlora_adapters_plan", "qlora_adapters_fwd", "qlora_adapters_bwd",
-           "qlora_distill_fwd", "qlora_distill_bwd")
+           "qlora_distill_fwd", "qlora_distill_bwd", "qlora_logprobs_fwd", "qlora_logprobs_bwd")
 
 QLORA_KERNEL_NONE = 0
 QLORA_KERNEL_FWD_GEMM = 1
@@ -48,6 +48,7 @@ QLORA_FMT_INT8 = 3
 FORMATS = {"nf4": QLORA_FMT_NF4, "int4": QLORA_FMT_INT4, "int8": QLORA_FMT_INT8}
 QLORA_ADAMW_MAX_TENSORS = 8
 QLORA_ADAPTERS_MAX = 1024
+QLORA_LOGPROBS_MAX_TOP = 256
 
 
 class QloraError(RuntimeError):
@@ -151,8 +152,10 @@ def _load():
                                        vp, sz, vp]
     lib.qlora_distill_fwd.argtypes = [vp, i32, i64, i64, i64, vp, i32, vp, i32, f32, vp, vp, vp, vp, vp]
     lib.qlora_distill_bwd.argtypes = [vp, i32, i64, i64, i64, vp, i32, vp, i32, f32, vp, vp, vp, vp]
+    lib.qlora_logprobs_fwd.argtypes = [vp, i32, i64, i64, i64, vp, f32, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp]
+    lib.qlora_logprobs_bwd.argtypes = [vp, i32, i64, i64, i64, vp, f32, vp, vp, vp, vp, vp, vp]
     for name in ("qlora_adapters_sizes", "qlora_adapters_plan", "qlora_adapters_fwd", "qlora_adapters_bwd",
-                 "qlora_distill_fwd", "qlora_distill_bwd"):
+                 "qlora_distill_fwd", "qlora_distill_bwd", "qlora_logprobs_fwd", "qlora_logprobs_bwd"):
         getattr(lib, name).restype = i32
     return lib
 
@@ -656,6 +659,60 @@ def qlora_distill_bwd(Z, top, top_index, tau: float, lse, weight, dZ, vocab=None
     dev, args, w, d = _distill_args(Z, top, top_index, weight, dZ, vocab)
     norm = _address(lse, "lse", (args[2],), (_torch().float32,), dev)
     _check(lib.qlora_distill_bwd(*args, tau, norm, w, d, _launch_stream(stream, dev)))
+
+
+def _logprobs_args(Z, target, d_logp, d_entropy, dZ, vocab):
+    """(device, the C arguments from Z to target, the addresses of the two incoming
+    gradients and of dZ)."""
+    torch = _torch()
+    f32 = (torch.float32,)
+    if Z is None or Z.dim() != 2:
+        raise ValueError("Z must be [M, ldz]")
+    M, ldz = shape = Z.shape
+    dev = Z.get_device()
+    z = _address(Z, "Z", shape, (torch.float32, torch.bfloat16, torch.float16), dev)
+    at = _address(target, "target", (M,), (torch.int32,), dev)
+    g = None if d_logp is None else _address(d_logp, "d_logp", (M,), f32, dev)
+    h = None if d_entropy is None else _address(d_entropy, "d_entropy", (M,), f32, dev)
+    d = None if dZ is None else _address(dZ, "dZ", shape, (Z.dtype,), dev)
+    return dev, (z, _dtype(Z, "Z"), M, ldz if vocab is None else int(vocab), ldz, at), g, h, d
+
+
+def qlora_logprobs_fwd(Z, target, tau: float, logp, lse=None, entropy=None, top_logp=None, top_index=None, d_logp=None,
+                       d_entropy=None, dZ=None, vocab=None, stream=None) -> None:
+    """logp[m] = log softmax(Z / tau)[target[m]] per token (0 for a target that is no
+    column), the log-sum-exp, the entropy, the top_logp.shape[1] most likely
+    columns, and, if dZ is given (it may be Z), the gradient of
+    Σ d_logp·logp + d_entropy·entropy.  vocab: the columns of Z that count (all
+    of them by default)."""
+    torch = _torch()
+    f32 = (torch.float32,)
+    dev, args, g, h, d = _logprobs_args(Z, target, d_logp, d_entropy, dZ, vocab)
+    M = args[2]
+    out = _address(logp, "logp", (M,), f32, dev)
+    norm = None if lse is None else _address(lse, "lse", (M,), f32, dev)
+    ent = None if entropy is None else _address(entropy, "entropy", (M,), f32, dev)
+    k, tl, ti = 0, None, None
+    if top_logp is not None or top_index is not None:
+        if top_logp is None or top_logp.dim() != 2:
+            raise ValueError("top_logp and top_index must be [M, k]")
+        k = top_logp.shape[1]
+        tl = _address(top_logp, "top_logp", (M, k), f32, dev)
+        ti = _address(top_index, "top_index", (M, k), (torch.int32,), dev)
+    _check(lib.qlora_logprobs_fwd(*args, tau, out, norm, ent, k, tl, ti, g, h, d, _launch_stream(stream, dev)))
+
+
+def qlora_logprobs_bwd(Z, target, tau: float, lse, d_logp, dZ, entropy=None, d_entropy=None, vocab=None,
+                       stream=None) -> None:
+    """The gradient alone, from the lse (and, with d_entropy, the entropy) of
+    qlora_logprobs_fwd; dZ may be Z."""
+    f32 = (_torch().float32,)
+    if dZ is None:
+        raise ValueError("dZ is None")
+    dev, args, g, h, d = _logprobs_args(Z, target, d_logp, d_entropy, dZ, vocab)
+    norm = _address(lse, "lse", (args[2],), f32, dev)
+    ent = None if entropy is None else _address(entropy, "entropy", (args[2],), f32, dev)
+    _check(lib.qlora_logprobs_bwd(*args, tau, norm, ent, g, h, d, _launch_stream(stream, dev)))
 
 
 class QTensor:

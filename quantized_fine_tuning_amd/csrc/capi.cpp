@@ -531,12 +531,8 @@ namespace {
 
 bool is_float_dtype(qlora_dtype d) { return d == QLORA_F32 || d == QLORA_BF16 || d == QLORA_F16; }
 
-// Arguments that both passes of the distillation loss share.
-qlora_status check_distill(const char* fn, const void* Z, qlora_dtype z_dtype, int64_t M, int64_t V, int64_t ldz,
-                           const void* top, qlora_dtype top_dtype, const int32_t* top_index, int32_t k, float tau,
-                           const float* weight, const void* dZ) {
-  if (!is_float_dtype(z_dtype) || !is_float_dtype(top_dtype))
-    return fail(QLORA_ERR_UNSUPPORTED_DTYPE, "%s: z_dtype=%d, top_dtype=%d (F32, BF16 or F16)", fn, z_dtype, top_dtype);
+// The shape of a batch of logits, and its temperature.
+qlora_status check_logits(const char* fn, int64_t M, int64_t V, int64_t ldz, float tau) {
   // (a launch holds fewer than 2^32 threads, up to 1,024 of them per token)
   if (M < 0 || M >= (int64_t(1) << 22))
     return fail(QLORA_ERR_INVALID_ARG, "%s: M=%lld outside [0, 2^22)", fn, (long long)M);
@@ -544,8 +540,19 @@ qlora_status check_distill(const char* fn, const void* Z, qlora_dtype z_dtype, i
     return fail(QLORA_ERR_INVALID_ARG, "%s: V=%lld, ldz=%lld (1 <= V <= ldz)", fn, (long long)V, (long long)ldz);
   if (ldz >= (int64_t(1) << 28) || (M > 0 && ldz > (int64_t(1) << 40) / M))
     return fail(QLORA_ERR_INVALID_ARG, "%s: ldz or M*ldz too large", fn);
-  if (k < 1 || k > qnf4::kMaxTop) return fail(QLORA_ERR_INVALID_ARG, "%s: k=%d outside [1, %d]", fn, k, qnf4::kMaxTop);
   if (!(tau >= 1e-6f && tau <= 1e6f)) return fail(QLORA_ERR_INVALID_ARG, "%s: tau=%g outside [1e-6, 1e6]", fn, tau);
+  return QLORA_OK;
+}
+
+// Arguments that both passes of the distillation loss share.
+qlora_status check_distill(const char* fn, const void* Z, qlora_dtype z_dtype, int64_t M, int64_t V, int64_t ldz,
+                           const void* top, qlora_dtype top_dtype, const int32_t* top_index, int32_t k, float tau,
+                           const float* weight, const void* dZ) {
+  if (!is_float_dtype(z_dtype) || !is_float_dtype(top_dtype))
+    return fail(QLORA_ERR_UNSUPPORTED_DTYPE, "%s: z_dtype=%d, top_dtype=%d (F32, BF16 or F16)", fn, z_dtype, top_dtype);
+  const qlora_status st = check_logits(fn, M, V, ldz, tau);
+  if (st != QLORA_OK) return st;
+  if (k < 1 || k > qnf4::kMaxTop) return fail(QLORA_ERR_INVALID_ARG, "%s: k=%d outside [1, %d]", fn, k, qnf4::kMaxTop);
   if (M > 0) {
     CHECK_PTR(Z);
     CHECK_PTR(top);
@@ -582,6 +589,69 @@ qlora_status qlora_distill_bwd(const void* Z, qlora_dtype z_dtype, int64_t M, in
   }
   const qnf4::DistillArgs a{Z, top, top_index, weight, lse, nullptr, nullptr, dZ, M, V, ldz, k, tau};
   return hip_status(fn, qnf4::launch_distill(a, z_dtype, top_dtype, static_cast<hipStream_t>(stream)));
+}
+
+namespace {
+
+// Arguments that both passes of the log-probabilities share.
+qlora_status check_logprobs(const char* fn, const void* Z, qlora_dtype z_dtype, int64_t M, int64_t V, int64_t ldz,
+                            const int32_t* target, float tau, const float* d_logp, const float* d_entropy,
+                            const void* dZ) {
+  if (!is_float_dtype(z_dtype))
+    return fail(QLORA_ERR_UNSUPPORTED_DTYPE, "%s: z_dtype=%d (F32, BF16 or F16)", fn, z_dtype);
+  const qlora_status st = check_logits(fn, M, V, ldz, tau);
+  if (st != QLORA_OK) return st;
+  if (M > 0) {
+    CHECK_PTR(Z);
+    CHECK_PTR(target);
+  }
+  CHECK_OPT_PTR(d_logp);
+  CHECK_OPT_PTR(d_entropy);
+  CHECK_OPT_PTR(dZ);
+  if (M > 0 && dZ != nullptr && d_logp == nullptr && d_entropy == nullptr)
+    return fail(QLORA_ERR_INVALID_ARG, "%s: dZ without d_logp or d_entropy", fn);
+  return QLORA_OK;
+}
+
+}  // namespace
+
+qlora_status qlora_logprobs_fwd(const void* Z, qlora_dtype z_dtype, int64_t M, int64_t V, int64_t ldz,
+                                const int32_t* target, float tau, float* logp, float* lse, float* entropy, int32_t k,
+                                float* top_logp, int32_t* top_index, const float* d_logp, const float* d_entropy,
+                                void* dZ, void* stream) {
+  const char* fn = "qlora_logprobs_fwd";
+  qlora_status st = check_logprobs(fn, Z, z_dtype, M, V, ldz, target, tau, d_logp, d_entropy, dZ);
+  if (st != QLORA_OK) return st;
+  if (k < 0 || k > qnf4::kMaxAlternatives)
+    return fail(QLORA_ERR_INVALID_ARG, "%s: k=%d outside [0, %d]", fn, k, qnf4::kMaxAlternatives);
+  if (M > 0) {
+    CHECK_PTR(logp);
+    if (k > 0) {
+      CHECK_PTR(top_logp);
+      CHECK_PTR(top_index);
+    }
+  }
+  CHECK_OPT_PTR(lse);
+  CHECK_OPT_PTR(entropy);
+  const qnf4::LogprobsArgs a{Z,    target,  dZ ? d_logp : nullptr, dZ ? d_entropy : nullptr, nullptr, nullptr, logp, lse,
+                             entropy, top_logp, top_index,            dZ,                       M,       V,       ldz,  k, tau};
+  return hip_status(fn, qnf4::launch_logprobs(a, z_dtype, static_cast<hipStream_t>(stream)));
+}
+
+qlora_status qlora_logprobs_bwd(const void* Z, qlora_dtype z_dtype, int64_t M, int64_t V, int64_t ldz,
+                                const int32_t* target, float tau, const float* lse, const float* entropy,
+                                const float* d_logp, const float* d_entropy, void* dZ, void* stream) {
+  const char* fn = "qlora_logprobs_bwd";
+  qlora_status st = check_logprobs(fn, Z, z_dtype, M, V, ldz, target, tau, d_logp, d_entropy, dZ);
+  if (st != QLORA_OK) return st;
+  if (M > 0) {
+    CHECK_PTR(lse);
+    CHECK_PTR(dZ);
+    if (d_entropy != nullptr) CHECK_PTR(entropy);
+  }
+  const qnf4::LogprobsArgs a{Z,       target,  d_logp, d_entropy, lse, entropy, nullptr, nullptr,
+                             nullptr, nullptr, nullptr, dZ,       M,   V,       ldz,     0,      tau};
+  return hip_status(fn, qnf4::launch_logprobs(a, z_dtype, static_cast<hipStream_t>(stream)));
 }
 
 namespace {

@@ -331,6 +331,28 @@ struct DistillArgs {
 // z_type, t_type: 0 fp32, 1 bf16, 2 fp16
 hipError_t launch_distill(const DistillArgs& a, int z_type, int t_type, hipStream_t st);
 
+// Log-probabilities of given tokens ----------------------------------------------
+constexpr int kMaxAlternatives = 256;
+struct LogprobsArgs {
+  const void* Z;           // logits [M, ldz]
+  const int32_t* target;   // [M]; outside [0, V): no token
+  const float* d_logp;     // [M] or null (0): the gradient of logp
+  const float* d_entropy;  // [M] or null (0): the gradient of entropy
+  const float* lse_in;     // [M]: the saved log-sum-exp (backward), or null
+  const float* entropy_in; // [M]: the saved entropy (backward with d_entropy), or null
+  float* logp;             // [M] or null
+  float* lse;              // [M] or null
+  float* entropy;          // [M] or null
+  float* top_logp;         // [M, k]
+  int32_t* top_index;      // [M, k]
+  void* dZ;                // [M, ldz] or null
+  int64_t M, V, ldz;
+  int k;                   // 0: no alternatives asked for
+  float tau;
+};
+// z_type: 0 fp32, 1 bf16, 2 fp16
+hipError_t launch_logprobs(const LogprobsArgs& a, int z_type, hipStream_t st);
+
 // Benchmark instrumentation -------------------------------------------------
 constexpr int kPeakWorkgroups = 2048;  // 8 waves per compute unit of an MI355X
 int64_t mfma_peak_flop(int64_t iters);

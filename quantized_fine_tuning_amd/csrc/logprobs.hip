@@ -1,0 +1,419 @@
+// Log-probabilities of given tokens, entropies, the most likely tokens, and
+// their gradient, gfx950.  Per token, with z its logits over V columns and t the
+// given column:
+//   q = softmax(z/tau),  logp = log q_t,  H = −Σ_v q_v·log q_v,
+//   dZ[v] = (g·([v = t] − q_v) − h·q_v·(log q_v + H))/tau
+// for the gradients g of logp and h of H.  A column outside [0, V) is no token:
+// logp 0, and g counts as 0.
+//
+// Masks and NaN are the distillation kernels': a logit of −infinity has q = 0; a
+// row whose largest logit lies below −1e30 has no columns (logp, H and the
+// gradient 0, lse −infinity); NaN passes through maxima unseen and shows in the
+// sums.  A logit below −1e30 is no alternative among the most likely.
+//
+// Everything in fp32, exponents in base 2 with c = log2(e)/tau: x = fma(z, c, −rc)
+// with rc = fl(max·c), S = Σ 2^x, W = Σ x·2^x; then
+//   logp = x_t·ln 2 − ln S,  H = ln S − ln 2·W/S,
+// none of which sees what rc was rounded by (it shifts every x and log2 S alike).
+//
+// Forward, with or without the gradient: one workgroup per token, the row in
+// registers between its passes (or, too long for that, read again from the
+// caches).
+//
+// The k most likely columns, equal logits by their index: every thread's largest
+// logit is known from the maximum, and the k-th largest of those is a bound that
+// at least k columns reach and few more do.  Those go to a list in LDS whose
+// order is then found by counting, so that it does not depend on who came first.
+// Where more reach it than the list holds (a row of equal logits), the k-th
+// largest is found bit by bit, and so is the last index among its equals.
+//
+// Gradient from a saved log-sum-exp (and entropy): no sums over the row, so rows
+// are cut into parts of 2,048 chunks, a workgroup each; log2 q takes z·c −
+// lse·log2(e) in two parts each (rounded ones would be off by an ulp of z/tau).
+#include "host.h"
+#include "rows.h"
+
+namespace qnf4 {
+namespace {
+
+constexpr float kLn2 = 0.693147182f;
+
+// An order of floats as unsigned numbers (−0 and +0 equal; NaN lowest).
+__device__ __forceinline__ uint32_t order_of(float v) {
+  if (v != v) return 0u;
+  const uint32_t u = __float_as_uint(v + 0.f);
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float of_order(uint32_t k) {
+  return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
+}
+// the lowest that is an alternative: the float above kMasked
+constexpr uint32_t kLowest = ~0xf149f2cau + 1u;
+
+constexpr int kCandidates = 2048;
+struct Candidates {
+  uint32_t key[kCandidates];
+  int col[kCandidates];
+  int n;
+  uint32_t bound;
+  int count[16];
+};
+
+// Σ over the workgroup of a per-thread count.
+template <int T>
+__device__ __forceinline__ int block_count(int n, int* s) {
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) n += __shfl_xor(n, o, 64);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = n;
+  __syncthreads();
+  int all = 0;
+#pragma unroll
+  for (int w = 0; w < T / 64; ++w) all += s[w];
+  return all;
+}
+
+// Fills `s` with the k first columns in order, or with all there are if fewer:
+// `each` calls its argument with (order, column) of every column of this thread.
+// BITS: how many of an order's high bits tell values apart.
+template <int T, int BITS, typename Each>
+__device__ __forceinline__ void find_top(Candidates& s, int k, float own_max, Each&& each) {
+  const int tid = threadIdx.x, lane = tid & 63;
+  s.key[tid] = order_of(own_max);
+  if (tid == 0) s.n = 0;
+  __syncthreads();
+  if (tid < 64) {
+    uint32_t own[T / 64], bound = 0u;
+#pragma unroll
+    for (int i = 0; i < T / 64; ++i) own[i] = s.key[lane + 64 * i];
+    for (int b = 31; b >= 32 - BITS; --b) {
+      const uint32_t next = bound | 1u << b;
+      int n = 0;
+#pragma unroll
+      for (int i = 0; i < T / 64; ++i) n += __popcll(__ballot(own[i] >= next));
+      if (n >= k) bound = next;
+    }
+    if (lane == 0) s.bound = bound > kLowest ? bound : kLowest;
+  }
+  __syncthreads();
+  const uint32_t bound = s.bound;
+  auto put = [&](uint32_t key, int col) __attribute__((always_inline)) {
+    const int at = atomicAdd(&s.n, 1);
+    if (at < kCandidates) {
+      s.key[at] = key;
+      s.col[at] = col;
+    }
+  };
+  each([&](uint32_t key, int col) __attribute__((always_inline)) {
+    if (key >= bound) put(key, col);
+  });
+  __syncthreads();
+  if (s.n <= kCandidates) return;
+  // the k-th largest, then the last index of those equal to it that are taken
+  uint32_t kth = 0u;
+  for (int b = 31; b >= 0; --b) {
+    const uint32_t next = kth | 1u << b;
+    int n = 0;
+    each([&](uint32_t key, int) __attribute__((always_inline)) { n += key >= next; });
+    if (block_count<T>(n, s.count) >= k) kth = next;
+  }
+  int n = 0;
+  each([&](uint32_t key, int) __attribute__((always_inline)) { n += key > kth; });
+  const int need = k - block_count<T>(n, s.count);
+  int last = 0;  // the least bound below which `need` of them lie
+  for (int b = 28; b >= 0; --b) {
+    const int next = last | 1 << b;
+    n = 0;
+    each([&](uint32_t key, int col) __attribute__((always_inline)) { n += key == kth && col < next; });
+    if (block_count<T>(n, s.count) < need) last = next;
+  }
+  __syncthreads();
+  if (tid == 0) s.n = 0;
+  __syncthreads();
+  each([&](uint32_t key, int col) __attribute__((always_inline)) {
+    if (key > kth || (key == kth && col <= last)) put(key, col);
+  });
+  __syncthreads();
+}
+
+// VECS > 0: the row's chunks in registers, VECS per thread of T; VECS == 0: any
+// number of chunks, two in flight per thread, read again for every further pass.
+template <int ZT, int T, int VECS>
+__global__ __launch_bounds__(T) void logprobs_kernel(LogprobsArgs a, float c) {
+  using C = Chunk<ZT>;
+  constexpr int kWaves = T / 64;
+  __shared__ float s_max[kWaves], s_sum[kWaves], s_dot[kWaves];
+  __shared__ Candidates s_top;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int64_t m = blockIdx.x;
+  const Row<ZT> R(a.Z, a.dZ, a.M, a.V, a.ldz, m);
+  constexpr int NV = VECS > 0 ? VECS : 2;
+  u32x4_t z[NV];
+  if constexpr (VECS > 0) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) z[j] = R.load(tid + j * T);
+  }
+  const int target = a.target[m];
+  const bool has = target >= 0 && target < R.V;
+  const float zt = load_as_f32<ZT>(a.Z, R.row + (has ? target : 0));
+  const bool want_dot = a.entropy || a.d_entropy;
+
+  auto chunk_max = [&](const u32x4_t& v, float high) __attribute__((always_inline)) {
+#pragma unroll
+    for (int k = 0; k < C::N; k += 2) high = max3(high, C::get(v, k), C::get(v, k + 1));
+    return high;
+  };
+  float rc = 0.f, sum = 0.f, dot = 0.f;
+  auto x = [&](float v) __attribute__((always_inline)) { return __builtin_fmaf(v, c, -rc); };
+  // (a masked column's x is −infinity, which times its 2^x of 0 would be NaN)
+  auto chunk_sum = [&](const u32x4_t& v) __attribute__((always_inline)) {
+    if (want_dot) {
+#pragma unroll
+      for (int k = 0; k < C::N; ++k) {
+        const float xk = x(C::get(v, k)), e = __builtin_amdgcn_exp2f(xk);
+        sum += e;
+        dot = __builtin_fmaf(fmaxf(xk, kMasked), e, dot);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < C::N; ++k) sum += __builtin_amdgcn_exp2f(x(C::get(v, k)));
+    }
+  };
+  // the sums of exponents over `before` as sums over rc
+  auto rescale = [&](bool some, float before) __attribute__((always_inline)) {
+    const float f = some ? __builtin_amdgcn_exp2f(before - rc) : 0.f;
+    if (want_dot) dot = some ? f * __builtin_fmaf(before - rc, sum, dot) : 0.f;
+    sum *= f;
+  };
+  float z_max = -INFINITY;
+  if constexpr (VECS > 0) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      z[j] = R.only_columns(tid + j * T, z[j]);
+      z_max = chunk_max(z[j], z_max);
+    }
+  } else {
+    // running maximum and sums of this thread's chunks
+    for (int i0 = tid; i0 < R.chunks; i0 += NV * T) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) z[j] = R.load(i0 + j * T);
+      float high = z_max;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        z[j] = R.only_columns(i0 + j * T, z[j]);
+        high = chunk_max(z[j], high);
+      }
+      if (high > z_max) {
+        const float before = rc;
+        rc = high > kMasked ? __fmul_rn(high, c) : 0.f;
+        rescale(z_max > kMasked, before);
+        z_max = high;
+      }
+#pragma unroll
+      for (int j = 0; j < NV; ++j) chunk_sum(opaque(z[j]));
+    }
+  }
+  const float own_max = z_max, own_rc = rc;
+  z_max = wave_max(z_max);
+  if (lane == 0) s_max[wave] = z_max;
+  __syncthreads();
+  z_max = s_max[0];
+#pragma unroll
+  for (int w = 1; w < kWaves; ++w) z_max = fmaxf(z_max, s_max[w]);
+  const bool masked = !(z_max > kMasked);
+  rc = masked ? 0.f : __fmul_rn(z_max, c);
+  if constexpr (VECS > 0) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) chunk_sum(z[j] = opaque(z[j]));
+  } else {
+    rescale(own_max > kMasked, own_rc);  // (a NaN among masked columns stays in the sum)
+  }
+  sum = wave_sum(sum);
+  if (want_dot) dot = wave_sum(dot);
+  if (lane == 0) {
+    s_sum[wave] = sum;
+    s_dot[wave] = dot;
+  }
+  __syncthreads();
+  sum = s_sum[0];
+  dot = s_dot[0];
+#pragma unroll
+  for (int w = 1; w < kWaves; ++w) {
+    sum += s_sum[w];
+    dot += s_dot[w];
+  }
+  // (maxima pass over NaN: where they say that every column is masked the sum has
+  // the last word, zero for masked columns, NaN where one is NaN)
+  const bool columns = !masked || sum != 0.f;
+  const float log_sum = logf(sum), inv = 1.0f / sum;
+  const float entropy = columns ? log_sum - kLn2 * (dot * inv) : 0.f;
+  auto log_q = [&](float v) __attribute__((always_inline)) { return __builtin_fmaf(x(v), kLn2, -log_sum); };
+  if (tid == 0) {
+    if (a.logp) a.logp[m] = has && columns ? log_q(zt) : 0.f;
+    if (a.lse) a.lse[m] = columns ? z_max / a.tau + (log_sum - kLn2 * x(z_max)) : -INFINITY;
+    if (a.entropy) a.entropy[m] = entropy;
+  }
+  // f(order, column) for this thread's columns
+  auto each = [&](auto&& f) __attribute__((always_inline)) {
+    auto chunk = [&](int i, const u32x4_t& v) __attribute__((always_inline)) {
+#pragma unroll
+      for (int k = 0; k < C::N; ++k) f(order_of(C::get(v, k)), i * C::N + k - R.head);
+    };
+    if constexpr (VECS > 0) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) chunk(tid + j * T, z[j] = opaque(z[j]));
+    } else {
+      for (int i = tid; i < R.chunks; i += T) chunk(i, R.only_columns(i, R.load(i)));
+    }
+  };
+  if (a.k > 0) {
+    find_top<T, ZT == kF32 ? 32 : ZT == kBf16 ? 16 : 19>(s_top, a.k, own_max, each);
+    const int n = s_top.n;
+    for (int i = tid; i < n; i += T) {
+      const uint32_t key = s_top.key[i];
+      const int col = s_top.col[i];
+      int rank = 0;
+      for (int j = 0; j < n; ++j) {
+        const uint32_t o = s_top.key[j];
+        rank += o > key || (o == key && s_top.col[j] < col);
+      }
+      if (rank < a.k) {
+        a.top_logp[m * a.k + rank] = log_q(of_order(key));
+        a.top_index[m * a.k + rank] = col;
+      }
+    }
+    for (int i = n + tid; i < a.k; i += T) {
+      a.top_logp[m * a.k + i] = -INFINITY;
+      a.top_index[m * a.k + i] = -1;
+    }
+  }
+  if (!a.dZ) return;
+  const float g = (has && a.d_logp ? a.d_logp[m] : 0.f) / a.tau, h = (a.d_entropy ? a.d_entropy[m] : 0.f) / a.tau;
+  const bool live = columns && (g != 0.f || h != 0.f);
+  const float gi = -g * inv, hi = -h * inv;
+  auto grad = [&](float v) __attribute__((always_inline)) {
+    if (!live) return 0.f;
+    const float xv = x(v), e = __builtin_amdgcn_exp2f(xv);
+    if (!want_dot) return gi * e;
+    // (fmaxf: a masked column's log q is −infinity, its q 0; a NaN row is NaN by inv)
+    return e * __builtin_fmaf(hi, fmaxf(__builtin_fmaf(xv, kLn2, -log_sum), kMasked) + entropy, gi);
+  };
+  // the given token's own element once more, by the thread that wrote its chunk
+  auto store = [&](int i, const u32x4_t& v) __attribute__((always_inline)) {
+    R.store(a.dZ, i, v, grad);
+    if (live && has && g != 0.f && (target + R.head) / C::N == i) {
+      const float q = __builtin_amdgcn_exp2f(x(zt)) * inv;
+      const float e = want_dot && q > 0.f ? h * q * (log_q(zt) + entropy) : 0.f;
+      store_rounded<ZT>(a.dZ, R.row + target, g * (1.f - q) - e);
+    }
+  };
+  if constexpr (VECS > 0) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if (tid + j * T < R.chunks) store(tid + j * T, z[j] = opaque(z[j]));
+  } else {
+    for (int i0 = tid; i0 < R.chunks; i0 += NV * T) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) z[j] = R.load(i0 + j * T);
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        if (i0 + j * T < R.chunks) store(i0 + j * T, R.only_columns(i0 + j * T, z[j]));
+    }
+  }
+  for (int i = R.chunks + tid; i < R.chunks_out; i += T)
+    R.store(a.dZ, i, u32x4_t{0u, 0u, 0u, 0u}, [](float) { return 0.f; });
+}
+
+// The gradient of 2,048 chunks of one row from what the forward pass saved.
+constexpr int kPartThreads = 256, kPartVecs = 8, kPart = kPartThreads * kPartVecs;
+template <int ZT>
+__global__ __launch_bounds__(kPartThreads) void logprobs_gradient_kernel(LogprobsArgs a, float chi, float clo) {
+  using C = Chunk<ZT>;
+  const int tid = threadIdx.x;
+  const int64_t m = blockIdx.x;
+  const Row<ZT> R(a.Z, a.dZ, a.M, a.V, a.ldz, m);
+  const int i0 = kPart * (int)blockIdx.y + tid;
+  u32x4_t z[kPartVecs];
+#pragma unroll
+  for (int j = 0; j < kPartVecs; ++j) z[j] = R.load(i0 + j * kPartThreads);
+  const int target = a.target[m];
+  const bool has = target >= 0 && target < R.V;
+  const float lse = a.lse_in[m];
+  const float g = (has && a.d_logp ? a.d_logp[m] : 0.f) / a.tau, h = (a.d_entropy ? a.d_entropy[m] : 0.f) / a.tau;
+  const float entropy = a.d_entropy ? a.entropy_in[m] : 0.f;
+  const bool live = lse != -INFINITY && (g != 0.f || h != 0.f);
+  // lse·log2(e) in two parts
+  const float rhi = __fmul_rn(lse, 1.44269502f);
+  const float rlo = __builtin_fmaf(lse, 1.92596303e-8f, __builtin_fmaf(lse, 1.44269502f, -rhi));
+  auto log2_q = [&](float v) __attribute__((always_inline)) {
+    v = v < kMasked ? kMasked : v;  // (−infinity·clo might be +infinity; NaN stays)
+    return __builtin_fmaf(v, chi, -rhi) + __builtin_fmaf(v, clo, -rlo);
+  };
+  auto value = [&](float v, float own) __attribute__((always_inline)) {
+    const float l = log2_q(v), q = __builtin_amdgcn_exp2f(l);
+    float d = own - g * q;
+    if (h != 0.f) d -= h * q * (__builtin_fmaf(l, kLn2, entropy));
+    return d;
+  };
+  auto grad = [&](float v) __attribute__((always_inline)) { return live ? value(v, 0.f) : 0.f; };
+#pragma unroll
+  for (int j = 0; j < kPartVecs; ++j) {
+    const int i = i0 + j * kPartThreads;
+    if (i >= R.chunks_out) continue;
+    const u32x4_t v = R.only_columns(i, z[j]);
+    R.store(a.dZ, i, v, grad);
+    // the given token's own element once more, by the thread that wrote its chunk
+    if (live && has && (target + R.head) / C::N == i) {
+      float zt = 0.f;
+#pragma unroll
+      for (int k = 0; k < C::N; ++k)
+        if (i * C::N + k - R.head == target) zt = C::get(v, k);
+      store_rounded<ZT>(a.dZ, R.row + target, value(zt, g));
+    }
+  }
+}
+
+template <int ZT>
+void launch(const LogprobsArgs& a, hipStream_t st) {
+  constexpr int N = Chunk<ZT>::N;
+  const double c = 1.4426950408889634 / (double)a.tau;
+  const float chi = (float)c, clo = (float)(c - (double)chi);
+  const unsigned grid = (unsigned)a.M;
+  if (a.lse_in) {
+    const int64_t parts = ((a.ldz + 2 * (N - 1)) / N + kPart - 1) / kPart;  // whatever the row's alignment
+    logprobs_gradient_kernel<ZT><<<dim3(grid, (unsigned)parts), kPartThreads, 0, st>>>(a, chi, clo);
+    return;
+  }
+  const int64_t chunks = (a.V + 2 * (N - 1)) / N;
+  // 512 threads and as few chunks a thread as hold the row; from 4,096 chunks on
+  // 1,024 threads; above 8,192 the running form
+#define QNF4_ROW(T, VECS) logprobs_kernel<ZT, T, VECS><<<grid, T, 0, st>>>(a, chi)
+  if (chunks <= 512)
+    QNF4_ROW(512, 1);
+  else if (chunks <= 1024)
+    QNF4_ROW(512, 2);
+  else if (chunks <= 2048)
+    QNF4_ROW(512, 4);
+  else if (chunks <= 4096)
+    QNF4_ROW(512, 8);
+  else if (chunks <= 8192)
+    QNF4_ROW(1024, 8);
+  else
+    QNF4_ROW(1024, 0);
+#undef QNF4_ROW
+}
+
+}  // namespace
+
+hipError_t launch_logprobs(const LogprobsArgs& a, int z_type, hipStream_t st) {
+  if (a.M == 0) return hipSuccess;
+  if (z_type == kF32)
+    launch<kF32>(a, st);
+  else if (z_type == kBf16)
+    launch<kBf16>(a, st);
+  else
+    launch<kF16>(a, st);
+  return hipGetLastError();
+}
+
+}  // namespace qnf4
