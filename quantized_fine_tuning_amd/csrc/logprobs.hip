@@ -138,12 +138,15 @@ __device__ __forceinline__ void find_top(Candidates& s, int k, float own_max, Ea
 
 // VECS > 0: the row's chunks in registers, VECS per thread of T; VECS == 0: any
 // number of chunks, two in flight per thread, read again for every further pass.
-template <int ZT, int T, int VECS>
-__global__ __launch_bounds__(T) void logprobs_kernel(LogprobsArgs a, float c) {
+// DOT: with W, for the entropy or its gradient; TOP: with the most likely columns.
+// (Registers of one variant would halve the workgroups that the others have
+// resident: 4096 x 32000 bf16 with gradient took 155 us with all in one kernel.)
+template <int ZT, int T, int VECS, bool DOT, bool TOP>
+__global__ __launch_bounds__(T, T == 1024 && (ZT != kF32 || VECS == 0) && !TOP ? 8 : 1) void logprobs_kernel(
+    LogprobsArgs a, float c) {
   using C = Chunk<ZT>;
   constexpr int kWaves = T / 64;
   __shared__ float s_max[kWaves], s_sum[kWaves], s_dot[kWaves];
-  __shared__ Candidates s_top;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t m = blockIdx.x;
   const Row<ZT> R(a.Z, a.dZ, a.M, a.V, a.ldz, m);
@@ -156,7 +159,6 @@ __global__ __launch_bounds__(T) void logprobs_kernel(LogprobsArgs a, float c) {
   const int target = a.target[m];
   const bool has = target >= 0 && target < R.V;
   const float zt = load_as_f32<ZT>(a.Z, R.row + (has ? target : 0));
-  const bool want_dot = a.entropy || a.d_entropy;
 
   auto chunk_max = [&](const u32x4_t& v, float high) __attribute__((always_inline)) {
 #pragma unroll
@@ -167,7 +169,7 @@ __global__ __launch_bounds__(T) void logprobs_kernel(LogprobsArgs a, float c) {
   auto x = [&](float v) __attribute__((always_inline)) { return __builtin_fmaf(v, c, -rc); };
   // (a masked column's x is −infinity, which times its 2^x of 0 would be NaN)
   auto chunk_sum = [&](const u32x4_t& v) __attribute__((always_inline)) {
-    if (want_dot) {
+    if constexpr (DOT) {
 #pragma unroll
       for (int k = 0; k < C::N; ++k) {
         const float xk = x(C::get(v, k)), e = __builtin_amdgcn_exp2f(xk);
@@ -182,7 +184,7 @@ __global__ __launch_bounds__(T) void logprobs_kernel(LogprobsArgs a, float c) {
   // the sums of exponents over `before` as sums over rc
   auto rescale = [&](bool some, float before) __attribute__((always_inline)) {
     const float f = some ? __builtin_amdgcn_exp2f(before - rc) : 0.f;
-    if (want_dot) dot = some ? f * __builtin_fmaf(before - rc, sum, dot) : 0.f;
+    if constexpr (DOT) dot = some ? f * __builtin_fmaf(before - rc, sum, dot) : 0.f;
     sum *= f;
   };
   float z_max = -INFINITY;
@@ -229,18 +231,18 @@ __global__ __launch_bounds__(T) void logprobs_kernel(LogprobsArgs a, float c) {
     rescale(own_max > kMasked, own_rc);  // (a NaN among masked columns stays in the sum)
   }
   sum = wave_sum(sum);
-  if (want_dot) dot = wave_sum(dot);
+  if constexpr (DOT) dot = wave_sum(dot);
   if (lane == 0) {
     s_sum[wave] = sum;
-    s_dot[wave] = dot;
+    if constexpr (DOT) s_dot[wave] = dot;
   }
   __syncthreads();
   sum = s_sum[0];
-  dot = s_dot[0];
+  if constexpr (DOT) dot = s_dot[0];
 #pragma unroll
   for (int w = 1; w < kWaves; ++w) {
     sum += s_sum[w];
-    dot += s_dot[w];
+    if constexpr (DOT) dot += s_dot[w];
   }
   // (maxima pass over NaN: where they say that every column is masked the sum has
   // the last word, zero for masked columns, NaN where one is NaN)
@@ -266,7 +268,8 @@ __global__ __launch_bounds__(T) void logprobs_kernel(LogprobsArgs a, float c) {
       for (int i = tid; i < R.chunks; i += T) chunk(i, R.only_columns(i, R.load(i)));
     }
   };
-  if (a.k > 0) {
+  if constexpr (TOP) {
+    __shared__ Candidates s_top;
     find_top<T, ZT == kF32 ? 32 : ZT == kBf16 ? 16 : 19>(s_top, a.k, own_max, each);
     const int n = s_top.n;
     for (int i = tid; i < n; i += T) {
@@ -294,7 +297,7 @@ __global__ __launch_bounds__(T) void logprobs_kernel(LogprobsArgs a, float c) {
   auto grad = [&](float v) __attribute__((always_inline)) {
     if (!live) return 0.f;
     const float xv = x(v), e = __builtin_amdgcn_exp2f(xv);
-    if (!want_dot) return gi * e;
+    if constexpr (!DOT) return gi * e;
     // (fmaxf: a masked column's log q is −infinity, its q 0; a NaN row is NaN by inv)
     return e * __builtin_fmaf(hi, fmaxf(__builtin_fmaf(xv, kLn2, -log_sum), kMasked) + entropy, gi);
   };
@@ -303,7 +306,7 @@ __global__ __launch_bounds__(T) void logprobs_kernel(LogprobsArgs a, float c) {
     R.store(a.dZ, i, v, grad);
     if (live && has && g != 0.f && (target + R.head) / C::N == i) {
       const float q = __builtin_amdgcn_exp2f(x(zt)) * inv;
-      const float e = want_dot && q > 0.f ? h * q * (log_q(zt) + entropy) : 0.f;
+      const float e = DOT && q > 0.f ? h * q * (log_q(zt) + entropy) : 0.f;
       store_rounded<ZT>(a.dZ, R.row + target, g * (1.f - q) - e);
     }
   };
@@ -387,19 +390,29 @@ void launch(const LogprobsArgs& a, hipStream_t st) {
   const int64_t chunks = (a.V + 2 * (N - 1)) / N;
   // 512 threads and as few chunks a thread as hold the row; from 4,096 chunks on
   // 1,024 threads; above 8,192 the running form
-#define QNF4_ROW(T, VECS) logprobs_kernel<ZT, T, VECS><<<grid, T, 0, st>>>(a, chi)
-  if (chunks <= 512)
-    QNF4_ROW(512, 1);
-  else if (chunks <= 1024)
-    QNF4_ROW(512, 2);
-  else if (chunks <= 2048)
-    QNF4_ROW(512, 4);
-  else if (chunks <= 4096)
-    QNF4_ROW(512, 8);
-  else if (chunks <= 8192)
-    QNF4_ROW(1024, 8);
-  else
-    QNF4_ROW(1024, 0);
+  const bool dot = a.entropy || a.d_entropy, top = a.k > 0;
+#define QNF4_ROW(T, VECS)                                               \
+  if (dot && top)                                                       \
+    logprobs_kernel<ZT, T, VECS, true, true><<<grid, T, 0, st>>>(a, chi);  \
+  else if (dot)                                                         \
+    logprobs_kernel<ZT, T, VECS, true, false><<<grid, T, 0, st>>>(a, chi); \
+  else if (top)                                                         \
+    logprobs_kernel<ZT, T, VECS, false, true><<<grid, T, 0, st>>>(a, chi); \
+  else                                                                  \
+    logprobs_kernel<ZT, T, VECS, false, false><<<grid, T, 0, st>>>(a, chi);
+  if (chunks <= 512) {
+    QNF4_ROW(512, 1)
+  } else if (chunks <= 1024) {
+    QNF4_ROW(512, 2)
+  } else if (chunks <= 2048) {
+    QNF4_ROW(512, 4)
+  } else if (chunks <= 4096) {
+    QNF4_ROW(512, 8)
+  } else if (chunks <= 8192) {
+    QNF4_ROW(1024, 8)
+  } else {
+    QNF4_ROW(1024, 0)
+  }
 #undef QNF4_ROW
 }
 
