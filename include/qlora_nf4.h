@@ -324,6 +324,107 @@ qlora_status qlora_adapters_bwd(const qlora_nf4_t* W, const void* X, const void*
                                 float* dA, float* dB, void* ws, size_t ws_bytes,
                                 void* stream);
 
+/* Dropout of an adapter's input, from a counter-based generator: D(X)_i is X_i
+ * times c where element i of the row-major X is kept and 0 where it is not,
+ * c = 65536 / (65536 - t) with t = round(65536 p) (p is taken in steps of 2^-16).
+ * Element i is kept where its 16 bits are at least t: of the four 32-bit words of
+ * Philox4x32-10 (Salmon, Moraes, Dror and Shaw 2011) for the key `seed` and the
+ * counter (i / 8, offset), low halves first, word (i % 8) / 2, low half for an even
+ * i, high half for an odd one.  The mask is stored nowhere: a backward pass given
+ * the same struct finds the same one.  A layer or step of its own takes a seed or
+ * an offset of its own.  `step` is NULL or a device number (16-byte aligned) that
+ * is added to `offset` when the kernels run: a step captured into a graph draws
+ * another mask in every replay if something raises it between them (after the
+ * backward pass, which has to see the forward pass's).
+ * 0 <= p < 1 - 2^-17; a NULL struct or p = 0: no dropout. */
+typedef struct {
+  float p;
+  uint64_t seed;
+  uint64_t offset;
+  const uint64_t* step;
+} qlora_dropout_t;
+
+/* Byte counts of one call's workspaces, for every M in [0, M_max]. */
+typedef struct {
+  size_t fwd_ws_bytes;
+  size_t bwd_ws_bytes;
+} qlora_block_sizes_t;
+
+/* The linear layer with dropout of the adapter's input, bf16 compute:
+ *   Y = X·Ŵᵀ + s·T·Bᵀ,  T = D(X)·Aᵀ,  s = alpha / r,
+ * accumulated in fp32 and rounded once; the frozen path sees X itself.
+ *   X, A, B, Y, y_dtype as in qlora_linear_fwd; r a multiple of 8, 8 <= r <= 256;
+ *   T_save  device fp32 [M, r] receiving T, or NULL.
+ * s·T enters a bf16 Y of 17 tokens and more to 16 bits and any other to 24, as in
+ * qlora_adapters_fwd.  Limits as there. */
+qlora_status qlora_dropout_linear_sizes(int64_t N, int64_t K, int64_t M_max, int32_t r,
+                                        qlora_block_sizes_t* out);
+qlora_status qlora_dropout_linear_fwd(const qlora_nf4_t* W, const void* X, int64_t M,
+                                      const void* A, const void* B, int32_t r, float alpha,
+                                      const qlora_dropout_t* drop, void* Y, qlora_dtype y_dtype,
+                                      float* T_save, void* ws, size_t ws_bytes, void* stream);
+
+/* Its gradients, the frozen weight excepted: with V = dY·B and keep_i = c or 0,
+ *   dX = dY·Ŵ + s·keep*(V·A),  dA = s·Vᵀ·D(X),  dB = s·dYᵀ·T.
+ *   drop     the forward pass's;
+ *   T_saved  device fp32 [M, r] from the forward pass, or NULL to recompute;
+ *   dX       device [M, K], bf16 or fp32 (dx_dtype); s·V enters a bf16 one to 16
+ *            bits, an fp32 one to 24;
+ *   dA, dB   device fp32 [r, K] and [N, r], overwritten (zeros with M = 0).
+ * Sums over tokens run in a fixed order: equal calls give equal bits. */
+qlora_status qlora_dropout_linear_bwd(const qlora_nf4_t* W, const void* X, const void* dY,
+                                      int64_t M, const void* A, const void* B, int32_t r,
+                                      float alpha, const qlora_dropout_t* drop,
+                                      const float* T_saved, void* dX, qlora_dtype dx_dtype,
+                                      float* dA, float* dB, void* ws, size_t ws_bytes, void* stream);
+
+/* The adapters of a gated block's two layers, bf16, of one rank and alpha:
+ * A_* [r, K], B_* [N, r], r a multiple of 8, 8 <= r <= 256. */
+typedef struct {
+  const void* A_gate;
+  const void* B_gate;
+  const void* A_up;
+  const void* B_up;
+  int32_t r;
+  float alpha;
+} qlora_gated_adapters_t;
+#define QLORA_ACT_SILU 1      /* act(g) = g / (1 + exp(-g)) */
+#define QLORA_ACT_GELU_TANH 2 /* act(g) = g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2 */
+
+/* The gated feed-forward block of two layers [N, K] with one input, bf16 compute:
+ *   G = X·Ŵ_gateᵀ + s·T_gate·B_gateᵀ,  U = X·Ŵ_upᵀ + s·T_up·B_upᵀ,
+ *   H = act(G)*U,  T_* = D(X)·A_*ᵀ,
+ * one D(X) for both adapters; sums and the product in fp32, H rounded once (not
+ * from the rounded G and U).
+ *   gate, up        host structs of the quantized weights, both [N, K];
+ *   drop            NULL or p = 0: no dropout;
+ *   H               device bf16 [M, N];
+ *   G_save, U_save  device bf16 [M, N] receiving G and U rounded, for the backward
+ *                   pass, or both NULL;
+ *   T_save          device fp32 [2, M, r] receiving T_gate and T_up, or NULL.
+ * Limits as for qlora_adapters_fwd; outputs must not alias inputs. */
+qlora_status qlora_gated_sizes(int64_t N, int64_t K, int64_t M_max, int32_t r,
+                               qlora_block_sizes_t* out);
+qlora_status qlora_gated_fwd(const qlora_nf4_t* gate, const qlora_nf4_t* up, const void* X,
+                             int64_t M, const qlora_gated_adapters_t* adapters, int32_t act,
+                             const qlora_dropout_t* drop, void* H, void* G_save, void* U_save,
+                             float* T_save, void* ws, size_t ws_bytes, void* stream);
+
+/* Its gradients.  With G and U as given,
+ *   dG = RNE_bf16(fl32(dH·U·act'(G))),  dU = RNE_bf16(fl32(dH·act(G)))
+ * (the exact values rounded to fp32 and from there to bf16, to the bit for
+ * finite inputs), and from those, with V_gate = dG·B_gate and V_up = dU·B_up,
+ *   dX = dG·Ŵ_gate + dU·Ŵ_up + s·keep*(V_gate·A_gate + V_up·A_up),
+ *   dA_* = s·V_*ᵀ·D(X),  dB_gate = s·dGᵀ·T_gate,  dB_up = s·dUᵀ·T_up;
+ * dX is summed over both layers in fp32 and rounded once.  Everything else as in
+ * qlora_dropout_linear_bwd (T_saved [2, M, r]). */
+qlora_status qlora_gated_bwd(const qlora_nf4_t* gate, const qlora_nf4_t* up, const void* X,
+                             const void* dH, const void* G, const void* U, int64_t M,
+                             const qlora_gated_adapters_t* adapters, int32_t act,
+                             const qlora_dropout_t* drop, const float* T_saved, void* dX,
+                             qlora_dtype dx_dtype, float* dA_gate, float* dB_gate, float* dA_up,
+                             float* dB_up, void* ws, size_t ws_bytes, void* stream);
+
 /* Distillation from a teacher's top logits: the loss that trains the adapters
  * of a quantized model on what the 16-bit model answers, and its gradient.
  * Per token m, with z the student's logits over V columns and t_i the

@@ -32,7 +32,9 @@ EXPORTS = ("qlora_nf4_sizes", "qlora_nf4_quantize", "qlora_dequantize", "qlora_l
            "qlora_linear_fwd_ex", "qlora_linear_bwd_ex", "qlora_linear_fwd_noalloc",
            "qlora_bench_mfma_peak", "qlora_bench_copy", "qlora_bench_wall_clock_khz",
            "qlora_adapters_sizes", "qlora_adapters_plan", "qlora_adapters_fwd", "qlora_adapters_bwd",
-           "qlora_distill_fwd", "qlora_distill_bwd", "qlora_logprobs_fwd", "qlora_logprobs_bwd")
+           "qlora_distill_fwd", "qlora_distill_bwd", "qlora_logprobs_fwd", "qlora_logprobs_bwd",
+           "qlora_dropout_linear_sizes", "qlora_dropout_linear_fwd", "qlora_dropout_linear_bwd",
+           "qlora_gated_sizes", "qlora_gated_fwd", "qlora_gated_bwd")
 
 QLORA_KERNEL_NONE = 0
 QLORA_KERNEL_FWD_GEMM = 1
@@ -46,6 +48,7 @@ QLORA_FMT_NF4 = 1
 QLORA_FMT_INT4 = 2
 QLORA_FMT_INT8 = 3
 FORMATS = {"nf4": QLORA_FMT_NF4, "int4": QLORA_FMT_INT4, "int8": QLORA_FMT_INT8}
+ACTIVATIONS = {"silu": 1, "gelu_tanh": 2}
 QLORA_ADAMW_MAX_TENSORS = 8
 QLORA_ADAPTERS_MAX = 1024
 QLORA_LOGPROBS_MAX_TOP = 256
@@ -88,6 +91,20 @@ class qlora_adapters_t(ctypes.Structure):
 class qlora_adapters_sizes_t(ctypes.Structure):
     _fields_ = [("plan_bytes", ctypes.c_size_t), ("fwd_ws_bytes", ctypes.c_size_t),
                 ("bwd_ws_bytes", ctypes.c_size_t)]
+
+
+class qlora_dropout_t(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_float), ("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64),
+                ("step", ctypes.c_void_p)]
+
+
+class qlora_block_sizes_t(ctypes.Structure):
+    _fields_ = [("fwd_ws_bytes", ctypes.c_size_t), ("bwd_ws_bytes", ctypes.c_size_t)]
+
+
+class qlora_gated_adapters_t(ctypes.Structure):
+    _fields_ = [("A_gate", ctypes.c_void_p), ("B_gate", ctypes.c_void_p), ("A_up", ctypes.c_void_p),
+                ("B_up", ctypes.c_void_p), ("r", ctypes.c_int32), ("alpha", ctypes.c_float)]
 
 
 def _load():
@@ -154,8 +171,18 @@ def _load():
     lib.qlora_distill_bwd.argtypes = [vp, i32, i64, i64, i64, vp, i32, vp, i32, f32, vp, vp, vp, vp]
     lib.qlora_logprobs_fwd.argtypes = [vp, i32, i64, i64, i64, vp, f32, vp, vp, vp, i32, vp, vp, vp, vp, vp, vp]
     lib.qlora_logprobs_bwd.argtypes = [vp, i32, i64, i64, i64, vp, f32, vp, vp, vp, vp, vp, vp]
+    nf4, drop, gated = P(qlora_nf4_t), P(qlora_dropout_t), P(qlora_gated_adapters_t)
+    lib.qlora_dropout_linear_sizes.argtypes = [i64, i64, i64, i32, P(qlora_block_sizes_t)]
+    lib.qlora_gated_sizes.argtypes = [i64, i64, i64, i32, P(qlora_block_sizes_t)]
+    lib.qlora_dropout_linear_fwd.argtypes = [nf4, vp, i64, vp, vp, i32, f32, drop, vp, i32, vp, vp, sz, vp]
+    lib.qlora_dropout_linear_bwd.argtypes = [nf4, vp, vp, i64, vp, vp, i32, f32, drop, vp, vp, i32, vp, vp, vp, sz, vp]
+    lib.qlora_gated_fwd.argtypes = [nf4, nf4, vp, i64, gated, i32, drop, vp, vp, vp, vp, vp, sz, vp]
+    lib.qlora_gated_bwd.argtypes = [nf4, nf4, vp, vp, vp, vp, i64, gated, i32, drop, vp, vp, i32, vp, vp, vp, vp, vp,
+                                    sz, vp]
     for name in ("qlora_adapters_sizes", "qlora_adapters_plan", "qlora_adapters_fwd", "qlora_adapters_bwd",
-                 "qlora_distill_fwd", "qlora_distill_bwd", "qlora_logprobs_fwd", "qlora_logprobs_bwd"):
+                 "qlora_distill_fwd", "qlora_distill_bwd", "qlora_logprobs_fwd", "qlora_logprobs_bwd",
+                 "qlora_dropout_linear_sizes", "qlora_dropout_linear_fwd", "qlora_dropout_linear_bwd",
+                 "qlora_gated_sizes", "qlora_gated_fwd", "qlora_gated_bwd"):
         getattr(lib, name).restype = i32
     return lib
 
@@ -621,6 +648,162 @@ def qlora_adapters_bwd(W: Nf4Tensor, X, dY, pool: AdapterPool, plan: AdapterPlan
     _check(lib.qlora_adapters_bwd(ctypes.byref(wd), x, dy, M, ctypes.byref(ad), buf, size, t, dx,
                                   QLORA_BF16 if dX.dtype == bf16 else QLORA_F32, da, db, w, nbytes,
                                   _launch_stream(stream, dev)))
+
+
+class Dropout:
+    """Dropout of an adapter's input: each element dropped with probability p (in
+    steps of 2^-16), by a generator that knows the element's index, `seed` and
+    `offset` alone.  The backward pass takes the forward pass's; every layer and
+    step takes a seed or an offset of its own.  step: None, or an int64 tensor [1]
+    that is added to the offset when the kernels run, so that a captured step draws
+    another mask in every replay once it is raised."""
+
+    def __init__(self, p: float, seed: int, offset: int = 0, step=None):
+        for name, v in (("seed", seed), ("offset", offset)):
+            if not 0 <= v < 2 ** 64:
+                raise ValueError(f"{name}={v} outside [0, 2^64)")
+        self.p, self.seed, self.offset, self.step = float(p), int(seed), int(offset), step
+        self._struct = qlora_dropout_t(self.p, self.seed, self.offset, None)
+
+
+def _drop_ref(drop, dev: int):
+    if drop is None:
+        return None
+    if drop.step is not None:
+        drop._struct.step = _address(drop.step, "step", (1,), (_torch().int64,), dev)
+    return ctypes.byref(drop._struct)
+
+
+def _block_sizes(call, N: int, K: int, M_max: int, r: int) -> dict:
+    out = qlora_block_sizes_t()
+    _check(call(N, K, M_max, r, ctypes.byref(out)))
+    return {name: int(getattr(out, name)) for name, _ in qlora_block_sizes_t._fields_}
+
+
+def qlora_dropout_linear_sizes(N: int, K: int, M_max: int, r: int) -> dict:
+    return _block_sizes(lib.qlora_dropout_linear_sizes, N, K, M_max, r)
+
+
+def qlora_gated_sizes(N: int, K: int, M_max: int, r: int) -> dict:
+    return _block_sizes(lib.qlora_gated_sizes, N, K, M_max, r)
+
+
+def _tokens(X) -> int:
+    if X is None or X.dim() != 2:
+        raise ValueError("X must be [M, K]")
+    return X.shape[0]
+
+
+def qlora_dropout_linear_fwd(W: Nf4Tensor, X, A, B, r: int, alpha: float, drop, Y, T_save, ws, stream=None) -> None:
+    """Y = X·Ŵᵀ + (alpha / r)·(D(X)·Aᵀ)·Bᵀ, D the Dropout `drop` (None: no dropout)."""
+    torch = _torch()
+    f32, bf16 = torch.float32, torch.bfloat16
+    M, N, K = _tokens(X), W.n_rows, W.n_cols
+    dev = X.get_device()
+    x, a = _address(X, "X", (M, K), (bf16,), dev), _address(A, "A", (r, K), (bf16,), dev)
+    b, y = _address(B, "B", (N, r), (bf16,), dev), _address(Y, "Y", (M, N), (f32, bf16), dev)
+    t = None if T_save is None else _address(T_save, "T_save", (M, r), (f32,), dev)
+    w, nbytes = _scratch(ws, "ws", dev)
+    wd = _weight_on(W, dev)
+    _check(lib.qlora_dropout_linear_fwd(ctypes.byref(wd), x, M, a, b, r, alpha, _drop_ref(drop, dev), y,
+                                        QLORA_BF16 if Y.dtype == bf16 else QLORA_F32, t, w, nbytes,
+                                        _launch_stream(stream, dev)))
+
+
+def qlora_dropout_linear_bwd(W: Nf4Tensor, X, dY, A, B, r: int, alpha: float, drop, T_saved, dX, dA, dB, ws,
+                             stream=None) -> None:
+    """dX, dA and dB of qlora_dropout_linear_fwd; drop is the forward pass's."""
+    torch = _torch()
+    f32, bf16 = torch.float32, torch.bfloat16
+    M, N, K = _tokens(X), W.n_rows, W.n_cols
+    dev = X.get_device()
+    x, dy = _address(X, "X", (M, K), (bf16,), dev), _address(dY, "dY", (M, N), (bf16,), dev)
+    a, b = _address(A, "A", (r, K), (bf16,), dev), _address(B, "B", (N, r), (bf16,), dev)
+    t = None if T_saved is None else _address(T_saved, "T_saved", (M, r), (f32,), dev)
+    dx = _address(dX, "dX", (M, K), (f32, bf16), dev)
+    da, db = _address(dA, "dA", (r, K), (f32,), dev), _address(dB, "dB", (N, r), (f32,), dev)
+    w, nbytes = _scratch(ws, "ws", dev)
+    wd = _weight_on(W, dev)
+    _check(lib.qlora_dropout_linear_bwd(ctypes.byref(wd), x, dy, M, a, b, r, alpha, _drop_ref(drop, dev), t, dx,
+                                        QLORA_BF16 if dX.dtype == bf16 else QLORA_F32, da, db, w, nbytes,
+                                        _launch_stream(stream, dev)))
+
+
+class GatedAdapters:
+    """The adapters of a gated block's two layers: A_* bf16 [r, K], B_* bf16 [N, r],
+    one rank (a multiple of 8) and one alpha."""
+
+    def __init__(self, A_gate, B_gate, A_up, B_up, alpha: float):
+        torch = _torch()
+        if A_gate is None or A_gate.dim() != 2 or B_gate is None or B_gate.dim() != 2:
+            raise ValueError("A_gate must be [r, K] and B_gate [N, r]")
+        self.r, self.n_cols = (int(x) for x in A_gate.shape)
+        self.n_rows = int(B_gate.shape[0])
+        for t, name, shape in self._tensors(A_gate, B_gate, A_up, B_up):
+            _expect(t, name, shape, (torch.bfloat16,))
+        self.A_gate, self.B_gate, self.A_up, self.B_up, self.alpha = A_gate, B_gate, A_up, B_up, float(alpha)
+
+    def _tensors(self, A_gate, B_gate, A_up, B_up):
+        a, b = (self.r, self.n_cols), (self.n_rows, self.r)
+        return ((A_gate, "A_gate", a), (B_gate, "B_gate", b), (A_up, "A_up", a), (B_up, "B_up", b))
+
+    def _struct_on(self, dev: int) -> qlora_gated_adapters_t:
+        bf16 = (_torch().bfloat16,)
+        at = [_address(t, name, shape, bf16, dev)
+              for t, name, shape in self._tensors(self.A_gate, self.B_gate, self.A_up, self.B_up)]
+        return qlora_gated_adapters_t(*at, self.r, self.alpha)
+
+
+def _check_gated(gate: Nf4Tensor, up: Nf4Tensor, X, adapters: GatedAdapters, act: str):
+    """(M, N, K, the activation's number)"""
+    N, K = adapters.n_rows, adapters.n_cols
+    for name, W in (("gate", gate), ("up", up)):
+        if W.n_rows != N or W.n_cols != K:
+            raise ValueError(f"{name} is [{W.n_rows}, {W.n_cols}], the adapters are for [{N}, {K}]")
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act {act!r}: one of {sorted(ACTIVATIONS)}")
+    return _tokens(X), N, K, ACTIVATIONS[act]
+
+
+def qlora_gated_fwd(gate: Nf4Tensor, up: Nf4Tensor, X, adapters: GatedAdapters, act: str, drop, H, G_save, U_save,
+                    T_save, ws, stream=None) -> None:
+    """H = act(G)*U with G and U the two layers of X; act "silu" or "gelu_tanh"; drop
+    a Dropout or None; G_save, U_save, T_save (fp32 [2, M, r]) for the backward pass
+    or None."""
+    torch = _torch()
+    f32, bf16 = (torch.float32,), (torch.bfloat16,)
+    M, N, K, a = _check_gated(gate, up, X, adapters, act)
+    dev = X.get_device()
+    x, h = _address(X, "X", (M, K), bf16, dev), _address(H, "H", (M, N), bf16, dev)
+    g = None if G_save is None else _address(G_save, "G_save", (M, N), bf16, dev)
+    u = None if U_save is None else _address(U_save, "U_save", (M, N), bf16, dev)
+    t = None if T_save is None else _address(T_save, "T_save", (2, M, adapters.r), f32, dev)
+    w, nbytes = _scratch(ws, "ws", dev)
+    w0, w1, ad = _weight_on(gate, dev), _weight_on(up, dev), adapters._struct_on(dev)
+    _check(lib.qlora_gated_fwd(ctypes.byref(w0), ctypes.byref(w1), x, M, ctypes.byref(ad), a, _drop_ref(drop, dev), h, g, u,
+                               t, w, nbytes, _launch_stream(stream, dev)))
+
+
+def qlora_gated_bwd(gate: Nf4Tensor, up: Nf4Tensor, X, dH, G, U, adapters: GatedAdapters, act: str, drop, T_saved, dX,
+                    dA_gate, dB_gate, dA_up, dB_up, ws, stream=None) -> None:
+    """dX and the adapters' gradients of qlora_gated_fwd from its G, U (and T, or
+    None to recompute it); drop is the forward pass's."""
+    torch = _torch()
+    f32, bf16 = (torch.float32,), (torch.bfloat16,)
+    M, N, K, a = _check_gated(gate, up, X, adapters, act)
+    r = adapters.r
+    dev = X.get_device()
+    x, dh = _address(X, "X", (M, K), bf16, dev), _address(dH, "dH", (M, N), bf16, dev)
+    g, u = _address(G, "G", (M, N), bf16, dev), _address(U, "U", (M, N), bf16, dev)
+    t = None if T_saved is None else _address(T_saved, "T_saved", (2, M, r), f32, dev)
+    dx = _address(dX, "dX", (M, K), f32 + bf16, dev)
+    out = [_address(dA_gate, "dA_gate", (r, K), f32, dev), _address(dB_gate, "dB_gate", (N, r), f32, dev),
+           _address(dA_up, "dA_up", (r, K), f32, dev), _address(dB_up, "dB_up", (N, r), f32, dev)]
+    w, nbytes = _scratch(ws, "ws", dev)
+    w0, w1, ad = _weight_on(gate, dev), _weight_on(up, dev), adapters._struct_on(dev)
+    _check(lib.qlora_gated_bwd(ctypes.byref(w0), ctypes.byref(w1), x, dh, g, u, M, ctypes.byref(ad), a, _drop_ref(drop, dev),
+                               t, dx, QLORA_BF16 if dX.dtype == torch.bfloat16 else QLORA_F32, *out, w, nbytes,
+                               _launch_stream(stream, dev)))
 
 
 def _distill_args(Z, top, top_index, weight, dZ, vocab):

@@ -12,6 +12,7 @@
 #include <algorithm>
 
 #include "host.h"
+#include "lowrank.h"
 #include "splitk.h"
 #include "tiling.h"
 
@@ -161,18 +162,8 @@ __global__ __launch_bounds__(64 * kPlanWaves) void adapters_plan_kernel(const in
 }
 
 // ---------------------------------------------------------------------------
-// Low-rank factors, three-part: v = s_a·D as hi + mid + lo in bf16 (24 bits:
-// products with it are as exact as fp32 ones).
+// Low-rank factors
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ void split3(float v, uint16_t* o) {
-#pragma unroll
-  for (int i = 0; i < 3; ++i) {
-    const uint32_t h = pack_bf16x2(v, 0.0f) & 0xffffu;
-    o[i] = (uint16_t)h;
-    v = __fsub_rn(v, __uint_as_float(h << 16));
-  }
-}
-
 // D[p][j] = Σ_k L[token(p)][k]·R_a(j, k) for the positions of one plan tile (up
 // to 64 of one adapter), 16·NJ ranks and one slice of the reduction, as fp32
 // partial sums P[slice][p][j].  R_a is A_a [r, Kred] (T = X·A_aᵀ) or, NATURAL,
@@ -192,14 +183,6 @@ struct DownJob {
   float* P;
   int slices;
 };
-// NATURAL: the 16-byte chunks of a reduction row (2·NJ of them) XORed by bits
-// of the row, so that the 4 rows of a transposing read lie on different banks.
-template <int NJ>
-__device__ __forceinline__ int rank_swz(int row) {
-  return NJ == 4 ? (row & 3) << 1 : NJ == 2 ? row & 2 : 0;
-}
-__device__ __forceinline__ int dswz(int row, int chunk) { return row * 128 + ((chunk ^ (row & 7)) << 4); }
-
 template <int NJ, bool NATURAL>
 __device__ __forceinline__ void down_tile(const DownJob& J, int tile, int slice, int j0, int64_t M,
                                           const AdapterView& ad, const PlanView& pl, char* sl, char* sr) {
@@ -428,14 +411,6 @@ __global__ __launch_bounds__(256) void adapters_factor_kernel(FactorJob t, Facto
 // faster (r = 256, 53 tokens of 8 adapters, 44.8 against 35.2; r = 128, K = 11008,
 // 58.4 against 44.5), but how many tokens share one is known on the device alone.
 constexpr int kFewTokens = 64, kFewRanks = 4;
-__device__ __forceinline__ float dot8(const u32x4_t a, const u32x4_t b, float acc) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    acc = __builtin_fmaf(bf16lo(a[i]), bf16lo(b[i]), acc);
-    acc = __builtin_fmaf(bf16hi(a[i]), bf16hi(b[i]), acc);
-  }
-  return acc;
-}
 // This thread's part of kFewRanks ranks of one token: x·R[j], rows of Kred.
 __device__ __forceinline__ void few_rows(const uint16_t* x_row, const uint16_t* R, int64_t Kred, int tid, float* acc) {
   constexpr int UN = 3;
@@ -587,17 +562,6 @@ struct GradientJob {
   float* out;        // [count][r·cols]
   int64_t part_off;  // of this job within a partial slot
 };
-// 16-byte chunk c of L row p at c ^ ((p & 3) << 1): the 4 rows of a transposing
-// read on different banks
-__device__ __forceinline__ int lswz(int row, int col) {
-  return row * 256 + (((col >> 3) ^ ((row & 3) << 1)) << 4) + 2 * (col & 7);
-}
-// The same for S rows of 6·NJ chunks (three parts of 2·NJ).
-template <int NJ>
-__device__ __forceinline__ int factor_swz(int row) {
-  return NJ == 4 ? (row & 3) << 1 : NJ == 2 ? row & 2 : 0;
-}
-
 // ALONG: out [cols][r] (dB), else [r][cols] (dA).
 template <int NJ, bool ALONG>
 __device__ __forceinline__ void gradient_unit(const GradientJob& J, int64_t c0, int j0, const int4 u, int64_t M,
@@ -626,7 +590,7 @@ __device__ __forceinline__ void gradient_unit(const GradientJob& J, int64_t c0, 
 #pragma unroll
     for (int c = 0; c < SI; ++c) {
       const int idx = 64 * (SI * wave + c) + lane, row = idx / (6 * NJ);
-      const int ch = (idx % (6 * NJ)) ^ factor_swz<NJ>(row), part = ch / (2 * NJ), j = j0 + 8 * (ch % (2 * NJ));
+      const int ch = (idx % (6 * NJ)) ^ rank_swz<NJ>(row), part = ch / (2 * NJ), j = j0 + 8 * (ch % (2 * NJ));
       const int pos = p0 + 32 * s + row;
       const bool in = row < 32 && pos < p1 && j < r;
       dma_lds16(rs, ss + b * SB + (SI * wave + c) * 1024,
@@ -649,8 +613,8 @@ __device__ __forceinline__ void gradient_unit(const GradientJob& J, int64_t c0, 
     u32x4_t a[2];
 #pragma unroll
     for (int pf = 0; pf < 2; ++pf) {
-      const u32x2_t h0 = lds_read_tr(lt + lswz(trow, 32 * wave + 16 * pf + tcol));
-      const u32x2_t h1 = lds_read_tr(lt + lswz(trow + 4, 32 * wave + 16 * pf + tcol));
+      const u32x2_t h0 = lds_read_tr(lt + gswz(trow, 32 * wave + 16 * pf + tcol));
+      const u32x2_t h1 = lds_read_tr(lt + gswz(trow + 4, 32 * wave + 16 * pf + tcol));
       a[pf] = u32x4_t{h0[0], h0[1], h1[0], h1[1]};
     }
 #pragma unroll
@@ -662,7 +626,7 @@ __device__ __forceinline__ void gradient_unit(const GradientJob& J, int64_t c0, 
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           const int row = trow + 4 * q;
-          h[q] = lds_read_tr(st + row * SROW + (((col >> 3) ^ factor_swz<NJ>(row)) << 4) + 2 * (col & 7));
+          h[q] = lds_read_tr(st + row * SROW + (((col >> 3) ^ rank_swz<NJ>(row)) << 4) + 2 * (col & 7));
         }
         const u32x4_t f = {h[0][0], h[0][1], h[1][0], h[1][1]};
 #pragma unroll

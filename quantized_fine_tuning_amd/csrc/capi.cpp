@@ -529,6 +529,198 @@ qlora_status qlora_adapters_bwd(const qlora_nf4_t* W, const void* X, const void*
 
 namespace {
 
+// The kernels' view of a dropout (NULL: none).
+qlora_status check_dropout(const char* fn, const qlora_dropout_t* drop, qnf4::DropView* out) {
+  *out = qnf4::DropView{0, 0, 0, 0, 0, 1.0f, nullptr};
+  if (drop == nullptr) return QLORA_OK;
+  const long pieces = drop->p >= 0.0f && drop->p < 1.0f ? std::lrint(65536.0 * (double)drop->p) : 65536;
+  if (pieces >= 65536) return fail(QLORA_ERR_INVALID_ARG, "%s: p=%g outside [0, 1)", fn, drop->p);
+  out->key0 = (uint32_t)drop->seed;
+  out->key1 = (uint32_t)(drop->seed >> 32);
+  out->off0 = (uint32_t)drop->offset;
+  out->off1 = (uint32_t)(drop->offset >> 32);
+  out->out = (uint32_t)pieces;
+  out->scale = (float)(65536.0 / (65536.0 - (double)pieces));
+  const uint64_t* step = drop->step;
+  CHECK_OPT_PTR(step);
+  out->step = step;
+  return QLORA_OK;
+}
+
+qlora_status block_sizes(const char* fn, int64_t N, int64_t K, int64_t M_max, int32_t r, int layers,
+                         qlora_block_sizes_t* out) {
+  if (out == nullptr) return fail(QLORA_ERR_INVALID_ARG, "%s: out is NULL", fn);
+  qlora_status st = check_shape(fn, N, K);
+  if (st != QLORA_OK) return st;
+  if ((st = check_adapter_shape(fn, r, 1)) != QLORA_OK) return st;
+  if (M_max < 0) return fail(QLORA_ERR_INVALID_ARG, "%s: M_max=%lld < 0", fn, (long long)M_max);
+  if ((st = check_adapter_limits(fn, M_max, N, K, r)) != QLORA_OK) return st;
+  out->fwd_ws_bytes = qnf4::block_fwd_ws_max(M_max, N, K, r, layers);
+  out->bwd_ws_bytes = qnf4::block_bwd_ws_max(M_max, N, K, r, layers);
+  return ok();
+}
+
+// Arguments of a pass over one or two layers that all of them share, and their view.
+qlora_status check_block(const char* fn, const qlora_nf4_t* const* W, int layers, const void* X, int64_t M,
+                         const void* const* A, const void* const* B, int32_t r, float alpha,
+                         const qlora_dropout_t* drop, qnf4::BlockView* out) {
+  qlora_status st;
+  for (int l = 0; l < layers; ++l)
+    if ((st = check_tensor(fn, W[l])) != QLORA_OK) return st;
+  const int64_t N = W[0]->n_rows, K = W[0]->n_cols;
+  if (layers == 2 && (W[1]->n_rows != N || W[1]->n_cols != K))
+    return fail(QLORA_ERR_INVALID_ARG, "%s: gate is %lldx%lld, up %lldx%lld", fn, (long long)N, (long long)K,
+                (long long)W[1]->n_rows, (long long)W[1]->n_cols);
+  if ((st = check_adapter_shape(fn, r, 1)) != QLORA_OK) return st;
+  if (M < 0) return fail(QLORA_ERR_INVALID_ARG, "%s: M=%lld < 0", fn, (long long)M);
+  if ((st = check_adapter_limits(fn, M, N, K, r)) != QLORA_OK) return st;
+  *out = qnf4::BlockView{};
+  for (int l = 0; l < layers; ++l) {
+    const void* Al = A[l];
+    const void* Bl = B[l];
+    CHECK_PTR(Al);
+    CHECK_PTR(Bl);
+    out->W[l] = view(W[l]);
+    out->A[l] = static_cast<const uint16_t*>(Al);
+    out->B[l] = static_cast<const uint16_t*>(Bl);
+  }
+  if (M > 0) CHECK_PTR(X);
+  out->r = r;
+  out->layers = layers;
+  out->scale = alpha / (float)r;
+  return check_dropout(fn, drop, &out->drop);
+}
+
+qlora_status check_workspace(const char* fn, const void* ws, size_t ws_bytes, size_t need) {
+  if (ws_bytes < need) return fail(QLORA_ERR_WORKSPACE_TOO_SMALL, "%s: workspace %zu < %zu bytes", fn, ws_bytes, need);
+  if (need > 0) CHECK_PTR(ws);
+  return QLORA_OK;
+}
+
+qlora_status check_act(const char* fn, int32_t act, int* out) {
+  if (act != QLORA_ACT_SILU && act != QLORA_ACT_GELU_TANH)
+    return fail(QLORA_ERR_INVALID_ARG, "%s: act=%d (SILU or GELU_TANH)", fn, act);
+  *out = act == QLORA_ACT_SILU ? qnf4::kActSilu : qnf4::kActGeluTanh;
+  return QLORA_OK;
+}
+
+}  // namespace
+
+qlora_status qlora_dropout_linear_sizes(int64_t N, int64_t K, int64_t M_max, int32_t r, qlora_block_sizes_t* out) {
+  return block_sizes("qlora_dropout_linear_sizes", N, K, M_max, r, 1, out);
+}
+qlora_status qlora_gated_sizes(int64_t N, int64_t K, int64_t M_max, int32_t r, qlora_block_sizes_t* out) {
+  return block_sizes("qlora_gated_sizes", N, K, M_max, r, 2, out);
+}
+
+qlora_status qlora_dropout_linear_fwd(const qlora_nf4_t* W, const void* X, int64_t M, const void* A, const void* B,
+                                      int32_t r, float alpha, const qlora_dropout_t* drop, void* Y, qlora_dtype y_dtype,
+                                      float* T_save, void* ws, size_t ws_bytes, void* stream) {
+  const char* fn = "qlora_dropout_linear_fwd";
+  qnf4::BlockView b;
+  qlora_status st = check_block(fn, &W, 1, X, M, &A, &B, r, alpha, drop, &b);
+  if (st != QLORA_OK) return st;
+  if (y_dtype != QLORA_F32 && y_dtype != QLORA_BF16)
+    return fail(QLORA_ERR_UNSUPPORTED_DTYPE, "%s: y_dtype=%d (F32 or BF16)", fn, y_dtype);
+  if (M > 0) CHECK_PTR(Y);
+  CHECK_OPT_PTR(T_save);
+  const qnf4::BlockFwdLayout L = qnf4::block_fwd_layout(M, W->n_rows, W->n_cols, r, 1);
+  if ((st = check_workspace(fn, ws, ws_bytes, L.total)) != QLORA_OK) return st;
+  return hip_status(fn, qnf4::launch_block_fwd(b, static_cast<const uint16_t*>(X), M, Y, y_dtype == QLORA_BF16, T_save,
+                                               qnf4::GatedOut{}, static_cast<char*>(ws), L,
+                                               static_cast<hipStream_t>(stream)));
+}
+
+qlora_status qlora_dropout_linear_bwd(const qlora_nf4_t* W, const void* X, const void* dY, int64_t M, const void* A,
+                                      const void* B, int32_t r, float alpha, const qlora_dropout_t* drop,
+                                      const float* T_saved, void* dX, qlora_dtype dx_dtype, float* dA, float* dB,
+                                      void* ws, size_t ws_bytes, void* stream) {
+  const char* fn = "qlora_dropout_linear_bwd";
+  qnf4::BlockView b;
+  qlora_status st = check_block(fn, &W, 1, X, M, &A, &B, r, alpha, drop, &b);
+  if (st != QLORA_OK) return st;
+  if (dx_dtype != QLORA_F32 && dx_dtype != QLORA_BF16)
+    return fail(QLORA_ERR_UNSUPPORTED_DTYPE, "%s: dx_dtype=%d (F32 or BF16)", fn, dx_dtype);
+  CHECK_PTR(dA);
+  CHECK_PTR(dB);
+  if (M > 0) {
+    CHECK_PTR(dY);
+    CHECK_PTR(dX);
+  }
+  CHECK_OPT_PTR(T_saved);
+  const qnf4::BlockBwdLayout L = qnf4::block_bwd_layout(M, W->n_rows, W->n_cols, r, 1);
+  if ((st = check_workspace(fn, ws, ws_bytes, L.total)) != QLORA_OK) return st;
+  float* const da[2] = {dA, nullptr};
+  float* const db[2] = {dB, nullptr};
+  return hip_status(fn, qnf4::launch_block_bwd(b, static_cast<const uint16_t*>(X), M, static_cast<const uint16_t*>(dY),
+                                               qnf4::GatedIn{}, T_saved, dX, dx_dtype == QLORA_BF16, da, db,
+                                               static_cast<char*>(ws), L, static_cast<hipStream_t>(stream)));
+}
+
+qlora_status qlora_gated_fwd(const qlora_nf4_t* gate, const qlora_nf4_t* up, const void* X, int64_t M,
+                             const qlora_gated_adapters_t* adapters, int32_t act, const qlora_dropout_t* drop, void* H,
+                             void* G_save, void* U_save, float* T_save, void* ws, size_t ws_bytes, void* stream) {
+  const char* fn = "qlora_gated_fwd";
+  if (adapters == nullptr) return fail(QLORA_ERR_INVALID_ARG, "%s: adapters is NULL", fn);
+  const qlora_nf4_t* const W[2] = {gate, up};
+  const void* const A[2] = {adapters->A_gate, adapters->A_up};
+  const void* const B[2] = {adapters->B_gate, adapters->B_up};
+  qnf4::BlockView b;
+  qlora_status st = check_block(fn, W, 2, X, M, A, B, adapters->r, adapters->alpha, drop, &b);
+  if (st != QLORA_OK) return st;
+  qnf4::GatedOut out{static_cast<uint16_t*>(H), static_cast<uint16_t*>(G_save), static_cast<uint16_t*>(U_save), 0};
+  if ((st = check_act(fn, act, &out.act)) != QLORA_OK) return st;
+  if (M > 0) CHECK_PTR(H);
+  if ((G_save == nullptr) != (U_save == nullptr))
+    return fail(QLORA_ERR_INVALID_ARG, "%s: one of G_save and U_save is NULL", fn);
+  CHECK_OPT_PTR(G_save);
+  CHECK_OPT_PTR(U_save);
+  CHECK_OPT_PTR(T_save);
+  const qnf4::BlockFwdLayout L = qnf4::block_fwd_layout(M, gate->n_rows, gate->n_cols, b.r, 2);
+  if ((st = check_workspace(fn, ws, ws_bytes, L.total)) != QLORA_OK) return st;
+  return hip_status(fn, qnf4::launch_block_fwd(b, static_cast<const uint16_t*>(X), M, nullptr, true, T_save, out,
+                                               static_cast<char*>(ws), L, static_cast<hipStream_t>(stream)));
+}
+
+qlora_status qlora_gated_bwd(const qlora_nf4_t* gate, const qlora_nf4_t* up, const void* X, const void* dH, const void* G,
+                             const void* U, int64_t M, const qlora_gated_adapters_t* adapters, int32_t act,
+                             const qlora_dropout_t* drop, const float* T_saved, void* dX, qlora_dtype dx_dtype,
+                             float* dA_gate, float* dB_gate, float* dA_up, float* dB_up, void* ws, size_t ws_bytes,
+                             void* stream) {
+  const char* fn = "qlora_gated_bwd";
+  if (adapters == nullptr) return fail(QLORA_ERR_INVALID_ARG, "%s: adapters is NULL", fn);
+  const qlora_nf4_t* const W[2] = {gate, up};
+  const void* const A[2] = {adapters->A_gate, adapters->A_up};
+  const void* const B[2] = {adapters->B_gate, adapters->B_up};
+  qnf4::BlockView b;
+  qlora_status st = check_block(fn, W, 2, X, M, A, B, adapters->r, adapters->alpha, drop, &b);
+  if (st != QLORA_OK) return st;
+  qnf4::GatedIn in{static_cast<const uint16_t*>(dH), static_cast<const uint16_t*>(G), static_cast<const uint16_t*>(U), 0};
+  if ((st = check_act(fn, act, &in.act)) != QLORA_OK) return st;
+  if (dx_dtype != QLORA_F32 && dx_dtype != QLORA_BF16)
+    return fail(QLORA_ERR_UNSUPPORTED_DTYPE, "%s: dx_dtype=%d (F32 or BF16)", fn, dx_dtype);
+  CHECK_PTR(dA_gate);
+  CHECK_PTR(dB_gate);
+  CHECK_PTR(dA_up);
+  CHECK_PTR(dB_up);
+  if (M > 0) {
+    CHECK_PTR(dH);
+    CHECK_PTR(G);
+    CHECK_PTR(U);
+    CHECK_PTR(dX);
+  }
+  CHECK_OPT_PTR(T_saved);
+  const qnf4::BlockBwdLayout L = qnf4::block_bwd_layout(M, gate->n_rows, gate->n_cols, b.r, 2);
+  if ((st = check_workspace(fn, ws, ws_bytes, L.total)) != QLORA_OK) return st;
+  float* const da[2] = {dA_gate, dA_up};
+  float* const db[2] = {dB_gate, dB_up};
+  return hip_status(fn, qnf4::launch_block_bwd(b, static_cast<const uint16_t*>(X), M, nullptr, in, T_saved, dX,
+                                               dx_dtype == QLORA_BF16, da, db, static_cast<char*>(ws), L,
+                                               static_cast<hipStream_t>(stream)));
+}
+
+namespace {
+
 bool is_float_dtype(qlora_dtype d) { return d == QLORA_F32 || d == QLORA_BF16 || d == QLORA_F16; }
 
 // The shape of a batch of logits, and its temperature.

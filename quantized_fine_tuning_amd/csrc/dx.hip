@@ -45,7 +45,9 @@
 //     to P[split][M][K], summed in split order by splitk_reduce_kernel.
 #include <type_traits>
 
+#include "dropout.h"
 #include "host.h"
+#include "modes.h"
 #include "tiling.h"
 
 namespace qnf4 {
@@ -94,7 +96,12 @@ __device__ __forceinline__ int dq_cg(int l) { return (l & 1) | ((l >> 2) & 6); }
 // the plan, and the LoRA steps run over the used adapters whose tokens the
 // tile holds, cols/64 steps each, rounded up (rows of other adapters read as
 // zero; the split reductions share these steps out as they do the n steps).
-template <int LSTEPS, bool F16, bool MULTI = false>
+// BLOCK: one layer (kBlock1) or the two of a gated block (kBlock2, whose rows n
+// follow one another in one reduction: dX is summed once and rounded once).  The
+// LoRA steps come first, from the three-part splits S and A in its own layout:
+// between them and the n steps the sums are the adapters' share of dX alone, and
+// where the adapters' input had dropout those of dropped elements become zero.
+template <int LSTEPS, bool F16, int MODE = kPlain>
 __global__ __launch_bounds__(kThreads, 1) void dx_gemm_kernel(Nf4View W, const uint16_t* __restrict__ dY,
                                                               int64_t M, const uint16_t* __restrict__ sU,
                                                               const uint16_t* __restrict__ AT2,
@@ -102,7 +109,9 @@ __global__ __launch_bounds__(kThreads, 1) void dx_gemm_kernel(Nf4View W, const u
                                                               int dx_bf16, int tiles_m, int tiles_k,
                                                               int splits, float* __restrict__ P,
                                                               Codebook cb,
-                                                              std::conditional_t<MULTI, AdapterGemmArgs, NoAdapters> ma) {
+                                                              ModeArgs<MODE> ma) {
+  constexpr bool MULTI = MODE == kMulti, BLOCK = MODE >= kBlock1, PAIR = MODE == kBlock2;
+  constexpr int LAYERS = PAIR ? 2 : 1;
   __shared__ __attribute__((aligned(16))) char sa0[TM * 128], sa1[TM * 128];  // A tiles: dY, then sU
   __shared__ __attribute__((aligned(16))) char sw[2][TK * 128];  // B tiles: Ŵᵀ, then AT2
   // per step slot: the row tables of each block column (row 8rg + i at
@@ -123,8 +132,8 @@ __global__ __launch_bounds__(kThreads, 1) void dx_gemm_kernel(Nf4View W, const u
   // this workgroup's n steps [nfirst, nfirst + nsteps) (step indices below
   // are relative to nfirst) and its LoRA steps
   const int nall = (int)((N + NSTEP - 1) / NSTEP);
-  const int nfirst = split_first(sp, splits, nall);
-  const int nsteps = split_first(sp + 1, splits, nall) - nfirst;
+  const int nfirst = split_first(sp, splits, LAYERS * nall);
+  const int nsteps = split_first(sp + 1, splits, LAYERS * nall) - nfirst;
   int lsteps = sp == splits - 1 ? LSTEPS : 0;
   // MULTI: this workgroup's LoRA steps [lfirst, lfirst + lsteps) of the
   // tile's; step i belongs to used adapter gfirst + i / lper, chunk i % lper
@@ -140,6 +149,19 @@ __global__ __launch_bounds__(kThreads, 1) void dx_gemm_kernel(Nf4View W, const u
       lsteps = split_first(sp + 1, splits, all) - lfirst;
     }
   }
+  // BLOCK: this workgroup's LoRA steps of the layers', lper each
+  if constexpr (BLOCK) {
+    lper = (ma.cols + 63) / 64;
+    lfirst = split_first(sp, splits, LAYERS * lper);
+    lsteps = split_first(sp + 1, splits, LAYERS * lper) - lfirst;
+  }
+  // (then n step t uses the buffers (t + wpar) % 2)
+  const int wpar = BLOCK ? lsteps & 1 : 0;
+  // n step t: its layer, and the step among that layer's
+  auto layer_of = [&](int t) __attribute__((always_inline)) { return PAIR && nfirst + t >= nall; };
+  auto step_of = [&](int t) __attribute__((always_inline)) {
+    return nfirst + t - (layer_of(t) ? nall : 0);
+  };
   // the sorted positions [p0, p1) of LoRA step l's adapter, relative to m0
   auto rows_of = [&](int l, int& p0, int& p1) __attribute__((always_inline)) {
     if constexpr (MULTI) {
@@ -212,8 +234,8 @@ __global__ __launch_bounds__(kThreads, 1) void dx_gemm_kernel(Nf4View W, const u
       lookup_cols(lb, we, wo, 1, v1);
       issue(1);
       __builtin_amdgcn_sched_barrier(0x8 | 0x4 | 0x10);
-      store_cols(sw[t & 1], st0, 0, v0);
-      store_cols(sw[t & 1], st0, 1, v1);
+      store_cols(sw[(t + wpar) & 1], st0, 0, v0);
+      store_cols(sw[(t + wpar) & 1], st0, 1, v1);
     } else {
       // addresses straight from the code dwords and lane offsets recomputed
       // here from an opaque copy of the lane index (kept from being hoisted
@@ -248,7 +270,7 @@ __global__ __launch_bounds__(kThreads, 1) void dx_gemm_kernel(Nf4View W, const u
         u32x4_t o;
 #pragma unroll
         for (int p = 0; p < 4; ++p) o[p] = v[2 * p] | (v[2 * p + 1] << 16);
-        *reinterpret_cast<u32x4_t*>(sw[t & 1] + ((st0 ^ (uint32_t)(16 * (c & 2))) + 128u * c)) = o;
+        *reinterpret_cast<u32x4_t*>(sw[(t + wpar) & 1] + ((st0 ^ (uint32_t)(16 * (c & 2))) + 128u * c)) = o;
       }
     }
   };
@@ -362,6 +384,46 @@ __global__ __launch_bounds__(kThreads, 1) void dx_gemm_kernel(Nf4View W, const u
       const int ln = opaque(lane);
       return *reinterpret_cast<const u32x4_t*>(scode[t & 1][2 * wave] + 16 * (8 * dq_rg(ln) + (dq_cg(ln) ^ dq_rg(ln))));
     };
+    if constexpr (BLOCK) {
+#pragma unroll 1
+      for (int l = -1; l < lsteps; ++l) {
+        if (l >= 0) lora_step(sab(l & 1), sw[l & 1]);
+        if (l + 1 == lsteps && dq) dequant_slice(std::false_type(), 0, 2 * wave, read_codes_mfma(0), no_issue);
+        __syncthreads();
+      }
+      if (lsteps > 0 && ma.drop.out > 0) {
+        const DropView drop = drawn(ma.drop);
+        // Lane L finds the masks of rows 32q + L/2 of the wave's 128, chunks
+        // 2j + L%2 of its eight, a byte each (16 generator calls, every element
+        // once); the lane that holds row 16i + 4kq + v, columns 16j + lr, takes its
+        // four bytes from lane 2·(row % 32) + lr/8.
+        const uint32_t c0 = (uint32_t)((m0 + 128 * wm + (lane >> 1)) * (K / 8) + (k0 + 64 * wk) / 8 + (lane & 1));
+        uint32_t keep[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          keep[q] = 0u;
+#pragma unroll 1
+          for (int j = 0; j < 4; ++j)
+            keep[q] |= keep8(drop, c0 + (uint32_t)(32 * q * (K / 8)) + 2u * j) << (8 * j);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            const int from = 2 * (16 * (i & 1) + 4 * kq + v) + (lr >> 3);
+            const uint32_t m = (uint32_t)__builtin_amdgcn_ds_bpermute(4 * from, (int)keep[i >> 1]) >> (lr & 7);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[i][j][v] = (m >> (8 * j)) & 1u ? acc[i][j][v] : 0.f;
+          }
+      }
+#pragma unroll 1
+      for (int s = 0; s + 1 < nsteps; ++s) {
+        mfma_step(sab((s + wpar) & 1), sw[(s + wpar) & 1]);
+        if (dq) dequant_slice(std::false_type(), s + 1, 2 * wave, read_codes_mfma(s + 1), no_issue);
+        __syncthreads();
+      }
+      mfma_step(sab((nsteps - 1 + wpar) & 1), sw[(nsteps - 1 + wpar) & 1]);
+    } else {
     if (dq) dequant_slice(std::false_type(), 0, 2 * wave, read_codes_mfma(0), no_issue);
     __syncthreads();  // step 0 in place
 #pragma unroll 1
@@ -393,6 +455,7 @@ __global__ __launch_bounds__(kThreads, 1) void dx_gemm_kernel(Nf4View W, const u
         if (apart) lora_step_rows(sab(s & 1), sw[s & 1], p0 - 128 * wm, p1 - 128 * wm);
         __syncthreads();
       }
+    }
     }
 
     // epilogue: lane holds rows 128wm + 16i + 4kq + v of column k0 + 64wk + 16j + lr
@@ -496,11 +559,15 @@ __global__ __launch_bounds__(kThreads, 1) void dx_gemm_kernel(Nf4View W, const u
   const uint32_t kpr = (uint32_t)(K / kBlock);
   const uint32_t kb = (uint32_t)(k0 / kBlock) + (uint32_t)p;  // this producer's block column
   const bool cols_ok = k0 + 64 * p < K;
-  const float mu = *W.mu;
+  const float mu1 = *W.mu, mu2 = *layer(W, ma, PAIR).mu;
   const rsrc_t rsu = make_rsrc(sU + m0 * 2 * Rp, (M - m0) * 2 * Rp * 2);
-  const rsrc_t rc = make_rsrc(W.codes, N * (K / 2));
-  const rsrc_t re = make_rsrc(W.e, N * kpr);
-  const rsrc_t rs = make_rsrc(W.s, ((N * kpr + kDqBlock - 1) / kDqBlock) * 4);
+  auto rc_of = [&](int t) __attribute__((always_inline)) {
+    return make_rsrc(layer(W, ma, layer_of(t)).codes, N * (K / 2));
+  };
+  auto re_of = [&](int t) __attribute__((always_inline)) { return make_rsrc(layer(W, ma, layer_of(t)).e, N * kpr); };
+  auto rs_of = [&](int t) __attribute__((always_inline)) {
+    return make_rsrc(layer(W, ma, layer_of(t)).s, ((N * kpr + kDqBlock - 1) / kDqBlock) * 4);
+  };
   const rsrc_t rat = make_rsrc(AT2 + k0 * 2 * Rp, (K - k0) * 2 * Rp * 2);
 
   // dY rows [64p, +64) of a step, copied straight into LDS: part c moves rows
@@ -513,6 +580,8 @@ __global__ __launch_bounds__(kThreads, 1) void dx_gemm_kernel(Nf4View W, const u
   const uint32_t vy = (uint32_t)(((64 * p + (lane >> 3)) * N + 8 * ylch) * 2);
   const uint32_t y_gstride = (uint32_t)(8 * N * 2);
   const i32x4_t ryw = MULTI ? rsrc_words(dY, M * N * 2) : rsrc_words(dY + m0 * N, (M - m0) * N * 2);
+  const uint16_t* dY2 = nullptr;
+  if constexpr (PAIR) dY2 = ma.dY2;
   // MULTI: the byte offset of each row's token (past every buffer for none);
   // chunks past a row's end read as zero (they are the next token's)
   uint32_t vtok[MULTI ? 8 : 1];
@@ -530,7 +599,14 @@ __global__ __launch_bounds__(kThreads, 1) void dx_gemm_kernel(Nf4View W, const u
   auto copy_y_part = [&](char* t, int s, int c) __attribute__((always_inline)) {
     uint32_t vo = vy + c * y_gstride;
     if constexpr (MULTI) vo = (int64_t)(nfirst + s) * NSTEP + 8 * ylch < N ? vtok[c] : 0x7fffffffu;
-    dma_lds16(ryw, t + (64 * p + 8 * c) * 128, vo, (uint32_t)(nfirst + s) * 128u);
+    if constexpr (BLOCK) {
+      // (chunks past a row's end are the next row's: zeros)
+      const i32x4_t ry = PAIR && layer_of(s) ? rsrc_words(dY2 + m0 * N, (M - m0) * N * 2) : ryw;
+      vo = (int64_t)step_of(s) * NSTEP + 8 * ylch < N ? vo : 0x7fffffffu;
+      dma_lds16(ry, t + (64 * p + 8 * c) * 128, vo, (uint32_t)step_of(s) * 128u);
+    } else {
+      dma_lds16(ryw, t + (64 * p + 8 * c) * 128, vo, (uint32_t)(nfirst + s) * 128u);
+    }
   };
   auto copy_y = [&](char* t, int s) __attribute__((always_inline)) {
 #pragma unroll
@@ -586,6 +662,30 @@ __global__ __launch_bounds__(kThreads, 1) void dx_gemm_kernel(Nf4View W, const u
     }
   };
 
+  // BLOCK: the same for one layer's S and A
+  auto copy_block = [&](char* ts, char* tf, int l) __attribute__((always_inline)) {
+    if constexpr (BLOCK) {
+      const int i = lfirst + l, q = PAIR && i >= lper ? 1 : 0, col0l = 64 * (i - q * lper);
+      const rsrc_t ru3 = make_rsrc(ma.S + (int64_t)q * M * ma.C, M * ma.C * 2);
+      const int colu = col0l + 8 * ylch;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const int row = 64 * p + 8 * c + (lane >> 3);
+        buf_load_lds16(ru3, ts + (64 * p + 8 * c) * 128,
+                       colu < ma.cols ? (uint32_t)(((m0 + row) * ma.C + colu) * 2) : 0x7fffffffu, 0u);
+      }
+      const rsrc_t rf = make_rsrc(ma.F[q], K * ma.r * 2);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const int row = 16 * p + 2 * c + (lane >> 5);
+        const int64_t k = k0 + 8 * ((lane & 31) ^ ((row & 3) << 1));
+        const int t = col0l + row;
+        buf_load_lds16(rf, tf + (16 * p + 2 * c) * 512,
+                       t < ma.cols && k < K ? (uint32_t)(((int64_t)(t % ma.r) * K + k) * 2) : 0x7fffffffu, 0u);
+      }
+    }
+  };
+
   // Codes of weight rows t*64 + 2m and 2m + 1 (m = lane & 31), columns
   // [64p + 32h, +32) of the tile (h = lane >> 5, slice 2p + h): 16 bytes of
   // each row.  A column group (4 columns, 2 bytes) of both rows is one
@@ -599,8 +699,9 @@ __global__ __launch_bounds__(kThreads, 1) void dx_gemm_kernel(Nf4View W, const u
     u32x4_t c0, c1;
   };
   auto load_codes = [&](Codes& r, int t) __attribute__((always_inline)) {
-    r.c0 = buf_load16(rc, vcode, (uint32_t)(nfirst + t) * code_sstride);
-    r.c1 = buf_load16(rc, vcode + (uint32_t)(K / 2), (uint32_t)(nfirst + t) * code_sstride);
+    const rsrc_t rc = rc_of(t);
+    r.c0 = buf_load16(rc, vcode, (uint32_t)step_of(t) * code_sstride);
+    r.c1 = buf_load16(rc, vcode + (uint32_t)(K / 2), (uint32_t)step_of(t) * code_sstride);
   };
   const int crg = cm >> 2;
   const uint32_t code_wbase = (uint32_t)(crg * 128 + 4 * (cm & 3));
@@ -626,13 +727,13 @@ __global__ __launch_bounds__(kThreads, 1) void dx_gemm_kernel(Nf4View W, const u
     uint32_t e, s;
   };
   auto load_consts = [&](Consts& r, int t) __attribute__((always_inline)) {
-    const uint32_t blk = ((uint32_t)(nfirst + t) * NSTEP + (uint32_t)tb_row) * kpr + kb;
-    r.e = buf_load1(re, blk, 0u);
-    r.s = buf_load4(rs, (blk / kDqBlock) * 4u, 0u);
+    const uint32_t blk = ((uint32_t)step_of(t) * NSTEP + (uint32_t)tb_row) * kpr + kb;
+    r.e = buf_load1(re_of(t), blk, 0u);
+    r.s = buf_load4(rs_of(t), (blk / kDqBlock) * 4u, 0u);
   };
   auto build_table = [&](int t, const Consts& r) __attribute__((always_inline)) {
-    const bool row_ok = cols_ok && ((int64_t)(nfirst + t) * NSTEP + tb_row < N);
-    const float cp = decode_constant(r.e, __uint_as_float(r.s), mu);
+    const bool row_ok = cols_ok && ((int64_t)step_of(t) * NSTEP + tb_row < N);
+    const float cp = decode_constant(r.e, __uint_as_float(r.s), layer_of(t) ? mu2 : mu1);
     u32x4_t t0, t1;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -650,7 +751,10 @@ __global__ __launch_bounds__(kThreads, 1) void dx_gemm_kernel(Nf4View W, const u
   {
     Codes c0;
     Consts k0c;
-    copy_y(sa0, 0);
+    if (BLOCK && lsteps > 0)
+      copy_block(sa0, sw[0], 0);
+    else
+      copy_y(sa0, 0);
     load_codes(c0, 0);
     load_codes(cn, 1);
     load_consts(k0c, 0);
@@ -662,9 +766,24 @@ __global__ __launch_bounds__(kThreads, 1) void dx_gemm_kernel(Nf4View W, const u
     build_table(1, cnx);
   }
   __syncthreads();  // codes and tables of steps 0 and 1 in place
-  dequant_slice(std::true_type(), 0, 2 * p + 1, read_codes(0, 2 * p + 1), no_issue);
-  wait_vmem();
-  __syncthreads();  // step 0 in place
+  if constexpr (BLOCK) {
+    // the LoRA steps: beside each, the next one's tiles or n step 0
+#pragma unroll 1
+    for (int l = 0; l <= lsteps; ++l) {
+      if (l < lsteps) {
+        if (l > 0) copy_block(sab(l & 1), sw[l & 1], l);
+      } else {
+        if (l > 0) copy_y(sab(l & 1), 0);
+        dequant_slice(std::true_type(), 0, 2 * p + 1, read_codes(0, 2 * p + 1), no_issue);
+      }
+      wait_vmem();
+      __syncthreads();
+    }
+  } else {
+    dequant_slice(std::true_type(), 0, 2 * p + 1, read_codes(0, 2 * p + 1), no_issue);
+    wait_vmem();
+    __syncthreads();  // step 0 in place
+  }
 
   // Reduction steps 0 .. nsteps-2: build the tables of step s+2 (that
   // buffer was last read in the previous iteration; the constants were
@@ -679,7 +798,7 @@ __global__ __launch_bounds__(kThreads, 1) void dx_gemm_kernel(Nf4View W, const u
   // buffers or return zeros, and it is not used.
 #pragma unroll 1
   for (int s = 0; s + 1 < nsteps; ++s) {
-    char* const yn = sab((s + 1) & 1);
+    char* const yn = sab((s + 1 + wpar) & 1);
     build_table(s + 2, cc);
     asm volatile("" ::: "memory");
     copy_y(yn, s + 1);
@@ -691,6 +810,7 @@ __global__ __launch_bounds__(kThreads, 1) void dx_gemm_kernel(Nf4View W, const u
     wait_vmem();
     __syncthreads();
   }
+  if constexpr (BLOCK) return;
   // last reduction step: copy LoRA step 0 (sU and AT2 tiles) into the other
   // buffers; then the LoRA steps
   if (lsteps > 0) {
@@ -759,8 +879,28 @@ hipError_t launch_dx_gemm_adapters(const Nf4View& W, const uint16_t* dY, int64_t
   const int tm = (int)((M + TM - 1) / TM), tk = (int)((W.K + TK - 1) / TK);
   const unsigned grid = tile_grid(tm, tk, splits);
   const uint16_t* none = nullptr;
-  hipLaunchKernelGGL((dx_gemm_kernel<0, false, true>), dim3(grid), dim3(kThreads), 0, st, W, dY, M, none, none,
+  hipLaunchKernelGGL((dx_gemm_kernel<0, false, kMulti>), dim3(grid), dim3(kThreads), 0, st, W, dY, M, none, none,
                      (int64_t)0, dX, dx16 ? 1 : 0, tm, tk, splits, P, codebook(), ma);
+  return hipGetLastError();
+}
+
+// Of two layers the reduction runs over the rows of both.
+int block_dx_splits(int64_t M, int64_t N, int64_t K, int layers) {
+  const int64_t tiles = ((M + TM - 1) / TM) * ((K + TK - 1) / TK);
+  return gemm_splits(tiles, layers * ((N + NSTEP - 1) / NSTEP), M, K, SIZE_MAX);
+}
+
+hipError_t launch_dx_gemm_block(const Nf4View& W, const uint16_t* dY, int64_t M, const BlockGemmArgs& ma, bool pair,
+                                void* dX, bool dx16, int splits, float* P, hipStream_t st) {
+  const int tm = (int)((M + TM - 1) / TM), tk = (int)((W.K + TK - 1) / TK);
+  const unsigned grid = tile_grid(tm, tk, splits);
+  const uint16_t* none = nullptr;
+  if (pair)
+    hipLaunchKernelGGL((dx_gemm_kernel<0, false, kBlock2>), dim3(grid), dim3(kThreads), 0, st, W, dY, M, none, none,
+                       (int64_t)0, dX, dx16 ? 1 : 0, tm, tk, splits, P, codebook(), ma);
+  else
+    hipLaunchKernelGGL((dx_gemm_kernel<0, false, kBlock1>), dim3(grid), dim3(kThreads), 0, st, W, dY, M, none, none,
+                       (int64_t)0, dX, dx16 ? 1 : 0, tm, tk, splits, P, codebook(), ma);
   return hipGetLastError();
 }
 

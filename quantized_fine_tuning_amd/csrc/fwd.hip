@@ -58,7 +58,9 @@
 //     to P[split][M][N], summed in split order by splitk_reduce_kernel.
 #include <type_traits>
 
+#include "gate.h"
 #include "host.h"
+#include "modes.h"
 #include "tiling.h"
 
 namespace qnf4 {
@@ -93,7 +95,12 @@ __device__ __forceinline__ int xswz(int row, int chunk) {
 // the plan, and the LoRA steps run over the used adapters whose tokens the
 // tile holds, cols/64 steps each, rounded up (rows of other adapters read as
 // zero; the split reductions share these steps out as they do the K steps).
-template <int LSTEPS, bool F16, int TMV, bool MULTI = false>
+// BLOCK: one layer (kBlock1) or the two of a gated block (kBlock2) whose low-rank
+// factors come as three-part splits (BlockGemmArgs).  Of two layers a tile holds
+// as many weight rows of each, the gate's first: an MFMA wave's 64 columns are 32
+// of each layer's, the same ones, so that a lane holds both factors of the outputs
+// it writes; a LoRA step belongs to one layer and adds to its half.
+template <int LSTEPS, bool F16, int TMV, int MODE = kPlain>
 __global__ __launch_bounds__(kThreads, 1) void fwd_gemm_kernel(Nf4View W, const uint16_t* __restrict__ X,
                                                                int64_t M, const uint16_t* __restrict__ sT,
                                                                const uint16_t* __restrict__ B2,
@@ -101,8 +108,10 @@ __global__ __launch_bounds__(kThreads, 1) void fwd_gemm_kernel(Nf4View W, const 
                                                                int y_bf16, int tiles_m, int tiles_n,
                                                                int splits, float* __restrict__ P,
                                                                Codebook cb,
-                                                               std::conditional_t<MULTI, AdapterGemmArgs, NoAdapters> ma) {
+                                                               ModeArgs<MODE> ma) {
+  constexpr bool MULTI = MODE == kMulti, BLOCK = MODE >= kBlock1, PAIR = MODE == kBlock2;
   constexpr int TM = TMV, TN = 65536 / TMV;
+  constexpr int LAYERS = PAIR ? 2 : 1;
   constexpr int WGN = TN / 64;           // MFMA waves along N (4 or 2), each 128 x 64
   constexpr int XR = TM / kProdWaves;    // X rows copied per producer and step (64 or 128)
   constexpr int WR = TN / kProdWaves;    // weight rows decoded per producer (64 or 32)
@@ -117,7 +126,7 @@ __global__ __launch_bounds__(kThreads, 1) void fwd_gemm_kernel(Nf4View W, const 
   // the copies derived from it are then formed by scalar instructions)
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t K = W.K, N = W.N;
-  const int64_t m0 = (int64_t)tmi * TM, n0 = (int64_t)tni * TN;
+  const int64_t m0 = (int64_t)tmi * TM, n0 = (int64_t)tni * (TN / LAYERS);
   // this workgroup's K steps [kfirst, kfirst + ksteps) (step indices below
   // are relative to kfirst) and its LoRA steps
   const int kall = (int)(K / KSTEP);
@@ -138,6 +147,12 @@ __global__ __launch_bounds__(kThreads, 1) void fwd_gemm_kernel(Nf4View W, const 
       lsteps = split_first(sp + 1, splits, all) - lfirst;
     }
   }
+  // BLOCK: this workgroup's LoRA steps of the layers', lper each
+  if constexpr (BLOCK) {
+    lper = (ma.cols + 63) / 64;
+    lfirst = split_first(sp, splits, LAYERS * lper);
+    lsteps = split_first(sp + 1, splits, LAYERS * lper) - lfirst;
+  }
   // the sorted positions [p0, p1) of LoRA step l's adapter, relative to m0
   auto rows_of = [&](int l, int& p0, int& p1) __attribute__((always_inline)) {
     if constexpr (MULTI) {
@@ -153,7 +168,9 @@ __global__ __launch_bounds__(kThreads, 1) void fwd_gemm_kernel(Nf4View W, const 
   // past M, rows past N only output columns past N; neither is stored.)
   // Reads of weight data one or two steps past the last step stay inside
   // these buffers or return zeros; their results are never used.
-  const rsrc_t rc = make_rsrc(W.codes + n0 * (K / 2), (N - n0) * (K / 2));
+  // (PAIR: producers 2 and 3 decode the second layer's rows)
+  const bool second = PAIR && wave >= kMfmaWaves + 2;
+  const rsrc_t rc = make_rsrc(layer(W, ma, second).codes + n0 * (K / 2), (N - n0) * (K / 2));
 
   auto no_issue = [](int) {};
 
@@ -175,12 +192,16 @@ __global__ __launch_bounds__(kThreads, 1) void fwd_gemm_kernel(Nf4View W, const 
     // five (LDS reads return in order; about 1% on the step).  The B
     // fragments of the second k-half are read right after the MFMAs of
     // group 7.
-    const int arow = 128 * wm + lr, brow = 64 * wn + lr;
+    const int arow = 128 * wm + lr, brow = 64 / LAYERS * wn + lr;
+    // tile row of column block j (PAIR: blocks 0, 1 are the gate's, 2, 3 the other layer's)
+    auto block_row = [&](int j) __attribute__((always_inline)) {
+      return PAIR ? brow + 16 * (j & 1) + TN / 2 * (j >> 1) : brow + 16 * j;
+    };
     u32x4_t bfr[4], anext;
     auto read_b = [&](const char* wb, int ks, u32x4_t* b) __attribute__((always_inline)) {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        b[j] = *reinterpret_cast<const u32x4_t*>(wb + xswz(brow + 16 * j, 2 * kq + ks));
+        b[j] = *reinterpret_cast<const u32x4_t*>(wb + xswz(block_row(j), 2 * kq + ks));
     };
     auto read_a = [&](const char* xa, int g) __attribute__((always_inline)) {
       return *reinterpret_cast<const u32x4_t*>(xa + xswz(arow + 16 * (g & 7), 2 * kq + (g >> 3)));
@@ -238,6 +259,24 @@ __global__ __launch_bounds__(kThreads, 1) void fwd_gemm_kernel(Nf4View W, const 
       }
     };
 
+    // PAIR, a LoRA step of layer q: its two column blocks alone
+    auto lora_step_half = [&](auto q, const char* xa, const char* wb) __attribute__((always_inline)) {
+      constexpr int J0 = 2 * decltype(q)::value;
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        u32x4_t b[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          b[j] = *reinterpret_cast<const u32x4_t*>(wb + xswz(block_row(J0 + j), 2 * kq + ks));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const u32x4_t a = read_a(xa, 8 * ks + i);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) acc[i][J0 + j] = mfma16<F16>(a, b[j], acc[i][J0 + j]);
+        }
+      }
+    };
+
     __syncthreads();  // (the producers' prologue)
     __syncthreads();  // step 0 in place
 #pragma unroll 1
@@ -245,7 +284,19 @@ __global__ __launch_bounds__(kThreads, 1) void fwd_gemm_kernel(Nf4View W, const 
       mfma_step(sxb(s & 1), sw[s & 1]);
       __syncthreads();
     }
-    if constexpr (!MULTI) {
+    if constexpr (PAIR) {
+      mfma_step(sxb((ksteps - 1) & 1), sw[(ksteps - 1) & 1]);
+      __syncthreads();
+#pragma unroll 1
+      for (int l = 0; l < lsteps; ++l) {
+        const int s = ksteps + l;
+        const bool up = lfirst + l >= lper;
+        if (!up) lora_step_half(std::integral_constant<int, 0>(), sxb(s & 1), sw[s & 1]);
+        asm volatile("" ::: "memory");  // (two branches, not one of two arms, whose sums would not stay in place)
+        if (up) lora_step_half(std::integral_constant<int, 1>(), sxb(s & 1), sw[s & 1]);
+        __syncthreads();
+      }
+    } else if constexpr (!MULTI) {
 #pragma unroll 1
       for (int s = ksteps - 1; s < ksteps + lsteps; ++s) {
         mfma_step(sxb(s & 1), sw[s & 1]);
@@ -276,10 +327,45 @@ __global__ __launch_bounds__(kThreads, 1) void fwd_gemm_kernel(Nf4View W, const 
     // epilogue: lane holds rows 128wm + 16i + 4kq + v of column 64wn + 16j + lr.
     // The row/column bases go through an empty asm so that their address
     // arithmetic is not hoisted above the main loop (it would stay live there).
-    int row0 = 128 * wm + 4 * kq, col0 = 64 * wn + lr;
+    int row0 = 128 * wm + 4 * kq, col0 = 64 / LAYERS * wn + lr;
     asm volatile("" : "+v"(row0), "+v"(col0));
-    const bool full = (m0 + TM <= M) && (n0 + TN <= N);
-    if constexpr (MULTI) {
+    const bool full = (m0 + TM <= M) && (n0 + TN / LAYERS <= N);
+    if constexpr (PAIR) {
+      if (splits > 1) {
+        // rows of a split's partials: the gate's N columns, then the other layer's
+        float* Pp = P + ((int64_t)sp * M + m0 + row0) * 2 * N + n0 + col0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int64_t m = m0 + row0 + 16 * i + v, n = n0 + col0 + 16 * (j & 1);
+              if (full || (m < M && n < N)) Pp[(16 * i + v) * 2 * N + (j >> 1) * N + 16 * (j & 1)] = acc[i][j][v];
+            }
+      } else {
+        uint16_t* const H = static_cast<uint16_t*>(Y);
+        const int64_t at0 = (m0 + row0) * N + n0 + col0;
+        const bool save = ma.G != nullptr;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const int64_t m = m0 + row0 + 16 * i + v, n = n0 + col0 + 16 * j;
+              if (!full && (m >= M || n >= N)) continue;
+              const int64_t at = at0 + (int64_t)(16 * i + v) * N + 16 * j;
+              const float g = acc[i][j][v], u = acc[i][j + 2][v];
+              H[at] = (uint16_t)(pack16<F16>(gate_act(ma.act, g) * u, 0.0f) & 0xffffu);
+              if (save) {
+                const uint32_t gu = pack16<F16>(g, u);
+                ma.G[at] = (uint16_t)(gu & 0xffffu);
+                ma.U[at] = (uint16_t)(gu >> 16);
+              }
+            }
+      }
+    } else if constexpr (MULTI) {
       // rows back to their tokens, as buffer stores: a row or column past the
       // output's end gets an offset past the buffer's (no branches; the 16-bit
       // output and the partials of a split are below 2^31 bytes)
@@ -378,10 +464,10 @@ __global__ __launch_bounds__(kThreads, 1) void fwd_gemm_kernel(Nf4View W, const 
   // XR = 128 on the tall one).
   const int p = wave - kMfmaWaves;
   const uint32_t kpr = (uint32_t)(K / kBlock);  // blocks per weight row
-  const float mu = *W.mu;
+  const float mu = *layer(W, ma, second).mu;
   const rsrc_t rt = make_rsrc(sT + m0 * 2 * Rp, (M - m0) * 2 * Rp * 2);
-  const rsrc_t re = make_rsrc(W.e + n0 * kpr, (N - n0) * kpr);
-  const rsrc_t rs = make_rsrc(W.s, ((N * kpr + kDqBlock - 1) / kDqBlock) * 4);
+  const rsrc_t re = make_rsrc(layer(W, ma, second).e + n0 * kpr, (N - n0) * kpr);
+  const rsrc_t rs = make_rsrc(layer(W, ma, second).s, ((N * kpr + kDqBlock - 1) / kDqBlock) * 4);
   const rsrc_t rb = make_rsrc(B2 + n0 * 2 * Rp, (N - n0) * 2 * Rp * 2);
 
   // X rows [XR p, +XR) of a step, copied straight into LDS: part c
@@ -452,6 +538,28 @@ __global__ __launch_bounds__(kThreads, 1) void fwd_gemm_kernel(Nf4View W, const 
       }
     }
   };
+  // BLOCK: the same for one layer's S and factor; of two layers the producers of
+  // the other one's rows copy S alone
+  auto copy_block = [&](char* ts, char* tf, int l) __attribute__((always_inline)) {
+    if constexpr (BLOCK) {
+      const int i = lfirst + l, q = PAIR && i >= lper ? 1 : 0, col = 64 * (i - q * lper) + 8 * xlch;
+      const bool in = col < ma.cols;
+      const rsrc_t rS = make_rsrc(ma.S + (int64_t)q * M * ma.C, M * ma.C * 2);
+#pragma unroll
+      for (int c = 0; c < XR / 8; ++c) {
+        const int row = XR * p + 8 * c + (lane >> 3);
+        buf_load_lds16(rS, ts + (XR * p + 8 * c) * 128, in ? (uint32_t)(((m0 + row) * ma.C + col) * 2) : 0x7fffffffu, 0u);
+      }
+      if (PAIR && q != (p >> 1)) return;
+      const rsrc_t rf = make_rsrc(ma.F[q], N * ma.r * 2);
+#pragma unroll
+      for (int c = 0; c < WR / 8; ++c) {
+        const int row = (PAIR ? WR * (p & 1) : WR * p) + 8 * c + (lane >> 3);
+        buf_load_lds16(rf, tf + (WR * p + 8 * c) * 128,
+                       in ? (uint32_t)(((n0 + row) * ma.r + col % ma.r) * 2) : 0x7fffffffu, 0u);
+      }
+    }
+  };
   using XRows = std::integral_constant<int, XR>;
   using WRows = std::integral_constant<int, WR>;
 
@@ -459,8 +567,9 @@ __global__ __launch_bounds__(kThreads, 1) void fwd_gemm_kernel(Nf4View W, const 
   // holding its e4m3 byte and its group scale, and per step its 32 bytes of
   // codes (the 16 of half lane / WR when two lanes share the row).
   const int trow = WR * p + lane % WR, half = lane / WR;
-  const uint32_t ve_me = (uint32_t)trow * kpr;
-  const uint32_t blk_me = (uint32_t)(n0 + trow) * kpr;
+  const int nrow = PAIR ? WR * (p & 1) + lane % WR : trow;  // from the layer's row n0 on
+  const uint32_t ve_me = (uint32_t)nrow * kpr;
+  const uint32_t blk_me = (uint32_t)(n0 + nrow) * kpr;
   struct Consts {
     uint32_t e, s;
   };
@@ -468,7 +577,7 @@ __global__ __launch_bounds__(kThreads, 1) void fwd_gemm_kernel(Nf4View W, const 
     r.e = buf_load4(re, (ve_me + (uint32_t)(kfirst + t)) & ~3u, 0u);
     r.s = buf_load4(rs, ((blk_me + (uint32_t)(kfirst + t)) / kDqBlock) * 4u, 0u);
   };
-  const uint32_t vrow = (uint32_t)trow * (uint32_t)(K / 2);
+  const uint32_t vrow = (uint32_t)nrow * (uint32_t)(K / 2);
   auto load_row = [&](u32x4_t* c, int t) __attribute__((always_inline)) {
     if constexpr (HALVES == 1) {
       c[0] = buf_load16(rc, vrow, (uint32_t)(kfirst + t) * 32u);
@@ -570,6 +679,8 @@ __global__ __launch_bounds__(kThreads, 1) void fwd_gemm_kernel(Nf4View W, const 
   if (lsteps > 0) {
     if constexpr (MULTI) {
       copy_multi(sxb(ksteps & 1), sw[ksteps & 1], 0);
+    } else if constexpr (BLOCK) {
+      copy_block(sxb(ksteps & 1), sw[ksteps & 1], 0);
     } else {
       copy_lora(rt, sxb(ksteps & 1), 0, XRows{});
       copy_lora(rb, sw[ksteps & 1], 0, WRows{});
@@ -583,6 +694,8 @@ __global__ __launch_bounds__(kThreads, 1) void fwd_gemm_kernel(Nf4View W, const 
     if (l + 1 < lsteps) {
       if constexpr (MULTI) {
         copy_multi(sxb((s + 1) & 1), sw[(s + 1) & 1], l + 1);
+      } else if constexpr (BLOCK) {
+        copy_block(sxb((s + 1) & 1), sw[(s + 1) & 1], l + 1);
       } else {
         copy_lora(rt, sxb((s + 1) & 1), l + 1, XRows{});
         copy_lora(rb, sw[(s + 1) & 1], l + 1, WRows{});
@@ -641,11 +754,43 @@ hipError_t launch_fwd_gemm_adapters(const Nf4View& W, const uint16_t* X, int64_t
   const unsigned grid = tile_grid(tm, tn, splits);
   const uint16_t* none = nullptr;
   if (tall)
-    hipLaunchKernelGGL((fwd_gemm_kernel<0, false, 512, true>), dim3(grid), dim3(kThreads), 0, st, W, X, M, none, none,
+    hipLaunchKernelGGL((fwd_gemm_kernel<0, false, 512, kMulti>), dim3(grid), dim3(kThreads), 0, st, W, X, M, none, none,
                        (int64_t)0, Y, y16 ? 1 : 0, tm, tn, splits, P, codebook(), ma);
   else
-    hipLaunchKernelGGL((fwd_gemm_kernel<0, false, 256, true>), dim3(grid), dim3(kThreads), 0, st, W, X, M, none, none,
+    hipLaunchKernelGGL((fwd_gemm_kernel<0, false, 256, kMulti>), dim3(grid), dim3(kThreads), 0, st, W, X, M, none, none,
                        (int64_t)0, Y, y16 ? 1 : 0, tm, tn, splits, P, codebook(), ma);
+  return hipGetLastError();
+}
+
+// Tiles of the gated block's forward, whose N is that of one layer: half a tile's
+// weight rows are the gate's.
+int gated_fwd_splits(int64_t M, int64_t N, int64_t K) {
+  const int64_t tiles = ((M + TM - 1) / TM) * ((2 * N + TN - 1) / TN);
+  return gemm_splits(tiles, K / KSTEP, M, 2 * N, SIZE_MAX);
+}
+
+hipError_t launch_fwd_gemm_block(const Nf4View& W, const uint16_t* X, int64_t M, const BlockGemmArgs& ma, bool pair,
+                                 void* Y, bool y16, int splits, float* P, hipStream_t st) {
+  const bool tall = fwd_tall(M);
+  const int tmv = tall ? 512 : 256, tnv = 65536 / tmv / (pair ? 2 : 1);
+  const int tm = (int)((M + tmv - 1) / tmv), tn = (int)((W.N + tnv - 1) / tnv);
+  const unsigned grid = tile_grid(tm, tn, splits);
+  const uint16_t* none = nullptr;
+#define QNF4_FWD_BLOCK(TMV, MODE)                                                                                  \
+  hipLaunchKernelGGL((fwd_gemm_kernel<0, false, TMV, MODE>), dim3(grid), dim3(kThreads), 0, st, W, X, M, none, none, \
+                     (int64_t)0, Y, y16 ? 1 : 0, tm, tn, splits, P, codebook(), ma)
+  if (pair) {
+    if (tall)
+      QNF4_FWD_BLOCK(512, kBlock2);
+    else
+      QNF4_FWD_BLOCK(256, kBlock2);
+  } else {
+    if (tall)
+      QNF4_FWD_BLOCK(512, kBlock1);
+    else
+      QNF4_FWD_BLOCK(256, kBlock1);
+  }
+#undef QNF4_FWD_BLOCK
   return hipGetLastError();
 }
 

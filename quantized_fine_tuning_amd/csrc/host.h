@@ -271,6 +271,79 @@ struct GemvAdapters {
 struct NoAdapters {};
 constexpr int64_t adapter_cols(int64_t r) { return round_up(3 * r, 64); }
 
+// Adapters with dropout, one layer or the two of a gated block -------------------
+// The kept share of an adapter's input (dropout.h): elements whose piece is below
+// `out` are dropped, the others count `scale` = 65536 / (65536 - out) times.
+// out = 0: nothing is dropped.  step: null, or a number in device memory that is
+// added to the offset when a kernel runs.
+struct DropView {
+  uint32_t key0, key1, off0, off1, out;
+  float scale;
+  const uint64_t* step;
+};
+enum { kActSilu = 0, kActGeluTanh = 1 };
+// The adapters' share of a dequant-in-tile GEMM over one or two layers of the
+// same N, K and r: S [layers][M, C] the three-part splits of the scaled low-rank
+// factors (as AdapterGemmArgs), F the adapters' factors: B [N, r] (forward) or A
+// [r, K] (dX).  Forward of two layers: the gate's weight is the kernel's W, the
+// up projection's W2, and the outputs are H = act(G)*U and, if given, G and U.
+// dX: dY2 is the second layer's, and the low-rank sums are kept by the mask of X.
+struct BlockGemmArgs {
+  const uint16_t* S;
+  const uint16_t* F[2];
+  int r, C, cols;  // cols: the columns of S that enter, 2r or 3r
+  Nf4View W2;
+  uint16_t *G, *U;
+  int act;
+  const uint16_t* dY2;
+  DropView drop;
+};
+
+// One layer (gate and up projection: two) with its adapters.
+struct BlockView {
+  Nf4View W[2];
+  const uint16_t* A[2];
+  const uint16_t* B[2];
+  int r, layers;
+  float scale;  // alpha / r
+  DropView drop;
+};
+// Outputs of the gated block's forward pass; G and U may be null.
+struct GatedOut {
+  uint16_t *H, *G, *U;
+  int act;
+};
+// Inputs of its backward pass.
+struct GatedIn {
+  const uint16_t *dH, *G, *U;
+  int act;
+};
+struct BlockFwdLayout {
+  // bf16 S [layers][M][C] of s·T; an fp32 area: the partial sums of T, then the
+  // GEMM's (splits > 1); M <= 16: T's partial tiles alone
+  size_t off_P, total;
+  int splits, slices;
+};
+struct BlockBwdLayout {
+  // two layers: bf16 dG, dU [2][M][N]; bf16 splits of s·V and s·T [layers][M][C];
+  // one fp32 area: the partial sums of V and T, the dX GEMM's, the gradients'
+  size_t off_dY, off_V, off_T, off_P, total;
+  int splits, slices_T, slices_V, units;
+  int64_t unit;
+};
+BlockFwdLayout block_fwd_layout(int64_t M, int64_t N, int64_t K, int r, int layers);
+BlockBwdLayout block_bwd_layout(int64_t M, int64_t N, int64_t K, int r, int layers);
+// The largest layout totals over M in [0, M_max].
+size_t block_fwd_ws_max(int64_t M_max, int64_t N, int64_t K, int r, int layers);
+size_t block_bwd_ws_max(int64_t M_max, int64_t N, int64_t K, int r, int layers);
+// T: [layers][M][r] or null.  One layer: Y; two: out.
+hipError_t launch_block_fwd(const BlockView& b, const uint16_t* X, int64_t M, void* Y, bool y16, float* T,
+                            const GatedOut& out, char* ws, const BlockFwdLayout& L, hipStream_t st);
+// One layer: dY; two: in.
+hipError_t launch_block_bwd(const BlockView& b, const uint16_t* X, int64_t M, const uint16_t* dY, const GatedIn& in,
+                            const float* T_saved, void* dX, bool dx16, float* const dA[2], float* const dB[2], char* ws,
+                            const BlockBwdLayout& L, hipStream_t st);
+
 // Tiles of a plan: one per 64 tokens and one per used adapter at most.
 inline int64_t plan_tiles(int64_t M, int count) { return M / 64 + (count < M ? count : M); }
 
