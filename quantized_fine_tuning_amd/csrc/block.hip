@@ -29,8 +29,8 @@ hipError_t launch_splitk_reduce(const float* P, int splits, int64_t n, void* out
 hipError_t launch_gemv_sums(const Nf4View& W, const uint16_t* X, int64_t M, const float* P, int S, int JT,
                             const uint16_t* B, int32_t r, float scale, void* Y, bool y16, float* T, bool f16,
                             hipStream_t st);
-hipError_t launch_gated_gemv(const BlockView& b, const uint16_t* X, int64_t M, const float* T, int t_layer,
-                             const GatedOut& out, hipStream_t st);
+hipError_t launch_gated_gemv(const BlockView& b, const uint16_t* X, int64_t M, const uint16_t* S, const GatedOut& out,
+                             hipStream_t st);
 int fwd_gemm_splits(int64_t M, int64_t N, int64_t K, size_t cap);
 int gated_fwd_splits(int64_t M, int64_t N, int64_t K);
 int block_dx_splits(int64_t M, int64_t N, int64_t K, int layers);
@@ -171,13 +171,15 @@ __global__ __launch_bounds__(256) void block_down_kernel(DownJob t, DownJob u, i
 }
 
 // T for up to 16 tokens, in one launch: a workgroup per (token, 4 ranks, layer),
-// its 4 waves sharing the reduction, 8 elements per lane and step.  T [layers][M]
-// [r] if given, and Tt in the dequant-GEMV's tile layout, t_layer floats a layer.
+// its 4 waves sharing the reduction, 8 elements per lane and step.  What is given
+// of: T [layers][M][r]; Tt, the single layer's in the dequant-GEMV's tile layout; S
+// [layers][M][C], the three-part splits of scale·T.
 constexpr int kFewRanks = 4;
 __global__ __launch_bounds__(256) void block_few_down_kernel(const uint16_t* __restrict__ X, int64_t M, int64_t K,
                                                              const uint16_t* __restrict__ A0,
                                                              const uint16_t* __restrict__ A1, int r, DropView drop,
-                                                             float* __restrict__ T, float* __restrict__ Tt, int t_layer) {
+                                                             float scale, float* __restrict__ T,
+                                                             float* __restrict__ Tt, uint16_t* __restrict__ S) {
   constexpr int UN = 2;
   __shared__ float s_part[4][kFewRanks];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -214,7 +216,13 @@ __global__ __launch_bounds__(256) void block_few_down_kernel(const uint16_t* __r
   const int j = j0 + tid;
   const float t = __fmul_rn(((s_part[0][tid] + s_part[1][tid]) + s_part[2][tid]) + s_part[3][tid], drop.scale);
   if (T) T[(layer * M + m) * r + j] = t;
-  Tt[layer * t_layer + (j >> 4) * 256 + 16 * m + (j & 15)] = t;
+  if (Tt) Tt[(j >> 4) * 256 + 16 * m + (j & 15)] = t;
+  if (S) {
+    uint16_t o[3];
+    split3(__fmul_rn(scale, t), o);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) S[(layer * M + m) * adapter_cols(r) + i * r + j] = o[i];
+  }
 }
 
 // The slices added in order, 16 tokens x 16 ranks per workgroup: v = mult·Σ, as
@@ -376,16 +384,30 @@ __device__ __forceinline__ void gradient_unit(const GradientJob& J, int layer, i
       }
 }
 
+// The sum of dX's split partials (n4 = 0: none), for the workgroups past the units'.
+struct SplitSum {
+  const f32x4_t* P;
+  int splits;
+  int64_t n4;
+  void* out;
+  int out16;
+};
 // blockIdx.x: 128 columns of dA, then of dB; y: the unit; z: block of 16·NJ ranks
 // of each layer in turn.  P [units][layers][r·(K + N)], or null with one unit.
 template <int NJ>
 __global__ __launch_bounds__(256) void block_gradient_kernel(GradientJob ja, GradientJob jb, unsigned tiles_a, int64_t M,
-                                                             int r, int64_t unit, int layers, DropView drop,
-                                                             float* __restrict__ P) {
+                                                             int r, int64_t unit, int units, int layers, DropView drop,
+                                                             float* __restrict__ P, SplitSum sum) {
   __shared__ __attribute__((aligned(1024))) char sl[kGradRing * 32 * 256];
   __shared__ __attribute__((aligned(1024))) char ss[kGradRing * 4 * (NJ == 4 ? 3 : NJ == 2 ? 2 : 1) * 1024];
   const int blocks = (r + 16 * NJ - 1) / (16 * NJ);
   const int layer = (int)blockIdx.z / blocks, j0 = 16 * NJ * ((int)blockIdx.z - layer * blocks);
+  if ((int)blockIdx.y >= units) {
+    const int64_t block = ((int64_t)(blockIdx.y - units) * gridDim.z + blockIdx.z) * gridDim.x + blockIdx.x;
+    const int64_t i = 256 * block + threadIdx.x;
+    if (i < sum.n4) splitk_sum4<false>(sum.P, sum.splits, sum.n4, i, sum.out, sum.out16);
+    return;
+  }
   const int64_t p0 = unit * blockIdx.y, p1 = std::min<int64_t>(p0 + unit, M);
   const int64_t part = ((int64_t)blockIdx.y * layers + layer) * r * (ja.cols + jb.cols);
   drop = drawn(drop);
@@ -420,17 +442,18 @@ __global__ __launch_bounds__(256) void block_gradient_finish_kernel(float* dA0, 
 // Element by element
 // ---------------------------------------------------------------------------
 
-// The gated block's split partials [splits][M][2N] (each row the gate's N columns,
-// then the other layer's) added in order, and its outputs; four columns a thread.
+// The gated block's split partials added in order, and its outputs; four columns a
+// thread.  rows: [splits][M][2N], each row the gate's N columns, then the other
+// layer's; else [2][splits][M][N].
 __global__ __launch_bounds__(256) void gated_reduce_kernel(const f32x4_t* __restrict__ P, int splits, int64_t M, int64_t N,
-                                                           GatedOut out) {
+                                                           bool rows, GatedOut out) {
   const int64_t n4 = N / 4, total = M * n4;
+  const int64_t up = rows ? n4 : splits * total, split = rows ? 2 * total : total;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += 256 * (int64_t)gridDim.x) {
-    const int64_t m = i / n4, c = i - m * n4;
-    const f32x4_t* const p = P + 2 * m * n4 + c;
-    f32x4_t g = p[0], u = p[n4];
+    const f32x4_t* const p = P + (rows ? i + i / n4 * n4 : i);
+    f32x4_t g = p[0], u = p[up];
     for (int s = 1; s < splits; ++s) {
-      const f32x4_t a = p[2 * s * total], b = p[2 * s * total + n4];
+      const f32x4_t a = p[s * split], b = p[s * split + up];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         g[e] += a[e];
@@ -552,13 +575,19 @@ BlockFwdLayout block_fwd_layout(int64_t M, int64_t N, int64_t K, int r, int laye
   L.splits = 1;
   if (M == 0) return L;
   if (M <= 16) {
-    L.total = layers * cdiv(r, 16) * 1024;  // T's tiles
+    L.total = layers == 1 ? (int64_t)cdiv(r, 16) * 1024 : 2 * M * adapter_cols(r) * 2;  // T's tiles; S
     return L;
   }
-  L.splits = layers == 2 ? gated_fwd_splits(M, N, K) : fwd_gemm_splits(M, N, K, SIZE_MAX);
-  L.slices = down_slices(M, K, r, layers);
+  if (M <= kMidTokens) {
+    L.splits = mid_fwd_plan(M, N, K).splits;
+  } else {
+    L.splits = layers == 2 ? gated_fwd_splits(M, N, K) : fwd_gemm_splits(M, N, K, SIZE_MAX);
+    L.slices = down_slices(M, K, r, layers);
+  }
   L.off_P = round_up(layers * M * adapter_cols(r) * 2, 256);
-  const int64_t gemm = L.splits > 1 ? (int64_t)L.splits * M * N * layers * 4 : 0;
+  // (two layers of few tokens leave fp32 sums whatever their splits)
+  const bool sums = L.splits > 1 || (layers == 2 && M <= kMidTokens);
+  const int64_t gemm = sums ? (int64_t)L.splits * M * N * layers * 4 : 0;
   L.total = L.off_P + round_up(std::max(gemm, (int64_t)L.slices * layers * M * r * 4), 256);
   return L;
 }
@@ -566,7 +595,7 @@ BlockFwdLayout block_fwd_layout(int64_t M, int64_t N, int64_t K, int r, int laye
 BlockBwdLayout block_bwd_layout(int64_t M, int64_t N, int64_t K, int r, int layers) {
   BlockBwdLayout L{};
   if (M == 0) return L;
-  L.splits = block_dx_splits(M, N, K, layers);
+  L.splits = M <= kMidTokens ? layers * mid_dx_splits(M, N, K) : block_dx_splits(M, N, K, layers);
   L.slices_T = down_slices(M, K, r, layers);
   L.slices_V = down_slices(M, N, r, layers);
   L.unit = gradient_unit(M, N, K, r, layers);
@@ -586,15 +615,17 @@ BlockBwdLayout block_bwd_layout(int64_t M, int64_t N, int64_t K, int r, int laye
   return L;
 }
 
-// The largest totals over M in [0, M_max].  Split counts are constant within a
-// band of 256 tokens and slice counts between multiples of 64, and what they
-// count grows with M: the last of every 64 and the first of the next are taken.
+// The largest totals over M in [0, M_max].  Up to kMidTokens tokens each is taken.
+// Above, split counts are constant within a band of 256 tokens and slice counts
+// between multiples of 64, and what they count grows with M: the last of every 64
+// and the first of the next are taken.
 namespace {
 template <typename F>
 size_t most_of(int64_t M_max, F&& total) {
   size_t most = 0;
-  for (int64_t M = 1; M <= std::min<int64_t>(M_max, 17); ++M) most = std::max(most, total(M));
-  for (int64_t top = 64; M_max > 17; top += 64) {
+  for (int64_t M = 1; M <= std::min(M_max, kMidTokens); ++M) most = std::max(most, total(M));
+  if (M_max > kMidTokens) most = std::max(most, total(kMidTokens + 1));
+  for (int64_t top = kMidTokens + 64; M_max > kMidTokens; top += 64) {
     most = std::max(most, total(std::min(top, M_max)));
     if (top >= M_max) break;
     most = std::max(most, total(top + 1));
@@ -616,16 +647,37 @@ hipError_t launch_block_fwd(const BlockView& b, const uint16_t* X, int64_t M, vo
   const bool pair = b.layers == 2;
   float* P = reinterpret_cast<float*>(ws + L.off_P);
   if (M <= 16) {
-    const int tiles = (int)cdiv(b.r, 16);
+    uint16_t* const S = pair ? reinterpret_cast<uint16_t*>(ws) : nullptr;
     block_few_down_kernel<<<dim3((unsigned)M, (unsigned)(b.r / kFewRanks), (unsigned)b.layers), 256, 0, st>>>(
-        X, M, K, b.A[0], b.A[1], b.r, b.drop, T, P, 256 * tiles);
+        X, M, K, b.A[0], b.A[1], b.r, b.drop, b.scale, T, pair ? nullptr : P, S);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     float* const kept = nullptr;  // (T is written)
-    return pair ? launch_gated_gemv(b, X, M, P, 256 * tiles, out, st)
-                : launch_gemv_sums(b.W[0], X, M, P, 1, tiles, b.B[0], b.r, b.scale, Y, y16, kept, false, st);
+    return pair ? launch_gated_gemv(b, X, M, S, out, st)
+                : launch_gemv_sums(b.W[0], X, M, P, 1, (int)cdiv(b.r, 16), b.B[0], b.r, b.scale, Y, y16, kept, false, st);
   }
   uint16_t* S = reinterpret_cast<uint16_t*>(ws);
+  const int C = (int)adapter_cols(b.r), cols = (pair || y16 ? 2 : 3) * b.r;
+  auto reduce = [&](bool rows) {
+    gated_reduce_kernel<<<std::min(cdiv(M * N / 4, 256), 2048u), 256, 0, st>>>(reinterpret_cast<const f32x4_t*>(P),
+                                                                               L.splits, M, N, rows, out);
+    return hipGetLastError();
+  };
+  if (M <= kMidTokens) {
+    float* const none = nullptr;
+    block_few_down_kernel<<<dim3((unsigned)M, (unsigned)(b.r / kFewRanks), (unsigned)b.layers), 256, 0, st>>>(
+        X, M, K, b.A[0], b.A[1], b.r, b.drop, b.scale, T, none, S);
+    hipError_t e = hipGetLastError();
+    const MidPlan plan = mid_fwd_plan(M, N, K);
+    for (int l = 0; l < b.layers && e == hipSuccess; ++l) {
+      float* const Pl = P + (int64_t)l * L.splits * M * N;
+      e = launch_mid_fwd_block(b.W[l], X, M, DenseGemmArgs{S + l * M * C, b.B[l], b.r, C, 1, cols, (int)M, b.drop},
+                               pair ? (void*)Pl : Y, !pair && y16, plan, Pl, st);
+    }
+    if (e != hipSuccess) return e;
+    if (pair) return reduce(false);
+    return L.splits > 1 ? launch_splitk_reduce(P, L.splits, M * N, Y, y16, false, st) : hipSuccess;
+  }
   const DownJob t{{X, X}, {b.A[0], b.A[1]}, K, P, L.slices};
   hipError_t e = launch_down(t, DownJob{}, M, b.r, b.layers, b.drop, st);
   if (e != hipSuccess) return e;
@@ -634,15 +686,10 @@ hipError_t launch_block_fwd(const BlockView& b, const uint16_t* X, int64_t M, vo
   if ((e = hipGetLastError()) != hipSuccess) return e;
   // (the partial sums of T have been consumed: P now takes the split partials.  16-bit outputs take
   // 16 bits of s·T, as AdapterGemmArgs says)
-  const BlockGemmArgs ma{S,          {b.B[0], b.B[1]}, b.r,   (int)adapter_cols(b.r), (pair || y16 ? 2 : 3) * b.r,
-                         b.W[pair ? 1 : 0], out.G,           out.U, out.act,                nullptr,
-                         b.drop};
+  const BlockGemmArgs ma{S, {b.B[0], b.B[1]}, b.r, C, cols, b.W[pair ? 1 : 0], out.G, out.U, out.act, nullptr, b.drop};
   e = launch_fwd_gemm_block(b.W[0], X, M, ma, pair, pair ? (void*)out.H : Y, y16, L.splits, P, st);
   if (e != hipSuccess || L.splits == 1) return e;
-  if (!pair) return launch_splitk_reduce(P, L.splits, M * N, Y, y16, false, st);
-  gated_reduce_kernel<<<std::min(cdiv(M * N / 4, 256), 2048u), 256, 0, st>>>(reinterpret_cast<const f32x4_t*>(P), L.splits,
-                                                                             M, N, out);
-  return hipGetLastError();
+  return pair ? reduce(true) : launch_splitk_reduce(P, L.splits, M * N, Y, y16, false, st);
 }
 
 hipError_t launch_block_bwd(const BlockView& b, const uint16_t* X, int64_t M, const uint16_t* dY, const GatedIn& in,
@@ -683,23 +730,36 @@ hipError_t launch_block_bwd(const BlockView& b, const uint16_t* X, int64_t M, co
   const FactorJob fv{PV, L.slices_V, nullptr, nullptr, SV, b.drop.scale, b.scale};
   block_factor_kernel<<<dim3(cdiv(M, 16), cdiv(r, 16), 2u * layers), 256, 0, st>>>(ft, fv, M, b.r, layers);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  const BlockGemmArgs ma{SV,  {b.A[0], b.A[1]}, b.r,     (int)adapter_cols(r), (dx16 ? 2 : 3) * b.r,
-                         b.W[pair ? 1 : 0],     nullptr, nullptr,              in.act,
-                         d[1], b.drop};
-  e = launch_dx_gemm_block(b.W[0], d[0], M, ma, pair, dX, dx16, L.splits, P, st);
-  if (e == hipSuccess && L.splits > 1) e = launch_splitk_reduce(P, L.splits, M * K, dX, dx16, false, st);
+  const int C = (int)adapter_cols(r), cols = (dx16 ? 2 : 3) * b.r;
+  if (M <= kMidTokens) {
+    // (each layer's splits into their own partials, added together)
+    const int splits = L.splits / layers;
+    for (int l = 0; l < layers && e == hipSuccess; ++l) {
+      float* const Pl = P + (int64_t)l * splits * M * K;
+      e = launch_mid_dx_block(b.W[l], d[l], M, DenseGemmArgs{SV + l * M * C, b.A[l], b.r, C, 1, cols, (int)M, b.drop},
+                              L.splits > 1 ? (void*)Pl : dX, L.splits == 1 && dx16, splits, Pl, st);
+    }
+  } else {
+    const BlockGemmArgs ma{SV, {b.A[0], b.A[1]}, b.r, C, cols, b.W[pair ? 1 : 0], nullptr, nullptr, in.act, d[1], b.drop};
+    e = launch_dx_gemm_block(b.W[0], d[0], M, ma, pair, dX, dx16, L.splits, P, st);
+  }
+  // one unit of tokens: the sum of dX's splits comes with the gradients
+  const bool tail = L.splits > 1 && L.units == 1;
+  if (e == hipSuccess && L.splits > 1 && !tail) e = launch_splitk_reduce(P, L.splits, M * K, dX, dx16, false, st);
   if (e != hipSuccess) return e;
   const GradientJob ja{{X, X}, SV, K, {dA[0], dA[1]}, 0}, jb{{d[0], d[1]}, ST, N, {dB[0], dB[1]}, r * K};
   const int nj = rank_blocks(b.r);
   const unsigned ta = cdiv(K, 128);
-  const dim3 grid(ta + cdiv(N, 128), (unsigned)L.units, (unsigned)layers * cdiv(r, 16 * nj));
+  const unsigned gx = ta + cdiv(N, 128), gz = (unsigned)layers * cdiv(r, 16 * nj);
+  const SplitSum sum{reinterpret_cast<const f32x4_t*>(P), L.splits, tail ? M * K / 4 : 0, dX, dx16 ? 1 : 0};
+  const dim3 grid(gx, (unsigned)L.units + cdiv(sum.n4, (int64_t)256 * gx * gz), gz);
   float* const parts = L.units > 1 ? P : nullptr;
   if (nj == 1)
-    block_gradient_kernel<1><<<grid, 256, 0, st>>>(ja, jb, ta, M, b.r, L.unit, layers, b.drop, parts);
+    block_gradient_kernel<1><<<grid, 256, 0, st>>>(ja, jb, ta, M, b.r, L.unit, L.units, layers, b.drop, parts, sum);
   else if (nj == 2)
-    block_gradient_kernel<2><<<grid, 256, 0, st>>>(ja, jb, ta, M, b.r, L.unit, layers, b.drop, parts);
+    block_gradient_kernel<2><<<grid, 256, 0, st>>>(ja, jb, ta, M, b.r, L.unit, L.units, layers, b.drop, parts, sum);
   else
-    block_gradient_kernel<4><<<grid, 256, 0, st>>>(ja, jb, ta, M, b.r, L.unit, layers, b.drop, parts);
+    block_gradient_kernel<4><<<grid, 256, 0, st>>>(ja, jb, ta, M, b.r, L.unit, L.units, layers, b.drop, parts, sum);
   e = hipGetLastError();
   if (e != hipSuccess || L.units == 1) return e;
   block_gradient_finish_kernel<<<dim3(std::min(cdiv(r * (K + N), 1024), 1024u), (unsigned)layers), 256, 0, st>>>(

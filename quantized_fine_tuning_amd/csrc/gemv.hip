@@ -549,96 +549,127 @@ __global__ __launch_bounds__(64 * WV) void gemv_adapters_kernel(Nf4View W, const
   }
 }
 
-// The gated block for few tokens: 16 weight rows of each layer per row group,
-// every X fragment multiplied with both, so that a workgroup holds G and U of its
-// outputs and writes H = act(G)*U.  The walk over row groups and the order of the
-// loads are gemv_adapters_kernel's; the threads that share an output are as many
-// as M leaves (16 of 256 for one token), each with every OT-th chunk of both
-// adapter rows.  T comes finished, a tile layout per layer.
-template <int XV, int WV>
-__global__ __launch_bounds__(64 * WV) void gated_gemv_kernel(Nf4View W0, Nf4View W1, const uint16_t* __restrict__ X, int M,
-                                                             const float* __restrict__ T, int t_layer,
-                                                             const uint16_t* __restrict__ B0,
-                                                             const uint16_t* __restrict__ B1, int r, float scale,
-                                                             GatedOut out, int row_groups, int share, Codebook cb) {
-  constexpr int NW = WV, NT = 64 * WV;
-  constexpr bool XL = XV > 0;
+// The gated block for few tokens: 16 weight rows of each layer per row group, so
+// that a workgroup holds G and U of its outputs and writes H = act(G)*U.  2·NW
+// waves, NW per layer, each with the block groups wave % NW, + NW, ... of every row
+// group that the workgroup walks over; the sums meet in LDS.  A wave's codes are
+// requested a block group ahead, across row groups.  The low-rank product is the
+// waves' too, 32 ranks each: the operand of their tokens, three parts of s·T from S
+// [layers][M][C], stays in registers, that of the adapter rows comes with a row
+// group's first codes.  (Added to the outputs after the sums, in fp32, its loads
+// lay behind codes of the next row group and waited for them: 13 tokens, r = 64,
+// 32.2 us.)  X is staged in LDS (XL) or loaded beside the codes.  The threads that
+// share an output are as many as M leaves.
+//
+// Bound by the decode: 77 % of the vector units' time and 40 % of the LDS's.  (Two
+// 11008 x 4096 weights, r = 16, graph-replayed with T's kernel: one token 21.2 us,
+// 46.6 MB at 2.2 TB/s, 13 tokens of r = 64 28.4 us.  Both layers in every wave took
+// 22.4 and 33.9; two block groups ahead 21.3; X's fragments kept in registers
+// across row groups 27.4, their spills' waits holding up the codes; levels looked
+// up in pairs, 64 KB of them, a third fewer vector instructions, 21.9 for want of
+// room for more than one workgroup.)
+template <int NW, bool XL>
+__global__ __launch_bounds__(128 * NW) void gated_gemv_kernel(Nf4View W0, Nf4View W1, const uint16_t* __restrict__ X,
+                                                              int M, const uint16_t* __restrict__ S,
+                                                              const uint16_t* __restrict__ B0,
+                                                              const uint16_t* __restrict__ B1, int r,
+                                                              GatedOut out, int row_groups, int share, Codebook cb) {
+  constexpr int NT = 128 * NW, DEPTH = 2;  // threads, sets of codes
   extern __shared__ __attribute__((aligned(16))) char sx[];  // X [M][K] bf16 (XL)
   __shared__ __attribute__((aligned(256))) float sq[16];
   __shared__ f32x4_t s_acc[2][NW][64];
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6) % NW;
+  const int own = __builtin_amdgcn_readfirstlane(tid / (64 * NW));  // this wave's layer
   const int lr = lane & 15, kq = lane >> 4;
   const int64_t K = W0.K, N = W0.N;
   const int nb = (int)(K / kBlock), ngroups = (nb + 3) / 4, per = (ngroups + NW - 1) / NW;
   const uint32_t kpr = (uint32_t)nb;
-  const float mu0 = *W0.mu, mu1 = *W1.mu;
+  const Nf4View W{own ? W1.codes : W0.codes, own ? W1.e : W0.e, own ? W1.s : W0.s, own ? W1.mu : W0.mu, N, K};
+  const float mu = *W.mu;
+  const rsrc_t rs = make_rsrc(W.s, ((N * kpr + kDqBlock - 1) / kDqBlock) * 4);
   const rsrc_t rx = make_rsrc(X, (int64_t)M * K * 2);
   const bool x_row = lr < M;
-  // output o = (token o / 16, row o % 16 of the group), this thread's part of it
-  const int OT = 1 << share, o_part = tid & (OT - 1), o_c = tid >> share & 15, o_m = tid >> share >> 4;
+  // this wave's ranks, and its tokens' operands
+  const int rank = 32 * wave + 8 * kq;
+  u32x4_t tf[3];
+  {
+    const int C = (int)adapter_cols(r);
+    const rsrc_t rS = make_rsrc(S + (int64_t)own * M * C, (int64_t)M * C * 2);
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+      tf[i] = buf_load16(rS, x_row && rank < r ? (uint32_t)((lr * C + i * r + rank) * 2) : 0x7fffffffu, 0u);
+  }
 
-  struct Half {
+  // output o = (token o / 16, row o % 16 of the group), the layer whose sum this
+  // thread has a part of (2^share threads an output, every other one the up
+  // projection's), and which part
+  const int OT = 1 << share >> 1, o_l = tid & 1, o_part = tid >> 1 & (OT - 1), o_c = tid >> share & 15,
+            o_m = tid >> share >> 4;
+
+  struct Group {
     u32x4_t c[2];  // the lane's 64 codes
     uint32_t e;    // e4m3 byte
     float s;       // group scale
+    u32x4_t b;     // with a row group's first: 8 ranks of an adapter row
+    u32x4_t x[XL ? 1 : 8];  // X fragments that come with the codes
   };
-  struct Group {
-    Half h[2];
-    u32x4_t x[XL ? 1 : 8];  // X fragments when X is not staged
-  };
-  // block group `step` of this wave in row group rg (zeros past the end)
-  auto load = [&](Group& g, int rg, int step) __attribute__((always_inline)) {
-    const int64_t n0 = (int64_t)rg * GEMV_ROWS;
-    const int grp = wave + NW * step, b = 4 * grp + kq;
-    const bool ok = rg < row_groups && grp < ngroups && b < nb;
+  int lrg = (int)blockIdx.x, lstep = 0;  // the next block group to request
+  auto load = [&](Group& g) __attribute__((always_inline)) {
+    const int64_t n0 = (int64_t)lrg * GEMV_ROWS;
+    const rsrc_t rc = make_rsrc(W.codes + n0 * (K / 2), (N - n0) * (K / 2));
+    const rsrc_t re = make_rsrc(W.e + n0 * kpr, (N - n0) * kpr);
+    const int b = 4 * (wave + NW * lstep) + kq;
+    const bool ok = lrg < row_groups && b < nb;
     const uint32_t off = ok ? (uint32_t)(lr * (K / 2) + b * 32) : 0x7fffffffu;
+    g.c[0] = buf_load16(rc, off, 0u);
+    g.c[1] = buf_load16(rc, off, 16u);
     const uint32_t blk = (uint32_t)(lr * kpr + b);
-#pragma unroll
-    for (int l = 0; l < 2; ++l) {
-      const Nf4View& W = l ? W1 : W0;
-      const rsrc_t rc = make_rsrc(W.codes + n0 * (K / 2), (N - n0) * (K / 2));
-      const rsrc_t re = make_rsrc(W.e + n0 * kpr, (N - n0) * kpr);
-      const rsrc_t rs = make_rsrc(W.s, ((N * kpr + kDqBlock - 1) / kDqBlock) * 4);
-      g.h[l].c[0] = buf_load16(rc, off, 0u);
-      g.h[l].c[1] = buf_load16(rc, off, 16u);
-      g.h[l].e = buf_load1(re, ok ? blk : 0x7fffffffu, 0u);
-      g.h[l].s = __uint_as_float(buf_load4(rs, ok ? (((uint32_t)n0 * kpr + blk) / kDqBlock) * 4u : 0x7fffffffu, 0u));
-    }
+    g.e = buf_load1(re, ok ? blk : 0x7fffffffu, 0u);
+    g.s = __uint_as_float(buf_load4(rs, ok ? (((uint32_t)n0 * kpr + blk) / kDqBlock) * 4u : 0x7fffffffu, 0u));
     if constexpr (!XL) {
       const uint32_t xo = ok && x_row ? (uint32_t)((lr * K + b * kBlock) * 2) : 0x7fffffffu;
 #pragma unroll
       for (int t = 0; t < 8; ++t) g.x[t] = buf_load16(rx, xo, 16u * t);
     }
+    if (lstep == 0) {
+      const rsrc_t rb = make_rsrc((own ? B1 : B0) + n0 * r, lrg < row_groups ? (N - n0) * r * 2 : 0);
+      g.b = buf_load16(rb, rank < r ? (uint32_t)((lr * r + rank) * 2) : 0x7fffffffu, 0u);
+    }
+    if (++lstep == per) {
+      lstep = 0;
+      lrg += (int)gridDim.x;
+    }
   };
-  f32x4_t acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+  f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
   auto consume = [&](const Group& g, int step) __attribute__((always_inline)) {
-    const float cp[2] = {decode_constant(g.h[0].e, g.h[0].s, mu0), decode_constant(g.h[1].e, g.h[1].s, mu1)};
-    const int grp = wave + NW * step, b = 4 * grp + kq;
-    const bool use_x = x_row && grp < ngroups && b < nb;
+    const float cp = __fadd_rn(__fmul_rn(__builtin_amdgcn_cvt_f32_fp8((int)g.e, 0), g.s), mu);
+    const int b = 4 * (wave + NW * step) + kq;
+    const bool use_x = x_row && b < nb;
     const char* xrow = sx + (size_t)(lr * K + (use_x ? b : 0) * kBlock) * 2;
     const uint32_t sqb = lds_offset(sq);
 #pragma unroll
     for (int t = 0; t < 8; ++t) {
+      const uint32_t w = g.c[t >> 2][t & 3];  // codes 8t .. 8t+7
+      const uint32_t we = (w << 2) & 0x3C3C3C3Cu, wo = (w >> 2) & 0x3C3C3C3Cu;
+      u32x4_t bfrag;
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        const float qe = *(const __attribute__((address_space(3))) float*)(uintptr_t)__builtin_amdgcn_perm(
+            sqb, we, 0x07060500u | (uint32_t)p);
+        const float qo = *(const __attribute__((address_space(3))) float*)(uintptr_t)__builtin_amdgcn_perm(
+            sqb, wo, 0x07060500u | (uint32_t)p);
+        bfrag[p] = pack_bf16x2(__fmul_rn(qe, cp), __fmul_rn(qo, cp));
+      }
       u32x4_t xa;
       if constexpr (XL)
         xa = use_x ? *reinterpret_cast<const u32x4_t*>(xrow + 16 * t) : u32x4_t{0u, 0u, 0u, 0u};
       else
         xa = g.x[t];
+      acc = mfma_16x16x32(xa, bfrag, acc);
+    }
+    if (step == 0) {
 #pragma unroll
-      for (int l = 0; l < 2; ++l) {
-        const uint32_t w = g.h[l].c[t >> 2][t & 3];  // codes 8t .. 8t+7
-        const uint32_t we = (w << 2) & 0x3C3C3C3Cu, wo = (w >> 2) & 0x3C3C3C3Cu;
-        u32x4_t bfrag;
-#pragma unroll
-        for (int p = 0; p < 4; ++p) {
-          const float qe = *(const __attribute__((address_space(3))) float*)(uintptr_t)__builtin_amdgcn_perm(
-              sqb, we, 0x07060500u | (uint32_t)p);
-          const float qo = *(const __attribute__((address_space(3))) float*)(uintptr_t)__builtin_amdgcn_perm(
-              sqb, wo, 0x07060500u | (uint32_t)p);
-          bfrag[p] = pack_bf16x2(__fmul_rn(qe, cp[l]), __fmul_rn(qo, cp[l]));
-        }
-        acc[l] = mfma_16x16x32(xa, bfrag, acc[l]);
-      }
+      for (int i = 0; i < 3; ++i) acc = mfma_16x16x32(tf[i], g.b, acc);
     }
   };
   auto barrier = [&]() __attribute__((always_inline)) {
@@ -648,104 +679,54 @@ __global__ __launch_bounds__(64 * WV) void gated_gemv_kernel(Nf4View W0, Nf4View
     asm volatile("" ::: "memory");
   };
 
-  u32x4_t xs[XL ? XV : 1];
-  const int nvec = (M * (int)K * 2) / 16;
-  if constexpr (XL) {
-#pragma unroll
-    for (int i = 0; i < XV; ++i) {
-      const int v = tid + i * NT;
-      xs[i] = buf_load16(rx, v < nvec ? (uint32_t)(16 * v) : 0x7fffffffu, 0u);
-    }
-  }
   const float cbq = cb.q[tid & 15];
-  __builtin_amdgcn_sched_barrier(0);
-  Group ga, gb;
-  int rg = (int)blockIdx.x, step = 0;
-  load(ga, rg, 0);
-  __builtin_amdgcn_sched_barrier(0);
   if constexpr (XL) {
-#pragma unroll
-    for (int i = 0; i < XV; ++i) {
-      const int v = tid + i * NT;
-      if (v < nvec) *reinterpret_cast<u32x4_t*>(sx + 16 * v) = xs[i];
-    }
+    const int nvec = (M * (int)K * 2) / 16;
+    for (int v = tid; v < nvec; v += NT) *reinterpret_cast<u32x4_t*>(sx + 16 * v) = buf_load16(rx, (uint32_t)(16 * v), 0u);
   }
+  __builtin_amdgcn_sched_barrier(0);
+  Group g[DEPTH];
+#pragma unroll
+  for (int d = 0; d + 1 < DEPTH; ++d) load(g[d]);
+  __builtin_amdgcn_sched_barrier(0);
   if (tid < 16) sq[tid] = cbq;
   barrier();
 
-  // one block group: the next one's codes requested, this one decoded; at the
-  // row group's end the outputs.  False after the last.
+  int rg = (int)blockIdx.x, step = 0;
+  // one block group: another one's codes requested, this one decoded; at the row
+  // group's end the outputs.  False after the last.
   auto turn = [&](const Group& cur, Group& nxt) __attribute__((always_inline)) {
-    const bool last = step + 1 == per;
-    const int64_t nn = (int64_t)rg * GEMV_ROWS + o_c;
-    const bool mine = o_m < M && nn < N;
-    u32x4_t bv[2];
-    f32x4_t tv[2][2];
-    auto t_at = [&](int l, int j, f32x4_t* t) __attribute__((always_inline)) {
-      const f32x4_t* const p = reinterpret_cast<const f32x4_t*>(T + l * t_layer + (j >> 4) * 256 + 16 * o_m + (j & 15));
-      t[0] = p[0];
-      t[1] = p[1];
-    };
-    if (last && mine) {
-      const int j = 8 * o_part < r ? 8 * o_part : 0;
-#pragma unroll
-      for (int l = 0; l < 2; ++l) {
-        bv[l] = *reinterpret_cast<const u32x4_t*>((l ? B1 : B0) + nn * r + j);
-        t_at(l, j, tv[l]);
-      }
-    }
-    __builtin_amdgcn_sched_barrier(0);
-    const int nrg = last ? rg + (int)gridDim.x : rg, nstep = last ? 0 : step + 1;
-    load(nxt, nrg, nstep);
+    load(nxt);
     __builtin_amdgcn_sched_barrier(0);
     consume(cur, step);
-    if (last) {
-#pragma unroll
-      for (int l = 0; l < 2; ++l) {
-        s_acc[l][wave][lane] = acc[l];
-        acc[l] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    if (++step < per) return true;
+    step = 0;
+    s_acc[own][wave][lane] = acc;
+    acc = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    barrier();
+    const int64_t nn = (int64_t)rg * GEMV_ROWS + o_c;
+    float v = 0.f;
+    if (o_m < M && nn < N)
+      for (int w = o_part; w < NW; w += OT) v += s_acc[o_l][w][16 * (o_m >> 2) + o_c][o_m & 3];
+    for (int o = 2; o <= OT; o <<= 1) v += __shfl_xor(v, o, 64);
+    const float u = __shfl_xor(v, 1, 64);
+    if (o_m < M && nn < N && o_part == 0 && o_l == 0) {
+      const int64_t o = (int64_t)o_m * N + nn;
+      out.H[o] = (uint16_t)(pack_bf16x2(gate_act(out.act, v) * u, 0.f) & 0xffffu);
+      if (out.G) {
+        const uint32_t gu = pack_bf16x2(v, u);
+        out.G[o] = (uint16_t)(gu & 0xffffu);
+        out.U[o] = (uint16_t)(gu >> 16);
       }
-      barrier();
-      float y[2];
-#pragma unroll
-      for (int l = 0; l < 2; ++l) {
-        float v = 0.f, dot = 0.f;
-        if (mine) {
-          for (int w = o_part; w < NW; w += OT) v += s_acc[l][w][16 * (o_m >> 2) + o_c][o_m & 3];
-          auto add8 = [&](const f32x4_t* t, const u32x4_t& b) __attribute__((always_inline)) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              dot = __builtin_fmaf(t[i >> 1][2 * (i & 1)], bf16lo(b[i]), dot);
-              dot = __builtin_fmaf(t[i >> 1][2 * (i & 1) + 1], bf16hi(b[i]), dot);
-            }
-          };
-          if (8 * o_part < r) add8(tv[l], bv[l]);
-          for (int j = 8 * (o_part + OT); j < r; j += 8 * OT) {
-            f32x4_t t[2];
-            t_at(l, j, t);
-            add8(t, *reinterpret_cast<const u32x4_t*>((l ? B1 : B0) + nn * r + j));
-          }
-        }
-        v = __builtin_fmaf(scale, dot, v);
-        for (int o = 1; o < OT; o <<= 1) v += __shfl_xor(v, o, 64);
-        y[l] = v;
-      }
-      if (mine && o_part == 0) {
-        const int64_t at = (int64_t)o_m * N + nn;
-        out.H[at] = (uint16_t)(pack_bf16x2(gate_act(out.act, y[0]) * y[1], 0.f) & 0xffffu);
-        if (out.G) {
-          const uint32_t gu = pack_bf16x2(y[0], y[1]);
-          out.G[at] = (uint16_t)(gu & 0xffffu);
-          out.U[at] = (uint16_t)(gu >> 16);
-        }
-      }
-      barrier();  // the tiles are read: the next row group may write its own
     }
-    rg = nrg;
-    step = nstep;
+    barrier();  // the sums are read: the next row group may write its own
+    rg += (int)gridDim.x;
     return rg < row_groups;
   };
-  while (turn(ga, gb) && turn(gb, ga)) {
+  for (;;) {
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d)
+      if (!turn(g[d], g[(d + DEPTH - 1) % DEPTH])) return;
   }
 }
 
@@ -843,32 +824,29 @@ hipError_t launch_gemv_adapters(const Nf4View& W, const uint16_t* X, int64_t M, 
   return hipGetLastError();
 }
 
-// T: the finished low-rank factors in the split kernel's tile layout, t_layer
-// floats a layer.
-hipError_t launch_gated_gemv(const BlockView& b, const uint16_t* X, int64_t M, const float* T, int t_layer,
-                             const GatedOut& out, hipStream_t st) {
+// S: the three-part splits of both layers' scaled low-rank factors.
+hipError_t launch_gated_gemv(const BlockView& b, const uint16_t* X, int64_t M, const uint16_t* S, const GatedOut& out,
+                             hipStream_t st) {
   const Nf4View& W = b.W[0];
   const int groups = (int)((W.N + GEMV_ROWS - 1) / GEMV_ROWS);
   const size_t xb = (size_t)M * W.K * 2;
-  const size_t shm = xb <= (size_t)kGemvXLdsBytes - 16 * 1024 ? xb : 0;
-#define QNF4_GEMV_LAUNCH(XV, WV, RES)                                                                              \
+#define QNF4_GEMV_LAUNCH(NW, XL, RES)                                                                              \
   {                                                                                                                \
-    int share = 0; /* threads per output: 64·WV over 16 rows of M tokens, within a wave */                        \
-    while (share < 6 && (32 << share) * M <= 64 * WV) ++share;                                                    \
-    hipLaunchKernelGGL((gated_gemv_kernel<XV, WV>), dim3((unsigned)std::min(groups, 256 * RES)), dim3(64 * WV), shm, \
-                       st, W, b.W[1], X, (int)M, T, t_layer, b.B[0], b.B[1], b.r, b.scale, out, groups, share,     \
-                       codebook());                                                                                \
+    int share = 0; /* threads per output: 128·NW over 16 rows of M tokens, two at least, within a wave */         \
+    while (share < 6 && (32 << share) * M <= 128 * NW) ++share;                                                   \
+    hipLaunchKernelGGL((gated_gemv_kernel<NW, XL>), dim3((unsigned)std::min(groups, 256 * RES)), dim3(128 * NW),   \
+                       XL ? xb : 0, st, W, b.W[1], X, (int)M, S, b.B[0], b.B[1], b.r, out, groups, share,         \
+                       codebook());                                                                               \
   }
-  // the workgroup shapes of the single layer's, as many of each as are resident at once
-  const bool narrow = groups > 256 && xb <= 32 * 1024, four = narrow && xb <= 8 * 1024;
-  if (four)
-    QNF4_GEMV_LAUNCH(2, 4, 4)
-  else if (narrow)
-    QNF4_GEMV_LAUNCH(4, 8, 2)
-  else if (shm)
-    QNF4_GEMV_LAUNCH(7, 16, 1)
+  // as many workgroups as are resident at once: three of 8 waves per compute unit
+  // where X is small (one of 16: one token 24.5 us, not 21.2) and four waves a layer
+  // hold the ranks, one of 16 beside a larger X in LDS, whose room sq and s_acc leave
+  if (xb <= 32 * 1024 && b.r <= 128)
+    QNF4_GEMV_LAUNCH(4, true, 3)
+  else if (xb <= (size_t)142 * 1024)
+    QNF4_GEMV_LAUNCH(8, true, 1)
   else
-    QNF4_GEMV_LAUNCH(0, 8, 1)
+    QNF4_GEMV_LAUNCH(8, false, 1)
 #undef QNF4_GEMV_LAUNCH
   return hipGetLastError();
 }

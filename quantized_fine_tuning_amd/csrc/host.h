@@ -258,6 +258,8 @@ struct AdapterGemmArgs {
   int r, C, count, cols;  // cols: the columns of S that enter, 2r or 3r
   __device__ __forceinline__ int held() const { return plan[1]; }
   __device__ __forceinline__ const int32_t* perm() const { return plan + kPlanHead + m_pad; }
+  __device__ __forceinline__ int token(int p) const { return perm()[p]; }
+  __device__ __forceinline__ int4 tokens4(int p) const { return *reinterpret_cast<const int4*>(perm() + p); }
   __device__ __forceinline__ int group(int p) const { return plan[kPlanHead + 2 * m_pad + p]; }
   __device__ __forceinline__ int id(int g) const { return plan[kPlanHead + 3 * m_pad + g]; }
   __device__ __forceinline__ int start(int g) const { return plan[kPlanHead + 3 * m_pad + c_pad + g]; }
@@ -297,6 +299,22 @@ struct BlockGemmArgs {
   int act;
   const uint16_t* dY2;
   DropView drop;
+};
+
+// The same for one adapter that all of M tokens carry, as one layer's share of
+// BlockGemmArgs: the batch in its own order.
+struct DenseGemmArgs {
+  const uint16_t* S;
+  const uint16_t* F;
+  int r, C, count, cols;  // count: 1
+  int M;
+  DropView drop;
+  __device__ __forceinline__ int held() const { return M; }
+  __device__ __forceinline__ int token(int p) const { return p; }
+  __device__ __forceinline__ int4 tokens4(int p) const { return int4{p, p + 1, p + 2, p + 3}; }
+  __device__ __forceinline__ int group(int) const { return 0; }
+  __device__ __forceinline__ int id(int) const { return 0; }
+  __device__ __forceinline__ int start(int g) const { return g > 0 ? M : 0; }
 };
 
 // One layer (gate and up projection: two) with its adapters.
@@ -360,6 +378,10 @@ hipError_t launch_mid_fwd(const Nf4View& W, const uint16_t* X, int64_t M, const 
 int mid_dx_splits(int64_t M, int64_t N, int64_t K);
 hipError_t launch_mid_dx(const Nf4View& W, const uint16_t* dY, int64_t M, const AdapterGemmArgs& ma, void* dX, bool dx16,
                          int splits, float* P, hipStream_t st);
+hipError_t launch_mid_fwd_block(const Nf4View& W, const uint16_t* X, int64_t M, const DenseGemmArgs& ma, void* Y, bool y16,
+                                const MidPlan& plan, float* P, hipStream_t st);
+hipError_t launch_mid_dx_block(const Nf4View& W, const uint16_t* dY, int64_t M, const DenseGemmArgs& ma, void* dX,
+                               bool dx16, int splits, float* P, hipStream_t st);
 
 struct AdaptersFwdLayout {
   // M <= 16: fp32 T in tiles; else bf16 S [M, C] of s·T; an fp32 area: the

@@ -1,5 +1,5 @@
-// Base products of a batch of few tokens that carry different adapters (17 to
-// kMidTokens), gfx950.  The dequant-in-tile GEMMs (fwd.hip, dx.hip) decode
+// Base products of a batch of few tokens (17 to kMidTokens) that carry different
+// adapters (AdapterGemmArgs), or one that may have dropout (DenseGemmArgs), gfx950.  The dequant-in-tile GEMMs (fwd.hip, dx.hip) decode
 // 256 weight rows for 256 tokens and are bound by that decode long before the
 // tokens are many; here a weight fragment goes from its codes to the MFMA
 // operand with as little between as its layout allows, and every tile of 16
@@ -11,7 +11,9 @@
 // reduction is split over workgroups, fp32 partial sums are added in split
 // order by splitk_reduce_kernel.
 #include <algorithm>
+#include <type_traits>
 
+#include "dropout.h"
 #include "host.h"
 #include "tiling.h"
 
@@ -24,11 +26,11 @@ namespace {
 template <int NT>
 struct RowTokens {
   int t[NT][4];
-  __device__ __forceinline__ RowTokens(const AdapterGemmArgs& ma, int p0, int64_t M, int kq) {
+  template <typename Args>
+  __device__ __forceinline__ RowTokens(const Args& ma, int p0, int64_t M, int kq) {
     int4 v[NT];
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
-      v[i] = *reinterpret_cast<const int4*>(ma.perm() + std::min(p0 + 16 * i + 4 * kq, ((int)M - 1) & ~3));
+    for (int i = 0; i < NT; ++i) v[i] = ma.tokens4(std::min(p0 + 16 * i + 4 * kq, ((int)M - 1) & ~3));
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       const int w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
@@ -58,13 +60,15 @@ struct LoraShare {
   // ((c + 0.5) / each is never nearer than 0.5 / each to a whole number)
   __device__ __forceinline__ int adapter_of(int c) const { return (int)(((float)c + 0.5f) * inv_each); }
   // the rows, from p0 on, of the adapter that columns [c, c + 32) belong to
-  __device__ __forceinline__ void rows(const AdapterGemmArgs& ma, int c, int p0, int64_t M, int& lo, int& hi) const {
+  template <typename Args>
+  __device__ __forceinline__ void rows(const Args& ma, int c, int p0, int64_t M, int& lo, int& hi) const {
     const int g = adapter_of(std::min(c, all - 32));
     lo = c < all ? ma.start(gfirst + g) - p0 : 0;
     hi = c < all ? std::min(ma.start(gfirst + g + 1), (int)M) - p0 : 0;
   }
 };
-__device__ __forceinline__ LoraShare lora_share(const AdapterGemmArgs& ma, int p0, int rows, int64_t M, int sp,
+template <typename Args>
+__device__ __forceinline__ LoraShare lora_share(const Args& ma, int p0, int rows, int64_t M, int sp,
                                                 int splits, int width) {
   const int each = (ma.cols + 31) & ~31;
   LoraShare s{0, each, 0, 0, 0, 1.0f / (float)each};
@@ -95,10 +99,10 @@ __device__ __forceinline__ LoraShare lora_share(const AdapterGemmArgs& ma, int p
 // WV waves: 8, or 16 with twice the weight rows (four waves on a SIMD cover each
 // other's lookups better, 2.9 us for a stage of twice the weights, but the
 // tiles are fewer: mid_fwd_plan).
-template <int NT, int WV>
+template <int NT, int WV, typename Args>
 __global__ __launch_bounds__(64 * WV) void mid_fwd_kernel(Nf4View W, const uint16_t* __restrict__ X, int64_t M,
                                                               void* __restrict__ Y, int y_bf16, int tiles_n, int splits,
-                                                              float* __restrict__ P, Codebook cb, AdapterGemmArgs ma) {
+                                                              float* __restrict__ P, Codebook cb, Args ma) {
   constexpr int TM = 16 * NT, ROW = 512, XB = TM * ROW, WB = 2560;  // bytes: X of a stage, one wave's codes and constants
   constexpr int D = WV == 16 ? 2 : NT == 2 ? 4 : 3, XI = 8 * NT / WV;                                // ring depth
   __shared__ __attribute__((aligned(1024))) char sx[D][XB];
@@ -125,7 +129,7 @@ __global__ __launch_bounds__(64 * WV) void mid_fwd_kernel(Nf4View W, const uint1
   {
     int tok[XI];
 #pragma unroll
-    for (int c = 0; c < XI; ++c) tok[c] = ma.perm()[std::min(p0 + 2 * (XI * wave + c) + (lane >> 5), (int)M - 1)];
+    for (int c = 0; c < XI; ++c) tok[c] = ma.token(std::min(p0 + 2 * (XI * wave + c) + (lane >> 5), (int)M - 1));
 #pragma unroll
     for (int c = 0; c < XI; ++c) {
       const int row = 2 * (XI * wave + c) + (lane >> 5);
@@ -302,10 +306,12 @@ constexpr int kDxThreads = 256;
 __device__ __forceinline__ int tswz(int row, int col) {
   return row * 256 + (((col >> 3) ^ ((row & 3) << 1)) << 4) + 2 * (col & 7);
 }
-template <int NT>
+// (DenseGemmArgs with dropout: between the adapters and the weight the sums are the
+// low-rank product alone, and those of dropped elements become zero.)
+template <int NT, typename Args>
 __global__ __launch_bounds__(kDxThreads) void mid_dx_kernel(Nf4View W, const uint16_t* __restrict__ dY, int64_t M,
                                                             void* __restrict__ dX, int dx_bf16, int tiles_k, int splits,
-                                                            float* __restrict__ P, Codebook cb, AdapterGemmArgs ma) {
+                                                            float* __restrict__ P, Codebook cb, Args ma) {
   constexpr int TM = 16 * NT, D = 3, YI = NT / 2;  // dY copies per wave and stage (8 rows each)
   __shared__ __attribute__((aligned(1024))) char sy[D][TM * 128];
   __shared__ __attribute__((aligned(1024))) char sc[D][4 * 1536];  // per wave: codes 1 KB, e4m3 dwords, scales
@@ -331,7 +337,7 @@ __global__ __launch_bounds__(kDxThreads) void mid_dx_kernel(Nf4View W, const uin
   {
     int tok[YI];
 #pragma unroll
-    for (int c = 0; c < YI; ++c) tok[c] = ma.perm()[std::min(p0 + 8 * (YI * wave + c) + (lane >> 3), (int)M - 1)];
+    for (int c = 0; c < YI; ++c) tok[c] = ma.token(std::min(p0 + 8 * (YI * wave + c) + (lane >> 3), (int)M - 1));
 #pragma unroll
     for (int c = 0; c < YI; ++c)
       vy[c] = p0 + 8 * (YI * wave + c) + (lane >> 3) < (int)M && (uint32_t)tok[c] < (uint32_t)M
@@ -470,6 +476,27 @@ __global__ __launch_bounds__(kDxThreads) void mid_dx_kernel(Nf4View W, const uin
     }
   }
 
+  if constexpr (std::is_same_v<Args, DenseGemmArgs>) {
+    if (L.first < L.last && ma.drop.out > 0) {
+      // lane l finds the masks of rows 16i + l/4, chunk l%4 of the wave's four; the
+      // lane of row 16i + 4kq + v, column 16f + lr takes them from lane
+      // 4·(4kq + v) + 2f + lr/8
+      const DropView drop = drawn(ma.drop);
+      const uint32_t c0 = (uint32_t)((p0 + (lane >> 2)) * (K / 8) + (k0 + 32 * wave) / 8 + (lane & 3));
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        const int keep = (int)keep8(drop, c0 + (uint32_t)(16 * i * (K / 8)));
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+#pragma unroll
+          for (int f = 0; f < 2; ++f) {
+            const int m = __builtin_amdgcn_ds_bpermute(4 * (4 * (4 * kq + v) + 2 * f + (lr >> 3)), keep) >> (lr & 7);
+            acc[f][i][v] = m & 1 ? acc[f][i][v] : 0.f;
+          }
+      }
+    }
+  }
+
   // stage s0 decoded; then per stage: its products, the next one's decode
   open_stage<PER>();  // (the levels are in LDS, and this wave's copies of stage s0)
   if (s0 < s1) decode(sc[0] + wave * 1536, sw[0], s0);
@@ -537,13 +564,16 @@ int mid_dx_splits(int64_t M, int64_t N, int64_t K) {
   return mid_splits(((M + tm - 1) / tm) * ((K + 127) / 128), (N + 63) / 64, M * K, 512, 1.0, 6.0).splits;
 }
 
-hipError_t launch_mid_fwd(const Nf4View& W, const uint16_t* X, int64_t M, const AdapterGemmArgs& ma, void* Y, bool y16,
-                          const MidPlan& plan, float* P, hipStream_t st) {
+namespace {
+
+template <typename Args>
+hipError_t launch_fwd(const Nf4View& W, const uint16_t* X, int64_t M, const Args& ma, void* Y, bool y16,
+                      const MidPlan& plan, float* P, hipStream_t st) {
   const int nt = mid_tiles(M), tm = 16 * nt, rows = 16 * plan.waves, tiles_n = (int)((W.N + rows - 1) / rows);
   const dim3 grid((unsigned)(tiles_n * ((M + tm - 1) / tm)), (unsigned)plan.splits);
-#define QNF4_MID(NT, WV)                                                                                        \
-  mid_fwd_kernel<NT, WV><<<grid, 64 * WV, 0, st>>>(W, X, M, Y, y16 ? 1 : 0, tiles_n, plan.splits, P, codebook(), \
-                                                   ma)
+#define QNF4_MID(NT, WV)                                                                                              \
+  mid_fwd_kernel<NT, WV, Args><<<grid, 64 * WV, 0, st>>>(W, X, M, Y, y16 ? 1 : 0, tiles_n, plan.splits, P, codebook(), \
+                                                         ma)
   if (plan.waves == 16) {
     if (nt == 2)
       QNF4_MID(2, 16);
@@ -559,18 +589,38 @@ hipError_t launch_mid_fwd(const Nf4View& W, const uint16_t* X, int64_t M, const 
   return hipGetLastError();
 }
 
-hipError_t launch_mid_dx(const Nf4View& W, const uint16_t* dY, int64_t M, const AdapterGemmArgs& ma, void* dX, bool dx16,
-                         int splits, float* P, hipStream_t st) {
+template <typename Args>
+hipError_t launch_dx(const Nf4View& W, const uint16_t* dY, int64_t M, const Args& ma, void* dX, bool dx16, int splits,
+                     float* P, hipStream_t st) {
   const int nt = mid_tiles(M), tm = 16 * nt, tiles_k = (int)((W.K + 127) / 128);
   const dim3 grid((unsigned)(tiles_k * ((M + tm - 1) / tm)), (unsigned)splits);
-#define QNF4_MID(NT) \
-  mid_dx_kernel<NT><<<grid, kDxThreads, 0, st>>>(W, dY, M, dX, dx16 ? 1 : 0, tiles_k, splits, P, codebook(), ma)
+#define QNF4_MID(NT)                                                                                              \
+  mid_dx_kernel<NT, Args><<<grid, kDxThreads, 0, st>>>(W, dY, M, dX, dx16 ? 1 : 0, tiles_k, splits, P, codebook(), ma)
   if (nt == 2)
     QNF4_MID(2);
   else
     QNF4_MID(4);
 #undef QNF4_MID
   return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_mid_fwd(const Nf4View& W, const uint16_t* X, int64_t M, const AdapterGemmArgs& ma, void* Y, bool y16,
+                          const MidPlan& plan, float* P, hipStream_t st) {
+  return launch_fwd(W, X, M, ma, Y, y16, plan, P, st);
+}
+hipError_t launch_mid_fwd_block(const Nf4View& W, const uint16_t* X, int64_t M, const DenseGemmArgs& ma, void* Y, bool y16,
+                                const MidPlan& plan, float* P, hipStream_t st) {
+  return launch_fwd(W, X, M, ma, Y, y16, plan, P, st);
+}
+hipError_t launch_mid_dx(const Nf4View& W, const uint16_t* dY, int64_t M, const AdapterGemmArgs& ma, void* dX, bool dx16,
+                         int splits, float* P, hipStream_t st) {
+  return launch_dx(W, dY, M, ma, dX, dx16, splits, P, st);
+}
+hipError_t launch_mid_dx_block(const Nf4View& W, const uint16_t* dY, int64_t M, const DenseGemmArgs& ma, void* dX,
+                               bool dx16, int splits, float* P, hipStream_t st) {
+  return launch_dx(W, dY, M, ma, dX, dx16, splits, P, st);
 }
 
 }  // namespace qnf4
