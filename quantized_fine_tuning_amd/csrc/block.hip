@@ -104,6 +104,15 @@ __device__ __forceinline__ void down_tile(const DownJob& J, int layer, int tile,
   for (int i = 0; i < NJ; ++i) acc[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int i = 0; i + 1 < kDownRing; ++i) issue(i, s0 + i);
+  // the generator's bits for a stage are found beside the products of the one before
+  u32x4_t bits[2];
+  auto draw = [&](int s) __attribute__((always_inline)) {
+    if (!dropping) return;
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+      bits[c] = philox(drop, chunk0 + (uint32_t)(8 * c * (Kred / 8)) + 8u * (uint32_t)s);
+  };
+  draw(s0);
   for (int s = s0; s < s1; ++s) {
     const int b = (s - s0) % kDownRing;
     if (dropping) {
@@ -113,11 +122,12 @@ __device__ __forceinline__ void down_tile(const DownJob& J, int layer, int tile,
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         u32x4_t* const at = reinterpret_cast<u32x4_t*>(sl + b * LB + (16 * wave + 8 * c) * 128 + 16 * lane);
-        *at = drop8(drop, chunk0 + (uint32_t)(8 * c * (Kred / 8)) + 8u * (uint32_t)s, *at);
+        *at = drop8(drop, bits[c], *at);
       }
     }
     open_stage<(kDownRing - 2) * (2 + RI)>();
     issue((s - s0 + kDownRing - 1) % kDownRing, s + kDownRing - 1);
+    draw(s + 1);
     const char* const lt = sl + b * LB;
     const char* const rt = sr + b * RB;
 #pragma unroll
@@ -201,7 +211,7 @@ __global__ __launch_bounds__(256) void block_few_down_kernel(const uint16_t* __r
     }
 #pragma unroll
     for (int u = 0; u < UN; ++u) {
-      if (drop.out > 0) x[u] = drop8(drop, (uint32_t)((m * K + k0 + 2048 * u) / 8), x[u]);
+      if (drop.out > 0) x[u] = drop8(drop, philox(drop, (uint32_t)((m * K + k0 + 2048 * u) / 8)), x[u]);
 #pragma unroll
       for (int j = 0; j < kFewRanks; ++j) acc[j] = dot8(x[u], w[u][j], acc[j]);
     }
@@ -326,6 +336,18 @@ __device__ __forceinline__ void gradient_unit(const GradientJob& J, int layer, i
     for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int i = 0; i + 1 < kGradRing; ++i) issue(i, i);
+  // the generator's bits for a stage are found beside the products of the one before
+  u32x4_t bits[2];
+  auto draw = [&](int s) __attribute__((always_inline)) {
+    if (!dropping) return;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int row = 8 * wave + 4 * c + (lane >> 4);
+      const int64_t chunk = (p0 + 32 * (int64_t)s + row) * (J.cols / 8) + c0 / 8 + ((lane & 15) ^ ((row & 3) << 1));
+      bits[c] = philox(drop, (uint32_t)chunk);
+    }
+  };
+  draw(0);
   for (int s = 0; s < stages; ++s) {
     if (dropping) {
       // this wave's own copies of the stage
@@ -333,15 +355,14 @@ __device__ __forceinline__ void gradient_unit(const GradientJob& J, int layer, i
       asm volatile("" ::: "memory");
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        const int row = 8 * wave + 4 * c + (lane >> 4);
-        const int64_t chunk = (p0 + 32 * (int64_t)s + row) * (J.cols / 8) + c0 / 8 + ((lane & 15) ^ ((row & 3) << 1));
         u32x4_t* const at =
             reinterpret_cast<u32x4_t*>(sl + (s % kGradRing) * LB + (8 * wave + 4 * c) * 256 + 16 * lane);
-        *at = drop8(drop, (uint32_t)chunk, *at);
+        *at = drop8(drop, bits[c], *at);
       }
     }
     open_stage<(kGradRing - 2) * (2 + SI)>();
     issue((s + kGradRing - 1) % kGradRing, s + kGradRing - 1);
+    draw(s + 1);
     const char* const lt = sl + (s % kGradRing) * LB;
     const char* const st = ss + (s % kGradRing) * SB;
     const int trow = 8 * kq + (lr >> 2), tcol = 4 * (lr & 3);  // this lane's part of a transposing read
@@ -411,11 +432,14 @@ __global__ __launch_bounds__(256) void block_gradient_kernel(GradientJob ja, Gra
   const int64_t p0 = unit * blockIdx.y, p1 = std::min<int64_t>(p0 + unit, M);
   const int64_t part = ((int64_t)blockIdx.y * layers + layer) * r * (ja.cols + jb.cols);
   drop = drawn(drop);
-  if (blockIdx.x < tiles_a)
-    gradient_unit<NJ, false>(ja, layer, 128 * (int64_t)blockIdx.x, j0, p0, p1, M, r, drop,
+  // (dA's tiles, whose masks cost vector time, spread evenly between dB's)
+  const unsigned tile_a = (unsigned)((uint64_t)blockIdx.x * tiles_a / gridDim.x);
+  const bool is_a = (uint64_t)(blockIdx.x + 1) * tiles_a / gridDim.x > tile_a;
+  if (is_a)
+    gradient_unit<NJ, false>(ja, layer, 128 * (int64_t)tile_a, j0, p0, p1, M, r, drop,
                              P ? P + part + ja.part_off : ja.out[layer], sl, ss);
   else
-    gradient_unit<NJ, true>(jb, layer, 128 * (int64_t)(blockIdx.x - tiles_a), j0, p0, p1, M, r, drop,
+    gradient_unit<NJ, true>(jb, layer, 128 * (int64_t)(blockIdx.x - tile_a), j0, p0, p1, M, r, drop,
                             P ? P + part + jb.part_off : jb.out[layer], sl, ss);
 }
 

@@ -36,10 +36,9 @@ __device__ __forceinline__ u32x4_t philox(const DropView& d, uint32_t chunk) {
   return u32x4_t{c0, c1, c2, c3};
 }
 
-// Eight 16-bit values of chunk `chunk` with zeros in the place of dropped ones
-// (whatever those are: NaN and infinities go too).
-__device__ __forceinline__ u32x4_t drop8(const DropView& d, uint32_t chunk, u32x4_t v) {
-  const u32x4_t bits = philox(d, chunk);
+// Eight 16-bit values with zeros in the place of those that the generator's bits
+// of their chunk drop (whatever those are: NaN and infinities go too).
+__device__ __forceinline__ u32x4_t drop8(const DropView& d, u32x4_t bits, u32x4_t v) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const uint32_t low = (bits[i] & 0xffffu) >= d.out ? 0xffffu : 0u;
