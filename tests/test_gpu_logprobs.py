@@ -227,6 +227,23 @@ def test_top_of_unusual_rows(z, V, kind):
         check(out["entropy"], b.entropy, b.lim_entropy, "f32", "entropy")
 
 
+@pytest.mark.parametrize("z", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("V", [300, 9000, 50000, 140000])
+@pytest.mark.parametrize("finite", [130, 200, 255])
+def test_fewer_alternatives_than_asked_for_side_by_side(z, V, finite):
+    """More columns next to one another than one wave lists, and still fewer than k."""
+    import torch as t
+    Z = t.full((2, V), -float("inf"))
+    Z[0, 17:17 + finite] = t.randn(finite, generator=t.Generator().manual_seed(V)).mul(2).round()
+    Z[1, V - finite:] = 0.5
+    if z != "f16":
+        Z[1, :8] = -1e30
+    Z, target = Z.to(types()[z]), t.tensor([20, V - 1], dtype=t.int32)
+    out = forward(Z, target, 1.0, V, 256)
+    check_top(out, Z, 1.0, V, 256, Bounds(Z, target, 1.0, V))
+    assert (out["top_index"][:, finite:] == -1).all()
+
+
 @pytest.mark.parametrize("z,V", [("bf16", 700), ("f32", 2000), ("f16", 33000), ("bf16", 70001)])
 def test_tokens_that_say_nothing(z, V):
     """No target, no gradient, masked rows: zeros, and untouched neighbours."""
