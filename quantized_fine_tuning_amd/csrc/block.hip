@@ -515,45 +515,57 @@ __device__ __noinline__ GateGradient gate_gradient_exact(int act, float g, float
   const double s = 1.0 / (1.0 + exp(-h)), r = 1.0 / (1.0 + exp(h));
   return {(float)((double)dh * u * (s * (1.0 + x * r * slope))), (float)((double)dh * (x * s))};
 }
-__device__ __forceinline__ float round_bf16(float v) { return bf16lo(pack_bf16x2(v, 0.f)); }
-__device__ __forceinline__ GateGradient gate_gradient(int act, float g, float u, float dh) {
-  float h = g, slope = 1.f, off = 24.f;  // (error of a term in units of 2^-24 of itself: about 20 roundings)
+// In 32 bits, and whether both round as the exact values do.  With u = 2^-24 and an
+// exponential and a reciprocal of 1 ulp, σ(−|h|) is off by (6 + 2|h|)u of itself and
+// σ(|h|) by 5u (GELU, whose h is off by 5u of itself: 6 + 7|h| and 6); dU adds two
+// roundings, dG three and those of t = g·σ(−h)·h', and the test's own is one more.
+__device__ __forceinline__ bool gate_gradient(int act, float g, float u, float dh, GateGradient& d) {
+  float h = g, slope = 1.f, per_h = 2.f * 0x1p-24f, more = 8.f * 0x1p-24f;
   if (act == kActGeluTanh) {
     const float g2 = g * g;
     h = (float)kGeluSlope * __builtin_fmaf((float)kGeluCube * g2, g, g);
     slope = (float)kGeluSlope * __builtin_fmaf(3.f * (float)kGeluCube, g2, 1.f);
-    off += 16.f * fabsf(h);  // (six roundings of h, in σ(h) and in σ(−h))
+    per_h = 8.f * 0x1p-24f;
+    more = 12.f * 0x1p-24f;
   }
-  const float e = expf(-fabsf(h)), inv = 1.f / (1.f + e);
-  const float near = inv, far = e * inv;  // σ(|h|), σ(−|h|)
+  const float e = __builtin_amdgcn_exp2f(fabsf(h) * -1.44269502f), near = __builtin_amdgcn_rcpf(1.f + e), far = e * near;
   const float s = h < 0.f ? far : near, r = h < 0.f ? near : far;
-  const float y = dh * s, t = g * r * slope;
-  const float du = y * g, dg = y * u * (1.f + t);
-  const float unit = off * 0x1p-24f;
+  const float y = dh * s, t = g * r * slope, yu = y * u;
+  d = {yu * (1.f + t), y * g};
+  const float unit = __builtin_fmaf(per_h, fabsf(h), 10.f * 0x1p-24f);
   // (2^-140: what underflows)
-  const float off_u = __builtin_fmaf(unit, fabsf(du), 0x1p-140f);
-  const float off_g = __builtin_fmaf(unit * (1.f + fabsf(t)), fabsf(y * u), 0x1p-140f);
-  // (below −80 the exponential nears fp32's end and loses bits)
-  const bool sure = h > -80.f && round_bf16(du - off_u) == round_bf16(du + off_u) &&
-                    round_bf16(dg - off_g) == round_bf16(dg + off_g);
-  if (sure) return {dg, du};
-  return gate_gradient_exact(act, g, u, dh);
+  const float off_u = __builtin_fmaf(unit, fabsf(d.du), 0x1p-140f);
+  const float off_g = __builtin_fmaf((unit + more) * (1.f + fabsf(t)), fabsf(yu), 0x1p-140f);
+  const uint32_t differ = pack_bf16x2(d.du - off_u, d.dg - off_g) ^ pack_bf16x2(d.du + off_u, d.dg + off_g);
+  // (zeros of either sign are alike; below −80 the exponential nears fp32's end and
+  // loses bits; NaN may be an infinity times what is 0 in fp32 alone)
+  return h > -80.f && (differ & 0x7fff7fffu) == 0u && !__builtin_isunordered(d.du, d.dg);
 }
-__global__ __launch_bounds__(256) void gate_gradient_kernel(const u32x4_t* __restrict__ dH, const u32x4_t* __restrict__ G,
-                                                            const u32x4_t* __restrict__ U, int64_t n8, int act,
-                                                            u32x4_t* __restrict__ dG, u32x4_t* __restrict__ dU) {
+__global__ __launch_bounds__(256) void gate_gradient_kernel(const uint16_t* __restrict__ dH, const uint16_t* __restrict__ G,
+                                                            const uint16_t* __restrict__ U, int64_t n8, int act,
+                                                            uint16_t* __restrict__ dG, uint16_t* __restrict__ dU) {
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n8; i += 256 * (int64_t)gridDim.x) {
-    const u32x4_t h = dH[i], g = G[i], u = U[i];
+    const u32x4_t h = reinterpret_cast<const u32x4_t*>(dH)[i], g = reinterpret_cast<const u32x4_t*>(G)[i],
+                  u = reinterpret_cast<const u32x4_t*>(U)[i];
     u32x4_t og, ou;
+    uint32_t unsure = 0u;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const GateGradient a = gate_gradient(act, bf16lo(g[q]), bf16lo(u[q]), bf16lo(h[q]));
-      const GateGradient b = gate_gradient(act, bf16hi(g[q]), bf16hi(u[q]), bf16hi(h[q]));
+      GateGradient a, b;
+      if (!gate_gradient(act, bf16lo(g[q]), bf16lo(u[q]), bf16lo(h[q]), a)) unsure |= 1u << (2 * q);
+      if (!gate_gradient(act, bf16hi(g[q]), bf16hi(u[q]), bf16hi(h[q]), b)) unsure |= 2u << (2 * q);
       og[q] = pack_bf16x2(a.dg, b.dg);
       ou[q] = pack_bf16x2(a.du, b.du);
     }
-    dG[i] = og;
-    dU[i] = ou;
+    reinterpret_cast<u32x4_t*>(dG)[i] = og;
+    reinterpret_cast<u32x4_t*>(dU)[i] = ou;
+    asm volatile("" ::: "memory");  // (the stores below come after those above)
+    for (; unsure != 0u; unsure &= unsure - 1u) {
+      const int64_t at = 8 * i + __builtin_ctz(unsure);
+      const GateGradient d = gate_gradient_exact(act, bf16lo(G[at]), bf16lo(U[at]), bf16lo(dH[at]));
+      dG[at] = (uint16_t)(pack_bf16x2(d.dg, 0.f) & 0xffffu);
+      dU[at] = (uint16_t)(pack_bf16x2(d.du, 0.f) & 0xffffu);
+    }
   }
 }
 
@@ -738,9 +750,7 @@ hipError_t launch_block_bwd(const BlockView& b, const uint16_t* X, int64_t M, co
     uint16_t* dG = reinterpret_cast<uint16_t*>(ws + L.off_dY);
     uint16_t* dU = dG + M * N;
     gate_gradient_kernel<<<std::min(cdiv(M * N / 8, 256), 8192u), 256, 0, st>>>(
-        reinterpret_cast<const u32x4_t*>(in.dH), reinterpret_cast<const u32x4_t*>(in.G),
-        reinterpret_cast<const u32x4_t*>(in.U), M * N / 8, in.act, reinterpret_cast<u32x4_t*>(dG),
-        reinterpret_cast<u32x4_t*>(dU));
+        in.dH, in.G, in.U, M * N / 8, in.act, dG, dU);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     d[0] = dG;
     d[1] = dU;

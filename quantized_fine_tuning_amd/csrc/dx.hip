@@ -132,8 +132,8 @@ __global__ __launch_bounds__(kThreads, 1) void dx_gemm_kernel(Nf4View W, const u
   // this workgroup's n steps [nfirst, nfirst + nsteps) (step indices below
   // are relative to nfirst) and its LoRA steps
   const int nall = (int)((N + NSTEP - 1) / NSTEP);
-  const int nfirst = split_first(sp, splits, LAYERS * nall);
-  const int nsteps = split_first(sp + 1, splits, LAYERS * nall) - nfirst;
+  int nfirst = split_first(sp, splits, LAYERS * nall);
+  int nsteps = split_first(sp + 1, splits, LAYERS * nall) - nfirst;
   int lsteps = sp == splits - 1 ? LSTEPS : 0;
   // MULTI: this workgroup's LoRA steps [lfirst, lfirst + lsteps) of the
   // tile's; step i belongs to used adapter gfirst + i / lper, chunk i % lper
@@ -152,8 +152,18 @@ __global__ __launch_bounds__(kThreads, 1) void dx_gemm_kernel(Nf4View W, const u
   // BLOCK: this workgroup's LoRA steps of the layers', lper each
   if constexpr (BLOCK) {
     lper = (ma.cols + 63) / 64;
-    lfirst = split_first(sp, splits, LAYERS * lper);
-    lsteps = split_first(sp + 1, splits, LAYERS * lper) - lfirst;
+    // Few enough for one split (the mask takes as long as four steps): the first
+    // takes them all, and fewer n steps.
+    const int all = LAYERS * lper, cost = all + (ma.drop.out > 0 ? 4 : 0), n = LAYERS * nall;
+    const int own = (n + cost + splits - 1) / splits - cost;
+    if (splits > 1 && own > 0) {
+      lsteps = sp == 0 ? all : 0;
+      nfirst = sp == 0 ? 0 : own + split_first(sp - 1, splits - 1, n - own);
+      nsteps = (sp == 0 ? own : own + split_first(sp, splits - 1, n - own)) - nfirst;
+    } else {
+      lfirst = split_first(sp, splits, all);
+      lsteps = split_first(sp + 1, splits, all) - lfirst;
+    }
   }
   // (then n step t uses the buffers (t + wpar) % 2)
   const int wpar = BLOCK ? lsteps & 1 : 0;
