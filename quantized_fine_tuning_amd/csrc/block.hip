@@ -646,7 +646,8 @@ BlockBwdLayout block_bwd_layout(int64_t M, int64_t N, int64_t K, int r, int laye
   L.off_P = off;
   const int64_t gemm = L.splits > 1 ? (int64_t)L.splits * M * K * 4 : 0;
   const int64_t factors = (int64_t)(L.slices_V + L.slices_T) * layers * M * r * 4;
-  const int64_t gradients = L.units > 1 ? (int64_t)L.units * layers * r * (K + N) * 4 : 0;
+  L.off_Q = off + round_up(gemm, 256);  // (read while the gradients' are written)
+  const int64_t gradients = L.units > 1 ? round_up(gemm, 256) + (int64_t)L.units * layers * r * (K + N) * 4 : 0;
   L.total = off + round_up(std::max({gemm, factors, gradients}), 256);
   return L;
 }
@@ -777,17 +778,15 @@ hipError_t launch_block_bwd(const BlockView& b, const uint16_t* X, int64_t M, co
     const BlockGemmArgs ma{SV, {b.A[0], b.A[1]}, b.r, C, cols, b.W[pair ? 1 : 0], nullptr, nullptr, in.act, d[1], b.drop};
     e = launch_dx_gemm_block(b.W[0], d[0], M, ma, pair, dX, dx16, L.splits, P, st);
   }
-  // one unit of tokens: the sum of dX's splits comes with the gradients
-  const bool tail = L.splits > 1 && L.units == 1;
-  if (e == hipSuccess && L.splits > 1 && !tail) e = launch_splitk_reduce(P, L.splits, M * K, dX, dx16, false, st);
   if (e != hipSuccess) return e;
+  // the gradients; with them the sum of dX's splits
   const GradientJob ja{{X, X}, SV, K, {dA[0], dA[1]}, 0}, jb{{d[0], d[1]}, ST, N, {dB[0], dB[1]}, r * K};
   const int nj = rank_blocks(b.r);
   const unsigned ta = cdiv(K, 128);
   const unsigned gx = ta + cdiv(N, 128), gz = (unsigned)layers * cdiv(r, 16 * nj);
-  const SplitSum sum{reinterpret_cast<const f32x4_t*>(P), L.splits, tail ? M * K / 4 : 0, dX, dx16 ? 1 : 0};
+  const SplitSum sum{reinterpret_cast<const f32x4_t*>(P), L.splits, L.splits > 1 ? M * K / 4 : 0, dX, dx16 ? 1 : 0};
   const dim3 grid(gx, (unsigned)L.units + cdiv(sum.n4, (int64_t)256 * gx * gz), gz);
-  float* const parts = L.units > 1 ? P : nullptr;
+  float* const parts = L.units > 1 ? reinterpret_cast<float*>(ws + L.off_Q) : nullptr;
   if (nj == 1)
     block_gradient_kernel<1><<<grid, 256, 0, st>>>(ja, jb, ta, M, b.r, L.unit, L.units, layers, b.drop, parts, sum);
   else if (nj == 2)
@@ -797,7 +796,7 @@ hipError_t launch_block_bwd(const BlockView& b, const uint16_t* X, int64_t M, co
   e = hipGetLastError();
   if (e != hipSuccess || L.units == 1) return e;
   block_gradient_finish_kernel<<<dim3(std::min(cdiv(r * (K + N), 1024), 1024u), (unsigned)layers), 256, 0, st>>>(
-      dA[0], dB[0], dA[1], dB[1], r * K, r * N, layers, P, L.units);
+      dA[0], dB[0], dA[1], dB[1], r * K, r * N, layers, parts, L.units);
   return hipGetLastError();
 }
 

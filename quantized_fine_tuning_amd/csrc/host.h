@@ -344,8 +344,9 @@ struct BlockFwdLayout {
 };
 struct BlockBwdLayout {
   // two layers: bf16 dG, dU [2][M][N]; bf16 splits of s·V and s·T [layers][M][C];
-  // one fp32 area: the partial sums of V and T, the dX GEMM's, the gradients'
-  size_t off_dY, off_V, off_T, off_P, total;
+  // one fp32 area: the partial sums of V and T, then the dX GEMM's, and behind those
+  // (off_Q) the gradients'
+  size_t off_dY, off_V, off_T, off_P, off_Q, total;
   int splits, slices_T, slices_V, units;
   int64_t unit;
 };
