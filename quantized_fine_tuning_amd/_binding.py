@@ -48,7 +48,9 @@ QLORA_FMT_NF4 = 1
 QLORA_FMT_INT4 = 2
 QLORA_FMT_INT8 = 3
 FORMATS = {"nf4": QLORA_FMT_NF4, "int4": QLORA_FMT_INT4, "int8": QLORA_FMT_INT8}
-ACTIVATIONS = {"silu": 1, "gelu_tanh": 2}
+QLORA_ACT_SILU = 1
+QLORA_ACT_GELU_TANH = 2
+ACTIVATIONS = {"silu": QLORA_ACT_SILU, "gelu_tanh": QLORA_ACT_GELU_TANH}
 QLORA_ADAMW_MAX_TENSORS = 8
 QLORA_ADAPTERS_MAX = 1024
 QLORA_LOGPROBS_MAX_TOP = 256
@@ -663,15 +665,13 @@ class Dropout:
             if not 0 <= v < 2 ** 64:
                 raise ValueError(f"{name}={v} outside [0, 2^64)")
         self.p, self.seed, self.offset, self.step = float(p), int(seed), int(offset), step
-        self._struct = qlora_dropout_t(self.p, self.seed, self.offset, None)
 
 
 def _drop_ref(drop, dev: int):
     if drop is None:
         return None
-    if drop.step is not None:
-        drop._struct.step = _address(drop.step, "step", (1,), (_torch().int64,), dev)
-    return ctypes.byref(drop._struct)
+    step = None if drop.step is None else _address(drop.step, "step", (1,), (_torch().int64,), dev)
+    return ctypes.byref(qlora_dropout_t(drop.p, drop.seed, drop.offset, step))
 
 
 def _block_sizes(call, N: int, K: int, M_max: int, r: int) -> dict:

@@ -1,0 +1,215 @@
+"""One fine-tuning step of a gated block and a quantized head as a program runs
+it: the block with dropout, the head with dropout of its own to the logits, the
+log-probabilities of the given tokens with their gradient in the logits' place,
+both backward passes and AdamW over all adapters.  Every stage is checked against
+the fp64 oracle on what the stage before it produced; the whole step is captured
+into a graph and replayed with other tokens and other masks; two steps run on two
+streams at once."""
+
+import numpy as np
+import pytest
+
+import quantized_fine_tuning_amd as q
+from oracle import adamw as ref_adamw
+from oracle import block as ref
+from tests import gpu_util as G
+from tests.test_gpu_adapters import within
+from tests.test_gpu_block import Case, HALF_BF16, check_gated, check_gated_backward, check_linear, check_linear_backward
+from tests.test_gpu_logprobs import Bounds, check, check_top
+
+pytestmark = pytest.mark.gpu
+
+VOCAB, LD, N, K, R, TOP, TAU, P = 501, 504, 320, 192, 16, 5, 1.5, 0.25
+SEED = 77
+
+
+class Step:
+    def __init__(self, M, act="silu", seed=12):
+        import torch as t
+        self.M = M
+        self.block, self.head = Case(M, N, K, R, 2, P, act, seed=seed), Case(M, LD, N, R, 1, P, seed=seed + 1)
+        self.at = t.tensor([1], dtype=t.int64, device="cuda")  # the masks' step
+        self.block.drop, self.head.drop = q.Dropout(P, SEED, 0, self.at), q.Dropout(P, SEED + 1, 0, self.at)
+        g = t.Generator().manual_seed(seed)
+        self.target = t.randint(0, VOCAB, (M,), generator=g).to(t.int32)
+        self.target[::5] = -100  # (prompts and padding)
+        self.target = self.target.cuda()
+        self.g = (t.rand(M, generator=g) - 0.8).cuda() / M  # gradients of log p, and of the entropy
+        self.h = t.full((M,), -0.02 / M, device="cuda")
+        e = lambda *s, dtype=t.float32: t.full(s, float("nan"), dtype=dtype, device="cuda")  # noqa: E731
+        bf = t.bfloat16
+        self.H, self.G, self.U, self.Z = e(M, N, dtype=bf), e(M, N, dtype=bf), e(M, N, dtype=bf), e(M, LD, dtype=bf)
+        self.T1, self.T2 = e(2, M, R), e(M, R)
+        self.logp, self.lse, self.entropy = e(M), e(M), e(M)
+        self.top, self.index = e(M, TOP), t.full((M, TOP), -7, dtype=t.int32, device="cuda")
+        self.dH, self.dX = e(M, N, dtype=bf), e(M, K, dtype=bf)
+        self.grads = [e(*s) for s in ((R, K), (N, R), (R, K), (N, R), (R, N), (LD, R))]
+        b, h = self.block.dev, self.head.dev
+        self.params = [b["A0"], b["B0"], b["A1"], b["B1"], h["A0"], h["B0"]]
+        self.moments = [(t.zeros_like(x), t.zeros_like(x)) for x in self.grads]
+        self.ws = [c.scratch(k) for c in (self.block, self.head) for k in ("fwd_ws_bytes", "bwd_ws_bytes")]
+
+    def forward(self):
+        b, h = self.block, self.head
+        q.qlora_gated_fwd(b.w[0], b.w[1], b.dev["X"], b.adapters, b.act, b.drop, self.H, self.G, self.U, self.T1, self.ws[0])
+        q.qlora_dropout_linear_fwd(h.w[0], self.H, h.dev["A0"], h.dev["B0"], R, h.alpha, h.drop, self.Z, self.T2, self.ws[2])
+
+    def gradient(self):
+        q.qlora_logprobs_fwd(self.Z, self.target, TAU, self.logp, self.lse, self.entropy, self.top, self.index,
+                             d_logp=self.g, d_entropy=self.h, dZ=self.Z, vocab=VOCAB)
+
+    def backward(self):
+        b, h, g = self.block, self.head, self.grads
+        q.qlora_dropout_linear_bwd(h.w[0], self.H, self.Z, h.dev["A0"], h.dev["B0"], R, h.alpha, h.drop, self.T2, self.dH,
+                                   g[4], g[5], self.ws[3])
+        q.qlora_gated_bwd(b.w[0], b.w[1], b.dev["X"], self.dH, self.G, self.U, b.adapters, b.act, b.drop, self.T1, self.dX,
+                          *g[:4], self.ws[1])
+
+    def update(self):
+        q.qlora_adamw_step([(p, g, m, v) for p, g, (m, v) in zip(self.params, self.grads, self.moments)], 1e-2, 0.9, 0.999,
+                           1e-8, 0.01, 1)
+
+    def run(self):
+        self.forward()
+        self.gradient()
+        self.backward()
+        self.update()
+
+    def results(self):
+        return [self.logp, self.entropy, self.top, self.index, self.dX, *self.grads, *self.params,
+                *(x for pair in self.moments for x in pair)]
+
+
+def take(case, **given):
+    """The case with tensors of a stage that ran, and the host's copies with them."""
+    for name, x in given.items():
+        case.dev[name] = x
+    case.host = {n: v.double().cpu().numpy() for n, v in case.dev.items()}
+
+
+@pytest.mark.parametrize("M,act", [(1, "silu"), (13, "gelu_tanh"), (40, "silu"), (150, "gelu_tanh"), (300, "silu")])
+def test_each_stage_on_what_the_one_before_gave(M, act):
+    import torch as t
+    print(f"block step M={M} {act}", flush=True)
+    s = Step(M, act)
+    b, h = s.block, s.head
+    b.mask, h.mask = ref.keep(M, K, P, SEED, 1), ref.keep(M, N, P, SEED + 1, 1)
+    s.forward()
+    got = check_gated(b)  # (the same call on tensors of its own, against the oracle)
+    assert all(t.equal(x, y) for x, y in zip(got, (s.H, s.G, s.U, s.T1)))
+    take(h, X=s.H)
+    Y, T = check_linear(h, t.bfloat16)
+    assert t.equal(Y, s.Z) and t.equal(T, s.T2)
+
+    logits = s.Z.clone()
+    s.gradient()
+    at = [logits.cpu(), s.target.cpu(), TAU, VOCAB, s.g.cpu(), s.h.cpu()]
+    bounds = Bounds(*at)
+    check(s.logp, bounds.logp, bounds.lim_logp, "f32", "logp")
+    check(s.entropy, bounds.entropy, bounds.lim_entropy, "f32", "entropy")
+    check(s.Z, bounds.dZ, bounds.lim_dZ, "bf16", "dZ")
+    check_top({"top_logp": s.top, "top_index": s.index}, logits.cpu(), TAU, VOCAB, TOP, bounds)
+    assert not s.Z[:, VOCAB:].any()
+
+    s.backward()
+    take(h, dY=s.Z)
+    got = check_linear_backward(h, t.bfloat16, s.T2)
+    assert all(t.equal(x, y) for x, y in zip(got, (s.dH, *s.grads[4:])))
+    take(b, dY=s.dH, G=s.G, U=s.U)
+    dX, got = check_gated_backward(b, t.bfloat16, s.T1)
+    assert t.equal(dX, s.dX) and all(t.equal(x, y) for x, y in zip(got, s.grads))
+
+    before = [G.host_bf16(p).copy().reshape(-1) for p in s.params]
+    s.update()
+    for bits, p, grad in zip(before, s.params, s.grads):
+        zeros = np.zeros(bits.size, np.float32)
+        want, _, _ = ref_adamw.step(bits, grad.cpu().numpy().reshape(-1), zeros, zeros, 1e-2, 0.9, 0.999, 1e-8, 0.01, 1,
+                                    param_bf16=True)
+        np.testing.assert_array_equal(G.host_bf16(p).reshape(-1), want)
+
+    # the same block and head without dropout serve a token of the batch
+    few = [x[:1].contiguous() for x in (b.dev["X"], s.H, s.Z)]
+    q.qlora_gated_fwd(b.w[0], b.w[1], few[0], b.adapters, act, None, few[1], None, None, None, s.ws[0])
+    q.qlora_dropout_linear_fwd(h.w[0], few[1], h.dev["A0"], h.dev["B0"], R, h.alpha, None, few[2], None, s.ws[2])
+    x, (A, B) = few[1].double().cpu().numpy(), (h.dev[n].double().cpu().numpy() for n in ("A0", "B0"))
+    want, size = (ref.forward(x, h.W[0], A, B, h.s, 1.0, a)[0] for a in (False, True))
+    within(few[2], want, size, 2 * N + 4 * R, "served token", HALF_BF16)
+
+
+@pytest.mark.parametrize("M", [9, 40, 200])
+def test_the_step_in_a_graph(M):
+    """Replays, each on another batch and with other masks, against the eager step from the same state."""
+    import torch as t
+    s = Step(M)
+    state = [*s.params, *(x for pair in s.moments for x in pair)]
+    side = t.cuda.Stream()
+    side.wait_stream(t.cuda.current_stream())
+    with t.cuda.stream(side):
+        s.run()
+    t.cuda.current_stream().wait_stream(side)
+    t.cuda.synchronize()
+    graph = t.cuda.CUDAGraph()
+    with t.cuda.graph(graph):
+        s.run()
+    g = t.Generator(device="cuda").manual_seed(8)
+    masks = []
+    for rep in range(4):
+        print(f"block step M={M} replay {rep}", flush=True)
+        s.at += 1
+        s.block.dev["X"].copy_(t.randn(M, K, generator=g, device="cuda"))
+        s.target.copy_(t.randint(-1, VOCAB + 1, (M,), generator=g, device="cuda", dtype=t.int32))
+        kept = [x.clone() for x in state]
+        s.run()
+        t.cuda.synchronize()
+        want = [x.clone() for x in s.results()]
+        for x, k in zip(state, kept):
+            x.copy_(k)
+        for x in (s.H, s.G, s.U, s.Z, s.T1, s.T2, s.logp, s.lse, s.entropy, s.top, s.dH, s.dX, *s.grads):
+            x.fill_(float("nan"))
+        for w in s.ws:
+            w.fill_(0xA5)
+        t.cuda.synchronize()
+        graph.replay()
+        t.cuda.synchronize()
+        assert all(t.equal(a, b) for a, b in zip(s.results(), want))
+        masks.append(s.grads[0].clone())
+    assert not t.equal(masks[0], masks[1])
+
+
+def test_two_steps_on_two_streams():
+    """Each with its own tensors and workspaces: as one after the other."""
+    import torch as t
+    print("block steps on two streams", flush=True)
+    a, b, alone = Step(150), Step(13, "gelu_tanh", seed=20), [Step(150), Step(13, "gelu_tanh", seed=20)]
+    for s in alone:
+        s.run()
+    t.cuda.synchronize()
+    streams = [t.cuda.Stream(), t.cuda.Stream()]
+    for s, stream in zip((a, b), streams):
+        with t.cuda.stream(stream):
+            s.run()
+    t.cuda.synchronize()
+    for s, want in zip((a, b), alone):
+        assert all(t.equal(x, y) for x, y in zip(s.results(), want.results()))
+
+
+def test_rows_behind_the_tokens_stay_as_they_were():
+    """A batch in larger tensors: what lies behind its last row is neither read nor written."""
+    import torch as t
+    for M in (7, 40, 70, 300):
+        print(f"rows behind {M} tokens", flush=True)
+        c = Case(M, N, K, R, 2, P, seed=30)
+        bf = t.bfloat16
+        wide = lambda x: t.cat([x, t.full((9, x.shape[1]), float("nan"), dtype=x.dtype, device="cuda")])  # noqa: E731
+        X, dY, Gv, Uv = (wide(c.dev[n]) for n in ("X", "dY", "G", "U"))
+        H, Gs, Us = (t.full((M + 9, N), 3.0, dtype=bf, device="cuda") for _ in range(3))
+        dX = t.full((M + 9, K), 3.0, device="cuda")
+        q.qlora_gated_fwd(c.w[0], c.w[1], X[:M], c.adapters, c.act, c.drop, H[:M], Gs[:M], Us[:M], None,
+                          c.scratch("fwd_ws_bytes"))
+        grads = [c.nan(*s) for s in ((R, K), (N, R)) * 2]
+        q.qlora_gated_bwd(c.w[0], c.w[1], X[:M], dY[:M], Gv[:M], Uv[:M], c.adapters, c.act, c.drop, None, dX[:M], *grads,
+                          c.scratch("bwd_ws_bytes"))
+        for x in (H, Gs, Us, dX):
+            assert (x[M:] == 3.0).all() and t.isfinite(x[:M]).all()
+        want, got = c.gated_backward(t.float32, None)
+        assert t.equal(dX[:M], want) and all(t.equal(x, y) for x, y in zip(grads, got))
