@@ -575,7 +575,7 @@ __global__ __launch_bounds__(128 * NW) void gated_gemv_kernel(Nf4View W0, Nf4Vie
                                                               const uint16_t* __restrict__ B1, int r,
                                                               GatedOut out, int row_groups, int share, Codebook cb) {
   constexpr int NT = 128 * NW, DEPTH = 2;  // threads, sets of codes
-  extern __shared__ __attribute__((aligned(16))) char sx[];  // X [M][K] bf16 (XL)
+  extern __shared__ __attribute__((aligned(128))) char s_x[];  // X bf16 (XL), as x_at says
   __shared__ __attribute__((aligned(256))) float sq[16];
   __shared__ f32x4_t s_acc[2][NW][64];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6) % NW;
@@ -589,6 +589,14 @@ __global__ __launch_bounds__(128 * NW) void gated_gemv_kernel(Nf4View W0, Nf4Vie
   const rsrc_t rs = make_rsrc(W.s, ((N * kpr + kDqBlock - 1) / kDqBlock) * 4);
   const rsrc_t rx = make_rsrc(X, (int64_t)M * K * 2);
   const bool x_row = lr < M;
+  // Byte in s_x of 8 elements, the c-th of block b of token m: rows of an even number
+  // of blocks, in which a token's index moves both the 16-byte pieces of a block and
+  // neighbouring blocks, so that the 64 lanes of a read are on all banks alike (as
+  // rows lie in memory all 16 tokens start on the same ones: 13 tokens, r = 64, 29.5 us, so 24.4).
+  const uint32_t x_stride = ((uint32_t)nb + 1u & ~1u) * 128u;
+  auto x_at = [&](uint32_t m, uint32_t b, uint32_t c) __attribute__((always_inline)) {
+    return m * x_stride + (b ^ (m >> 3 & 1u)) * 128u + 16u * (c ^ (m & 7u));
+  };
   // this wave's ranks, and its tokens' operands
   const int rank = 32 * wave + 8 * kq;
   u32x4_t tf[3];
@@ -645,7 +653,7 @@ __global__ __launch_bounds__(128 * NW) void gated_gemv_kernel(Nf4View W0, Nf4Vie
     const float cp = __fadd_rn(__fmul_rn(__builtin_amdgcn_cvt_f32_fp8((int)g.e, 0), g.s), mu);
     const int b = 4 * (wave + NW * step) + kq;
     const bool use_x = x_row && b < nb;
-    const char* xrow = sx + (size_t)(lr * K + (use_x ? b : 0) * kBlock) * 2;
+    const uint32_t xrow = lds_offset(s_x) + x_at(lr, use_x ? b : 0, 0);
     const uint32_t sqb = lds_offset(sq);
 #pragma unroll
     for (int t = 0; t < 8; ++t) {
@@ -662,7 +670,7 @@ __global__ __launch_bounds__(128 * NW) void gated_gemv_kernel(Nf4View W0, Nf4Vie
       }
       u32x4_t xa;
       if constexpr (XL)
-        xa = use_x ? *reinterpret_cast<const u32x4_t*>(xrow + 16 * t) : u32x4_t{0u, 0u, 0u, 0u};
+        xa = use_x ? *(const __attribute__((address_space(3))) u32x4_t*)(uintptr_t)(xrow ^ (uint32_t)(16 * t)) : u32x4_t{0u, 0u, 0u, 0u};
       else
         xa = g.x[t];
       acc = mfma_16x16x32(xa, bfrag, acc);
@@ -681,8 +689,18 @@ __global__ __launch_bounds__(128 * NW) void gated_gemv_kernel(Nf4View W0, Nf4Vie
 
   const float cbq = cb.q[tid & 15];
   if constexpr (XL) {
-    const int nvec = (M * (int)K * 2) / 16;
-    for (int v = tid; v < nvec; v += NT) *reinterpret_cast<u32x4_t*>(sx + 16 * v) = buf_load16(rx, (uint32_t)(16 * v), 0u);
+    constexpr int AT_ONCE = NW == 4 ? 1 : 8;  // (16 waves have more to copy each)
+    const uint32_t row = (uint32_t)K / 8, nvec = (uint32_t)M * row;
+    for (uint32_t v0 = 0; v0 < nvec; v0 += AT_ONCE * NT) {
+      u32x4_t x[AT_ONCE];
+#pragma unroll
+      for (int i = 0; i < AT_ONCE; ++i) x[i] = buf_load16(rx, 16u * (v0 + i * NT + tid), 0u);
+#pragma unroll
+      for (int i = 0; i < AT_ONCE; ++i) {
+        const uint32_t v = v0 + i * NT + tid, m = v / row, c = v - m * row;
+        if (v < nvec) *reinterpret_cast<u32x4_t*>(s_x + x_at(m, c >> 3, c & 7u)) = x[i];
+      }
+    }
   }
   __builtin_amdgcn_sched_barrier(0);
   Group g[DEPTH];
@@ -829,7 +847,7 @@ hipError_t launch_gated_gemv(const BlockView& b, const uint16_t* X, int64_t M, c
                              hipStream_t st) {
   const Nf4View& W = b.W[0];
   const int groups = (int)((W.N + GEMV_ROWS - 1) / GEMV_ROWS);
-  const size_t xb = (size_t)M * W.K * 2;
+  const size_t xb = (size_t)M * round_up(W.K, 2 * kBlock) * 2;  // (rows of an even number of blocks)
 #define QNF4_GEMV_LAUNCH(NW, XL, RES)                                                                              \
   {                                                                                                                \
     int share = 0; /* threads per output: 128·NW over 16 rows of M tokens, two at least, within a wave */         \
