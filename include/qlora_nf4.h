@@ -402,7 +402,7 @@ typedef struct {
  *   G_save, U_save  device bf16 [M, N] receiving G and U rounded, for the backward
  *                   pass, or both NULL;
  *   T_save          device fp32 [2, M, r] receiving T_gate and T_up, or NULL.
- * Limits as for qlora_adapters_fwd; outputs must not alias inputs. */
+ * s·T_* enters G and U of up to 16 tokens to 24 bits, of more to 16.  Limits as for qlora_adapters_fwd; outputs must not alias inputs. */
 qlora_status qlora_gated_sizes(int64_t N, int64_t K, int64_t M_max, int32_t r,
                                qlora_block_sizes_t* out);
 qlora_status qlora_gated_fwd(const qlora_nf4_t* gate, const qlora_nf4_t* up, const void* X,

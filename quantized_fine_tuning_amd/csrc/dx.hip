@@ -101,6 +101,9 @@ __device__ __forceinline__ int dq_cg(int l) { return (l & 1) | ((l >> 2) & 6); }
 // LoRA steps come first, from the three-part splits S and A in its own layout:
 // between them and the n steps the sums are the adapters' share of dX alone, and
 // where the adapters' input had dropout those of dropped elements become zero.
+// The masks of a tile's 65,536 elements take as long as four steps, 2 us of the 320
+// of 4096 tokens over 11008 x 4096.  (Found before the first step they need registers
+// that the sums hold, 391 us; beside the first n step's products it was slower too.)
 template <int LSTEPS, bool F16, int MODE = kPlain>
 __global__ __launch_bounds__(kThreads, 1) void dx_gemm_kernel(Nf4View W, const uint16_t* __restrict__ dY,
                                                               int64_t M, const uint16_t* __restrict__ sU,

@@ -100,6 +100,8 @@ __device__ __forceinline__ int xswz(int row, int chunk) {
 // as many weight rows of each, the gate's first: an MFMA wave's 64 columns are 32
 // of each layer's, the same ones, so that a lane holds both factors of the outputs
 // it writes; a LoRA step belongs to one layer and adds to its half.
+// (4096 tokens, two of 11008 x 4096, r = 64: 662 us with H alone, 683 with G and U
+// too, 1.1 PFLOP/s, where two plain layers take 645; with dropout 694 in all.)
 template <int LSTEPS, bool F16, int TMV, int MODE = kPlain>
 __global__ __launch_bounds__(kThreads, 1) void fwd_gemm_kernel(Nf4View W, const uint16_t* __restrict__ X,
                                                                int64_t M, const uint16_t* __restrict__ sT,

@@ -562,12 +562,12 @@ __global__ __launch_bounds__(64 * WV) void gemv_adapters_kernel(Nf4View W, const
 // share an output are as many as M leaves.
 //
 // Bound by the decode: 77 % of the vector units' time and 40 % of the LDS's.  (Two
-// 11008 x 4096 weights, r = 16, graph-replayed with T's kernel: one token 21.2 us,
-// 46.6 MB at 2.2 TB/s, 13 tokens of r = 64 28.4 us.  Both layers in every wave took
-// 22.4 and 33.9; two block groups ahead 21.3; X's fragments kept in registers
-// across row groups 27.4, their spills' waits holding up the codes; levels looked
-// up in pairs, 64 KB of them, a third fewer vector instructions, 21.9 for want of
-// room for more than one workgroup.)
+// 11008 x 4096 weights, graph-replayed with T's kernel: one token, r = 16, 21.8 us, of
+// them 17.4 this kernel's, 47.7 MB at 2.7 TB/s; 13 tokens, r = 64, 24.4.  Both layers
+// in every wave took 22.4 for one token where this form took 21.2, two block groups
+// ahead 21.3; X's fragments kept in registers across row groups 27.4, their spills'
+// waits holding up the codes; levels looked up in pairs, 64 KB of them, a third
+// fewer vector instructions, 21.9 for want of room for more than one workgroup.)
 template <int NW, bool XL>
 __global__ __launch_bounds__(128 * NW) void gated_gemv_kernel(Nf4View W0, Nf4View W1, const uint16_t* __restrict__ X,
                                                               int M, const uint16_t* __restrict__ S,

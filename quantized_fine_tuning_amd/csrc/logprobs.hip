@@ -18,7 +18,9 @@
 //
 // Forward, with or without the gradient: one workgroup per token, the row in
 // registers between its passes (or, too long for that, read again from the
-// caches).
+// caches).  4096 x 32000 bf16 with the gradient 100 us, 524 MB at 5.2 TB/s, more than a
+// large copy's rate; the values alone 40.  Few rows are latency: 32 x 32000 4.5 us, with
+// 20 alternatives and entropy 9.8.
 //
 // The k most likely columns, equal logits by their index: every thread's largest
 // logit is known from the maximum, and the k-th largest of those is a bound that
@@ -29,7 +31,8 @@
 //
 // Gradient from a saved log-sum-exp (and entropy): no sums over the row, so rows
 // are cut into parts of 2,048 chunks, a workgroup each; log2 q takes z·c −
-// lse·log2(e) in two parts each (rounded ones would be off by an ulp of z/tau).
+// lse·log2(e) in two parts each (rounded ones would be off by an ulp of z/tau).  777 x
+// 50001 fp32 66 us, 311 MB at 4.7 TB/s.
 #include "host.h"
 #include "rows.h"
 
