@@ -190,18 +190,33 @@ __global__ __launch_bounds__(256) void block_down_kernel(DownJob t, DownJob u, i
 // of: T [layers][M][r]; Tt, the single layer's in the dequant-GEMV's tile layout; S
 // [layers][M][C], the three-part splits of scale·T.
 constexpr int kFewRanks = 4;
-__global__ __launch_bounds__(256) void block_few_down_kernel(const uint16_t* __restrict__ X, int64_t M, int64_t K,
-                                                             const uint16_t* __restrict__ A0,
-                                                             const uint16_t* __restrict__ A1, int r, DropView drop,
-                                                             float scale, float* __restrict__ T,
-                                                             float* __restrict__ Tt, uint16_t* __restrict__ S) {
-  constexpr int UN = 2;
-  __shared__ float s_part[4][kFewRanks];
+// The sums of each wave's v[j] added in wave order, for thread j < R.
+template <int R>
+__device__ __forceinline__ float few_sum(float (&v)[R]) {
+  __shared__ float s_part[4][R];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int m = (int)blockIdx.x, j0 = kFewRanks * (int)blockIdx.y, layer = (int)blockIdx.z;
-  drop = drawn(drop);
+#pragma unroll
+  for (int j = 0; j < R; ++j) {
+    v[j] = wave_sum(v[j]);
+    if (lane == 0) s_part[wave][j] = v[j];
+  }
+  __syncthreads();
+  const int j = tid < R ? tid : 0;
+  return ((s_part[0][j] + s_part[1][j]) + s_part[2][j]) + s_part[3][j];
+}
+__device__ __forceinline__ void few_split(float v, uint16_t* S, int r) {
+  uint16_t o[3];
+  split3(v, o);
+#pragma unroll
+  for (int i = 0; i < 3; ++i) S[i * r] = o[i];
+}
+// Thread j < kFewRanks: T[m][j0 + j] of the layer with A.
+__device__ __forceinline__ float few_down(const uint16_t* __restrict__ X, int64_t m, int64_t K,
+                                          const uint16_t* __restrict__ A, int j0, const DropView& drop) {
+  constexpr int UN = 2;
+  const int tid = threadIdx.x;
   const rsrc_t rl = make_rsrc(X + m * K, K * 2);
-  const rsrc_t rr = make_rsrc((layer ? A1 : A0) + j0 * K, (int64_t)kFewRanks * K * 2);
+  const rsrc_t rr = make_rsrc(A + j0 * K, (int64_t)kFewRanks * K * 2);
   float acc[kFewRanks] = {};
   for (int64_t k0 = 8 * tid; k0 < K; k0 += 2048 * UN) {
     u32x4_t x[UN], w[UN][kFewRanks];
@@ -221,23 +236,70 @@ __global__ __launch_bounds__(256) void block_few_down_kernel(const uint16_t* __r
       for (int j = 0; j < kFewRanks; ++j) acc[j] = dot8(x[u], w[u][j], acc[j]);
     }
   }
-#pragma unroll
-  for (int j = 0; j < kFewRanks; ++j) {
-    acc[j] = wave_sum(acc[j]);
-    if (lane == 0) s_part[wave][j] = acc[j];
-  }
-  __syncthreads();
-  if (tid >= kFewRanks) return;
-  const int j = j0 + tid;
-  const float t = __fmul_rn(((s_part[0][tid] + s_part[1][tid]) + s_part[2][tid]) + s_part[3][tid], drop.scale);
+  return __fmul_rn(few_sum(acc), drop.scale);
+}
+__global__ __launch_bounds__(256) void block_few_down_kernel(const uint16_t* __restrict__ X, int64_t M, int64_t K,
+                                                             const uint16_t* __restrict__ A0,
+                                                             const uint16_t* __restrict__ A1, int r, DropView drop,
+                                                             float scale, float* __restrict__ T,
+                                                             float* __restrict__ Tt, uint16_t* __restrict__ S) {
+  const int m = (int)blockIdx.x, j0 = kFewRanks * (int)blockIdx.y, layer = (int)blockIdx.z;
+  const float t = few_down(X, m, K, layer ? A1 : A0, j0, drawn(drop));
+  if (threadIdx.x >= kFewRanks) return;
+  const int j = j0 + (int)threadIdx.x;
   if (T) T[(layer * M + m) * r + j] = t;
   if (Tt) Tt[(j >> 4) * 256 + 16 * m + (j & 15)] = t;
-  if (S) {
-    uint16_t o[3];
-    split3(__fmul_rn(scale, t), o);
-#pragma unroll
-    for (int i = 0; i < 3; ++i) S[(layer * M + m) * adapter_cols(r) + i * r + j] = o[i];
+  if (S) few_split(__fmul_rn(scale, t), S + (layer * M + m) * adapter_cols(r) + j, r);
+}
+
+// The splits of s·T (ST; from T_in where it was saved) and of s·V (SV) of few tokens
+// in one launch, in place of block_down_kernel and block_factor_kernel: a workgroup
+// per (token, 4 ranks of T) and, blockIdx.z >= layers, one per (token, 8 ranks of V),
+// whose threads take two rows of B a step, 16 bytes of each.
+__global__ __launch_bounds__(256) void block_few_factors_kernel(DownJob t, DownJob u, const float* __restrict__ T_in,
+                                                                int64_t M, int r, int layers, DropView drop, float scale,
+                                                                uint16_t* __restrict__ ST, uint16_t* __restrict__ SV) {
+  const int tid = threadIdx.x, m = (int)blockIdx.x, z = (int)blockIdx.z, layer = z % layers;
+  const int64_t at = layer * M + m;
+  if (z < layers) {
+    const int j0 = kFewRanks * (int)blockIdx.y;
+    float v = 0.f;
+    if (!T_in)
+      v = few_down(t.L[layer], m, t.Kred, t.R[layer], j0, drawn(drop));
+    else if (tid < kFewRanks)
+      v = T_in[at * r + j0 + tid];
+    if (tid < kFewRanks) few_split(__fmul_rn(scale, v), ST + at * adapter_cols(r) + j0 + tid, r);
+    return;
   }
+  const int j0 = 8 * (int)blockIdx.y;
+  if (j0 >= r) return;
+  constexpr int UN = 4;
+  const int64_t N = u.Kred;
+  const rsrc_t ry = make_rsrc(u.L[layer] + m * N, N * 2), rb = make_rsrc(u.R[layer], N * r * 2);
+  float acc[8] = {};
+  for (int64_t n0 = 2 * tid; n0 < N; n0 += 512 * UN) {
+    uint32_t y[UN];
+    u32x4_t b[UN][2];
+#pragma unroll
+    for (int i = 0; i < UN; ++i) {
+      const int64_t n = n0 + 512 * i;
+      const bool in = n < N;
+      y[i] = buf_load4(ry, in ? (uint32_t)(n * 2) : 0x7fffffffu, 0u);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) b[i][h] = buf_load16(rb, in ? (uint32_t)(((n + h) * r + j0) * 2) : 0x7fffffffu, 0u);
+    }
+#pragma unroll
+    for (int i = 0; i < UN; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float d = h ? bf16hi(y[i]) : bf16lo(y[i]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          acc[j] = __builtin_fmaf(d, j & 1 ? bf16hi(b[i][h][j >> 1]) : bf16lo(b[i][h][j >> 1]), acc[j]);
+      }
+  }
+  const float v = __fmul_rn(few_sum(acc), drop.scale);  // (the mask's scale, for dX and dA)
+  if (tid < 8) few_split(__fmul_rn(scale, v), SV + at * adapter_cols(r) + j0 + tid, r);
 }
 
 // The slices added in order, 16 tokens x 16 ranks per workgroup: v = mult·Σ, as
@@ -606,6 +668,17 @@ hipError_t launch_down(const DownJob& t, const DownJob& u, int64_t M, int r, int
   return hipGetLastError();
 }
 
+// Whether a backward pass takes its factors from block_few_factors_kernel: one launch
+// for two, but each token reads its 16 bytes of every row of B, lines of which hold
+// other ranks'.  (A whole pass of 61 tokens, N x K, replayed, us against the two:
+// 4096 x 4096 r = 8 28.0 and 32.1, r = 32 30.3 and 33.2, r = 64 38.0 and 35.1; 4096 x
+// 11008 r = 16 39.7 and 46.3, r = 32 43.0 and 47.1, r = 64 51.6 and 49.3; 11008 x 4096
+// r = 16 38.7 and 39.0, r = 32 43.0 and 40.2.  4 tokens: 21.4 and 24.3, 32.7 and 39.2,
+// 33.5 and 32.8 at r = 8, 16 and 16.)
+bool few_factors(int64_t M, int64_t N, int64_t K, int r) {
+  return M <= kMidTokens && (r <= 16 || (r <= 32 && N <= K));
+}
+
 // Units of tokens of the gradients' reduction: as many as fill the chip about
 // twice over, of 64 tokens or more.
 int64_t gradient_unit(int64_t M, int64_t N, int64_t K, int r, int layers) {
@@ -770,10 +843,15 @@ hipError_t launch_block_bwd(const BlockView& b, const uint16_t* X, int64_t M, co
   const int slices_T = T_saved ? 0 : L.slices_T;
   float* const PV = P + (int64_t)slices_T * layers * M * r;
   const DownJob t{{X, X}, {b.A[0], b.A[1]}, K, P, slices_T}, v{{d[0], d[1]}, {b.B[0], b.B[1]}, N, PV, L.slices_V};
-  if ((e = launch_down(t, v, M, b.r, layers, b.drop, st)) != hipSuccess) return e;
-  const FactorJob ft{P, slices_T, T_saved, nullptr, ST, b.drop.scale, b.scale};
-  const FactorJob fv{PV, L.slices_V, nullptr, nullptr, SV, b.drop.scale, b.scale};
-  block_factor_kernel<<<dim3(cdiv(M, 16), cdiv(r, 16), 2u * layers), 256, 0, st>>>(ft, fv, M, b.r, layers);
+  if (few_factors(M, N, K, r)) {
+    block_few_factors_kernel<<<dim3((unsigned)M, (unsigned)(r / kFewRanks), 2u * layers), 256, 0, st>>>(
+        t, v, T_saved, M, r, layers, b.drop, b.scale, ST, SV);
+  } else {
+    if ((e = launch_down(t, v, M, r, layers, b.drop, st)) != hipSuccess) return e;
+    const FactorJob ft{P, slices_T, T_saved, nullptr, ST, b.drop.scale, b.scale};
+    const FactorJob fv{PV, L.slices_V, nullptr, nullptr, SV, b.drop.scale, b.scale};
+    block_factor_kernel<<<dim3(cdiv(M, 16), cdiv(r, 16), 2u * layers), 256, 0, st>>>(ft, fv, M, r, layers);
+  }
   if ((e = hipGetLastError()) != hipSuccess) return e;
   const int C = (int)adapter_cols(r), cols = (dx16 ? 2 : 3) * b.r;
   if (M <= kMidTokens) {
