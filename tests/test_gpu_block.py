@@ -396,3 +396,45 @@ def test_full_size():
         within(grads[2 * l], s * (V.T @ (x * mask)), s * ((np.abs(d[l]) @ np.abs(b)).T @ (np.abs(x) * mask)), N + 3 * M, "dA")
         within(grads[2 * l + 1], s * (d[l].T @ Tl), s * (np.abs(d[l]).T @ np.abs(Tl)), K + 3 * M, "dB")
     within(dX[t.from_numpy(rows).cuda()], want_dX, lim_dX, 4 * N + 8 * r, "dX")
+
+
+@pytest.mark.parametrize("M,K", [(16, 4416), (16, 4480), (16, 4544), (11, 6528), (8, 2048), (8, 2112), (3, 5312)])
+@pytest.mark.parametrize("r", [8, 136])
+def test_few_tokens_about_the_room_for_them(M, K, r):
+    """X that just fits, or just does not, where the kernels of few tokens keep it."""
+    print(f"few tokens M={M} K={K} r={r}", flush=True)
+    check_gated(Case(M, 40, K, r, 2, 0.1, seed=31))
+
+
+def test_outputs_past_32_bits():
+    """fp32 outputs of more than 2^31 bytes, sampled rows against the oracle."""
+    import torch as t
+    print("outputs past 32 bits", flush=True)
+    M, wide, r, p, s = 70001, 8192, 8, 0.1, 2.0
+    dev = t.Generator("cuda").manual_seed(5)
+    rows = np.array([0, 1, 32767, 65535, 65536, 69887, 69888, 70000])
+    at = t.from_numpy(rows).cuda()
+
+    def bf(*shape, scale=1.0):
+        return (t.randn(*shape, generator=dev, device="cuda") * scale).to(t.bfloat16)
+
+    def f64(x):
+        return x.double().cpu().numpy()
+
+    # Y [M, 8192] from K = 64, then dX [M, 8192] of a layer with 64 rows
+    for N, K in ((wide, 64), (64, wide)):
+        w = G.gpu_quantize(t.randn(N, K, generator=dev, device="cuda") * 0.1)
+        W, A, B, drop = f64(G.gpu_dequantize(w)), bf(r, K, scale=0.1), bf(N, r, scale=0.1), q.Dropout(p, 3, 4)
+        X, size = bf(M, K), q.qlora_dropout_linear_sizes(N, K, M, r)
+        mask = ref.keep(M, K, p, 3, 4)[rows]
+        if N == wide:
+            Y = t.empty(M, N, device="cuda")
+            q.qlora_dropout_linear_fwd(w, X, A, B, r, s * r, drop, Y, None, q.workspace(size["fwd_ws_bytes"]))
+            want, lim = (ref.forward(f64(X[at]), W, f64(A), f64(B), s, mask, a)[0] for a in (False, True))
+            within(Y[at], want, lim, 2 * K + 4 * r, "Y")
+            del Y
+        else:
+            dY, dX, dA, dB = bf(M, N), t.empty(M, K, device="cuda"), t.empty(r, K, device="cuda"), t.empty(N, r, device="cuda")
+            q.qlora_dropout_linear_bwd(w, X, dY, A, B, r, s * r, drop, None, dX, dA, dB, q.workspace(size["bwd_ws_bytes"]))
+            want, lim = (ref.backward(f64(X[at]), f64(dY[at]), W, f64(A), f64(B), s, mask, None, a)[0] for a in (False, True))
+            within(dX[at], want, lim, 2 * N + 4 * r, "dX")
