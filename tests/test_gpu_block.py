@@ -47,7 +47,7 @@ class Case:
 
     def scratch(self, key):
         import torch as t
-        return t.full((max(256, self.sizes[key]),), 0xA5, dtype=t.uint8, device="cuda")
+        return t.full((max(256, self.sizes[key]),), 0xFF, dtype=t.uint8, device="cuda")
 
     def nan(self, *shape, dtype=None):
         import torch as t

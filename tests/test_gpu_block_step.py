@@ -167,7 +167,7 @@ def test_the_step_in_a_graph(M):
         for x in (s.H, s.G, s.U, s.Z, s.T1, s.T2, s.logp, s.lse, s.entropy, s.top, s.dH, s.dX, *s.grads):
             x.fill_(float("nan"))
         for w in s.ws:
-            w.fill_(0xA5)
+            w.fill_(0xFF)
         t.cuda.synchronize()
         graph.replay()
         t.cuda.synchronize()
