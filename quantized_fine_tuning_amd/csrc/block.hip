@@ -31,8 +31,7 @@ hipError_t launch_gemv_sums(const Nf4View& W, const uint16_t* X, int64_t M, cons
                             hipStream_t st);
 hipError_t launch_gated_gemv(const BlockView& b, const uint16_t* X, int64_t M, const uint16_t* S, const GatedOut& out,
                              hipStream_t st);
-int fwd_gemm_splits(int64_t M, int64_t N, int64_t K, size_t cap);
-int gated_fwd_splits(int64_t M, int64_t N, int64_t K);
+int block_fwd_splits(int64_t M, int64_t N, int64_t K, int layers);
 int block_dx_splits(int64_t M, int64_t N, int64_t K, int layers);
 
 namespace {
@@ -700,7 +699,7 @@ BlockFwdLayout block_fwd_layout(int64_t M, int64_t N, int64_t K, int r, int laye
   if (M <= kMidTokens) {
     L.splits = mid_fwd_plan(M, N, K).splits;
   } else {
-    L.splits = layers == 2 ? gated_fwd_splits(M, N, K) : fwd_gemm_splits(M, N, K, SIZE_MAX);
+    L.splits = block_fwd_splits(M, N, K, layers);
     L.slices = down_slices(M, K, r, layers);
   }
   L.off_P = round_up(layers * M * adapter_cols(r) * 2, 256);
@@ -736,9 +735,9 @@ BlockBwdLayout block_bwd_layout(int64_t M, int64_t N, int64_t K, int r, int laye
 }
 
 // The largest totals over M in [0, M_max].  Up to kMidTokens tokens each is taken.
-// Above, split counts are constant within a band of 256 tokens and slice counts
-// between multiples of 64, and what they count grows with M: the last of every 64
-// and the first of the next are taken.
+// Above, split and slice counts are constant between multiples of 64 tokens, and
+// what they count grows with M: the last of every 64 and the first of the next are
+// taken.
 namespace {
 template <typename F>
 size_t most_of(int64_t M_max, F&& total) {

@@ -897,10 +897,15 @@ hipError_t launch_dx_gemm_adapters(const Nf4View& W, const uint16_t* dY, int64_t
   return hipGetLastError();
 }
 
-// Of two layers the reduction runs over the rows of both.
+// Of two layers the reduction runs over the rows of both.  Short ones are split down
+// to four steps: the sum of the partials comes in the gradients' launch anyway (whole
+// passes, us with eight and with four: 382 tokens, 520 x 512, r = 88, 47.5 and 38.1; 121,
+// 648 x 2752, 51.4 and 40.0; 1000, 512 x 2048, 54.6 and 49.2; longer, 200, 2048 x 2048,
+// 43.7 and 44.8).
 int block_dx_splits(int64_t M, int64_t N, int64_t K, int layers) {
   const int64_t tiles = ((M + TM - 1) / TM) * ((K + TK - 1) / TK);
-  return gemm_splits(tiles, layers * ((N + NSTEP - 1) / NSTEP), M, K, SIZE_MAX);
+  const int64_t steps = layers * ((N + NSTEP - 1) / NSTEP);
+  return gemm_splits(tiles, steps, M, K, SIZE_MAX, steps < 24 ? 4 : 8);
 }
 
 hipError_t launch_dx_gemm_block(const Nf4View& W, const uint16_t* dY, int64_t M, const BlockGemmArgs& ma, bool pair,

@@ -766,9 +766,15 @@ hipError_t launch_fwd_gemm_adapters(const Nf4View& W, const uint16_t* X, int64_t
 
 // Tiles of the gated block's forward, whose N is that of one layer: half a tile's
 // weight rows are the gate's.
-int gated_fwd_splits(int64_t M, int64_t N, int64_t K) {
-  const int64_t tiles = ((M + TM - 1) / TM) * ((2 * N + TN - 1) / TN);
-  return gemm_splits(tiles, K / KSTEP, M, 2 * N, SIZE_MAX);
+// Short reductions are split down to four steps where the sum of the partials, a
+// launch of its own, is small (us with eight and with four, one layer and two: 153
+// tokens, 2536 x 768, r = 112, 38.7 and 30.3, 41.6 and 34.4; 300, 1024 x 1024, 31.9 and
+// 27.9, 33.8 and 30.8; larger, 1000, 2048 x 512, 29.1 and 35.8, 31.2 and 39.5; longer,
+// 200, 2048 x 2048, 32.5 and 33.0).
+int block_fwd_splits(int64_t M, int64_t N, int64_t K, int layers) {
+  const int64_t tiles = ((M + TM - 1) / TM) * ((layers * N + TN - 1) / TN), steps = K / KSTEP;
+  const bool small = round_up(M, 64) * layers * N <= (int64_t)1 << 20;
+  return gemm_splits(tiles, steps, M, layers * N, SIZE_MAX, small && steps < 24 ? 4 : 8);
 }
 
 hipError_t launch_fwd_gemm_block(const Nf4View& W, const uint16_t* X, int64_t M, const BlockGemmArgs& ma, bool pair,

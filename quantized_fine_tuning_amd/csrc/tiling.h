@@ -33,13 +33,13 @@ inline unsigned tile_grid(int tiles_m, int tiles_n, int splits = 1) {
 
 // Number of reduction splits for a GEMM of `tiles` output tiles and `steps`
 // reduction steps: 1 while the tiles fill at least 3/4 of the compute units,
-// else as many as fit one round of workgroups, with at least 8 steps each,
+// else as many as fit one round of workgroups, with at least `least` steps each,
 // fewer while the fp32 partials (splits x rows x cols x 4 bytes) exceed
 // `cap` bytes.
-inline int gemm_splits(int64_t tiles, int64_t steps, int64_t rows, int64_t cols, size_t cap) {
+inline int gemm_splits(int64_t tiles, int64_t steps, int64_t rows, int64_t cols, size_t cap, int least = 8) {
   if (tiles <= 0 || 4 * tiles >= 3 * kGemmCus) return 1;
   int64_t s = kGemmCus / tiles;
-  s = s < steps / 8 ? s : steps / 8;
+  s = s < steps / least ? s : steps / least;
   while (s > 1 && (size_t)s * (size_t)rows * (size_t)cols * 4u > cap) --s;
   return s > 1 ? (int)s : 1;
 }
