@@ -697,7 +697,7 @@ BlockFwdLayout block_fwd_layout(int64_t M, int64_t N, int64_t K, int r, int laye
     return L;
   }
   if (M <= kMidTokens) {
-    L.splits = mid_fwd_plan(M, N, K).splits;
+    L.splits = mid_fwd_plan(M, N, K, layers).splits;
   } else {
     L.splits = block_fwd_splits(M, N, K, layers);
     L.slices = down_slices(M, K, r, layers);
@@ -713,7 +713,7 @@ BlockFwdLayout block_fwd_layout(int64_t M, int64_t N, int64_t K, int r, int laye
 BlockBwdLayout block_bwd_layout(int64_t M, int64_t N, int64_t K, int r, int layers) {
   BlockBwdLayout L{};
   if (M == 0) return L;
-  L.splits = M <= kMidTokens ? layers * mid_dx_splits(M, N, K) : block_dx_splits(M, N, K, layers);
+  L.splits = M <= kMidTokens ? layers * mid_dx_splits(M, N, K, layers) : block_dx_splits(M, N, K, layers);
   L.slices_T = down_slices(M, K, r, layers);
   L.slices_V = down_slices(M, N, r, layers);
   L.unit = gradient_unit(M, N, K, r, layers);
@@ -787,12 +787,11 @@ hipError_t launch_block_fwd(const BlockView& b, const uint16_t* X, int64_t M, vo
     block_few_down_kernel<<<dim3((unsigned)M, (unsigned)(b.r / kFewRanks), (unsigned)b.layers), 256, 0, st>>>(
         X, M, K, b.A[0], b.A[1], b.r, b.drop, b.scale, T, none, S);
     hipError_t e = hipGetLastError();
-    const MidPlan plan = mid_fwd_plan(M, N, K);
-    for (int l = 0; l < b.layers && e == hipSuccess; ++l) {
-      float* const Pl = P + (int64_t)l * L.splits * M * N;
-      e = launch_mid_fwd_block(b.W[l], X, M, DenseGemmArgs{S + l * M * C, b.B[l], b.r, C, 1, cols, (int)M, b.drop},
-                               pair ? (void*)Pl : Y, !pair && y16, plan, Pl, st);
-    }
+    if (e != hipSuccess) return e;
+    const DenseGemmArgs ma{S, b.B[0], b.r, C, 1, cols, (int)M, b.drop, b.W[pair ? 1 : 0], X, b.B[pair ? 1 : 0],
+                           M * C, (int64_t)L.splits * M * N};
+    e = launch_mid_fwd_block(b.W[0], X, M, ma, pair ? (void*)P : Y, !pair && y16, mid_fwd_plan(M, N, K, b.layers), P,
+                             b.layers, st);
     if (e != hipSuccess) return e;
     if (pair) return reduce(false);
     return L.splits > 1 ? launch_splitk_reduce(P, L.splits, M * N, Y, y16, false, st) : hipSuccess;
@@ -856,11 +855,10 @@ hipError_t launch_block_bwd(const BlockView& b, const uint16_t* X, int64_t M, co
   if (M <= kMidTokens) {
     // (each layer's splits into their own partials, added together)
     const int splits = L.splits / layers;
-    for (int l = 0; l < layers && e == hipSuccess; ++l) {
-      float* const Pl = P + (int64_t)l * splits * M * K;
-      e = launch_mid_dx_block(b.W[l], d[l], M, DenseGemmArgs{SV + l * M * C, b.A[l], b.r, C, 1, cols, (int)M, b.drop},
-                              L.splits > 1 ? (void*)Pl : dX, L.splits == 1 && dx16, splits, Pl, st);
-    }
+    const DenseGemmArgs ma{SV, b.A[0], b.r, C, 1, cols, (int)M, b.drop, b.W[pair ? 1 : 0], d[1], b.A[pair ? 1 : 0],
+                           M * C, (int64_t)splits * M * K};
+    e = launch_mid_dx_block(b.W[0], d[0], M, ma, L.splits > 1 ? (void*)P : dX, L.splits == 1 && dx16, splits, P, layers,
+                            st);
   } else {
     const BlockGemmArgs ma{SV, {b.A[0], b.A[1]}, b.r, C, cols, b.W[pair ? 1 : 0], nullptr, nullptr, in.act, d[1], b.drop};
     e = launch_dx_gemm_block(b.W[0], d[0], M, ma, pair, dX, dx16, L.splits, P, st);

@@ -249,6 +249,7 @@ hipError_t launch_adapters_plan(const int32_t* index, int64_t M, int count, cons
 // tokens of 40 adapters, 8192 x 8192, r = 64, 368 against 357; 512 tokens of as
 // many adapters, 4096 x 4096, r = 64, 394 against 317.)
 struct AdapterGemmArgs {
+  static constexpr bool kPair = false;
   // (the plan as one address and two strides: the kernels are short of scalar
   // registers)
   const int32_t* plan;
@@ -309,6 +310,12 @@ struct DenseGemmArgs {
   int r, C, count, cols;  // count: 1
   int M;
   DropView drop;
+  // the other layer of a gated block, in the same launch: its weight, tokens and
+  // factors, and how far behind S and the fp32 output or partials its own lie
+  static constexpr bool kPair = true;
+  Nf4View W1;
+  const uint16_t *L1, *F1;
+  int64_t next_S, next_P;
   __device__ __forceinline__ int held() const { return M; }
   __device__ __forceinline__ int token(int p) const { return p; }
   __device__ __forceinline__ int4 tokens4(int p) const { return int4{p, p + 1, p + 2, p + 3}; }
@@ -373,16 +380,16 @@ struct MidPlan {
   int splits, waves;
   double us;  // estimated
 };
-MidPlan mid_fwd_plan(int64_t M, int64_t N, int64_t K);
+MidPlan mid_fwd_plan(int64_t M, int64_t N, int64_t K, int layers = 1);
 hipError_t launch_mid_fwd(const Nf4View& W, const uint16_t* X, int64_t M, const AdapterGemmArgs& ma, void* Y, bool y16,
                           const MidPlan& plan, float* P, hipStream_t st);
-int mid_dx_splits(int64_t M, int64_t N, int64_t K);
+int mid_dx_splits(int64_t M, int64_t N, int64_t K, int layers = 1);
 hipError_t launch_mid_dx(const Nf4View& W, const uint16_t* dY, int64_t M, const AdapterGemmArgs& ma, void* dX, bool dx16,
                          int splits, float* P, hipStream_t st);
 hipError_t launch_mid_fwd_block(const Nf4View& W, const uint16_t* X, int64_t M, const DenseGemmArgs& ma, void* Y, bool y16,
-                                const MidPlan& plan, float* P, hipStream_t st);
+                                const MidPlan& plan, float* P, int layers, hipStream_t st);
 hipError_t launch_mid_dx_block(const Nf4View& W, const uint16_t* dY, int64_t M, const DenseGemmArgs& ma, void* dX,
-                               bool dx16, int splits, float* P, hipStream_t st);
+                               bool dx16, int splits, float* P, int layers, hipStream_t st);
 
 struct AdaptersFwdLayout {
   // M <= 16: fp32 T in tiles; else bf16 S [M, C] of s·T; an fp32 area: the

@@ -22,6 +22,18 @@
 namespace qnf4 {
 namespace {
 
+// blockIdx.z = 1: the second layer of a pair, which has fp32 outputs.
+__device__ __forceinline__ void other_layer(Nf4View& W, const uint16_t* __restrict__& L, void* __restrict__& out,
+                                            float* __restrict__& P, DenseGemmArgs& ma) {
+  if (blockIdx.z == 0) return;
+  W = ma.W1;
+  L = ma.L1;
+  ma.F = ma.F1;
+  ma.S += ma.next_S;
+  out = static_cast<float*>(out) + ma.next_P;
+  P += ma.next_P;
+}
+
 // Output rows of an accumulator tile back to their tokens: lane holds rows
 // 4kq + v of each 16-position tile, one column; the tokens of its rows are
 // loaded at the kernel's start.
@@ -106,6 +118,7 @@ __global__ __launch_bounds__(64 * WV) void mid_fwd_kernel(Nf4View W, const uint1
                                                               void* __restrict__ Y, int y_bf16, int tiles_n, int splits,
                                                               float* __restrict__ P, Codebook cb, Args ma) {
   constexpr int TM = 16 * NT, ROW = 512, XB = TM * ROW, WB = 2560;  // bytes: X of a stage, one wave's codes and constants
+  if constexpr (Args::kPair) other_layer(W, X, Y, P, ma);
   constexpr int D = WV == 16 ? 2 : NT == 2 ? 4 : 3, XI = 8 * NT / WV;                                // ring depth
   __shared__ __attribute__((aligned(1024))) char sx[D][XB];
   __shared__ __attribute__((aligned(1024))) char sc[D][WV * WB];
@@ -314,6 +327,7 @@ template <int NT, typename Args>
 __global__ __launch_bounds__(kDxThreads) void mid_dx_kernel(Nf4View W, const uint16_t* __restrict__ dY, int64_t M,
                                                             void* __restrict__ dX, int dx_bf16, int tiles_k, int splits,
                                                             float* __restrict__ P, Codebook cb, Args ma) {
+  if constexpr (Args::kPair) other_layer(W, dY, dX, P, ma);
   constexpr int TM = 16 * NT, D = 3, YI = NT / 2;  // dY copies per wave and stage (8 rows each)
   __shared__ __attribute__((aligned(1024))) char sy[D][TM * 128];
   __shared__ __attribute__((aligned(1024))) char sc[D][4 * 1536];  // per wave: codes 1 KB, e4m3 dwords, scales
@@ -553,26 +567,26 @@ MidPlan mid_splits(int64_t tiles, int64_t stages, int64_t elements, int64_t slot
 // One workgroup per compute unit (its LDS), 2.3 us a stage with 8 waves and 2.9
 // with 16: 64 tokens, 4096 x 4096, 24 us in all with 8 and 27 with 16; 11008 x
 // 4096, 41 and 36.
-MidPlan mid_fwd_plan(int64_t M, int64_t N, int64_t K) {
-  const int64_t tm = 16 * mid_tiles(M), mt = (M + tm - 1) / tm, stages = (K + 255) / 256;
-  const MidPlan narrow = mid_splits(mt * ((N + 127) / 128), stages, M * N, 256, 2.3, 7.7);
-  MidPlan wide = mid_splits(mt * ((N + 255) / 256), stages, M * N, 256, 2.9, 7.5);
+MidPlan mid_fwd_plan(int64_t M, int64_t N, int64_t K, int layers) {
+  const int64_t tm = 16 * mid_tiles(M), mt = layers * ((M + tm - 1) / tm), stages = (K + 255) / 256;
+  const MidPlan narrow = mid_splits(mt * ((N + 127) / 128), stages, layers * M * N, 256, 2.3, 7.7);
+  MidPlan wide = mid_splits(mt * ((N + 255) / 256), stages, layers * M * N, 256, 2.9, 7.5);
   wide.waves = 16;
   return wide.us < narrow.us ? wide : narrow;
 }
 // Two workgroups per compute unit.
-int mid_dx_splits(int64_t M, int64_t N, int64_t K) {
-  const int64_t tm = 16 * mid_tiles(M);
-  return mid_splits(((M + tm - 1) / tm) * ((K + 127) / 128), (N + 63) / 64, M * K, 512, 1.0, 6.0).splits;
+int mid_dx_splits(int64_t M, int64_t N, int64_t K, int layers) {
+  const int64_t tm = 16 * mid_tiles(M), tiles = layers * ((M + tm - 1) / tm) * ((K + 127) / 128);
+  return mid_splits(tiles, (N + 63) / 64, layers * M * K, 512, 1.0, 6.0).splits;
 }
 
 namespace {
 
 template <typename Args>
 hipError_t launch_fwd(const Nf4View& W, const uint16_t* X, int64_t M, const Args& ma, void* Y, bool y16,
-                      const MidPlan& plan, float* P, hipStream_t st) {
+                      const MidPlan& plan, float* P, int layers, hipStream_t st) {
   const int nt = mid_tiles(M), tm = 16 * nt, rows = 16 * plan.waves, tiles_n = (int)((W.N + rows - 1) / rows);
-  const dim3 grid((unsigned)(tiles_n * ((M + tm - 1) / tm)), (unsigned)plan.splits);
+  const dim3 grid((unsigned)(tiles_n * ((M + tm - 1) / tm)), (unsigned)plan.splits, (unsigned)layers);
 #define QNF4_MID(NT, WV)                                                                                              \
   mid_fwd_kernel<NT, WV, Args><<<grid, 64 * WV, 0, st>>>(W, X, M, Y, y16 ? 1 : 0, tiles_n, plan.splits, P, codebook(), \
                                                          ma)
@@ -593,9 +607,9 @@ hipError_t launch_fwd(const Nf4View& W, const uint16_t* X, int64_t M, const Args
 
 template <typename Args>
 hipError_t launch_dx(const Nf4View& W, const uint16_t* dY, int64_t M, const Args& ma, void* dX, bool dx16, int splits,
-                     float* P, hipStream_t st) {
+                     float* P, int layers, hipStream_t st) {
   const int nt = mid_tiles(M), tm = 16 * nt, tiles_k = (int)((W.K + 127) / 128);
-  const dim3 grid((unsigned)(tiles_k * ((M + tm - 1) / tm)), (unsigned)splits);
+  const dim3 grid((unsigned)(tiles_k * ((M + tm - 1) / tm)), (unsigned)splits, (unsigned)layers);
 #define QNF4_MID(NT)                                                                                              \
   mid_dx_kernel<NT, Args><<<grid, kDxThreads, 0, st>>>(W, dY, M, dX, dx16 ? 1 : 0, tiles_k, splits, P, codebook(), ma)
   if (nt == 2)
@@ -610,19 +624,19 @@ hipError_t launch_dx(const Nf4View& W, const uint16_t* dY, int64_t M, const Args
 
 hipError_t launch_mid_fwd(const Nf4View& W, const uint16_t* X, int64_t M, const AdapterGemmArgs& ma, void* Y, bool y16,
                           const MidPlan& plan, float* P, hipStream_t st) {
-  return launch_fwd(W, X, M, ma, Y, y16, plan, P, st);
+  return launch_fwd(W, X, M, ma, Y, y16, plan, P, 1, st);
 }
 hipError_t launch_mid_fwd_block(const Nf4View& W, const uint16_t* X, int64_t M, const DenseGemmArgs& ma, void* Y, bool y16,
-                                const MidPlan& plan, float* P, hipStream_t st) {
-  return launch_fwd(W, X, M, ma, Y, y16, plan, P, st);
+                                const MidPlan& plan, float* P, int layers, hipStream_t st) {
+  return launch_fwd(W, X, M, ma, Y, y16, plan, P, layers, st);
 }
 hipError_t launch_mid_dx(const Nf4View& W, const uint16_t* dY, int64_t M, const AdapterGemmArgs& ma, void* dX, bool dx16,
                          int splits, float* P, hipStream_t st) {
-  return launch_dx(W, dY, M, ma, dX, dx16, splits, P, st);
+  return launch_dx(W, dY, M, ma, dX, dx16, splits, P, 1, st);
 }
 hipError_t launch_mid_dx_block(const Nf4View& W, const uint16_t* dY, int64_t M, const DenseGemmArgs& ma, void* dX,
-                               bool dx16, int splits, float* P, hipStream_t st) {
-  return launch_dx(W, dY, M, ma, dX, dx16, splits, P, st);
+                               bool dx16, int splits, float* P, int layers, hipStream_t st) {
+  return launch_dx(W, dY, M, ma, dX, dx16, splits, P, layers, st);
 }
 
 }  // namespace qnf4
