@@ -372,6 +372,9 @@ __device__ __forceinline__ void gradient_unit(const GradientJob& J, int layer, i
                                               char* ss) {
   constexpr int SI = NJ == 4 ? 3 : NJ == 2 ? 2 : 1;  // S copies per wave and stage
   constexpr int LB = 32 * 256, SB = 4 * SI * 1024, SROW = 96 * NJ;
+  // a wave's column and rank blocks: 32 columns of all ranks, of 64 ranks 64 of half of
+  // them (20 reads of LDS a stage in place of 28)
+  constexpr int PF = NJ == 4 ? 4 : 2, WC = 8 / PF, JF = NJ * WC / 4;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lr = lane & 15, kq = lane >> 4, C = (int)adapter_cols(r);
   const int stages = (int)((p1 - p0 + 31) / 32);
@@ -398,11 +401,12 @@ __device__ __forceinline__ void gradient_unit(const GradientJob& J, int layer, i
                 row < 32 && m < p1 && j < r ? (uint32_t)((m * C + part * r + j) * 2) : 0x7fffffffu, 0u);
     }
   };
-  f32x4_t acc[2][NJ];
+  const int wc = 16 * PF * (wave % WC), wj = JF * (wave / WC);
+  f32x4_t acc[PF][JF];
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < PF; ++i)
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < JF; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int i = 0; i + 1 < kGradRing; ++i) issue(i, i);
   // the generator's bits for a stage are found beside the products of the one before
@@ -435,18 +439,18 @@ __device__ __forceinline__ void gradient_unit(const GradientJob& J, int layer, i
     const char* const lt = sl + (s % kGradRing) * LB;
     const char* const st = ss + (s % kGradRing) * SB;
     const int trow = 8 * kq + (lr >> 2), tcol = 4 * (lr & 3);  // this lane's part of a transposing read
-    u32x4_t a[2];
+    u32x4_t a[PF];
 #pragma unroll
-    for (int pf = 0; pf < 2; ++pf) {
-      const u32x2_t h0 = lds_read_tr(lt + gswz(trow, 32 * wave + 16 * pf + tcol));
-      const u32x2_t h1 = lds_read_tr(lt + gswz(trow + 4, 32 * wave + 16 * pf + tcol));
+    for (int pf = 0; pf < PF; ++pf) {
+      const u32x2_t h0 = lds_read_tr(lt + gswz(trow, wc + 16 * pf + tcol));
+      const u32x2_t h1 = lds_read_tr(lt + gswz(trow + 4, wc + 16 * pf + tcol));
       a[pf] = u32x4_t{h0[0], h0[1], h1[0], h1[1]};
     }
 #pragma unroll
     for (int part = 0; part < 3; ++part)
 #pragma unroll
-      for (int jf = 0; jf < NJ; ++jf) {
-        const int col = 16 * (NJ * part + jf) + tcol;
+      for (int jf = 0; jf < JF; ++jf) {
+        const int col = 16 * (NJ * part + wj + jf) + tcol;
         u32x2_t h[2];
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
@@ -455,19 +459,19 @@ __device__ __forceinline__ void gradient_unit(const GradientJob& J, int layer, i
         }
         const u32x4_t f = {h[0][0], h[0][1], h[1][0], h[1][1]};
 #pragma unroll
-        for (int pf = 0; pf < 2; ++pf)
+        for (int pf = 0; pf < PF; ++pf)
           acc[pf][jf] = ALONG ? mfma_16x16x32(a[pf], f, acc[pf][jf]) : mfma_16x16x32(f, a[pf], acc[pf][jf]);
       }
   }
   wait_vmem();  // no copy may land in LDS after the workgroup ends
 #pragma unroll
-  for (int pf = 0; pf < 2; ++pf)
+  for (int pf = 0; pf < PF; ++pf)
 #pragma unroll
-    for (int jf = 0; jf < NJ; ++jf)
+    for (int jf = 0; jf < JF; ++jf)
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
-        const int64_t cb = c0 + 32 * wave + 16 * pf;
-        const int jbase = j0 + 16 * jf;
+        const int64_t cb = c0 + wc + 16 * pf;
+        const int jbase = j0 + 16 * (wj + jf);
         const int64_t c = ALONG ? cb + 4 * kq + v : cb + lr;
         const int j = ALONG ? jbase + lr : jbase + 4 * kq + v;
         if (c < J.cols && j < r) out[ALONG ? c * r + j : j * J.cols + c] = acc[pf][jf][v];
