@@ -351,8 +351,8 @@ __global__ __launch_bounds__(256) void block_factor_kernel(FactorJob t, FactorJo
 // their own layouts (X with its dropped elements cleared by the wave that copied
 // them); the MFMA operands, 8 consecutive tokens of one column, are transposing
 // reads.  One unit writes the gradient itself, several partial sums that are added
-// in unit order.  (4096 tokens, r = 64: one layer of 4096 x 11008 59 us, both of a pair
-// of 11008 x 4096 90, 246 MB of X, dG and dU at 2.7 TB/s; LDS reads of three parts of S
+// in unit order.  (4096 tokens, r = 64: one layer of 4096 x 11008 57 us, both of a pair
+// of 11008 x 4096 88, 246 MB of X, dG and dU at 2.8 TB/s; LDS reads of three parts of S
 // for each column block, the generator for X of either layer, 10 us of it, and memory
 // share the time.  256 columns a workgroup gained nothing.)
 // ---------------------------------------------------------------------------
