@@ -608,13 +608,16 @@ __device__ __forceinline__ bool gate_gradient(int act, float g, float u, float d
   const float y = dh * s, t = g * r * slope, yu = y * u;
   d = {yu * (1.f + t), y * g};
   const float unit = __builtin_fmaf(per_h, fabsf(h), 10.f * 0x1p-24f);
-  // (2^-140: what underflows)
+  // (2^-140: what underflows behind y, 2^-150 times 1 + |t|, below 200 where h is above −80)
   const float off_u = __builtin_fmaf(unit, fabsf(d.du), 0x1p-140f);
   const float off_g = __builtin_fmaf((unit + more) * (1.f + fabsf(t)), fabsf(yu), 0x1p-140f);
   const uint32_t differ = pack_bf16x2(d.du - off_u, d.dg - off_g) ^ pack_bf16x2(d.du + off_u, d.dg + off_g);
+  // (what dh·σ loses below fp32's normal numbers, U and G may bring back up; σ itself is
+  // one above h = −80, and a dH of 0 loses nothing)
+  const bool whole = fabsf(y) >= 0x1p-126f || dh == 0.f;
   // (zeros of either sign are alike; below −80 the exponential nears fp32's end and
   // loses bits; NaN may be an infinity times what is 0 in fp32 alone)
-  return h > -80.f && (differ & 0x7fff7fffu) == 0u && !__builtin_isunordered(d.du, d.dg);
+  return whole && h > -80.f && (differ & 0x7fff7fffu) == 0u && !__builtin_isunordered(d.du, d.dg);
 }
 __global__ __launch_bounds__(256) void gate_gradient_kernel(const uint16_t* __restrict__ dH, const uint16_t* __restrict__ G,
                                                             const uint16_t* __restrict__ U, int64_t n8, int act,
