@@ -9,11 +9,22 @@ namespace qnf4 {
 
 constexpr double kGeluSlope = 1.5957691216057307, kGeluCube = 0.044715;  // 2·sqrt(2/π)
 
-// act(g) within a few ulps of fp32: h, an exponential and a reciprocal of 1 ulp each.
+// act(g), off by its exponent's rounding: with u = 2^-24, (6 + 2|h|)u of itself for SiLU,
+// (6 + 7|h|)u for GELU (h is off by 5u of itself); below 2^-126 a step of fp32.  FAR:
+// whether g may be below far_gate(act).  There exp(−h) passes 2^95 and more, the
+// reciprocal of 1 + exp(−h) is exp(h) in fp32, and exp(h) is taken 2^64 times as large:
+// the reciprocal instruction gives 0 for results below 2^-126, from h = −87 on, where g
+// times them is still a normal number.
+template <bool FAR = true>
 __device__ __forceinline__ float gate_act(int act, float g) {
   float h = g;
   if (act == kActGeluTanh) h = (float)kGeluSlope * __builtin_fmaf((float)kGeluCube * g * g, g, g);
-  return g * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(h * -1.44269502f));
+  const float x = h * -1.44269502f;
+  if constexpr (FAR)
+    if (x > 100.f) return g * __builtin_amdgcn_exp2f(64.f - x) * 0x1p-64f;
+  return g * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(x));
 }
+// (h = −69 and −66, x = 99.5 and 95.8)
+__device__ __forceinline__ float far_gate(int act) { return act == kActGeluTanh ? -9.f : -69.f; }
 
 }  // namespace qnf4
