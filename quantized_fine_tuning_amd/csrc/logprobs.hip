@@ -11,10 +11,20 @@
 // gradient 0, lse −infinity); NaN passes through maxima unseen and shows in the
 // sums.  A logit below −1e30 is no alternative among the most likely.
 //
-// Everything in fp32, exponents in base 2 with c = log2(e)/tau: x = fma(z, c, −rc)
-// with rc = fl(max·c), S = Σ 2^x, W = Σ x·2^x; then
-//   logp = x_t·ln 2 − ln S,  H = ln S − ln 2·W/S,
-// none of which sees what rc was rounded by (it shifts every x and log2 S alike).
+// Everything in fp32, exponents in base 2 with c = log2(e)/tau: x = (z − max)·c, S =
+// Σ 2^x, W = Σ x·2^x; then
+//   logp = x_t·ln 2 − ln S,  H = ln S − ln 2·W/S.
+// The difference comes first, so that x is 0 at the maximum wherever the row lies.
+// A row in registers takes x = fma(z, c, −rc) with rc = fl(max·c), one operation in place
+// of two (values and entropy of 4096 x 32000 bf16 40.0 us against 41.0): every x and log2 S
+// are off alike by what rc was rounded by, and no result sees it, 2^-6 at most below
+// |rc| = 2^19 (`far` is what lies beyond, a mask of −1e10, say).  In far rows of 16-bit
+// logits none but the maximum has a share that fp32 holds: the next lies 2^-11 of |max|
+// or more below, 256 and more times 1/c.  There c becomes the power of two that puts
+// |rc| into [2^19, 2^20), so that rc is exact, x 0 at the maximum and −256 or less
+// elsewhere.  Far rows of 32 bits take the maximum off their registers first.  Of far
+// rows log q is found from the difference.  Rows too long for registers have the
+// difference throughout.
 //
 // Forward, with or without the gradient: one workgroup per token, the row in
 // registers between its passes (or, too long for that, read again from the
@@ -42,6 +52,11 @@ namespace qnf4 {
 namespace {
 
 constexpr float kLn2 = 0.693147182f;
+
+// A value that is the same in every lane, in a scalar register.
+__device__ __forceinline__ float uniform(float v) {
+  return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(v)));
+}
 
 // An order of floats as unsigned numbers (−0 and +0 equal; NaN lowest).
 __device__ __forceinline__ uint32_t order_of(float v) {
@@ -224,8 +239,14 @@ __global__ __launch_bounds__(T, T == 1024 && (ZT != kF32 || VECS == 0) && !TOP ?
     for (int k = 0; k < C::N; k += 2) high = max3(high, C::get(v, k), C::get(v, k + 1));
     return high;
   };
-  float rc = 0.f, sum = 0.f, dot = 0.f;
-  auto x = [&](float v) __attribute__((always_inline)) { return __builtin_fmaf(v, c, -rc); };
+  // (ref: the maximum, 0 while every column is masked; cr, rc, far: as above)
+  float ref = 0.f, cr = c, rc = 0.f, sum = 0.f, dot = 0.f;
+  bool far = VECS == 0;
+  // the exponent of a logit, and of one of the registers'
+  auto x_of = [&](float v) __attribute__((always_inline)) {
+    return VECS == 0 || (ZT == kF32 && far) ? (v - ref) * c : __builtin_fmaf(v, cr, -rc);
+  };
+  auto x = [&](float v) __attribute__((always_inline)) { return VECS == 0 ? (v - ref) * c : __builtin_fmaf(v, cr, -rc); };
   // (a masked column's x is −infinity, which times its 2^x of 0 would be NaN)
   auto chunk_sum = [&](const u32x4_t& v) __attribute__((always_inline)) {
     if constexpr (DOT) {
@@ -240,10 +261,12 @@ __global__ __launch_bounds__(T, T == 1024 && (ZT != kF32 || VECS == 0) && !TOP ?
       for (int k = 0; k < C::N; ++k) sum += __builtin_amdgcn_exp2f(x(C::get(v, k)));
     }
   };
-  // the sums of exponents over `before` as sums over rc
-  auto rescale = [&](bool some, float before) __attribute__((always_inline)) {
-    const float f = some ? __builtin_amdgcn_exp2f(before - rc) : 0.f;
-    if constexpr (DOT) dot = some ? f * __builtin_fmaf(before - rc, sum, dot) : 0.f;
+  // the sums over ref as sums over v
+  auto rescale = [&](bool some, float v) __attribute__((always_inline)) {
+    const float before = ref;
+    ref = v > kMasked ? v : 0.f;
+    const float down = fmaxf((before - ref) * c, kMasked), f = some ? __builtin_amdgcn_exp2f(down) : 0.f;
+    if constexpr (DOT) dot = some ? f * __builtin_fmaf(down, sum, dot) : 0.f;
     sum *= f;
   };
   float z_max = -INFINITY;
@@ -265,16 +288,14 @@ __global__ __launch_bounds__(T, T == 1024 && (ZT != kF32 || VECS == 0) && !TOP ?
         high = chunk_max(z[j], high);
       }
       if (high > z_max) {
-        const float before = rc;
-        rc = high > kMasked ? __fmul_rn(high, c) : 0.f;
-        rescale(z_max > kMasked, before);
+        rescale(z_max > kMasked, high);
         z_max = high;
       }
 #pragma unroll
       for (int j = 0; j < NV; ++j) chunk_sum(opaque(z[j]));
     }
   }
-  const float own_max = z_max, own_rc = rc;
+  const float own_max = z_max;
   z_max = wave_max(z_max);
   if (lane == 0) s_max[wave] = z_max;
   __syncthreads();
@@ -282,12 +303,25 @@ __global__ __launch_bounds__(T, T == 1024 && (ZT != kF32 || VECS == 0) && !TOP ?
 #pragma unroll
   for (int w = 1; w < kWaves; ++w) z_max = fmaxf(z_max, s_max[w]);
   const bool masked = !(z_max > kMasked);
-  rc = masked ? 0.f : __fmul_rn(z_max, c);
   if constexpr (VECS > 0) {
+    ref = uniform(masked ? 0.f : z_max);
+    rc = __fmul_rn(ref, c);
+    far = fabsf(rc) >= 0x1p19f;
+    if constexpr (ZT != kF32) {
+      // (2^(19 − ref's exponent))
+      cr = uniform(far ? __uint_as_float((273u - (__float_as_uint(ref) >> 23 & 255u)) << 23) : c);
+      rc = __fmul_rn(ref, cr);
+    } else if (far) {
+      rc = 0.f;
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) z[j][k] = __float_as_uint(__uint_as_float(z[j][k]) - ref);
+    }
 #pragma unroll
     for (int j = 0; j < NV; ++j) chunk_sum(z[j] = opaque(z[j]));
   } else {
-    rescale(own_max > kMasked, own_rc);  // (a NaN among masked columns stays in the sum)
+    rescale(own_max > kMasked, z_max);  // (a NaN among masked columns stays in the sum)
   }
   sum = wave_sum(sum);
   if constexpr (DOT) dot = wave_sum(dot);
@@ -308,10 +342,12 @@ __global__ __launch_bounds__(T, T == 1024 && (ZT != kF32 || VECS == 0) && !TOP ?
   const bool columns = !masked || sum != 0.f;
   const float log_sum = logf(sum), inv = 1.0f / sum;
   const float entropy = columns ? log_sum - kLn2 * (dot * inv) : 0.f;
-  auto log_q = [&](float v) __attribute__((always_inline)) { return __builtin_fmaf(x(v), kLn2, -log_sum); };
+  auto log_q = [&](float v) __attribute__((always_inline)) {
+    return far ? (v - ref) * (c * kLn2) - log_sum : __builtin_fmaf(x_of(v), kLn2, -log_sum);
+  };
   if (tid == 0) {
     if (a.logp) a.logp[m] = has && columns ? log_q(zt) : 0.f;
-    if (a.lse) a.lse[m] = columns ? z_max / a.tau + (log_sum - kLn2 * x(z_max)) : -INFINITY;
+    if (a.lse) a.lse[m] = columns ? z_max / a.tau + (log_sum - kLn2 * x_of(z_max)) : -INFINITY;
     if (a.entropy) a.entropy[m] = entropy;
   }
   auto again = [&](auto&& f) __attribute__((always_inline)) {
@@ -328,7 +364,8 @@ __global__ __launch_bounds__(T, T == 1024 && (ZT != kF32 || VECS == 0) && !TOP ?
 #pragma unroll
       for (int k = 0; k < C::N; ++k) f(C::get(v, k), i * C::N + k - R.head);
     };
-    if constexpr (VECS > 0) {
+    // (registers that no longer hold the logits themselves: from memory)
+    if (VECS > 0 && !(ZT == kF32 && far)) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) chunk(tid + j * T, z[j] = opaque(z[j]));
     } else {
@@ -373,7 +410,8 @@ __global__ __launch_bounds__(T, T == 1024 && (ZT != kF32 || VECS == 0) && !TOP ?
   if (!a.dZ) return;
   const float g = (has && a.d_logp ? a.d_logp[m] : 0.f) / a.tau, h = (a.d_entropy ? a.d_entropy[m] : 0.f) / a.tau;
   const bool live = columns && (g != 0.f || h != 0.f);
-  const float gi = -g * inv, hi = -h * inv;
+  const float gi = -g * inv, hi = -h * inv, qt = uniform(__builtin_amdgcn_exp2f(x_of(zt)) * inv);
+  const float log_qt = DOT ? uniform(log_q(zt)) : 0.f;
   auto grad = [&](float v) __attribute__((always_inline)) {
     if (!live) return 0.f;
     const float xv = x(v), e = __builtin_amdgcn_exp2f(xv);
@@ -385,9 +423,8 @@ __global__ __launch_bounds__(T, T == 1024 && (ZT != kF32 || VECS == 0) && !TOP ?
   auto store = [&](int i, const u32x4_t& v) __attribute__((always_inline)) {
     R.store(a.dZ, i, v, grad);
     if (live && has && g != 0.f && (target + R.head) / C::N == i) {
-      const float q = __builtin_amdgcn_exp2f(x(zt)) * inv;
-      const float e = DOT && q > 0.f ? h * q * (log_q(zt) + entropy) : 0.f;
-      store_rounded<ZT>(a.dZ, R.row + target, g * (1.f - q) - e);
+      const float e = DOT && qt > 0.f ? h * qt * (log_qt + entropy) : 0.f;
+      store_rounded<ZT>(a.dZ, R.row + target, g * (1.f - qt) - e);
     }
   };
   if constexpr (VECS > 0) {
