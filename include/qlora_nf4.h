@@ -491,7 +491,8 @@ qlora_status qlora_distill_bwd(const void* Z, qlora_dtype z_dtype, int64_t M, in
  * entropy and gradient 0, lse -infinity.  A token whose g and h are 0 has a zero
  * gradient whatever its logits are.  A NaN or +infinity among a row's logits makes
  * its lse, entropy, gradient and (of a given token) logp NaN; a NaN is never among
- * the top. */
+ * the top.  Logits may be of any size: all but lse come from differences (lse is
+ * infinite where the largest logit over tau passes fp32). */
 #define QLORA_LOGPROBS_MAX_TOP 256
 qlora_status qlora_logprobs_fwd(const void* Z, qlora_dtype z_dtype, int64_t M, int64_t V, int64_t ldz,
                                 const int32_t* target, float tau, float* logp, float* lse,
@@ -499,7 +500,9 @@ qlora_status qlora_logprobs_fwd(const void* Z, qlora_dtype z_dtype, int64_t M, i
                                 const float* d_logp, const float* d_entropy, void* dZ, void* stream);
 
 /* The gradient alone, from the lse (and, with d_entropy, the entropy) that
- * qlora_logprobs_fwd saved.  dZ may be Z itself. */
+ * qlora_logprobs_fwd saved.  dZ may be Z itself.  q is off by half a step of lse, times
+ * itself; from |lse| = 65536 on, where a step is 2^-7 and more, a row's sum is taken
+ * again from its logits. */
 qlora_status qlora_logprobs_bwd(const void* Z, qlora_dtype z_dtype, int64_t M, int64_t V, int64_t ldz,
                                 const int32_t* target, float tau, const float* lse,
                                 const float* entropy, const float* d_logp, const float* d_entropy,

@@ -53,11 +53,6 @@ namespace {
 
 constexpr float kLn2 = 0.693147182f;
 
-// A value that is the same in every lane, in a scalar register.
-__device__ __forceinline__ float uniform(float v) {
-  return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(v)));
-}
-
 // An order of floats as unsigned numbers (−0 and +0 equal; NaN lowest).
 __device__ __forceinline__ uint32_t order_of(float v) {
   if (v != v) return 0u;
@@ -306,10 +301,9 @@ __global__ __launch_bounds__(T, T == 1024 && (ZT != kF32 || VECS == 0) && !TOP ?
   if constexpr (VECS > 0) {
     ref = uniform(masked ? 0.f : z_max);
     rc = __fmul_rn(ref, c);
-    far = fabsf(rc) >= 0x1p19f;
+    far = fabsf(rc) >= kFarRow;
     if constexpr (ZT != kF32) {
-      // (2^(19 − ref's exponent))
-      cr = uniform(far ? __uint_as_float((273u - (__float_as_uint(ref) >> 23 & 255u)) << 23) : c);
+      cr = uniform(far ? far_scale(ref) : c);
       rc = __fmul_rn(ref, cr);
     } else if (far) {
       rc = 0.f;
@@ -444,7 +438,9 @@ __global__ __launch_bounds__(T, T == 1024 && (ZT != kF32 || VECS == 0) && !TOP ?
     R.store(a.dZ, i, u32x4_t{0u, 0u, 0u, 0u}, [](float) { return 0.f; });
 }
 
-// The gradient of 2,048 chunks of one row from what the forward pass saved.
+// The gradient of 2,048 chunks of one row from what the forward pass saved; of a far
+// row's (kFarLse) first part all of it, for in place the other parts' logits are needed
+// until its sum is known.
 constexpr int kPartThreads = 256, kPartVecs = 8, kPart = kPartThreads * kPartVecs;
 template <int ZT>
 __global__ __launch_bounds__(kPartThreads) void logprobs_gradient_kernel(LogprobsArgs a, float chi, float clo) {
@@ -461,27 +457,16 @@ __global__ __launch_bounds__(kPartThreads) void logprobs_gradient_kernel(Logprob
   const float lse = a.lse_in[m];
   const float g = (has && a.d_logp ? a.d_logp[m] : 0.f) / a.tau, h = (a.d_entropy ? a.d_entropy[m] : 0.f) / a.tau;
   const float entropy = a.d_entropy ? a.entropy_in[m] : 0.f;
-  const bool live = lse != -INFINITY && (g != 0.f || h != 0.f);
-  // lse·log2(e) in two parts
-  const float rhi = __fmul_rn(lse, 1.44269502f);
-  const float rlo = __builtin_fmaf(lse, 1.92596303e-8f, __builtin_fmaf(lse, 1.44269502f, -rhi));
-  auto log2_q = [&](float v) __attribute__((always_inline)) {
-    v = v < kMasked ? kMasked : v;  // (−infinity·clo might be +infinity; NaN stays)
-    return __builtin_fmaf(v, chi, -rhi) + __builtin_fmaf(v, clo, -rlo);
-  };
-  auto value = [&](float v, float own) __attribute__((always_inline)) {
-    const float l = log2_q(v), q = __builtin_amdgcn_exp2f(l);
-    float d = own - g * q;
-    if (h != 0.f) d -= h * q * (__builtin_fmaf(l, kLn2, entropy));
-    return d;
-  };
-  auto grad = [&](float v) __attribute__((always_inline)) { return live ? value(v, 0.f) : 0.f; };
-#pragma unroll
-  for (int j = 0; j < kPartVecs; ++j) {
-    const int i = i0 + j * kPartThreads;
-    if (i >= R.chunks_out) continue;
-    const u32x4_t v = R.only_columns(i, z[j]);
-    R.store(a.dZ, i, v, grad);
+  bool live = lse != -INFINITY && (g != 0.f || h != 0.f);
+  // chunk i of the gradient, from log2 q
+  auto write = [&](int i, const u32x4_t& v, auto&& log2_q) __attribute__((always_inline)) {
+    auto value = [&](float v, float own) __attribute__((always_inline)) {
+      const float l = log2_q(v), q = __builtin_amdgcn_exp2f(l);
+      float d = own - g * q;
+      if (h != 0.f) d -= h * q * (__builtin_fmaf(l, kLn2, entropy));
+      return d;
+    };
+    R.store(a.dZ, i, v, [&](float v) __attribute__((always_inline)) { return live ? value(v, 0.f) : 0.f; });
     // the given token's own element once more, by the thread that wrote its chunk
     if (live && has && (target + R.head) / C::N == i) {
       float zt = 0.f;
@@ -490,6 +475,31 @@ __global__ __launch_bounds__(kPartThreads) void logprobs_gradient_kernel(Logprob
         if (i * C::N + k - R.head == target) zt = C::get(v, k);
       store_rounded<ZT>(a.dZ, R.row + target, value(zt, g));
     }
+  };
+  if (live && fabsf(lse) >= kFarLse) {
+    if (blockIdx.y > 0) return;
+    const RowSum S = sum_row<ZT, kPartThreads>(R, chi);
+    live = S.sum != 0.f;
+    const float log2_s = log2f(S.sum);
+    auto log2_q = [&](float v) __attribute__((always_inline)) {
+      const float l = (v - S.ref) * chi - log2_s;
+      return l < kMasked ? kMasked : l;  // (times a q of 0; NaN stays)
+    };
+#pragma unroll 1
+    for (int i = tid; i < R.chunks_out; i += kPartThreads) write(i, R.only_columns(i, R.load(i)), log2_q);
+    return;
+  }
+  // lse·log2(e) in two parts
+  const float rhi = __fmul_rn(lse, 1.44269502f);
+  const float rlo = __builtin_fmaf(lse, 1.92596303e-8f, __builtin_fmaf(lse, 1.44269502f, -rhi));
+  auto log2_q = [&](float v) __attribute__((always_inline)) {
+    v = v < kMasked ? kMasked : v;  // (−infinity·clo might be +infinity; NaN stays)
+    return __builtin_fmaf(v, chi, -rhi) + __builtin_fmaf(v, clo, -rlo);
+  };
+#pragma unroll
+  for (int j = 0; j < kPartVecs; ++j) {
+    const int i = i0 + j * kPartThreads;
+    if (i < R.chunks_out) write(i, R.only_columns(i, z[j]), log2_q);
   }
 }
 

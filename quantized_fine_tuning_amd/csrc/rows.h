@@ -119,4 +119,57 @@ struct Row {
   }
 };
 
+// A value that is the same in every lane, in a scalar register.
+__device__ __forceinline__ float uniform(float v) {
+  return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(v)));
+}
+
+// What |max·log2(e)/tau| a row is far from zero from, and for one of 16-bit logits the power
+// of two that max times is in [2^19, 2^20) (logprobs.hip).
+constexpr float kFarRow = 0x1p19f;
+__device__ __forceinline__ float far_scale(float max) {
+  return __uint_as_float((273u - (__float_as_uint(max) >> 23 & 255u)) << 23);
+}
+
+// A log-sum-exp of this size and more is held in steps of 2^-7 and more (1,024 at
+// 1e10), no measure for the exponents of its row: a gradient from it takes the sum
+// again, by differences from the row's maximum.
+constexpr float kFarLse = 65536.f;
+
+// A row's maximum (0 if every column is masked) and Σ 2^((z − it)·c), for every thread
+// of a workgroup of T that reads the row twice.
+struct RowSum {
+  float ref, sum;
+};
+template <int ZT, int T>
+__device__ __forceinline__ RowSum sum_row(const Row<ZT>& R, float c) {
+  using C = Chunk<ZT>;
+  __shared__ float s_row[2][T / 64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  float high = -INFINITY, sum = 0.f;
+#pragma unroll 1
+  for (int i = threadIdx.x; i < R.chunks; i += T) {
+    const u32x4_t v = R.only_columns(i, R.load(i));
+#pragma unroll
+    for (int k = 0; k < C::N; k += 2) high = max3(high, C::get(v, k), C::get(v, k + 1));
+  }
+  high = wave_max(high);
+  if (lane == 0) s_row[0][wave] = high;
+  __syncthreads();
+  for (int w = 0; w < T / 64; ++w) high = fmaxf(high, s_row[0][w]);
+  const float ref = high > kMasked ? high : 0.f;
+#pragma unroll 1
+  for (int i = threadIdx.x; i < R.chunks; i += T) {
+    const u32x4_t v = R.only_columns(i, R.load(i));
+#pragma unroll
+    for (int k = 0; k < C::N; ++k) sum += __builtin_amdgcn_exp2f((C::get(v, k) - ref) * c);
+  }
+  sum = wave_sum(sum);
+  if (lane == 0) s_row[1][wave] = sum;
+  __syncthreads();
+  sum = 0.f;
+  for (int w = 0; w < T / 64; ++w) sum += s_row[1][w];
+  return {ref, sum};
+}
+
 }  // namespace qnf4

@@ -90,8 +90,8 @@ class Far:
 
 def check(got, want, lim, kind, what):
     got = L.numpy(got)
-    want = np.where(np.abs(want) > np.finfo(np.float32).max, np.sign(want) * INF, want)
     with np.errstate(invalid="ignore"):
+        want = np.where(np.abs(want) > np.finfo(np.float32).max, np.sign(want) * INF, want)
         far = np.abs(got - want) - lim - L.HALF[kind] * (np.abs(want) + lim) - L.TINY[kind]
     far = np.where(got == want, -1.0, far)  # (equal infinities)
     assert not np.isnan(got).any(), f"{what}: NaN"
@@ -129,3 +129,72 @@ def test_forward(z, V, ld, tau):
         bg = Far(Z, target, tau, V, g)
         likelihood = L.forward(Z, target, tau, V, 0, g, None, in_place=True)
         check(likelihood["dZ"], bg.dZ, bg.lim_dZ, z, "dZ of the likelihood")
+
+
+@pytest.mark.parametrize("z,V,ld", FORMS)
+@pytest.mark.parametrize("tau", [1.0, 0.1, 1e-5])
+def test_backward(z, V, ld, tau):
+    """From the saved sums.  fp32 holds a log-sum-exp of 65536 and more in steps of 2^-7 and
+    more; those rows find their sum again, the others count from the lse they are given."""
+    import torch as t
+    for base in BASES[z]:
+        print(f"far logprobs backward {z} {V} base={base} tau={tau}", flush=True)
+        Z, target, g, h = far_rows(V, ld, z, base, seed=V + 1)
+        g, h = g * tau, h * tau
+        target[4] = -100
+        h[3] = 0.0
+        target[6] = -1 if V % 2 else target[6]
+        out = L.forward(Z, target, tau, V)
+        lse, entropy = out["lse"].cpu(), out["entropy"].cpu()
+        far = lse.abs().numpy() >= 65536
+        gone = ((target < 0) & (h == 0)).numpy()
+        for dl, de in ((g, None), (None, h), (g, h)):
+            with_target = t.where(target < 0, 0, target)
+            own = None if dl is None else t.where(target < 0, 0.0, dl)
+            b = Far(Z, with_target, tau, V, own, de)
+            if (~far).any():
+                n = L.Bounds(Z[~far], target[~far], float(np.float32(tau)), V, None if dl is None else dl[~far],
+                             None if de is None else de[~far], lse[~far], entropy[~far])
+                b.dZ[~far] = n.dZ
+                # (an exponential below fp32's normal numbers is 0: 2^-126 times its factor, log q of -88 in it)
+                size = sum(np.abs(x.numpy()) * y for x, y in ((dl, 1), (de, 100)) if x is not None) / tau
+                b.lim_dZ[~far] = n.lim_dZ + 2.0 ** -126 * size[~far, None]
+            got = L.backward(Z, target, tau, V, lse, entropy, dl, de)
+            check(got, b.dZ, b.lim_dZ, z, "dZ")
+            assert not L.numpy(got)[gone].any()
+            assert t.equal(L.backward(Z, target, tau, V, lse, entropy, dl, de, in_place=True), got)
+
+
+def test_a_saved_lse_past_fp32():
+    """A logit over tau that fp32 does not hold: its lse is infinite, the gradient the differences'."""
+    import torch as t
+    Z, target, g, h = far_rows(5000, 5000, "f32", 3e36, seed=1)
+    tau = 1e-4
+    g, h = g * tau, h * tau
+    b = Far(Z, target, tau, 5000, g, h)
+    out = L.forward(Z, target, tau, 5000, 0, g, h)
+    check(out["dZ"], b.dZ, b.lim_dZ, "f32", "dZ")
+    lse = out["lse"].cpu()
+    assert (lse == INF).any()
+    got = L.backward(Z, target, tau, 5000, lse, out["entropy"].cpu(), g, h)
+    rows = (lse.abs() >= 65536).numpy()
+    check(got[t.from_numpy(rows).cuda()], b.dZ[rows], b.lim_dZ[rows], "f32", "dZ from the saved sums")
+
+
+@pytest.mark.parametrize("z,V,ld", [FORMS[0], FORMS[5]])
+def test_not_a_number_in_far_rows(z, V, ld):
+    import torch as t
+    Z, target, g, h = far_rows(V, ld, z, -1e10, seed=3)
+    Z[0, 5], Z[1, V // 2], Z[7, V - 1] = float("nan"), INF, float("nan")
+    out = L.forward(Z, target, 1.0, V, 4, g, h)
+    lse, entropy = out["lse"].cpu(), out["entropy"].cpu()
+    want = [m in (0, 1, 7) for m in range(8)]
+    back = L.backward(Z, target, 1.0, V, lse, entropy, g, h)
+    for x in (out["lse"], out["entropy"], out["logp"]):
+        assert x.isnan().tolist() == want
+    given = lse.clone()
+    given[[0, 1, 7]] = -1e10                # a number, of another pass over the logits
+    other = L.backward(Z, target, 1.0, V, given, t.nan_to_num(entropy), g, h)
+    for x in (out["dZ"], back, other):
+        assert x[:, :V].isnan().all(1).tolist() == want and x.isnan().any(1).tolist() == want
+        assert not x[:, V:].any()
