@@ -448,8 +448,8 @@ qlora_status qlora_gated_bwd(const qlora_nf4_t* gate, const qlora_nf4_t* up, con
  * whatever its logits are.  A logit of −infinity is a masked column (q = 0);
  * a row whose largest logit is below -1e30 has no columns: loss 0, zero
  * gradient, lse −infinity.  An entry of logit −infinity has p = 0.  Entries'
- * logits may be of any size, a row's largest logit over tau has to be a finite
- * fp32 number.  For any other token NaN stays NaN: a NaN or +infinity among its
+ * logits may be of any size, and so may the student's: all but lse comes from
+ * differences (lse is infinite where the largest logit over tau passes fp32).  For any other token NaN stays NaN: a NaN or +infinity among its
  * logits makes loss, lse and its columns of dZ NaN, one among its entries' logits
  * the loss and dZ at the entries' columns. */
 qlora_status qlora_distill_fwd(const void* Z, qlora_dtype z_dtype, int64_t M, int64_t V,

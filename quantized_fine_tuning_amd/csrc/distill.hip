@@ -12,10 +12,10 @@
 //
 // Everything in fp32, exponents in base 2 with c = log2(e)/tau.
 //
-// Forward (with or without the gradient): one workgroup per token.  With ref
-// the row's maximum and rc = fl(ref·c) an exponent is fma(z, c, −rc), off by
-// an ulp of itself; what rc was rounded by is the same factor for the whole
-// row and comes back into the log-sum-exp alone.  Bound by HBM: a row is read
+// Forward (with or without the gradient): one workgroup per token.  Exponents and log
+// q come from differences to the row's maximum, wherever the row lies; a row in
+// registers has them as one operation, fma(z, c, −rc) with rc = fl(max·c), and rows
+// far from zero in the ways that logprobs.hip gives.  Bound by HBM: a row is read
 // once and its gradient written once.  The row stays in registers between
 // the two (VECS 16-byte chunks a thread, the loads of all of them in flight
 // together); a row too long for that is read once for a running maximum and
@@ -134,9 +134,11 @@ __global__ __launch_bounds__(T, T == 1024 && (ZT != kF32 || VECS == 0) ? 8 : 1) 
     for (int k = 0; k < C::N; k += 2) high = max3(high, C::get(v, k), C::get(v, k + 1));
     return high;
   };
-  float rc = 0.f;
+  // (ref: the maximum, 0 while every column is masked)
+  float ref = 0.f, cr = c, rc = 0.f;
+  bool far = VECS == 0;
   auto e = [&](float x) __attribute__((always_inline)) {
-    return __builtin_amdgcn_exp2f(__builtin_fmaf(x, c, -rc));
+    return __builtin_amdgcn_exp2f(VECS == 0 ? (x - ref) * c : __builtin_fmaf(x, cr, -rc));
   };
   auto chunk_sum = [&](const u32x4_t& v, float sum) __attribute__((always_inline)) {
 #pragma unroll
@@ -152,7 +154,7 @@ __global__ __launch_bounds__(T, T == 1024 && (ZT != kF32 || VECS == 0) ? 8 : 1) 
     }
   } else {
     // running maximum and sum of this thread's chunks (as long as it has met
-    // masked columns alone, rc is 0 and they add zeros, a NaN itself)
+    // masked columns alone, ref is 0 and they add zeros, a NaN itself)
     for (int i0 = tid; i0 < R.chunks; i0 += NV * T) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) z[j] = R.load(i0 + j * T);
@@ -163,16 +165,16 @@ __global__ __launch_bounds__(T, T == 1024 && (ZT != kF32 || VECS == 0) ? 8 : 1) 
         high = chunk_max(z[j], high);
       }
       if (high > z_max) {
-        const float before = rc;
-        rc = high > kMasked ? __fmul_rn(high, c) : 0.f;
-        sum *= z_max > kMasked ? __builtin_amdgcn_exp2f(before - rc) : 0.f;
+        const float before = ref;
+        ref = high > kMasked ? high : 0.f;
+        sum *= z_max > kMasked ? e(before) : 0.f;
         z_max = high;
       }
 #pragma unroll
       for (int j = 0; j < NV; ++j) sum = chunk_sum(opaque(z[j]), sum);
     }
   }
-  const float own_max = z_max, own_rc = rc;
+  const float own_max = z_max, own_ref = ref;
   z_max = wave_max(z_max);
   if (lane == 0) s_max[wave] = z_max;
   __syncthreads();
@@ -182,12 +184,24 @@ __global__ __launch_bounds__(T, T == 1024 && (ZT != kF32 || VECS == 0) ? 8 : 1) 
   // (maxima pass over NaN: where they say that every column is masked the sum
   // has the last word, zero for masked columns, NaN where one is NaN)
   const bool masked = !(z_max > kMasked);
-  rc = masked ? 0.f : __fmul_rn(z_max, c);
+  ref = uniform(masked ? 0.f : z_max);
   if constexpr (VECS > 0) {
+    rc = __fmul_rn(ref, c);
+    far = fabsf(rc) >= kFarRow;
+    if constexpr (ZT != kF32) {
+      cr = uniform(far ? far_scale(ref) : c);
+      rc = __fmul_rn(ref, cr);
+    } else if (far) {
+      rc = 0.f;
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) z[j][k] = __float_as_uint(__uint_as_float(z[j][k]) - ref);
+    }
 #pragma unroll
     for (int j = 0; j < NV; ++j) sum = chunk_sum(z[j] = opaque(z[j]), sum);
   } else {
-    sum *= own_max > kMasked ? __builtin_amdgcn_exp2f(own_rc - rc) : 0.f;
+    sum *= own_max > kMasked ? e(own_ref) : 0.f;
   }
   sum = wave_sum(sum);
   if (lane == 0) s_sum[wave] = sum;
@@ -199,13 +213,14 @@ __global__ __launch_bounds__(T, T == 1024 && (ZT != kF32 || VECS == 0) ? 8 : 1) 
   const bool columns = !masked || sum != 0.f;
   const bool live = columns && w != 0.f && s.any;
   if (wave == 0) {
-    const float log_sum = logf(sum) - 0.693147182f * __builtin_fmaf(z_max, c, -rc);
+    // (log Σ exp((z − max)/tau), less what rc was rounded by)
+    const float log_sum = logf(sum) - (far ? 0.f : 0.693147182f * __builtin_fmaf(z_max, c, -rc));
     const float lse = columns ? z_max / a.tau + log_sum : -INFINITY;
     if (a.lse && lane == 0) a.lse[m] = lse;
     float loss = 0.f;
     if (live)
       for (int i = lane; i < a.k; i += 64)
-        if (s.p[i] != 0.f) loss += s.p[i] * ((s.t[i] - s.t_max) / a.tau - s.t_log - (s.z[i] / a.tau - lse));
+        if (s.p[i] != 0.f) loss += s.p[i] * ((s.t[i] - s.t_max) / a.tau - s.t_log - ((s.z[i] - ref) / a.tau - log_sum));
     loss = wave_sum(loss);
     if (lane == 0) a.loss[m] = live ? w * a.tau * a.tau * loss : 0.f;
   }
@@ -227,7 +242,10 @@ __global__ __launch_bounds__(T, T == 1024 && (ZT != kF32 || VECS == 0) ? 8 : 1) 
   }
   for (int i = R.chunks + tid; i < R.chunks_out; i += T)
     R.store(a.dZ, i, u32x4_t{0u, 0u, 0u, 0u}, [](float) { return 0.f; });
-  if (live) take_entries<ZT>(s, a, R.row, 0, R.V, g, [&](float x) { return e(x) * inv; });
+  if (live)
+    take_entries<ZT>(s, a, R.row, 0, R.V, g, [&](float x) {
+      return (ZT == kF32 && far ? __builtin_amdgcn_exp2f((x - ref) * c) : e(x)) * inv;
+    });
 }
 
 // The gradient of 2,048 chunks of one row from its saved log-sum-exp.
