@@ -449,9 +449,10 @@ qlora_status qlora_gated_bwd(const qlora_nf4_t* gate, const qlora_nf4_t* up, con
  * a row whose largest logit is below -1e30 has no columns: loss 0, zero
  * gradient, lse −infinity.  An entry of logit −infinity has p = 0.  Entries'
  * logits may be of any size, and so may the student's: all but lse comes from
- * differences (lse is infinite where the largest logit over tau passes fp32).  For any other token NaN stays NaN: a NaN or +infinity among its
- * logits makes loss, lse and its columns of dZ NaN, one among its entries' logits
- * the loss and dZ at the entries' columns. */
+ * differences (lse is infinite where the largest logit over tau passes fp32, the
+ * loss where an entry's log q does).  For any other token NaN stays NaN: a NaN or
+ * +infinity among its logits makes loss, lse and its columns of dZ NaN, one among
+ * its entries' logits the loss and dZ at the entries' columns. */
 qlora_status qlora_distill_fwd(const void* Z, qlora_dtype z_dtype, int64_t M, int64_t V,
                                int64_t ldz, const void* top, qlora_dtype top_dtype,
                                const int32_t* top_index, int32_t k, float tau,
@@ -459,7 +460,9 @@ qlora_status qlora_distill_fwd(const void* Z, qlora_dtype z_dtype, int64_t M, in
                                void* stream);
 
 /* The gradient alone, from the lse that qlora_distill_fwd saved; weight is
- * then w times the gradient that reaches loss[m].  dZ may be Z itself. */
+ * then w times the gradient that reaches loss[m].  dZ may be Z itself.  q is off by
+ * half a step of lse, times itself; from |lse| = 65536 on, where a step is 2^-7 and
+ * more, a row's sum is taken again from its logits. */
 qlora_status qlora_distill_bwd(const void* Z, qlora_dtype z_dtype, int64_t M, int64_t V,
                                int64_t ldz, const void* top, qlora_dtype top_dtype,
                                const int32_t* top_index, int32_t k, float tau,

@@ -248,7 +248,9 @@ __global__ __launch_bounds__(T, T == 1024 && (ZT != kF32 || VECS == 0) ? 8 : 1) 
     });
 }
 
-// The gradient of 2,048 chunks of one row from its saved log-sum-exp.
+// The gradient of 2,048 chunks of one row from its saved log-sum-exp; of a far row's
+// (kFarLse) first part all of it, for in place the other parts' logits are needed until
+// its sum is known.
 constexpr int kPartThreads = 256, kPartVecs = 8, kPart = kPartThreads * kPartVecs;
 template <int ZT, int TT>
 __global__ __launch_bounds__(kPartThreads) void distill_gradient_kernel(DistillArgs a, float chi, float clo) {
@@ -271,35 +273,52 @@ __global__ __launch_bounds__(kPartThreads) void distill_gradient_kernel(DistillA
   }
   bool live = lse != -INFINITY && w != 0.f;  // (a NaN lse, of a row with a NaN or an infinity, is no masked row's)
   const float g = w * a.tau;
+  const bool far = live && fabsf(lse) >= kFarLse;
+  if (far && blockIdx.y > 0) return;
+  auto rest = [&](auto&& q) __attribute__((always_inline)) {
+    auto grad = [&](float x) __attribute__((always_inline)) { return live ? g * q(x) : 0.f; };
+    auto write = [&]() __attribute__((always_inline)) {
+      if (far) {
+#pragma unroll 1
+        for (int i = tid; i < R.chunks_out; i += kPartThreads) R.store(a.dZ, i, R.only_columns(i, R.load(i)), grad);
+        return;
+      }
+#pragma unroll
+      for (int j = 0; j < kPartVecs; ++j)
+        if (i0 + j * kPartThreads < R.chunks_out) {
+          z[j] = R.only_columns(i0 + j * kPartThreads, z[j]);
+          R.store(a.dZ, i0 + j * kPartThreads, z[j], grad);
+        }
+    };
+    write();
+    // (the exponentials are written before the entries are waited for; a row
+    // without entries gets its zeros now)
+    if (tid < 64) {
+      if (!in_place) load_entries<ZT, TT>(s, a, m, R.row, tid);
+      entry_softmax(s, a.k, a.tau, tid);
+    }
+    __syncthreads();
+    if (live && !s.any) {
+      live = false;
+      write();
+    }
+    const int v0 = far ? 0 : kPart * (int)blockIdx.y * C::N - R.head, v1 = far ? R.V : v0 + kPart * C::N;
+    if (live) take_entries<ZT>(s, a, R.row, std::max(v0, 0), std::min(v1, R.V), g, q);
+  };
+  if (far) {
+    const RowSum S = sum_row<ZT, kPartThreads>(R, chi);
+    live = S.sum != 0.f;
+    const float inv = 1.0f / S.sum;
+    rest([&](float x) __attribute__((always_inline)) { return __builtin_amdgcn_exp2f((x - S.ref) * chi) * inv; });
+    return;
+  }
   // lse·log2(e) in two parts
   const float rhi = __fmul_rn(lse, 1.44269502f);
   const float rlo = __builtin_fmaf(lse, 1.92596303e-8f, __builtin_fmaf(lse, 1.44269502f, -rhi));
-  auto q = [&](float x) __attribute__((always_inline)) {
+  rest([&](float x) __attribute__((always_inline)) {
     x = x < kMasked ? kMasked : x;  // (−infinity·clo might be +infinity; NaN stays)
     return __builtin_amdgcn_exp2f(__builtin_fmaf(x, chi, -rhi) + __builtin_fmaf(x, clo, -rlo));
-  };
-  auto grad = [&](float x) __attribute__((always_inline)) { return live ? g * q(x) : 0.f; };
-#pragma unroll
-  for (int j = 0; j < kPartVecs; ++j)
-    if (i0 + j * kPartThreads < R.chunks_out) {
-      z[j] = R.only_columns(i0 + j * kPartThreads, z[j]);
-      R.store(a.dZ, i0 + j * kPartThreads, z[j], grad);
-    }
-  // (the exponentials are written before the entries are waited for; a row
-  // without entries gets its zeros now)
-  if (tid < 64) {
-    if (!in_place) load_entries<ZT, TT>(s, a, m, R.row, tid);
-    entry_softmax(s, a.k, a.tau, tid);
-  }
-  __syncthreads();
-  if (live && !s.any) {
-    live = false;
-#pragma unroll
-    for (int j = 0; j < kPartVecs; ++j)
-      if (i0 + j * kPartThreads < R.chunks_out) R.store(a.dZ, i0 + j * kPartThreads, z[j], grad);
-  }
-  const int v0 = kPart * (int)blockIdx.y * C::N - R.head;
-  if (live) take_entries<ZT>(s, a, R.row, std::max(v0, 0), std::min(v0 + kPart * C::N, R.V), g, q);
+  });
 }
 
 template <int ZT, int TT>
