@@ -588,7 +588,8 @@ __device__ __noinline__ GateGradient gate_gradient_exact(int act, float g, float
     slope = kGeluSlope * (1.0 + 3.0 * kGeluCube * x * x);
   }
   const double s = 1.0 / (1.0 + exp(-h)), r = 1.0 / (1.0 + exp(h));
-  return {(float)((double)dh * u * (s * (1.0 + x * r * slope))), (float)((double)dh * (x * s))};
+  const double t = r > 0.0 ? x * r * slope : 0.0;  // (0 in the limit of an infinite g)
+  return {(float)((double)dh * u * (s * (1.0 + t))), (float)((double)dh * (x * s))};
 }
 // In 32 bits, and whether both round as the exact values do.  With u = 2^-24 and an
 // exponential and a reciprocal of 1 ulp, σ(−|h|) is off by (6 + 2|h|)u of itself and
