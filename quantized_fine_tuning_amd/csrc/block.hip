@@ -46,9 +46,9 @@ unsigned cdiv(int64_t a, int64_t b) { return (unsigned)((a + b - 1) / b); }
 // whose operand fragments are transposing reads).  Bound by reading L; both
 // operands are copied straight into a ring of LDS stages of 64 reduction
 // elements, all but one in flight.  4 waves: NJ across the ranks, 4/NJ across the
-// rows.  (4096 tokens, K = 4096, r = 64, T with dropout 16.5 us, 33 MB at 2.5 TB/s, the
-// generator's calls beside the products; V of two layers of 11008 rows 44 us, 180 MB
-// at 4.1.  V in the kernel that finds dG and dU, from its registers through LDS: 124 us
+// rows.  (4096 tokens, K = 4096, r = 64, T with dropout 15.1 us, 34 MB of X at 2.2 TB/s, the
+// generator's calls beside the products; V of two layers of 11008 rows 45 us, 180 MB of dG
+// and dU at 4.0.  V in the kernel that finds dG and dU, from its registers through LDS: 124 us
 // for both, against 75 + 44: half the waves, and a barrier between what they load and
 // what they multiply.)
 // ---------------------------------------------------------------------------
@@ -351,8 +351,9 @@ __global__ __launch_bounds__(256) void block_factor_kernel(FactorJob t, FactorJo
 // their own layouts (X with its dropped elements cleared by the wave that copied
 // them); the MFMA operands, 8 consecutive tokens of one column, are transposing
 // reads.  One unit writes the gradient itself, several partial sums that are added
-// in unit order.  (4096 tokens, r = 64: one layer of 4096 x 11008 57 us, both of a pair
-// of 11008 x 4096 88, 246 MB of X, dG and dU at 2.8 TB/s; LDS reads of three parts of S
+// in unit order.  (4096 tokens, r = 64: one layer of 4096 x 11008 53 us, both of a pair
+// of 11008 x 4096 82, 246 MB of X, dG and dU at 3.0 TB/s, the units' sum in a launch after
+// it 5 and 6 more; LDS reads of three parts of S
 // for each column block, the generator for X of either layer, 10 us of it, and memory
 // share the time.  256 columns a workgroup gained nothing.)
 // ---------------------------------------------------------------------------
@@ -791,6 +792,7 @@ hipError_t launch_block_fwd(const BlockView& b, const uint16_t* X, int64_t M, vo
     return hipGetLastError();
   };
   if (M <= kMidTokens) {
+    // (at every rank; launch_down's tiles were not measured here)
     float* const none = nullptr;
     block_few_down_kernel<<<dim3((unsigned)M, (unsigned)(b.r / kFewRanks), (unsigned)b.layers), 256, 0, st>>>(
         X, M, K, b.A[0], b.A[1], b.r, b.drop, b.scale, T, none, S);

@@ -561,10 +561,12 @@ __global__ __launch_bounds__(64 * WV) void gemv_adapters_kernel(Nf4View W, const
 // 32.2 us.)  X is staged in LDS (XL) or loaded beside the codes.  The threads that
 // share an output are as many as M leaves.
 //
-// Bound by the decode: 77 % of the vector units' time and 40 % of the LDS's.  (Two
-// 11008 x 4096 weights, graph-replayed with T's kernel: one token, r = 16, 21.8 us, of
-// them 17.4 this kernel's, 47.7 MB at 2.7 TB/s; 13 tokens, r = 64, 24.4.  Both layers
-// in every wave took 22.4 for one token where this form took 21.2, two block groups
+// Bound by the decode and by latency: vector instructions issue in 73 % of the cycles
+// in which a compute unit holds waves, 41 % of the launch's, whose start and end are
+// waiting; no unit is full.  (Two 11008 x 4096 weights, whole calls with T's kernel: one
+// token, r = 16, 20.9 us, of them 18.2 this kernel's, 47.7 MB at 2.6 TB/s; 13 tokens, r =
+// 64, 24.4 and 21.1.  Both layers in every wave took 22.4 for one token where this
+// form, replayed from a graph like the rest here, took 21.2, two block groups
 // ahead 21.3; X's fragments kept in registers across row groups 27.4, their spills'
 // waits holding up the codes; levels looked up in pairs, 64 KB of them, a third
 // fewer vector instructions, 21.9 for want of room for more than one workgroup.)
@@ -858,7 +860,10 @@ hipError_t launch_gated_gemv(const BlockView& b, const uint16_t* X, int64_t M, c
   }
   // as many workgroups as are resident at once: three of 8 waves per compute unit
   // where X is small (one of 16: one token 24.5 us, not 21.2) and four waves a layer
-  // hold the ranks, one of 16 beside a larger X in LDS, whose room sq and s_acc leave
+  // hold the ranks, one of 16 beside a larger X in LDS, whose room sq and s_acc leave.
+  // (An X past that is read again for every row group, and registers spill: r = 64, 13824
+  // x 5120, 14 tokens 38.5 us, 15 69, 16 72, 17 in mid.hip's kernels 45; 22016 x 8192, 8
+  // tokens 65, 9 115, 16 144, 17 96.)
   if (xb <= 32 * 1024 && b.r <= 128)
     QNF4_GEMV_LAUNCH(4, true, 3)
   else if (xb <= (size_t)142 * 1024)

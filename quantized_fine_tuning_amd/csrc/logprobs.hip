@@ -30,14 +30,16 @@
 // registers between its passes (or, too long for that, read again from the
 // caches).  4096 x 32000 bf16 with the gradient 100 us, 524 MB at 5.2 TB/s, more than a
 // large copy's rate; the values alone 40.  Few rows are latency: 32 x 32000 4.5 us, with
-// 20 alternatives and entropy 8.9.
+// 20 alternatives and entropy 9.0.
 //
 // The k most likely columns, equal logits by their index: every thread's largest
 // logit is known from the maximum, and the k-th largest of those is a bound that
 // at least k columns reach and few more do.  Those go to a list in LDS whose
 // order is then found by counting, so that it does not depend on who came first.
-// Where more reach it than the list holds (a row of equal logits), the k-th
-// largest is found bit by bit, and so is the last index among its equals.
+// Where a wave has more of them than its part of the list holds (equal logits, or
+// likely columns side by side, as where logits fall with the index), the k-th largest
+// is found bit by bit, and so is the last index among its equals, in 62 passes over
+// the row (32 x 32000, k = 64, such logits 242 us, independent ones 11).
 //
 // Gradient from a saved log-sum-exp (and entropy): no sums over the row, so rows
 // are cut into parts of 2,048 chunks, a workgroup each; log2 q takes z·c −
@@ -440,7 +442,8 @@ __global__ __launch_bounds__(T, T == 1024 && (ZT != kF32 || VECS == 0) && !TOP ?
 
 // The gradient of 2,048 chunks of one row from what the forward pass saved; of a far
 // row's (kFarLse) first part all of it, for in place the other parts' logits are needed
-// until its sum is known.
+// until its sum is known (4096 x 32000 bf16, all rows far, 185 us, near 107).  Rows without
+// a gradient are read like any other.
 constexpr int kPartThreads = 256, kPartVecs = 8, kPart = kPartThreads * kPartVecs;
 template <int ZT>
 __global__ __launch_bounds__(kPartThreads) void logprobs_gradient_kernel(LogprobsArgs a, float chi, float clo) {

@@ -1,7 +1,7 @@
 // Base products of a batch of few tokens (17 to kMidTokens) that carry different
 // adapters (AdapterGemmArgs), or one that may have dropout (DenseGemmArgs: in dX the
 // adapter's share is summed and masked before the base product; 61 tokens, 4096 x
-// 4096, 17.5 us of 28.8 for the pass), gfx950.  The dequant-in-tile GEMMs (fwd.hip,
+// 4096, 17.6 us of 26.1 for the pass), gfx950.  The dequant-in-tile GEMMs (fwd.hip,
 // dx.hip) decode 256 weight rows for 256 tokens and are bound by that decode long
 // before the tokens are many; here a weight fragment goes from its codes to the MFMA
 // operand with as little between as its layout allows, and every tile of 16
