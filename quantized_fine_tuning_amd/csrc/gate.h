@@ -9,8 +9,8 @@ namespace qnf4 {
 
 constexpr double kGeluSlope = 1.5957691216057307, kGeluCube = 0.044715;  // 2·sqrt(2/π)
 
-// act(g), off by its exponent's rounding: with u = 2^-24, (6 + 2|h|)u of itself for SiLU,
-// (6 + 7|h|)u for GELU (h is off by 5u of itself); below 2^-126 a step of fp32.  FAR:
+// act(g), off by its exponent's roundings: with u = 2^-24, (6 + 3|h|)u of itself for SiLU,
+// (6 + 8|h|)u for GELU (h is off by 5u of itself); below 2^-126 a step of fp32.  FAR:
 // whether g may be below far_gate(act).  There exp(−h) passes 2^95 and more, the
 // reciprocal of 1 + exp(−h) is exp(h) in fp32, and exp(h) is taken 2^64 times as large:
 // the reciprocal instruction gives 0 for results below 2^-126, from h = −87 on, where g
